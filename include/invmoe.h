@@ -66,6 +66,14 @@ extern "C" {
 #define INVMOE_ERR_CUDA                -5  /* a CUDA runtime/driver call or a launch failed      */
 #define INVMOE_ERR_DEVICE_TIMEOUT      -6  /* a kernel's bounded wait ran out (invmoe_check)     */
 
+/* Element types of arguments that take more than one. */
+#define INVMOE_BF16 0
+#define INVMOE_F32  1
+
+/* Expert scores (moe_route_select). */
+#define INVMOE_SCORE_SIGMOID 0
+#define INVMOE_SCORE_SOFTMAX 1
+
 /* Library version (major*10000 + minor*100 + patch). */
 int invmoe_version(void);
 
@@ -456,6 +464,129 @@ int moe_route_backward(const void* x, const void* w_router, const int32_t* topk_
                        const float* dgate, const float* dxp, const int32_t* plan, const float* dx_shared,
                        int T, int H, int E, int k, float* dx, float* dw_router, void* workspace,
                        size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The 8-bit block: residual + norm -> scored routing -> e4m3 experts
+ *
+ * add_rms_norm makes the router's bf16 input and the experts' e4m3 input in one
+ * pass; moe_router_logits and moe_route_select choose the experts;
+ * moe_permute_fp8, moe_grouped_swiglu_fp8 and moe_grouped_down_fp8 run them;
+ * moe_combine ends the layer.  Every per-token output depends on that token
+ * alone, with one reduction order (the conventions above).
+ *
+ * e4m3 tensors (finite up to 448, no infinity) are passed as void*, one byte per
+ * element, row-major, with fp32 scales: an activation [rows, cols] has
+ * scale[rows, ceil(cols / 128)], a weight [rows, cols] scale[ceil(rows / 128),
+ * ceil(cols / 128)]; an element stands for its value times its block's scale.
+ * Quantising a block: scale = max(amax / 448, 2^-126) and
+ * q = e4m3_rne(clip(v * (1 / scale), +-448)), every step rounded to fp32; amax is
+ * the largest absolute value that is not NaN, a NaN stays NaN, and a block with
+ * an infinity gets an infinite scale (its infinities become NaN, the rest 0).
+ * Scale pointers are 4-byte aligned; the other pointers are 16-byte aligned.
+ * ------------------------------------------------------------------------- */
+
+/* logits [T, E] fp32 = x [T, H] bf16 . w_router [E, H]^T: moe_route_topk's router
+ * GEMM alone (the same bits).  workspace: at least 256 bytes.
+ * Shapes: H % 64 == 0, E % 4 == 0, E <= 1024. */
+int moe_router_logits(const void* x, const void* w_router, int T, int H, int E, float* logits, void* workspace,
+                      size_t ws_bytes, void* stream);
+
+/* Experts and weights from logits [T, E] fp32 (any E <= 1024).
+ *   score_e  = 1 / (1 + exp(-l_e))  or  exp(l_e - max l) / sum_i exp(l_i - max l)
+ *   choice_e = score_e + bias_e if bias [E] fp32 is given, else l_e (the scores increase
+ *              with it: the same choice, undisturbed by scores that round to the same value)
+ *   groups   the E experts are n_group groups of E / n_group neighbours; only the
+ *            topk_group groups of the largest value stay.  A group's value is the sum of
+ *            its two largest choices if bias is given (its one choice for groups of one),
+ *            else its largest choice
+ *   topk_idx [T, k] int32: the k largest choices left, largest first
+ *   topk_w   [T, k] fp32 = scale * score_j, divided first by sum_j score_j (rank order) if
+ *            renormalize; a sum of 0 (a row of -inf logits) gives weights of 0
+ * Ties, of experts and of groups, go to the lower index; -0 ties with +0; NaN ranks below
+ * every number.  The softmax denominator is summed in fixed point (steps of 2^-42), so no
+ * choice depends on a summation order.
+ * plan (nullable): also builds the dispatch plan (invmoe_plan_len) from the choice; the
+ * workspace (only used then) is invmoe_workspace_size(T, H, E, k, ...) bytes.
+ * Shapes: 1 <= n_group <= 32 dividing E, 1 <= topk_group <= n_group,
+ * 1 <= k <= min(32, topk_group * E / n_group). */
+int moe_route_select(const float* logits, const float* bias, int T, int E, int k, int score, int n_group,
+                     int topk_group, int renormalize, float scale, int32_t* topk_idx, float* topk_w, int32_t* plan,
+                     void* workspace, size_t ws_bytes, void* stream);
+
+/* Gradient of topk_w with respect to the logits, the choice held fixed (the bias has none):
+ * dw [T, k] fp32 -> dlogits [T, E] fp32 and/or dlogits_bf16 [T, E] (each nullable, not both).
+ * An entry of topk_idx outside [0, E) takes no part. */
+int moe_route_select_backward(const float* logits, const int32_t* topk_idx, const float* dw, int T, int E, int k,
+                              int score, int renormalize, float scale, float* dlogits, void* dlogits_bf16,
+                              void* stream);
+
+/* moe_route_backward's GEMMs and sum for given dlogits_bf16 [T, E]:
+ * dx [T, H] fp32 = dlogits W_router + (the slots' dxp) + dx_shared, dw_router [E, H] fp32
+ * (nullable) = dlogits^T x.  workspace: at least 256 bytes.  Shapes: H % 64 == 0, E % 8 == 0. */
+int moe_router_backward(const void* x, const void* w_router, const void* dlogits_bf16, const float* dxp,
+                        const int32_t* plan, const float* dx_shared, int T, int H, int E, int k, float* dx,
+                        float* dw_router, void* workspace, size_t ws_bytes, void* stream);
+
+/* r = x + residual (fp32 sum, rounded to the residual's type and stored in residual_out, which
+ * may be residual itself; without a residual r = x and residual_out is NULL);
+ * rstd = 1 / sqrt(mean(r^2) + eps) in fp32; y = (r * rstd) * weight;
+ * out [T, H] bf16 (nullable) = y; q [T, H] e4m3 with scale [T, ceil(H / 128)] (nullable,
+ * together) = y quantised from fp32; rstd [T] fp32 (nullable).  One of out and q is given.
+ * x, residual: INVMOE_BF16 or INVMOE_F32; weight [H] bf16.  Shapes: H % 16 == 0, H <= 32768. */
+int add_rms_norm(const void* x, int x_type, const void* residual, int residual_type, const void* weight, int T, int H,
+                 float eps, void* residual_out, void* out, void* q, float* scale, float* rstd, void* stream);
+
+/* Workspace of add_rms_norm_backward with dweight (status block, then partial sums). */
+size_t rms_norm_backward_workspace_size(int T, int H);
+
+/* Backward of add_rms_norm at the stored r (x here: residual_out, or x without a residual) and
+ * its rstd; rounding and quantisation are passed straight through:
+ *   g = dy * weight, n = r * rstd
+ *   dx = rstd * (g - n * mean(g * n)) + dres      [T, H], x's type: the gradient of r, so of
+ *                                                  both x and residual
+ *   dweight = sum_t dy * n                        [H] fp32 (nullable), rows in a fixed order
+ * dy [T, H] of dy_type; dres [T, H] of x's type (nullable): the gradient that reaches r from
+ * the residual stream; dx may be dres.  workspace is used for dweight alone. */
+int add_rms_norm_backward(const void* dy, int dy_type, const void* x, int x_type, const void* weight,
+                          const float* rstd, const void* dres, int T, int H, void* dx, float* dweight, void* workspace,
+                          size_t ws_bytes, void* stream);
+
+/* x [banks, rows, cols] bf16 or fp32 -> q e4m3 of the same shape and its scales:
+ * block_rows 1: [banks, rows, ceil(cols / 128)] (activations); block_rows 128:
+ * [banks, ceil(rows / 128), ceil(cols / 128)] (weights).  Shapes: cols % 16 == 0. */
+int fp8_quantize(const void* x, int x_type, int banks, int rows, int cols, int block_rows, void* q, float* scale,
+                 void* stream);
+
+/* xp[r] = q[row_token[r]] and its scales for every permuted row r of the plan.
+ * q [T, H] e4m3, scale [T, ceil(H / 128)], xp [T*k, H], xp_scale [T*k, ceil(H / 128)].
+ * Shapes: H % 16 == 0, H <= 32768, k <= 32. */
+int moe_permute_fp8(const void* q, const float* scale, const int32_t* plan, int T, int H, int E, int k, void* xp,
+                    float* xp_scale, void* stream);
+
+/* out[m, n] = sum over blocks of 128 along K, ascending, of
+ *   (a_scale[m, kb] * b_scale[n / 128, kb]) * (sum_{k in kb} a[m, k] * b[n, k])
+ * the inner sum on the tensor cores in fp32, the outer one an fp32 fused multiply-add per
+ * block; out [M, N] bf16 or fp32.  a [M, K] e4m3 (scale per row), b [N, K] e4m3 (scale per
+ * 128 x 128).  workspace: at least 256 bytes (status).  Shapes: K % 16 == 0, any M, N. */
+int fp8_gemm(const void* a, const float* a_scale, const void* b, const float* b_scale, int M, int N, int K, void* out,
+             int out_type, void* workspace, size_t ws_bytes, void* stream);
+
+/* The experts' gate/up product, SwiGLU and re-quantisation: for every expert e and its rows r,
+ *   g, u = fp8_gemm of xp[r] with w13[e] (gate rows 0..F-1, up rows F..2F-1), not stored
+ *   h[r] = g / (1 + exp(-g)) * u in fp32, quantised per 128 columns: h [T*k, F] e4m3 with
+ *          h_scale [T*k, F / 128]
+ * w13 [E, 2F, H] e4m3, w13_scale [E, 2F / 128, ceil(H / 128)].  plan as moe_grouped_ffn's;
+ * NULL with E = k = 1: one expert for all T rows (a shared expert).
+ * workspace: at least 256 bytes.  Shapes: H % 16 == 0, F % 128 == 0, E <= 1024. */
+int moe_grouped_swiglu_fp8(const void* xp, const float* xp_scale, const int32_t* plan, const void* w13,
+                           const float* w13_scale, int T, int H, int E, int k, int F, void* h, float* h_scale,
+                           void* workspace, size_t ws_bytes, void* stream);
+
+/* The experts' down product: y [T*k, H] fp32 = fp8_gemm of h[r] with w2[e] [H, F].
+ * w2 [E, H, F] e4m3, w2_scale [E, ceil(H / 128), F / 128]; plan, workspace, shapes as above. */
+int moe_grouped_down_fp8(const void* h, const float* h_scale, const int32_t* plan, const void* w2,
+                         const float* w2_scale, int T, int H, int E, int k, int F, float* y, void* workspace,
+                         size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * rl_token_loss -- IcePop-masked clipped policy loss and DIS weights per token

@@ -45,6 +45,18 @@ PROTOTYPES = {
                                       _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _sz, _vp]),
     "moe_route_backward": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _sz,
                                 _vp]),
+    "moe_router_logits": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, _sz, _vp]),
+    "moe_route_select": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_route_select_backward": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp]),
+    "moe_router_backward": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _sz, _vp]),
+    "add_rms_norm": (_i, [_vp, _i, _vp, _i, _vp, _i, _i, _f, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "rms_norm_backward_workspace_size": (_sz, [_i, _i]),
+    "add_rms_norm_backward": (_i, [_vp, _i, _vp, _i, _vp, _vp, _vp, _i, _i, _vp, _vp, _vp, _sz, _vp]),
+    "fp8_quantize": (_i, [_vp, _i, _i, _i, _i, _i, _vp, _vp, _vp]),
+    "moe_permute_fp8": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp]),
+    "fp8_gemm": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _vp, _sz, _vp]),
+    "moe_grouped_swiglu_fp8": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _sz, _vp]),
+    "moe_grouped_down_fp8": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _sz, _vp]),
     "invmoe_gemm_bf16": (_i, [_vp, _vp, _i, _i, _i, _vp, _i, _vp, _sz, _vp]),
     "invmoe_debug_timeout_probe": (_i, [_vp, _sz, _i, _vp]),
     "invmoe_profile_enable": (_i, [_i]),

@@ -8,6 +8,7 @@
 #include <mutex>
 #include <vector>
 
+#include "checks.h"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -16,12 +17,6 @@ namespace invmoe {
 namespace {
 thread_local char g_last_error[512] = "";
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-size_t route_ws(int T, int E) {
-  const size_t NC = (static_cast<size_t>(T) + kDispatchChunk - 1) / kDispatchChunk;
-  return align_up(NC * static_cast<size_t>(E) * sizeof(int32_t), 256);
-}
 size_t replay_ws(int T, int E, int k) {
   return route_ws(T, E) + align_up(static_cast<size_t>(T) * k * sizeof(int32_t), 256);
 }
@@ -62,8 +57,6 @@ BwdLayout bwd_layout(int T, int E, int k, int F, int Fs) {
   return L;
 }
 
-unsigned int* status_word(void* ws) { return static_cast<unsigned int*>(ws); }
-uint8_t* scratch(void* ws) { return static_cast<uint8_t*>(ws) + kStatusBytes; }
 }  // namespace
 
 int set_error(int code, const char* fmt, ...) {
@@ -208,6 +201,42 @@ GemmVariant router_variant(int T, int E) {
   return units64 <= sms ? GV_F32_BN64_MT1 : GV_F32_BN128_MT1;
 }
 
+// The router's part of the layer backward from dlogits [T, E] bf16: dx = dlogits W_router plus the expert slots' and
+// the shared expert's parts, dw_router = dlogits^T x.
+int router_backward_run(const void* dlog, const void* x, const void* w_router, const float* dxp, const int32_t* plan,
+                        const float* dx_shared, int T, int H, int E, int k, float* dx, float* dw_router,
+                        unsigned int* status, cudaStream_t st) {
+  // router part of dx: dlog [T, E] (K = E) times w_router [E, H] read MN-major
+  GemmCall a{};
+  a.name = "router_dx";
+  a.variant = GV_PAIR_F32_BMN;
+  a.A = dlog; a.a_rows = T; a.B = w_router; a.b_rows = H; a.K = E; a.N = H; a.M = T;
+  a.out = dx; a.ldo = H; a.status = status;
+  int rc = gemm_run(a, st);
+  if (rc) return rc;
+  if (dw_router) {
+    GemmCall b{};
+    b.name = "router_dw";
+    b.variant = GV_PAIR_F32_AMN_BMN;
+    b.A = dlog; b.a_rows = E; b.B = x; b.b_rows = H; b.K = T; b.N = H; b.M = E;
+    b.out = dw_router; b.ldo = H; b.status = status;
+    if ((rc = gemm_run(b, st))) return rc;
+  }
+  const int32_t* slot_row = plan + 2 * E + 1 + static_cast<long long>(T) * k;
+  return unpermute_sum_launch(dxp, slot_row, dx_shared, T, H, k, dx, st);
+}
+
+// logits [T, E] = x w_router^T on the router's tile for this batch.
+int router_gemm_run(const void* x, const void* w_router, int T, int H, int E, float* logits, unsigned int* status,
+                    cudaStream_t st) {
+  GemmCall g{};
+  g.name = "router_gemm";
+  g.variant = router_variant(T, E);
+  g.A = x; g.a_rows = T; g.B = w_router; g.b_rows = E; g.K = H; g.N = E; g.M = T; g.G = 0;
+  g.out = logits; g.ldo = E; g.status = status;
+  return gemm_run(g, st);
+}
+
 int shared_expert_run(const void* x, const void* ws13, const void* ws2, int T, int H, int F_shared, float* y_shared,
                       void* hs, unsigned int* status, cudaStream_t st, int* sched) {
   // at most 64 tokens (decode): the small-M kernel, one 32-column tile of h (64 of y) per CTA and four K
@@ -233,14 +262,6 @@ int shared_expert_run(const void* x, const void* ws13, const void* ws2, int T, i
 }  // namespace invmoe
 
 using namespace invmoe;
-
-#define REQUIRE(cond, code, ...)             \
-  do {                                       \
-    if (!(cond)) return set_error(code, __VA_ARGS__); \
-  } while (0)
-
-#define REQUIRE_PTR(p) REQUIRE((p) != nullptr, INVMOE_ERR_INVALID_ARG, "%s is NULL", #p)
-#define REQUIRE_ALIGNED(p) REQUIRE(aligned16(p), INVMOE_ERR_MISALIGNED, "%s is not 16-byte aligned", #p)
 
 extern "C" {
 
@@ -864,26 +885,10 @@ int moe_route_backward(const void* x, const void* w_router, const int32_t* topk_
   if (dx_shared) REQUIRE_ALIGNED(dx_shared);
   if (dw_router) REQUIRE_ALIGNED(dw_router);
   void* dlog = scratch(workspace) + L.dlog;
-  unsigned int* status = status_word(workspace);
-  int rc = router_bwd_launch(topk_idx, topk_w, dgate, T, E, k, dlog, st);
+  const int rc = router_bwd_launch(topk_idx, topk_w, dgate, T, E, k, dlog, st);
   if (rc) return rc;
-  // router part of dx: dlog [T, E] (K = E) times w_router [E, H] read MN-major
-  GemmCall a{};
-  a.name = "router_dx";
-  a.variant = GV_PAIR_F32_BMN;
-  a.A = dlog; a.a_rows = T; a.B = w_router; a.b_rows = H; a.K = E; a.N = H; a.M = T;
-  a.out = dx; a.ldo = H; a.status = status;
-  if ((rc = gemm_run(a, st))) return rc;
-  if (dw_router) {
-    GemmCall b{};
-    b.name = "router_dw";
-    b.variant = GV_PAIR_F32_AMN_BMN;
-    b.A = dlog; b.a_rows = E; b.B = x; b.b_rows = H; b.K = T; b.N = H; b.M = E;
-    b.out = dw_router; b.ldo = H; b.status = status;
-    if ((rc = gemm_run(b, st))) return rc;
-  }
-  const int32_t* slot_row = plan + 2 * E + 1 + static_cast<long long>(T) * k;
-  return unpermute_sum_launch(dxp, slot_row, dx_shared, T, H, k, dx, st);
+  return router_backward_run(dlog, x, w_router, dxp, plan, dx_shared, T, H, E, k, dx, dw_router,
+                             status_word(workspace), st);
 }
 
 int rl_token_loss(const float* logp_train, const float* logp_old, const float* logp_rollout, const float* advantage,

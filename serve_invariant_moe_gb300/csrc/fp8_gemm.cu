@@ -1,0 +1,608 @@
+// fp8_gemm.cu -- e4m3 matrix product with a scale per 1 x 128 of the tokens and 128 x 128 of the weights (sm_103a).
+//
+//   out[t, n] = sum_kb (as[t, kb] * ws[n / 128, kb]) * p_kb[t, n],   p_kb = sum_{k in block kb} a[t, k] * w[n, k]
+//
+// p_kb comes from the tensor cores (tcgen05 kind::f8f6f4, four K = 32 steps, fp32 in TMEM, a fresh accumulator for every
+// block); its scale is an arbitrary fp32 number, so the sum over blocks cannot stay in TMEM: eight warps read each p_kb
+// and keep acc = fma(p_kb, as * ws, acc) in fp32 registers, kb ascending.  No split of K, one order for every tile
+// shape, and a column's chain depends on its own token only: the bits do not depend on the batch.
+//
+// Weights are the MMA's M side (128 rows = exactly one scale block of the weights, so ws is one number per sub-tile and
+// block) and tokens its N side, in multiples of 16: a group of 20 tokens costs 32 columns, not 128 rows, and decode and
+// prefill run the same kernel with another NT.
+//   * one producer thread: per 128-byte K block one TMA box of 128 weight rows per sub-tile (MT of them) and one box of
+//     NT token rows, 128-byte swizzle (the K-major operand layout; a block is one swizzle row);
+//   * one MMA thread: 4 * MT MMAs per block into one of ACC TMEM buffers;
+//   * two warpgroups, each with half of the token columns and all 128 lanes.  TMEM is read in the 16x256b shape: a
+//     thread then holds 4 rows x NT/8 columns instead of one row x NT/2 columns, so it needs a quarter of the per-token
+//     scales from shared memory (one row per thread would make those broadcast reads the bound).
+// SwiGLU (MT = 2): sub-tile 0 holds 128 gate rows, sub-tile 1 the matching up rows; h = silu(g) * u, its absolute
+// maximum over the 128 rows of the block, and e4m3(h / scale) leave the kernel, never g, u or an unquantised h.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+
+#include "fp8.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace invmoe {
+
+namespace {
+
+enum Fp8Epi : int { FP8_F32 = 0, FP8_BF16 = 1, FP8_SWIGLU = 2 };
+
+struct Fp8Params {
+  const float* a_scale;     // [token rows, KB]
+  const float* w_scale;     // [G][w_srows][KB]
+  int KB;                   // blocks of 128 along K
+  int N;                    // weight rows of one group that are outputs (SwiGLU: F)
+  int w_group_rows;         // weight rows of one group (SwiGLU: 2F)
+  int w_srows;              // rows of one group's scales
+  int n_blocks;             // units along the weight rows
+  int M;                    // token rows (dense)
+  int G;                    // groups (0 = dense)
+  const int* counts;
+  const int* offsets;
+  void* out;                // [token rows, N] fp32 / bf16 / e4m3
+  float* out_scale;         // SwiGLU: [token rows, N / 128]
+  int vec_scale;            // KB % 4 == 0 and aligned bases: scales in 16-byte loads
+  int vec_out;              // N % 4 == 0: outputs in vectors
+  unsigned int* status;
+  unsigned long long timeout_ns;
+};
+
+constexpr int kWTile = 128;                         // weight rows per sub-tile
+constexpr int kWBytes = kWTile * kFp8Block;         // 16 KB
+constexpr int kMaxGroups = 1024;
+constexpr int kEpiWarps = 8;
+constexpr int kFirstEpiWarp = 4;                    // warps 0..3: producer, MMA issuer, prefix sums, idle
+constexpr int kFp8Threads = 32 * (kFirstEpiWarp + kEpiWarps);
+// Registers per thread: 168 at launch (65,536 / 384, whole units of 8).  A tile of 256 x 128 leaves 128 accumulators in
+// each of the 256 epilogue threads, so there the first warpgroup hands registers over: 56 + 2 * 224 = 3 * 168.
+constexpr int kLaunchRegs = 168, kLoaderRegs = 56, kEpiRegs = 224;
+static_assert(kLoaderRegs + 2 * kEpiRegs <= 3 * kLaunchRegs, "register split");
+constexpr int kStageF32 = kWTile + 4;               // floats per staged token row (conflict-free fragment writes)
+constexpr int kStageFp8 = kWTile + 16;              // bytes per staged token row
+constexpr int kStagingBytes = 9216;                 // per warpgroup: 16 x 132 floats or 64 x 144 bytes
+static_assert(16 * kStageF32 * 4 <= kStagingBytes && 64 * kStageFp8 <= kStagingBytes, "staging");
+
+template <int MT, int NT>
+struct Fp8Shape {
+  static constexpr int STAGE_BYTES = MT * kWBytes + NT * kFp8Block;
+  static constexpr int ACC_COLS = MT * NT;
+  static constexpr int ACC = 512 / ACC_COLS < 4 ? 512 / ACC_COLS : 4;   // TMEM buffers
+  static constexpr int TMEM_COLS = ACC * ACC_COLS < 32 ? 32 : ACC * ACC_COLS;
+  static constexpr int HALF = NT / 2;                                   // token columns of a warpgroup
+  static constexpr int SCALE_BYTES = 2 * 2 * MT * HALF * 4;             // [warpgroup][buffer][sub-tile][column]
+  static constexpr int AMAX_BYTES = 2 * 4 * HALF * 4;                   // [warpgroup][warp][column]
+  static constexpr int FIXED = 1024 + 2 * kStagingBytes + SCALE_BYTES + AMAX_BYTES + 256 + 4 * (kMaxGroups + 1) + 12;
+  static constexpr int STAGES = (232448 - FIXED) / STAGE_BYTES < 8 ? (232448 - FIXED) / STAGE_BYTES : 8;
+  static constexpr int SMEM_BYTES = FIXED + STAGES * STAGE_BYTES;
+  static_assert(SMEM_BYTES <= 232448 && STAGES >= 3, "shared memory");
+  static_assert(8 * (2 * STAGES + 2 * ACC) + 16 <= 256, "barriers");
+};
+
+// Instruction descriptor, kind::f8f6f4: e4m3 A and B (formats 0), fp32 D, both K-major.
+__device__ __forceinline__ uint32_t idesc_e4m3_f32(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void umma_fp8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 16 TMEM lanes x 8 * X columns (16x256b shape): register 4i + {0, 1} holds lane t / 4, columns 8i + 2(t % 4) + {0, 1},
+// register 4i + {2, 3} the same columns of lane t / 4 + 8 (t = lane of the warp).
+template <int X>
+__device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[4 * X]) {
+  static_assert(X == 1 || X == 2 || X == 4 || X == 8, "repeat");
+  if constexpr (X == 1) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr));
+  } else if constexpr (X == 2) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+  } else if constexpr (X == 4) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+  }
+}
+
+// The registers are seen as redefined here (after tcgen05.wait::ld), so no use of them moves above the wait.
+template <int R>
+__device__ __forceinline__ void reg_fence(uint32_t (&r)[R]) {
+#pragma unroll
+  for (int i = 0; i < R; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// All four warps of a warpgroup execute the one instruction of its side of the split.
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoaderRegs)); }
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs)); }
+
+__device__ __forceinline__ void bar_wg(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+
+struct Fp8Unit {
+  int row0;      // first token row
+  int cols;      // tokens of this unit (1..NT)
+  int g;         // group
+  int nb;        // block of weight rows
+};
+
+// Units of a group: weight blocks outermost, token chunks innermost, so that the CTAs which share a weight tile run at
+// about the same time and its second reader finds it in L2.
+template <int NT>
+__device__ __forceinline__ Fp8Unit fp8_unit(int u, const Fp8Params& p, const int* prefix, int total_chunks) {
+  Fp8Unit U;
+  if (p.G == 0) {
+    U.g = 0;
+    U.nb = u / total_chunks;
+    const int c = u - U.nb * total_chunks;
+    U.row0 = c * NT;
+    U.cols = min(NT, p.M - U.row0);
+    return U;
+  }
+  const int v = u / p.n_blocks;       // chunk index: group g owns [prefix[g], prefix[g + 1])
+  int lo = 0, hi = p.G - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (prefix[mid + 1] > v) hi = mid;
+    else lo = mid + 1;
+  }
+  U.g = lo;
+  const int n_ch = prefix[lo + 1] - prefix[lo];
+  const int r = u - prefix[lo] * p.n_blocks;
+  U.nb = r / n_ch;
+  const int c = r - U.nb * n_ch;
+  U.row0 = __ldg(p.offsets + lo) + c * NT;
+  U.cols = min(NT, __ldg(p.counts + lo) - c * NT);
+  return U;
+}
+
+template <int MT, int NT, int EPI>
+__global__ void __launch_bounds__(kFp8Threads, 1)
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
+                    const Fp8Params p) {
+  using S = Fp8Shape<MT, NT>;
+  static_assert(EPI != FP8_SWIGLU || MT == 2, "SwiGLU pairs a gate sub-tile with its up sub-tile");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* staging = ring + S::STAGES * S::STAGE_BYTES;
+  float* s_scale = reinterpret_cast<float*>(staging + 2 * kStagingBytes);
+  float* s_amax = s_scale + S::SCALE_BYTES / 4;
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(s_amax) + S::AMAX_BYTES);
+  uint64_t* empty_bar = full_bar + S::STAGES;
+  uint64_t* accf_bar = empty_bar + S::STAGES;
+  uint64_t* acce_bar = accf_bar + S::ACC;
+  uint32_t* misc = reinterpret_cast<uint32_t*>(acce_bar + S::ACC);
+  uint32_t* tmem_slot = misc;
+  volatile int* s_abort = reinterpret_cast<volatile int*>(misc + 1);
+  int* s_total = reinterpret_cast<int*>(misc + 2);
+  int* s_prefix = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full_bar) + 256);   // [G + 1]
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::STAGES; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int a = 0; a < S::ACC; ++a) {
+      mbar_init(&accf_bar[a], 1);
+      mbar_init(&acce_bar[a], kEpiWarps);
+    }
+    *s_abort = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmA);
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, S::TMEM_COLS);
+  // everything above touches only shared memory, TMEM and the kernel parameters
+  pdl_wait();
+  pdl_trigger();
+  if (warp == 2) {
+    if (p.G > 0) {
+      const int per = (p.G + 31) / 32;
+      const int g0 = lane * per;
+      int local = 0;
+      for (int i = 0; i < per; ++i)
+        if (g0 + i < p.G) local += (__ldg(p.counts + g0 + i) + NT - 1) / NT;
+      int incl = local;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += v;
+      }
+      int run = incl - local;
+      for (int i = 0; i < per; ++i)
+        if (g0 + i < p.G) {
+          s_prefix[g0 + i] = run;
+          run += (__ldg(p.counts + g0 + i) + NT - 1) / NT;
+        }
+      if (lane == 31) {
+        s_prefix[p.G] = incl;
+        *s_total = incl;
+      }
+    } else if (lane == 0) {
+      *s_total = (p.M + NT - 1) / NT;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  const uint32_t tmem_base = *tmem_slot;
+  const int total_chunks = *s_total;
+  const int total_units = total_chunks * p.n_blocks;
+  WaitCtl wc{s_abort, p.status, p.timeout_ns};
+
+  constexpr bool SPLIT_REGS = MT * NT >= 256;
+  if (warp < kFirstEpiWarp) {
+    if constexpr (SPLIT_REGS) give_registers();
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------------- producer
+      int stage = 0;
+      uint32_t phase = 0;
+      int filled_phase[S::STAGES];
+#pragma unroll
+      for (int s = 0; s < S::STAGES; ++s) filled_phase[s] = -1;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < total_units; u += gridDim.x) {
+        const Fp8Unit U = fp8_unit<NT>(u, p, s_prefix, total_chunks);
+        int wrow[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          wrow[m] = EPI == FP8_SWIGLU ? U.g * p.w_group_rows + m * p.N + U.nb * kWTile
+                                      : U.g * p.w_group_rows + (U.nb * MT + m) * kWTile;
+        for (int kb = 0; kb < p.KB; ++kb) {
+          if (!mbar_wait(&empty_bar[stage], phase ^ 1u, wc)) { ok = false; break; }
+          uint8_t* st = ring + stage * S::STAGE_BYTES;
+          mbar_arrive_expect_tx(&full_bar[stage], S::STAGE_BYTES);   // a box counts its full size, filled rows included
+#pragma unroll
+          for (int m = 0; m < MT; ++m) tma_load_2d(st + m * kWBytes, &tmW, &full_bar[stage], kb * kFp8Block, wrow[m]);
+          tma_load_2d(st + MT * kWBytes, &tmA, &full_bar[stage], kb * kFp8Block, U.row0);
+          filled_phase[stage] = static_cast<int>(phase);
+          if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+      // every copy this thread issued lands before the CTA can exit
+      WaitCtl drain{nullptr, p.status, p.timeout_ns};
+#pragma unroll
+      for (int s = 0; s < S::STAGES; ++s)
+        if (filled_phase[s] >= 0) mbar_wait(&full_bar[s], static_cast<uint32_t>(filled_phase[s]), drain);
+    } else if (warp == 1 && lane == 0) {
+      // ---------------------------------------------------------- MMA issuer
+      const uint64_t wdesc0 = sdesc_k_sw128(smem_u32(ring));
+      const uint64_t adesc0 = sdesc_k_sw128(smem_u32(ring + MT * kWBytes));
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true;
+      bool issued = false;
+      int last_acc = 0;
+      uint32_t last_phase = 0;
+      for (int u = blockIdx.x; ok && u < total_units; u += gridDim.x) {
+        const Fp8Unit U = fp8_unit<NT>(u, p, s_prefix, total_chunks);
+        const uint32_t idesc = idesc_e4m3_f32(kWTile, (U.cols + 15) & ~15);
+        for (int kb = 0; kb < p.KB; ++kb) {
+          if (!mbar_wait(&acce_bar[acc], acc_phase ^ 1u, wc) || !mbar_wait(&full_bar[stage], phase, wc)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t so = static_cast<uint64_t>((stage * S::STAGE_BYTES) >> 4);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const uint32_t d = tmem_base + static_cast<uint32_t>(acc * S::ACC_COLS + m * NT);
+#pragma unroll
+            for (int kk = 0; kk < kFp8Block / 32; ++kk)   // K = 32 steps: 32 bytes on inside the swizzle row
+              umma_fp8(d, wdesc0 + so + static_cast<uint64_t>(m * (kWBytes >> 4)) + 2u * kk, adesc0 + so + 2u * kk, idesc,
+                       kk != 0 ? 1u : 0u);
+          }
+          umma_commit(&empty_bar[stage]);
+          umma_commit(&accf_bar[acc]);
+          issued = true;
+          last_acc = acc;
+          last_phase = acc_phase;
+          if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
+          if (++acc == S::ACC) { acc = 0; acc_phase ^= 1u; }
+        }
+      }
+      if (!ok) *s_abort = 1;
+      // every MMA issued here has finished before the CTA releases TMEM
+      WaitCtl drain{nullptr, p.status, p.timeout_ns};
+      if (issued) mbar_wait(&accf_bar[last_acc], last_phase, drain);
+    }
+  } else {
+    // ------------------------------------------------------------ scaling and epilogue
+    if constexpr (SPLIT_REGS) take_registers();
+    // All eight warps walk the same units and blocks whatever happens, so the warpgroup barriers always meet; after a
+    // wait that ran out (ok = false) a warp only keeps those barriers.
+    constexpr int X = NT / 16;                         // 8-column fragments of a warpgroup's columns
+    const int q = warp & 3;                            // TMEM lane quadrant
+    const int half = (warp - kFirstEpiWarp) >> 2;                  // warpgroup: token columns [half * HALF, +HALF)
+    const int tid = q * 32 + lane;                     // thread of the warpgroup
+    const int bar_id = 1 + half;
+    float* my_scale = s_scale + half * (2 * MT * S::HALF);
+    float* my_amax = s_amax + half * (4 * S::HALF);
+    uint8_t* stg = staging + half * kStagingBytes;
+    const int sm_m = tid / S::HALF;                    // the scale this thread prepares: sub-tile, column
+    const int sm_c = tid % S::HALF;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    int sbuf = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; u < total_units; u += gridDim.x) {
+      const Fp8Unit U = fp8_unit<NT>(u, p, s_prefix, total_chunks);
+      const int wg_cols = U.cols - half * S::HALF;     // this warpgroup's tokens (may be <= 0)
+      const float* ap = p.a_scale + static_cast<long long>(U.row0 + min(half * S::HALF + sm_c, U.cols - 1)) * p.KB;
+      const int srow = EPI == FP8_SWIGLU ? sm_m * (p.N / kFp8Block) + U.nb : U.nb * MT + sm_m;
+      const float* wp = p.w_scale + (static_cast<long long>(U.g) * p.w_srows + min(srow, p.w_srows - 1)) * p.KB;
+      float v[MT][2][4 * X];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4 * X; ++i) v[m][h][i] = 0.0f;
+      float s_next = 0.0f;
+      if (sm_m < MT) s_next = __fmul_rn(__ldg(ap), __ldg(wp));
+      for (int kb = 0; kb < p.KB; ++kb) {
+        float* sb = my_scale + sbuf * (MT * S::HALF);
+        if (sm_m < MT) {
+          sb[sm_m * S::HALF + sm_c] = s_next;
+          if (kb + 1 < p.KB) s_next = __fmul_rn(__ldg(ap + kb + 1), __ldg(wp + kb + 1));
+        }
+        bar_wg(bar_id);
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(&accf_bar[acc], acc_phase, wc));
+        if (ok) {
+          tc_fence_after();
+          if (wg_cols > 0) {
+            const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                                static_cast<uint32_t>(acc * S::ACC_COLS + half * S::HALF);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t r[4 * X];
+                tmem_ld_16x256b<X>(tb + (static_cast<uint32_t>(h * 16) << 16) + static_cast<uint32_t>(m * NT), r);
+                tmem_ld_wait();
+                reg_fence(r);
+#pragma unroll
+                for (int i = 0; i < X; ++i) {
+                  const float2 s = *reinterpret_cast<const float2*>(sb + m * S::HALF + 8 * i + 2 * (lane & 3));
+                  v[m][h][4 * i] = fmaf(__uint_as_float(r[4 * i]), s.x, v[m][h][4 * i]);
+                  v[m][h][4 * i + 1] = fmaf(__uint_as_float(r[4 * i + 1]), s.y, v[m][h][4 * i + 1]);
+                  v[m][h][4 * i + 2] = fmaf(__uint_as_float(r[4 * i + 2]), s.x, v[m][h][4 * i + 2]);
+                  v[m][h][4 * i + 3] = fmaf(__uint_as_float(r[4 * i + 3]), s.y, v[m][h][4 * i + 3]);
+                }
+              }
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acce_bar[acc]);
+        }
+        if (++acc == S::ACC) { acc = 0; acc_phase ^= 1u; }
+        sbuf ^= 1;
+      }
+      const long long out_row0 = static_cast<long long>(U.row0) + half * S::HALF;
+      if constexpr (EPI == FP8_SWIGLU) {
+        // h in place of the gate values; each column's absolute maximum over the thread's 4 rows, the warp's 32
+        // (lanes that differ in lane / 4) and the 4 warps
+#pragma unroll
+        for (int i = 0; i < X; ++i) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float mx = 0.0f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float& g = v[0][h][4 * i + j + 2 * e];
+                g = __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), v[1][h][4 * i + j + 2 * e]);
+                mx = fmaxf(mx, fabsf(g));
+              }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            if (lane < 4) my_amax[q * S::HALF + 8 * i + 2 * lane + j] = mx;
+          }
+        }
+        bar_wg(bar_id);
+        float my_s = 0.0f;
+        if (tid < S::HALF) {
+          const float a = fmaxf(fmaxf(my_amax[tid], my_amax[S::HALF + tid]),
+                                fmaxf(my_amax[2 * S::HALF + tid], my_amax[3 * S::HALF + tid]));
+          my_s = fp8_scale(a);
+        }
+        bar_wg(bar_id);
+        if (tid < S::HALF) {
+          my_amax[tid] = __frcp_rn(my_s);
+          if (ok && tid < wg_cols) p.out_scale[(out_row0 + tid) * (p.N / kFp8Block) + U.nb] = my_s;
+        }
+        bar_wg(bar_id);
+#pragma unroll
+        for (int i = 0; i < X; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int col = 8 * i + 2 * (lane & 3) + j;
+            const float inv = my_amax[col];
+            uint8_t* d = stg + col * kStageFp8 + q * 32 + (lane >> 2);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) d[16 * h + 8 * e] = fp8_one(v[0][h][4 * i + j + 2 * e], inv);
+          }
+        bar_wg(bar_id);
+        // 8 lanes of 16 bytes per token row
+        uint8_t* out = static_cast<uint8_t*>(p.out) + out_row0 * p.N + static_cast<long long>(U.nb) * kWTile;
+        for (int t = tid >> 3; t < S::HALF; t += 16)
+          if (ok && t < wg_cols)
+            *reinterpret_cast<uint4*>(out + static_cast<long long>(t) * p.N + 16 * (tid & 7)) =
+                *reinterpret_cast<const uint4*>(stg + t * kStageFp8 + 16 * (tid & 7));
+        // the next unit's first staging write comes after at least one warpgroup barrier
+      } else {
+        constexpr int CI = X < 2 ? 1 : 2;              // fragments (8 tokens each) staged at a time
+        float* stf = reinterpret_cast<float*>(stg);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const int n0 = (U.nb * MT + m) * kWTile;
+#pragma unroll
+          for (int i0 = 0; i0 < X; i0 += CI) {
+            bar_wg(bar_id);
+#pragma unroll
+            for (int ii = 0; ii < CI; ++ii)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  stf[(8 * ii + 2 * (lane & 3) + (e & 1)) * kStageF32 + q * 32 + 16 * h + 8 * (e >> 1) + (lane >> 2)] =
+                      v[m][h][4 * (i0 + ii) + e];
+            bar_wg(bar_id);
+            // one warp per token row: 4 outputs per lane
+#pragma unroll
+            for (int tt = q; tt < 8 * CI; tt += 4) {
+              const int t = 8 * i0 + tt;
+              const int n = n0 + 4 * lane;
+              if (!ok || t >= wg_cols || n >= p.N) continue;
+              const float4 o = *reinterpret_cast<const float4*>(stf + tt * kStageF32 + 4 * lane);
+              const long long at = (out_row0 + t) * p.N + n;
+              if constexpr (EPI == FP8_F32) {
+                float* d = static_cast<float*>(p.out) + at;
+                if (p.vec_out) {
+                  *reinterpret_cast<float4*>(d) = o;
+                } else {
+                  d[0] = o.x;
+                  if (n + 1 < p.N) d[1] = o.y;
+                  if (n + 2 < p.N) d[2] = o.z;
+                  if (n + 3 < p.N) d[3] = o.w;
+                }
+              } else {
+                __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.out) + at;
+                if (p.vec_out) {
+                  const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
+                  *reinterpret_cast<uint2*>(d) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                            *reinterpret_cast<const uint32_t*>(&hi));
+                } else {
+                  d[0] = __float2bfloat16_rn(o.x);
+                  if (n + 1 < p.N) d[1] = __float2bfloat16_rn(o.y);
+                  if (n + 2 < p.N) d[2] = __float2bfloat16_rn(o.z);
+                  if (n + 3 < p.N) d[3] = __float2bfloat16_rn(o.w);
+                }
+              }
+            }
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, S::TMEM_COLS);
+  }
+}
+
+template <int MT, int NT, int EPI>
+int launch_fp8(const Fp8Call& c, Fp8Params p, cudaStream_t st) {
+  using S = Fp8Shape<MT, NT>;
+  p.n_blocks = EPI == FP8_SWIGLU ? c.N / kWTile : (c.N + MT * kWTile - 1) / (MT * kWTile);
+  const long long max_chunks =
+      c.G > 0 ? (static_cast<long long>(c.rows) / NT + (c.rows < c.G ? c.rows : c.G)) : (c.rows + NT - 1LL) / NT;
+  if (max_chunks * p.n_blocks > 0x7fffffffLL)
+    return set_error(INVMOE_ERR_UNSUPPORTED_SHAPE, "%s: too many tiles for one launch", c.name);
+  CUtensorMap tmW, tmA;
+  int rc = make_tmap_fp8(&tmW, c.w, c.K, static_cast<long long>(p.w_group_rows) * (c.G > 0 ? c.G : 1), kWTile);
+  if (rc) return rc;
+  if ((rc = make_tmap_fp8(&tmA, c.a, c.K, c.rows, NT))) return rc;
+  static std::atomic<uint64_t> attr_set{0};
+  if ((rc = set_smem_attr(reinterpret_cast<const void*>(fp8_gemm_kernel<MT, NT, EPI>), S::SMEM_BYTES, attr_set)))
+    return rc;
+  if constexpr (MT * NT >= 256) {
+    // the register split above must not ask for more than the launch holds: a kernel that waits for registers never ends
+    static std::atomic<int> regs{0};
+    int r = regs.load(std::memory_order_relaxed);
+    if (r == 0) {
+      cudaFuncAttributes fa;
+      if ((rc = check_cuda(cudaFuncGetAttributes(&fa, reinterpret_cast<const void*>(fp8_gemm_kernel<MT, NT, EPI>)),
+                           "cudaFuncGetAttributes")))
+        return rc;
+      r = fa.numRegs;
+      regs.store(r, std::memory_order_relaxed);
+    }
+    if (r != kLaunchRegs) return set_error(INVMOE_ERR_CUDA, "%s: compiled with %d registers, not %d", c.name, r, kLaunchRegs);
+  }
+  int sms = 0;
+  if ((rc = device_sm_count(&sms))) return rc;
+  const long long units = max_chunks * p.n_blocks;
+  const unsigned grid = static_cast<unsigned>(units < sms ? units : sms);
+  ProfScope prof(c.name, st);
+  return check_cuda(launch_kernel(fp8_gemm_kernel<MT, NT, EPI>, dim3(grid), dim3(kFp8Threads), S::SMEM_BYTES, st, tmW,
+                                  tmA, p),
+                    c.name);
+}
+
+template <int MT, int EPI>
+int launch_fp8_nt(const Fp8Call& c, const Fp8Params& p, long long per_group, cudaStream_t st) {
+  if (per_group <= 16) return launch_fp8<MT, 16, EPI>(c, p, st);
+  if (per_group <= 32) return launch_fp8<MT, 32, EPI>(c, p, st);
+  if (per_group <= 64) return launch_fp8<MT, 64, EPI>(c, p, st);
+  return launch_fp8<MT, 128, EPI>(c, p, st);
+}
+
+}  // namespace
+
+int fp8_gemm_run(const Fp8Call& c, cudaStream_t st) {
+  if (c.rows == 0) return INVMOE_OK;
+  Fp8Params p{};
+  const bool swiglu = c.out_kind == FP8_OUT_SWIGLU;
+  p.a_scale = c.a_scale;
+  p.w_scale = c.w_scale;
+  p.KB = (c.K + kFp8Block - 1) / kFp8Block;
+  p.N = c.N;
+  p.w_group_rows = swiglu ? 2 * c.N : c.N;
+  p.w_srows = (p.w_group_rows + kFp8Block - 1) / kFp8Block;
+  p.M = c.rows;
+  p.G = c.G;
+  p.counts = c.counts;
+  p.offsets = c.offsets;
+  p.out = c.out;
+  p.out_scale = c.out_scale;
+  p.vec_out = c.N % 4 == 0;
+  p.status = c.status;
+  p.timeout_ns = kTimeoutNs;
+  const long long per_group = c.G > 0 ? (static_cast<long long>(c.rows) + c.G - 1) / c.G : c.rows;
+  if (swiglu) return launch_fp8_nt<2, FP8_SWIGLU>(c, p, per_group, st);
+  if (c.out_kind == FP8_OUT_F32) return launch_fp8_nt<2, FP8_F32>(c, p, per_group, st);
+  return launch_fp8_nt<2, FP8_BF16>(c, p, per_group, st);
+}
+
+}  // namespace invmoe

@@ -13,6 +13,21 @@
 
 namespace invmoe {
 
+// Raise a kernel's dynamic shared-memory limit once per device (devices 0..63
+// are remembered in `done`; a higher device index sets it on every call).
+int set_smem_attr(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  int rc = check_cuda(cudaGetDevice(&dev), "cudaGetDevice");
+  if (rc) return rc;
+  const uint64_t bit = dev < 64 ? (uint64_t{1} << dev) : 0;
+  if (bit != 0 && (done.load(std::memory_order_acquire) & bit)) return INVMOE_OK;
+  rc = check_cuda(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes),
+                  "cudaFuncSetAttribute");
+  if (rc) return rc;
+  if (bit != 0) done.fetch_or(bit, std::memory_order_release);
+  return INVMOE_OK;
+}
+
 namespace {
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -103,21 +118,6 @@ int make_tmap_out_grouped_f32(CUtensorMap* m, void* base, long long N, long long
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return set_error(INVMOE_ERR_CUDA, "cuTensorMapEncodeTiled (output) failed (%d)", (int)r);
-  return INVMOE_OK;
-}
-
-// Raise a kernel's dynamic shared-memory limit once per device (devices 0..63
-// are remembered in `done`; a higher device index sets it on every call).
-int set_smem_attr(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  int rc = check_cuda(cudaGetDevice(&dev), "cudaGetDevice");
-  if (rc) return rc;
-  const uint64_t bit = dev < 64 ? (uint64_t{1} << dev) : 0;
-  if (bit != 0 && (done.load(std::memory_order_acquire) & bit)) return INVMOE_OK;
-  rc = check_cuda(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes),
-                  "cudaFuncSetAttribute");
-  if (rc) return rc;
-  if (bit != 0) done.fetch_or(bit, std::memory_order_release);
   return INVMOE_OK;
 }
 
@@ -352,6 +352,22 @@ int launch_small(const GemmCall& c, cudaStream_t st) {
 }
 
 }  // namespace
+
+// Row-major e4m3 [rows, inner] matrix; box = 128 elements (128 B, one swizzle row) x box_rows.  A last block of fewer
+// than 128 columns is filled with zeros.
+int make_tmap_fp8(CUtensorMap* m, const void* base, long long inner, long long rows, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return set_error(INVMOE_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(inner)};
+  cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(INVMOE_ERR_CUDA, "cuTensorMapEncodeTiled (e4m3) failed (%d)", (int)r);
+  return INVMOE_OK;
+}
 
 int gemm_run(const GemmCall& c, cudaStream_t st) {
   if (c.a_rows <= 0 || (c.G == 0 && c.M <= 0)) return INVMOE_OK;

@@ -1,7 +1,9 @@
 // internal.h -- host-side declarations shared by the library's translation units.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -178,5 +180,49 @@ int router_bwd_launch(const int32_t* topk_idx, const float* topk_w, const float*
                       void* dlog, cudaStream_t st);
 int unpermute_sum_launch(const float* dxp, const int32_t* slot_row, const float* dx_shared, int T, int H, int k,
                          float* dx, cudaStream_t st);
+
+// ---------------------------------------------------------------- scored routing
+int router_gemm_run(const void* x, const void* w_router, int T, int H, int E, float* logits, unsigned int* status,
+                    cudaStream_t st);
+int router_backward_run(const void* dlog, const void* x, const void* w_router, const float* dxp, const int32_t* plan,
+                        const float* dx_shared, int T, int H, int E, int k, float* dx, float* dw_router,
+                        unsigned int* status, cudaStream_t st);
+int select_launch(const float* logits, const float* bias, int T, int E, int k, int softmax, int n_group, int topk_group,
+                  int renorm, float scale, int32_t* idx, float* w, cudaStream_t st);
+int select_bwd_launch(const float* logits, const int32_t* idx, const float* dw, int T, int E, int k, int softmax,
+                      int renorm, float scale, float* dl, void* dl_bf16, cudaStream_t st);
+
+// ---------------------------------------------------------------- norm and e4m3
+int norm_launch(const void* x, int x_f32, const void* res, int res_f32, const void* weight, int T, int H, float eps,
+                void* res_out, void* out, void* q, float* scale, float* rstd, cudaStream_t st);
+int norm_bwd_rows(int T);
+int norm_bwd_launch(const void* dy, int dy_f32, const void* x, int x_f32, const void* weight, const float* rstd,
+                    const void* dres, int T, int H, void* dx, float* dw, float* part, cudaStream_t st);
+int quantize_launch(const void* x, int x_f32, long long banks, int rows, int cols, int block_rows, void* q,
+                    float* scale, cudaStream_t st);
+int permute_fp8_launch(const void* q, const float* scale, const int32_t* slot_row, int T, int k, int H, void* xp,
+                       float* xp_scale, cudaStream_t st);
+
+enum Fp8Out : int { FP8_OUT_F32 = 0, FP8_OUT_BF16 = 1, FP8_OUT_SWIGLU = 2 };
+
+struct Fp8Call {
+  const char* name;
+  const void* a;          // [rows, K] e4m3 tokens
+  const float* a_scale;   // [rows, ceil(K / 128)]
+  int rows;
+  const void* w;          // [G, N, K] e4m3 (SwiGLU: [G, 2N, K], gate rows then up rows)
+  const float* w_scale;   // [G, ceil(rows of w / 128), ceil(K / 128)]
+  int K, N, G;            // G = 0: dense, one weight
+  const int* counts;
+  const int* offsets;
+  void* out;              // [rows, N]
+  float* out_scale;       // SwiGLU: [rows, N / 128]
+  Fp8Out out_kind;
+  unsigned int* status;
+};
+
+int fp8_gemm_run(const Fp8Call& c, cudaStream_t st);
+int make_tmap_fp8(CUtensorMap* m, const void* base, long long inner, long long rows, int box_rows);
+int set_smem_attr(const void* kernel, int bytes, std::atomic<uint64_t>& done);
 
 }  // namespace invmoe

@@ -1,0 +1,476 @@
+// norm_fp8.cu -- residual addition + RMSNorm with bf16 and/or e4m3 output, its backward, e4m3 quantisation and the
+// permute of quantised rows.
+//
+// The norm is bound by memory: per element it reads x and the residual once and writes the new residual, the bf16 row
+// and the e4m3 row once.  One block holds one row in registers between the two uses of it (sum of squares, then the
+// scaled output), 8 consecutive elements per vector, so 16 lanes own one block of 128 columns and its maximum takes
+// four shuffles.  The reduction order depends on H alone, never on the batch.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "fp8.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace invmoe {
+
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+
+// 8 consecutive elements, bf16 or fp32.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+}
+
+__device__ __forceinline__ uint32_t bf16x2_bits(float a, float b) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
+
+// Stores v and replaces it by the values stored.
+template <typename T>
+__device__ __forceinline__ void store8(T* p, float (&v)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = bf16x2_bits(v[2 * i], v[2 * i + 1]);
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+// Sum over the block, the same in every thread: xor butterfly per warp, then the warps' sums in ascending order.
+__device__ __forceinline__ float block_sum(float v, float* s_part, int warp, int lane, int nwarps) {
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+  if (nwarps == 1) return v;
+  if (lane == 0) s_part[warp] = v;
+  __syncthreads();
+  float s = 0.0f;
+  for (int w = 0; w < nwarps; ++w) s += s_part[w];
+  return s;
+}
+
+// e4m3 of 8 values; the 16 lanes of a block of 128 columns agree on its scale.  Lanes past the row hold zeros.
+__device__ __forceinline__ void quant8(const float (&y)[8], bool in, uint8_t* q, float* scale, int lane) {
+  float a = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(y[i]));
+#pragma unroll
+  for (int d = 8; d >= 1; d >>= 1) a = fmaxf(a, __shfl_xor_sync(kFull, a, d));
+  const float s = fp8_scale(a), inv = __frcp_rn(s);
+  if (in) {
+    *reinterpret_cast<uint2*>(q) = make_uint2(fp8_pack4(y[0], y[1], y[2], y[3], inv),
+                                              fp8_pack4(y[4], y[5], y[6], y[7], inv));
+    if ((lane & 15) == 0) *scale = s;
+  }
+}
+
+template <int V, typename TX, typename TR>
+__global__ void __launch_bounds__(1024) norm_kernel(const TX* __restrict__ x, const TR* res,
+                                                    const __nv_bfloat16* __restrict__ weight, int H, float eps,
+                                                    TR* res_out, __nv_bfloat16* __restrict__ out,
+                                                    uint8_t* __restrict__ q, float* __restrict__ scale,
+                                                    float* __restrict__ rstd_out) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float s_part[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+  const long long t = blockIdx.x;
+  const long long base = t * H;
+  float r[V][8];
+  float ss = 0.0f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = (v * blockDim.x + threadIdx.x) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[v][i] = 0.0f;
+    if (c < H) load8(x + base + c, r[v]);
+  }
+  if (res != nullptr) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * blockDim.x + threadIdx.x) * 8;
+      if (c < H) {
+        float b[8];
+        load8(res + base + c, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[v][i] = __fadd_rn(r[v][i], b[i]);
+        // the norm reads the residual as it is stored: the next layer and the backward see the same row
+        store8(res_out + base + c, r[v]);
+      }
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(r[v][i], r[v][i], ss);
+  ss = block_sum(ss, s_part, warp, lane, nwarps);
+  const float rstd = __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(ss, static_cast<float>(H)), eps)));
+  if (rstd_out != nullptr && threadIdx.x == 0) rstd_out[t] = rstd;
+  const int nb = (H + kFp8Block - 1) / kFp8Block;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = (v * blockDim.x + threadIdx.x) * 8;
+    const bool in = c < H;
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 0.0f;
+    if (in) load8(weight + c, w);
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = in ? __fmul_rn(__fmul_rn(r[v][i], rstd), w[i]) : 0.0f;
+    if (q != nullptr) quant8(y, in, q + base + c, scale + t * nb + c / kFp8Block, lane);
+    if (out != nullptr && in) store8(out + base + c, y);
+  }
+}
+
+// Backward: g = dy * w, n = r * rstd, dr = rstd * (g - n * mean(g n)) + dres; dw = sum_t dy n.  A block walks
+// rows_per_block consecutive rows and keeps its share of dw in registers; the partial rows are summed in order by
+// dweight_kernel, so no atomics and one order for a given T and H.
+template <int V, typename TX, typename TD>
+__global__ void __launch_bounds__(1024) norm_bwd_kernel(const TD* __restrict__ dy, const TX* __restrict__ x,
+                                                        const __nv_bfloat16* __restrict__ weight,
+                                                        const float* __restrict__ rstd, const TX* dres, int T, int H,
+                                                        int rows_per_block, TX* dx, float* __restrict__ dw_part) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float s_part[2][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+  float w[V][8], dw[V][8];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = (v * blockDim.x + threadIdx.x) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[v][i] = dw[v][i] = 0.0f;
+    if (c < H) load8(weight + c, w[v]);
+  }
+  const long long t0 = static_cast<long long>(blockIdx.x) * rows_per_block;
+  const long long t1 = min(static_cast<long long>(T), t0 + rows_per_block);
+  int buf = 0;
+  for (long long t = t0; t < t1; ++t) {
+    const long long base = t * H;
+    const float rs = __ldg(rstd + t);
+    float g[V][8], n[V][8];
+    float dot = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * blockDim.x + threadIdx.x) * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[v][i] = n[v][i] = 0.0f;
+      if (c < H) {
+        load8(dy + base + c, g[v]);
+        load8(x + base + c, n[v]);
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        n[v][i] *= rs;
+        dw[v][i] = fmaf(g[v][i], n[v][i], dw[v][i]);
+        g[v][i] *= w[v][i];
+        dot = fmaf(g[v][i], n[v][i], dot);
+      }
+    dot = block_sum(dot, s_part[buf], warp, lane, nwarps);   // two buffers: one barrier per row
+    buf ^= 1;
+    const float mean = __fdiv_rn(dot, static_cast<float>(H));
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * blockDim.x + threadIdx.x) * 8;
+      if (c < H) {
+        float d[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] = rs * (g[v][i] - n[v][i] * mean);
+        if (dres != nullptr) {
+          float b[8];
+          load8(dres + base + c, b);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d[i] += b[i];
+        }
+        store8(dx + base + c, d);
+      }
+    }
+  }
+  if (dw_part != nullptr) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * blockDim.x + threadIdx.x) * 8;
+      if (c < H) store8(dw_part + static_cast<long long>(blockIdx.x) * H + c, dw[v]);
+    }
+  }
+}
+
+// dw[h] = sum over P partial rows: 32 columns per block, thread row y adds rows y, y + 32, ... ascending, then the 32
+// sums ascending.
+__global__ void __launch_bounds__(1024) dweight_kernel(const float* __restrict__ part, int P, int H,
+                                                       float* __restrict__ dw) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float s[32][33];
+  const int c = blockIdx.x * 32 + threadIdx.x;
+  float v = 0.0f;
+  if (c < H) {
+    int r = threadIdx.y;
+    for (; r + 96 < P; r += 128) {
+      const float a0 = part[static_cast<long long>(r) * H + c], a1 = part[static_cast<long long>(r + 32) * H + c];
+      const float a2 = part[static_cast<long long>(r + 64) * H + c], a3 = part[static_cast<long long>(r + 96) * H + c];
+      v = ((v + a0) + a1) + (a2 + a3);
+    }
+    for (; r < P; r += 32) v += part[static_cast<long long>(r) * H + c];
+  }
+  s[threadIdx.y][threadIdx.x] = v;
+  __syncthreads();
+  if (threadIdx.y == 0 && c < H) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int y = 0; y < 32; ++y) sum += s[y][threadIdx.x];
+    dw[c] = sum;
+  }
+}
+
+// e4m3 of row-major [rows, cols] with a scale per row and 128 columns: 16 lanes per block, 2 blocks per warp.
+template <typename TX>
+__global__ void __launch_bounds__(256) quant_rows_kernel(const TX* __restrict__ x, long long rows, int cols, int nb,
+                                                         uint8_t* __restrict__ q, float* __restrict__ scale) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const long long total = rows * nb;
+  const long long step = static_cast<long long>(gridDim.x) * (blockDim.x / 16);
+  // both halves of a warp make the same number of turns: the loop runs on the warp's first block
+  for (long long b0 = (static_cast<long long>(blockIdx.x) * blockDim.x + (threadIdx.x & ~31)) / 16; b0 < total;
+       b0 += step) {
+    const long long b = b0 + (lane >> 4);
+    const long long r = b / nb;
+    const int c = static_cast<int>(b - r * nb) * kFp8Block + (lane & 15) * 8;
+    const bool in = b < total && c < cols;
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = 0.0f;
+    if (in) load8(x + r * cols + c, y);
+    quant8(y, in, q + r * cols + c, scale + b, lane);
+  }
+}
+
+// e4m3 of [rows, cols] with a scale per 128 x 128 block: one thread block of 256 per block, 8 elements x 8 rows each.
+template <typename TX>
+__global__ void __launch_bounds__(256) quant_blocks_kernel(const TX* __restrict__ x, int rows, int cols, int nb,
+                                                           int rb, uint8_t* __restrict__ q, float* __restrict__ scale) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float s_max[8];
+  const long long bank = blockIdx.x / (static_cast<long long>(nb) * rb);
+  const int in_bank = static_cast<int>(blockIdx.x - bank * nb * rb);
+  const int br = in_bank / nb, bc = in_bank - br * nb;
+  const int c = bc * kFp8Block + (threadIdx.x & 15) * 8;
+  const long long first = bank * rows + static_cast<long long>(br) * kFp8Block;
+  const int n_rows = min(kFp8Block, rows - br * kFp8Block);
+  float y[8][8];
+  float a = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int r = j * 16 + (threadIdx.x >> 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[j][i] = 0.0f;
+    if (r < n_rows && c < cols) load8(x + (first + r) * cols + c, y[j]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(y[j][i]));
+  }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) a = fmaxf(a, __shfl_xor_sync(kFull, a, d));
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = a;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) a = fmaxf(a, s_max[w]);
+  const float s = fp8_scale(a), inv = __frcp_rn(s);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int r = j * 16 + (threadIdx.x >> 4);
+    if (r < n_rows && c < cols)
+      *reinterpret_cast<uint2*>(q + (first + r) * cols + c) =
+          make_uint2(fp8_pack4(y[j][0], y[j][1], y[j][2], y[j][3], inv),
+                     fp8_pack4(y[j][4], y[j][5], y[j][6], y[j][7], inv));
+  }
+  if (threadIdx.x == 0) scale[blockIdx.x] = s;
+}
+
+// xp[slot_row[t, j]] = x[t] for e4m3 rows (16-byte vectors) and their scales: one warp per token, each row read once.
+__global__ void __launch_bounds__(256) permute_fp8_kernel(const uint4* __restrict__ q, const float* __restrict__ scale,
+                                                          const int32_t* __restrict__ slot_row, long long T, int k,
+                                                          int vec, int nb, uint4* __restrict__ xp,
+                                                          float* __restrict__ xp_scale) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  // a warp copies segment `seg` (64 vectors) of token t; segment 0 also copies the scales
+  const int nseg = (vec + 63) / 64;
+  const long long items = T * nseg;
+  for (long long it = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < items;
+       it += static_cast<long long>(gridDim.x) * 8) {
+    const long long t = it / nseg;
+    const int seg = static_cast<int>(it - t * nseg);
+    const int my_row = lane < k ? __ldg(slot_row + t * k + lane) : 0;
+    const int c0 = seg * 64 + lane, c1 = c0 + 32;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    const uint4 v0 = c0 < vec ? __ldg(q + t * vec + c0) : zero;
+    const uint4 v1 = c1 < vec ? __ldg(q + t * vec + c1) : zero;
+    for (int j = 0; j < k; ++j) {
+      const long long row = __shfl_sync(kFull, my_row, j);
+      if (c0 < vec) xp[row * vec + c0] = v0;
+      if (c1 < vec) xp[row * vec + c1] = v1;
+    }
+    if (seg == 0)
+      for (int c = lane; c < nb; c += 32) {
+        const float s = __ldg(scale + t * nb + c);
+        for (int j = 0; j < k; ++j) xp_scale[static_cast<long long>(__ldg(slot_row + t * k + j)) * nb + c] = s;
+      }
+  }
+}
+
+// Threads of a row: one vector of 8 per thread up to H = 2048, then two, then four (1024 threads at H = 32768).
+struct RowShape {
+  int v, threads;
+};
+RowShape row_shape(int H) {
+  const int vecs = H / 8;
+  const int v = vecs <= 256 ? 1 : vecs <= 2048 ? 2 : 4;
+  return {v, ((vecs + v - 1) / v + 31) / 32 * 32};
+}
+
+template <typename TX, typename TR>
+cudaError_t norm_typed(const void* x, const void* res, const void* weight, int T, int H, float eps, void* res_out,
+                       void* out, void* q, float* scale, float* rstd, cudaStream_t st) {
+  const RowShape s = row_shape(H);
+  auto go = [&](auto kernel) {
+    return launch_kernel(kernel, dim3(T), dim3(s.threads), 0, st, static_cast<const TX*>(x),
+                         static_cast<const TR*>(res), static_cast<const __nv_bfloat16*>(weight), H, eps,
+                         static_cast<TR*>(res_out), static_cast<__nv_bfloat16*>(out), static_cast<uint8_t*>(q), scale,
+                         rstd);
+  };
+  if (s.v == 1) return go(norm_kernel<1, TX, TR>);
+  if (s.v == 2) return go(norm_kernel<2, TX, TR>);
+  return go(norm_kernel<4, TX, TR>);
+}
+
+template <typename TX, typename TD>
+cudaError_t norm_bwd_typed(const void* dy, const void* x, const void* weight, const float* rstd, const void* dres,
+                           int T, int H, int rows, int P, void* dx, float* part, cudaStream_t st) {
+  const RowShape s = row_shape(H);
+  auto go = [&](auto kernel) {
+    return launch_kernel(kernel, dim3(P), dim3(s.threads), 0, st, static_cast<const TD*>(dy),
+                         static_cast<const TX*>(x), static_cast<const __nv_bfloat16*>(weight), rstd,
+                         static_cast<const TX*>(dres), T, H, rows, static_cast<TX*>(dx), part);
+  };
+  if (s.v == 1) return go(norm_bwd_kernel<1, TX, TD>);
+  if (s.v == 2) return go(norm_bwd_kernel<2, TX, TD>);
+  return go(norm_bwd_kernel<4, TX, TD>);
+}
+
+}  // namespace
+
+int norm_launch(const void* x, int x_f32, const void* res, int res_f32, const void* weight, int T, int H, float eps,
+                void* res_out, void* out, void* q, float* scale, float* rstd, cudaStream_t st) {
+  ProfScope prof("add_rms_norm", st);
+  cudaError_t e;
+  if (x_f32)
+    e = res_f32 ? norm_typed<float, float>(x, res, weight, T, H, eps, res_out, out, q, scale, rstd, st)
+                : norm_typed<float, __nv_bfloat16>(x, res, weight, T, H, eps, res_out, out, q, scale, rstd, st);
+  else
+    e = res_f32 ? norm_typed<__nv_bfloat16, float>(x, res, weight, T, H, eps, res_out, out, q, scale, rstd, st)
+                : norm_typed<__nv_bfloat16, __nv_bfloat16>(x, res, weight, T, H, eps, res_out, out, q, scale, rstd, st);
+  return check_cuda(e, "norm_kernel");
+}
+
+// Rows of one block, and so of one partial row of dw: about 4 blocks per SM for a large batch, a function of T alone
+// (not of the device), so that the order of the sum is too.
+int norm_bwd_rows(int T) { return (T + 607) / 608; }
+
+int norm_bwd_launch(const void* dy, int dy_f32, const void* x, int x_f32, const void* weight, const float* rstd,
+                    const void* dres, int T, int H, void* dx, float* dw, float* part, cudaStream_t st) {
+  const int rows = norm_bwd_rows(T), P = (T + rows - 1) / rows;
+  {
+    ProfScope prof("rms_norm_bwd", st);
+    cudaError_t e;
+    float* pp = dw != nullptr ? part : nullptr;
+    if (x_f32)
+      e = dy_f32 ? norm_bwd_typed<float, float>(dy, x, weight, rstd, dres, T, H, rows, P, dx, pp, st)
+                 : norm_bwd_typed<float, __nv_bfloat16>(dy, x, weight, rstd, dres, T, H, rows, P, dx, pp, st);
+    else
+      e = dy_f32 ? norm_bwd_typed<__nv_bfloat16, float>(dy, x, weight, rstd, dres, T, H, rows, P, dx, pp, st)
+                 : norm_bwd_typed<__nv_bfloat16, __nv_bfloat16>(dy, x, weight, rstd, dres, T, H, rows, P, dx, pp, st);
+    const int rc = check_cuda(e, "norm_bwd_kernel");
+    if (rc || dw == nullptr) return rc;
+  }
+  ProfScope prof("rms_norm_dweight", st);
+  return check_cuda(launch_kernel(dweight_kernel, dim3((H + 31) / 32), dim3(32, 32), 0, st,
+                                  static_cast<const float*>(part), P, H, dw),
+                    "dweight_kernel");
+}
+
+int quantize_launch(const void* x, int x_f32, long long banks, int rows, int cols, int block_rows, void* q,
+                    float* scale, cudaStream_t st) {
+  const int nb = (cols + kFp8Block - 1) / kFp8Block;
+  uint8_t* qq = static_cast<uint8_t*>(q);
+  ProfScope prof("fp8_quantize", st);
+  if (block_rows == 1) {
+    const long long total = banks * rows;
+    const long long want = (total * nb + 15) / 16;
+    int sms = 0;
+    const int rc = device_sm_count(&sms);
+    if (rc) return rc;
+    const dim3 g(static_cast<unsigned>(want < sms * 16LL ? want : sms * 16LL));
+    return check_cuda(x_f32 ? launch_kernel(quant_rows_kernel<float>, g, dim3(256), 0, st, static_cast<const float*>(x),
+                                            total, cols, nb, qq, scale)
+                            : launch_kernel(quant_rows_kernel<__nv_bfloat16>, g, dim3(256), 0, st,
+                                            static_cast<const __nv_bfloat16*>(x), total, cols, nb, qq, scale),
+                      "quant_rows_kernel");
+  }
+  const int rb = (rows + kFp8Block - 1) / kFp8Block;
+  const long long blocks = banks * rb * nb;
+  if (blocks > 0x7fffffffLL) return set_error(INVMOE_ERR_UNSUPPORTED_SHAPE, "too many blocks for one launch");
+  const dim3 g(static_cast<unsigned>(blocks));
+  return check_cuda(x_f32 ? launch_kernel(quant_blocks_kernel<float>, g, dim3(256), 0, st, static_cast<const float*>(x),
+                                          rows, cols, nb, rb, qq, scale)
+                          : launch_kernel(quant_blocks_kernel<__nv_bfloat16>, g, dim3(256), 0, st,
+                                          static_cast<const __nv_bfloat16*>(x), rows, cols, nb, rb, qq, scale),
+                    "quant_blocks_kernel");
+}
+
+int permute_fp8_launch(const void* q, const float* scale, const int32_t* slot_row, int T, int k, int H, void* xp,
+                       float* xp_scale, cudaStream_t st) {
+  const int vec = H / 16, nb = (H + kFp8Block - 1) / kFp8Block;
+  int sms = 0;
+  const int rc = device_sm_count(&sms);
+  if (rc) return rc;
+  const long long want = (static_cast<long long>(T) * ((vec + 63) / 64) + 7) / 8;
+  const dim3 g(static_cast<unsigned>(want < sms * 8LL ? want : sms * 8LL));
+  ProfScope prof("permute_fp8", st);
+  return check_cuda(launch_kernel(permute_fp8_kernel, g, dim3(256), 0, st, static_cast<const uint4*>(q), scale,
+                                  slot_row, static_cast<long long>(T), k, vec, nb, static_cast<uint4*>(xp), xp_scale),
+                    "permute_fp8_kernel");
+}
+
+}  // namespace invmoe

@@ -157,6 +157,22 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, WaitCt
   return mbar_test<CLUSTER>(bar, parity) || mbar_wait_slow<CLUSTER>(bar, parity, w);
 }
 
+// mbar_wait with its slow path in line, for a warp that holds many registers: a call would have to save them all.
+__device__ __forceinline__ bool mbar_wait_inline(uint64_t* bar, uint32_t parity, const WaitCtl& w) {
+  if (mbar_test(bar, parity)) return true;
+  uint64_t t0 = 0;
+  for (uint32_t it = 0; it < (1u << 28); ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (w.abort != nullptr && *w.abort) return false;
+    const uint64_t t = global_timer_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > w.limit_ns) break;
+  }
+  if (w.abort != nullptr) *w.abort = 1;
+  atomicOr(w.status, kStatusTimeout);
+  return false;
+}
+
 // ---------------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {

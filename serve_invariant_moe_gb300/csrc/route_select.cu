@@ -1,0 +1,304 @@
+// route_select.cu -- expert choice by scores: sigmoid or softmax, a balance bias, expert groups, top-k, renormalised
+// weights; and the gradient of the weights with respect to the logits.
+//
+// One warp per token, lane l holding experts l, l + 32, ...  Everything that decides a choice is either exact or a
+// single correctly defined fp32 value, so the chosen experts do not depend on any summation order:
+//   * without a bias the choice is by logit (both scores increase with it), so no score is computed for the losers;
+//   * with a bias the choice is by score + bias, one fp32 addition; a group's value is the sum of its two largest;
+//   * the softmax denominator is summed in fixed point (steps of 2^-42, integers), exact whatever the order.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace invmoe {
+
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kSelThreads = 256;
+
+// Larger = ranks earlier; NaN -> 0 (below every number); -0 and +0 tie.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  if (v != v) return 0u;
+  const uint32_t b = __float_as_uint(v == 0.0f ? 0.0f : v);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+__device__ __forceinline__ float key_value(uint32_t key) {
+  if (key == 0u) return __uint_as_float(0x7fc00000u);
+  return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
+}
+
+__device__ __forceinline__ float sigmoid_f32(float l) { return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-l))); }
+
+// Shift and denominator of the softmax over a row held as l[i] = logit of expert i * 32 + lane.  A row of -inf alone
+// has shift 0 and denominator 0; a row with a NaN or +inf has a NaN denominator.
+struct SoftmaxStats {
+  float shift, total;
+};
+template <int EPL>
+__device__ __forceinline__ SoftmaxStats softmax_stats(const float (&l)[EPL], int E, int lane) {
+  uint32_t best = 0u;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i)
+    if (i * 32 + lane < E) best = max(best, order_key(l[i]));
+  SoftmaxStats s;
+  const float m = key_value(__reduce_max_sync(kFull, best));
+  s.shift = m == -INFINITY ? 0.0f : m;
+  // e = (hi + lo * 2^-21) * 2^-21 up to 2^-42: hi <= 2^21, lo < 2^21, at most 1024 experts: no overflow in 32 bits
+  unsigned hi = 0u, lo = 0u;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    if (i * 32 + lane < E) {
+      const float e = expf(__fsub_rn(l[i], s.shift));
+      if (e <= 1.0f) {
+        const float t = __fmul_rn(e, 2097152.0f);
+        const unsigned h = static_cast<unsigned>(t);
+        hi += h;
+        lo += static_cast<unsigned>(__fmul_rn(__fsub_rn(t, static_cast<float>(h)), 2097152.0f));
+      } else {
+        bad = true;
+      }
+    }
+  }
+  hi = __reduce_add_sync(kFull, hi);
+  lo = __reduce_add_sync(kFull, lo);
+  const unsigned long long sum = (static_cast<unsigned long long>(hi) << 21) + lo;
+  s.total = __any_sync(kFull, bad) ? __uint_as_float(0x7fc00000u)
+                                   : __fmul_rn(__ull2float_rn(sum), 2.2737367544323206e-13f);   // 2^-42
+  return s;
+}
+
+// p = exp(l - shift) / total; an empty row's scores are 0.
+__device__ __forceinline__ float softmax_score(float l, const SoftmaxStats& s) {
+  return s.total == 0.0f ? 0.0f : __fdiv_rn(expf(__fsub_rn(l, s.shift)), s.total);
+}
+
+struct SelectParams {
+  const float* logits;
+  const float* bias;
+  int T, E, k, n_group, topk_group, renorm;
+  float scale;
+  int32_t* idx;
+  float* w;
+};
+
+template <int EPL, bool SOFTMAX, bool GROUPS>
+__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p) {
+  pdl_wait();
+  pdl_trigger();
+  extern __shared__ uint32_t sm_keys[];      // GROUPS: per warp E choice keys, padded by one word per 32
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long t = static_cast<long long>(blockIdx.x) * (kSelThreads / 32) + warp;
+  if (t >= p.T) return;
+  const float* row = p.logits + t * p.E;
+  float l[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) l[i] = i * 32 + lane < p.E ? __ldg(row + i * 32 + lane) : -INFINITY;
+  SoftmaxStats st{0.0f, 1.0f};
+  if (SOFTMAX) st = softmax_stats<EPL>(l, p.E, lane);
+  uint32_t key[EPL];
+  uint32_t live = 0u;                         // bit i: expert i * 32 + lane may still be chosen
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = i * 32 + lane;
+    key[i] = 0u;
+    if (e < p.E) {
+      float c = l[i];
+      if (p.bias != nullptr) c = __fadd_rn(SOFTMAX ? softmax_score(c, st) : sigmoid_f32(c), __ldg(p.bias + e));
+      key[i] = order_key(c);
+      live |= 1u << i;
+    }
+  }
+  if (GROUPS) {
+    const int per = p.E / p.n_group;
+    uint32_t* sk = sm_keys + warp * (p.E + p.E / 32 + 1);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (i * 32 + lane < p.E) sk[i * 33 + lane] = key[i];
+    __syncwarp();
+    // lane g: the two largest keys of group g
+    uint32_t gkey = 0u;
+    if (lane < p.n_group) {
+      uint32_t a = 0u, b = 0u;
+      for (int j = 0; j < per; ++j) {
+        const int e = lane * per + j;
+        const uint32_t v = sk[e + (e >> 5)];
+        b = max(b, min(a, v));
+        a = max(a, v);
+      }
+      gkey = p.bias != nullptr && per > 1 ? order_key(__fadd_rn(key_value(a), key_value(b))) : a;
+    }
+    int rank = 0;
+    for (int g = 0; g < p.n_group; ++g) {
+      const uint32_t o = __shfl_sync(kFull, gkey, g);
+      if (o > gkey || (o == gkey && g < lane)) ++rank;
+    }
+    const unsigned kept = __ballot_sync(kFull, lane < p.n_group && rank < p.topk_group);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = i * 32 + lane;
+      if (e < p.E && !((kept >> (e / per)) & 1u)) live &= ~(1u << i);
+    }
+  }
+  int my_e = 0;
+  for (int j = 0; j < p.k; ++j) {
+    uint32_t best = 0u;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if ((live >> i) & 1u) best = max(best, key[i]);
+    const uint32_t gbest = __reduce_max_sync(kFull, best);
+    uint32_t cand = 0xffffffffu;
+#pragma unroll
+    for (int i = EPL - 1; i >= 0; --i)
+      if (((live >> i) & 1u) && key[i] == gbest) cand = static_cast<uint32_t>(i * 32 + lane);
+    const int e = static_cast<int>(__reduce_min_sync(kFull, cand));
+    if ((e & 31) == lane) live &= ~(1u << (e >> 5));
+    if (lane == j) my_e = e;
+  }
+  float s = 0.0f;
+  if (lane < p.k) {
+    const float lj = __ldg(row + my_e);
+    s = SOFTMAX ? softmax_score(lj, st) : sigmoid_f32(lj);
+  }
+  if (p.renorm) {
+    float sum = 0.0f;
+    for (int j = 0; j < p.k; ++j) sum = __fadd_rn(sum, __shfl_sync(kFull, s, j));
+    s = sum == 0.0f ? 0.0f : __fdiv_rn(s, sum);
+  }
+  if (lane < p.k) {
+    p.idx[t * p.k + lane] = my_e;
+    p.w[t * p.k + lane] = __fmul_rn(s, p.scale);
+  }
+}
+
+// Gradient of the weights: with s_j the chosen scores, S = sum_j s_j, d_j = scale * dw_j,
+//   renormalised      ds_j = (d_j - sum_i d_i s_i / S) / S        (0 where S = 0)
+//   otherwise         ds_j = d_j
+//   sigmoid           dl_j = ds_j s_j (1 - s_j), other experts 0
+//   softmax           dl_e = p_e (ds_e - sum_j ds_j p_j), ds_e = 0 for experts not chosen; renormalised, the sum is 0
+//                     and only the chosen experts have a gradient
+// One warp per token; an entry of topk_idx outside [0, E) takes no part.
+template <int EPL, bool SOFTMAX>
+__global__ void __launch_bounds__(kSelThreads)
+    select_bwd_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx, const float* __restrict__ dw,
+                      int T, int E, int k, int renorm, float scale, float* __restrict__ dl,
+                      __nv_bfloat16* __restrict__ dl_bf16) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const long long t = static_cast<long long>(blockIdx.x) * (kSelThreads / 32) + (threadIdx.x >> 5);
+  if (t >= T) return;
+  const float* row = logits + t * E;
+  SoftmaxStats st{0.0f, 1.0f};
+  float l[SOFTMAX ? EPL : 1];
+  if constexpr (SOFTMAX) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) l[i] = i * 32 + lane < E ? __ldg(row + i * 32 + lane) : -INFINITY;
+    st = softmax_stats<EPL>(l, E, lane);
+  }
+  int e = -1;
+  float s = 0.0f, d = 0.0f;
+  if (lane < k) {
+    e = __ldg(idx + t * k + lane);
+    if (e < 0 || e >= E) e = -1;
+    if (e >= 0) {
+      const float lj = __ldg(row + e);
+      s = SOFTMAX ? softmax_score(lj, st) : sigmoid_f32(lj);
+      d = __fmul_rn(__ldg(dw + t * k + lane), scale);
+    }
+  }
+  float sum = 0.0f, dot = 0.0f;
+  for (int j = 0; j < k; ++j) {
+    const float sj = __shfl_sync(kFull, s, j);
+    sum += sj;
+    dot = fmaf(__shfl_sync(kFull, d, j), sj, dot);
+  }
+  if (renorm) d = sum == 0.0f ? 0.0f : __fdiv_rn(d - __fdiv_rn(dot, sum), sum);
+  // value of a chosen expert's entry beyond what every expert gets
+  const float mine = SOFTMAX ? __fmul_rn(d, s) : d * s * (1.0f - s);
+  const float all = SOFTMAX && !renorm ? dot : 0.0f;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int c = i * 32 + lane;
+    float v = 0.0f;
+    for (int j = 0; j < k; ++j) {
+      const int ej = __shfl_sync(kFull, e, j);
+      const float vj = __shfl_sync(kFull, mine, j);
+      if (ej == c) v += vj;
+    }
+    if (c < E) {
+      if constexpr (SOFTMAX)
+        if (!renorm) v -= __fmul_rn(all, softmax_score(l[i], st));
+      if (dl != nullptr) dl[t * E + c] = v;
+      if (dl_bf16 != nullptr) dl_bf16[t * E + c] = __float2bfloat16_rn(v);
+    }
+  }
+}
+
+template <int EPL>
+cudaError_t select_epl(const SelectParams& p, int softmax, dim3 g, cudaStream_t st) {
+  const dim3 b(kSelThreads);
+  if (p.n_group > 1) {
+    const size_t smem = (kSelThreads / 32) * (static_cast<size_t>(p.E) + p.E / 32 + 1) * 4;
+    return softmax ? launch_kernel(select_kernel<EPL, true, true>, g, b, smem, st, p)
+                   : launch_kernel(select_kernel<EPL, false, true>, g, b, smem, st, p);
+  }
+  return softmax ? launch_kernel(select_kernel<EPL, true, false>, g, b, 0, st, p)
+                 : launch_kernel(select_kernel<EPL, false, false>, g, b, 0, st, p);
+}
+
+template <int EPL>
+cudaError_t select_bwd_epl(const float* logits, const int32_t* idx, const float* dw, int T, int E, int k, int softmax,
+                           int renorm, float scale, float* dl, void* dl_bf16, dim3 g, cudaStream_t st) {
+  __nv_bfloat16* db = static_cast<__nv_bfloat16*>(dl_bf16);
+  return softmax ? launch_kernel(select_bwd_kernel<EPL, true>, g, dim3(kSelThreads), 0, st, logits, idx, dw, T, E, k,
+                                 renorm, scale, dl, db)
+                 : launch_kernel(select_bwd_kernel<EPL, false>, g, dim3(kSelThreads), 0, st, logits, idx, dw, T, E, k,
+                                 renorm, scale, dl, db);
+}
+
+dim3 warp_per_token(int T) {
+  return dim3(static_cast<unsigned>((static_cast<long long>(T) * 32 + kSelThreads - 1) / kSelThreads));
+}
+
+}  // namespace
+
+int select_launch(const float* logits, const float* bias, int T, int E, int k, int softmax, int n_group, int topk_group,
+                  int renorm, float scale, int32_t* idx, float* w, cudaStream_t st) {
+  // all groups kept: the choice is over every expert, no group value matters
+  const SelectParams p{logits, bias, T, E, k, topk_group == n_group ? 1 : n_group, topk_group, renorm, scale, idx, w};
+  const dim3 g = warp_per_token(T);
+  const int epl = (E + 31) / 32;
+  ProfScope prof("route_select", st);
+  cudaError_t e;
+  if (epl <= 1) e = select_epl<1>(p, softmax, g, st);
+  else if (epl <= 2) e = select_epl<2>(p, softmax, g, st);
+  else if (epl <= 4) e = select_epl<4>(p, softmax, g, st);
+  else if (epl <= 8) e = select_epl<8>(p, softmax, g, st);
+  else if (epl <= 16) e = select_epl<16>(p, softmax, g, st);
+  else e = select_epl<32>(p, softmax, g, st);
+  return check_cuda(e, "select_kernel");
+}
+
+int select_bwd_launch(const float* logits, const int32_t* idx, const float* dw, int T, int E, int k, int softmax,
+                      int renorm, float scale, float* dl, void* dl_bf16, cudaStream_t st) {
+  const dim3 g = warp_per_token(T);
+  const int epl = (E + 31) / 32;
+  ProfScope prof("route_select_bwd", st);
+  cudaError_t e;
+  if (epl <= 1) e = select_bwd_epl<1>(logits, idx, dw, T, E, k, softmax, renorm, scale, dl, dl_bf16, g, st);
+  else if (epl <= 2) e = select_bwd_epl<2>(logits, idx, dw, T, E, k, softmax, renorm, scale, dl, dl_bf16, g, st);
+  else if (epl <= 4) e = select_bwd_epl<4>(logits, idx, dw, T, E, k, softmax, renorm, scale, dl, dl_bf16, g, st);
+  else if (epl <= 8) e = select_bwd_epl<8>(logits, idx, dw, T, E, k, softmax, renorm, scale, dl, dl_bf16, g, st);
+  else if (epl <= 16) e = select_bwd_epl<16>(logits, idx, dw, T, E, k, softmax, renorm, scale, dl, dl_bf16, g, st);
+  else e = select_bwd_epl<32>(logits, idx, dw, T, E, k, softmax, renorm, scale, dl, dl_bf16, g, st);
+  return check_cuda(e, "select_bwd_kernel");
+}
+
+}  // namespace invmoe
