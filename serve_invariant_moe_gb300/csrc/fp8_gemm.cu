@@ -49,7 +49,7 @@ struct Fp8Params {
   const int* offsets;
   void* out;                // [token rows, N] fp32 / bf16 / e4m3
   float* out_scale;         // SwiGLU: [token rows, N / 128]
-  int vec_scale;            // KB % 4 == 0 and aligned bases: scales in 16-byte loads
+  int vec_scale;            // KB % 4 == 0 and 16-byte aligned bases: four blocks' scales in one load
   int vec_out;              // N % 4 == 0: outputs in vectors
   unsigned int* status;
   unsigned long long timeout_ns;
@@ -59,7 +59,8 @@ constexpr int kWTile = 128;                         // weight rows per sub-tile
 constexpr int kWBytes = kWTile * kFp8Block;         // 16 KB
 constexpr int kMaxGroups = 1024;
 constexpr int kEpiWarps = 8;
-constexpr int kFirstEpiWarp = 4;                    // warps 0..3: producer, MMA issuer, prefix sums, idle
+constexpr int kScaleWarps = 2;
+constexpr int kFirstEpiWarp = 2 + kScaleWarps;      // warp 0: producer, warp 1: MMA issuer, warps 2 and 3: scales
 constexpr int kFp8Threads = 32 * (kFirstEpiWarp + kEpiWarps);
 // Registers per thread: 168 at launch (65,536 / 384, whole units of 8).  A tile of 256 x 128 leaves 128 accumulators in
 // each of the 256 epilogue threads, so there the first warpgroup hands registers over: 56 + 2 * 224 = 3 * 168.
@@ -77,7 +78,8 @@ struct Fp8Shape {
   static constexpr int ACC = 512 / ACC_COLS < 4 ? 512 / ACC_COLS : 4;   // TMEM buffers
   static constexpr int TMEM_COLS = ACC * ACC_COLS < 32 ? 32 : ACC * ACC_COLS;
   static constexpr int HALF = NT / 2;                                   // token columns of a warpgroup
-  static constexpr int SCALE_BYTES = 2 * 2 * MT * HALF * 4;             // [warpgroup][buffer][sub-tile][column]
+  static constexpr int SLOT = NT + 4;                                   // a buffer's scales: NT tokens, MT weight blocks
+  static constexpr int SCALE_BYTES = ACC * SLOT * 4;
   static constexpr int AMAX_BYTES = 2 * 4 * HALF * 4;                   // [warpgroup][warp][column]
   static constexpr int FIXED = 1024 + 2 * kStagingBytes + SCALE_BYTES + AMAX_BYTES + 256 + 4 * (kMaxGroups + 1) + 12;
   static constexpr int STAGES = (232448 - FIXED) / STAGE_BYTES < 8 ? (232448 - FIXED) / STAGE_BYTES : 8;
@@ -141,11 +143,39 @@ __device__ __forceinline__ void reg_fence(uint32_t (&r)[R]) {
   for (int i = 0; i < R; ++i) asm volatile("" : "+r"(r[i]));
 }
 
+// Two fp32 fused multiply-adds, and two products, per instruction (each correctly rounded).
+__device__ __forceinline__ void fma2(unsigned long long& acc, unsigned long long a, unsigned long long b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long pack2(uint32_t lo, uint32_t hi) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ float unpack2(unsigned long long v, int hi) {
+  return __uint_as_float(static_cast<uint32_t>(hi ? v >> 32 : v));
+}
+
 // All four warps of a warpgroup execute the one instruction of its side of the split.
 __device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoaderRegs)); }
 __device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs)); }
 
 __device__ __forceinline__ void bar_wg(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+
+// Scales of blocks kb .. kb + 3 of one row (zeros past the last).
+__device__ __forceinline__ float4 load_scales(const float* src, int kb, const Fp8Params& p) {
+  if (p.vec_scale) return __ldg(reinterpret_cast<const float4*>(src + kb));
+  float4 v = make_float4(__ldg(src + kb), 0.0f, 0.0f, 0.0f);
+  if (kb + 1 < p.KB) v.y = __ldg(src + kb + 1);
+  if (kb + 2 < p.KB) v.z = __ldg(src + kb + 2);
+  if (kb + 3 < p.KB) v.w = __ldg(src + kb + 3);
+  return v;
+}
 
 struct Fp8Unit {
   int row0;      // first token row
@@ -184,6 +214,35 @@ __device__ __forceinline__ Fp8Unit fp8_unit(int u, const Fp8Params& p, const int
   return U;
 }
 
+// One warp: prefix[g] = chunks of CH rows in the groups before g, and their total.
+template <int CH>
+__device__ __forceinline__ void prefix_chunks(const Fp8Params& p, int* prefix, int* total, int lane) {
+  if (p.G == 0) {
+    if (lane == 0) *total = (p.M + CH - 1) / CH;
+    return;
+  }
+  const int per = (p.G + 31) / 32;
+  const int g0 = lane * per;
+  int local = 0;
+  for (int i = 0; i < per; ++i)
+    if (g0 + i < p.G) local += (__ldg(p.counts + g0 + i) + CH - 1) / CH;
+  int incl = local;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += v;
+  }
+  int run = incl - local;
+  for (int i = 0; i < per; ++i)
+    if (g0 + i < p.G) {
+      prefix[g0 + i] = run;
+      run += (__ldg(p.counts + g0 + i) + CH - 1) / CH;
+    }
+  if (lane == 31) {
+    prefix[p.G] = incl;
+    *total = incl;
+  }
+}
+
 template <int MT, int NT, int EPI>
 __global__ void __launch_bounds__(kFp8Threads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
@@ -213,7 +272,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       mbar_init(&empty_bar[s], 1);
     }
     for (int a = 0; a < S::ACC; ++a) {
-      mbar_init(&accf_bar[a], 1);
+      mbar_init(&accf_bar[a], 1 + kScaleWarps);
       mbar_init(&acce_bar[a], kEpiWarps);
     }
     *s_abort = 0;
@@ -225,32 +284,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
   // everything above touches only shared memory, TMEM and the kernel parameters
   pdl_wait();
   pdl_trigger();
-  if (warp == 2) {
-    if (p.G > 0) {
-      const int per = (p.G + 31) / 32;
-      const int g0 = lane * per;
-      int local = 0;
-      for (int i = 0; i < per; ++i)
-        if (g0 + i < p.G) local += (__ldg(p.counts + g0 + i) + NT - 1) / NT;
-      int incl = local;
-      for (int d = 1; d < 32; d <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += v;
-      }
-      int run = incl - local;
-      for (int i = 0; i < per; ++i)
-        if (g0 + i < p.G) {
-          s_prefix[g0 + i] = run;
-          run += (__ldg(p.counts + g0 + i) + NT - 1) / NT;
-        }
-      if (lane == 31) {
-        s_prefix[p.G] = incl;
-        *s_total = incl;
-      }
-    } else if (lane == 0) {
-      *s_total = (p.M + NT - 1) / NT;
-    }
-  }
+  if (warp == 2) prefix_chunks<NT>(p, s_prefix, s_total, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -337,70 +371,135 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       // every MMA issued here has finished before the CTA releases TMEM
       WaitCtl drain{nullptr, p.status, p.timeout_ns};
       if (issued) mbar_wait(&accf_bar[last_acc], last_phase, drain);
+    } else if (warp >= 2) {
+      // ---------------------------------------------------------- scales
+      // Thread j prepares the scales of tokens j and j + 64 for every block, as they are needed: buffer `acc` gets them
+      // together with its products (its barrier counts the MMA's commit and these two warps).  Four blocks' scales
+      // come in one load (or four), issued four blocks ahead.
+      constexpr int PER = NT > 64 ? NT / 64 : 1;
+      const int j0 = (warp - 2) * 32 + lane;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < total_units; u += gridDim.x) {
+        const Fp8Unit U = fp8_unit<NT>(u, p, s_prefix, total_chunks);
+        // PER token rows, then (threads below MT) a weight block row
+        const float* src[PER + 1];
+        bool on[PER + 1];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int c = j0 + 64 * i;
+          src[i] = p.a_scale + static_cast<long long>(U.row0 + min(c, U.cols - 1)) * p.KB;
+          on[i] = c < NT;
+        }
+        {
+          const int srow = EPI == FP8_SWIGLU ? j0 * (p.N / kFp8Block) + U.nb : U.nb * MT + j0;
+          src[PER] = p.w_scale + (static_cast<long long>(U.g) * p.w_srows + min(srow, p.w_srows - 1)) * p.KB;
+          on[PER] = j0 < MT;
+        }
+        float4 next[PER + 1];
+#pragma unroll
+        for (int i = 0; i <= PER; ++i) next[i] = on[i] ? load_scales(src[i], 0, p) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int kb0 = 0; ok && kb0 < p.KB; kb0 += 4) {
+          float4 cur[PER + 1];
+#pragma unroll
+          for (int i = 0; i <= PER; ++i) {
+            cur[i] = next[i];
+            if (on[i] && kb0 + 4 < p.KB) next[i] = load_scales(src[i], kb0 + 4, p);
+          }
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            if (kb0 + d >= p.KB) break;
+            ok = __all_sync(0xffffffffu, mbar_wait(&acce_bar[acc], acc_phase ^ 1u, wc));
+            if (!ok) break;
+            float* slot = s_scale + acc * S::SLOT;
+#pragma unroll
+            for (int i = 0; i <= PER; ++i)
+              if (on[i]) {
+                const float v = d == 0 ? cur[i].x : d == 1 ? cur[i].y : d == 2 ? cur[i].z : cur[i].w;
+                slot[i < PER ? j0 + 64 * i : NT + j0] = v;
+              }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&accf_bar[acc]);
+            if (++acc == S::ACC) { acc = 0; acc_phase ^= 1u; }
+          }
+        }
+      }
     }
   } else {
     // ------------------------------------------------------------ scaling and epilogue
     if constexpr (SPLIT_REGS) take_registers();
-    // All eight warps walk the same units and blocks whatever happens, so the warpgroup barriers always meet; after a
+    // All eight warps walk the same units whatever happens, so the warpgroup barriers always meet; after a
     // wait that ran out (ok = false) a warp only keeps those barriers.
     constexpr int X = NT / 16;                         // 8-column fragments of a warpgroup's columns
     const int q = warp & 3;                            // TMEM lane quadrant
     const int half = (warp - kFirstEpiWarp) >> 2;                  // warpgroup: token columns [half * HALF, +HALF)
     const int tid = q * 32 + lane;                     // thread of the warpgroup
     const int bar_id = 1 + half;
-    float* my_scale = s_scale + half * (2 * MT * S::HALF);
     float* my_amax = s_amax + half * (4 * S::HALF);
     uint8_t* stg = staging + half * kStagingBytes;
-    const int sm_m = tid / S::HALF;                    // the scale this thread prepares: sub-tile, column
-    const int sm_c = tid % S::HALF;
     int acc = 0;
     uint32_t acc_phase = 0;
-    int sbuf = 0;
     bool ok = true;
     for (int u = blockIdx.x; u < total_units; u += gridDim.x) {
       const Fp8Unit U = fp8_unit<NT>(u, p, s_prefix, total_chunks);
       const int wg_cols = U.cols - half * S::HALF;     // this warpgroup's tokens (may be <= 0)
-      const float* ap = p.a_scale + static_cast<long long>(U.row0 + min(half * S::HALF + sm_c, U.cols - 1)) * p.KB;
-      const int srow = EPI == FP8_SWIGLU ? sm_m * (p.N / kFp8Block) + U.nb : U.nb * MT + sm_m;
-      const float* wp = p.w_scale + (static_cast<long long>(U.g) * p.w_srows + min(srow, p.w_srows - 1)) * p.KB;
-      float v[MT][2][4 * X];
+      // accumulators in pairs of neighbouring columns: [sub-tile][16-lane half][fragment, row of 8]
+      unsigned long long v2[MT][2][2 * X];
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int i = 0; i < 4 * X; ++i) v[m][h][i] = 0.0f;
-      float s_next = 0.0f;
-      if (sm_m < MT) s_next = __fmul_rn(__ldg(ap), __ldg(wp));
+          for (int i = 0; i < 2 * X; ++i) v2[m][h][i] = 0ull;
       for (int kb = 0; kb < p.KB; ++kb) {
-        float* sb = my_scale + sbuf * (MT * S::HALF);
-        if (sm_m < MT) {
-          sb[sm_m * S::HALF + sm_c] = s_next;
-          if (kb + 1 < p.KB) s_next = __fmul_rn(__ldg(ap + kb + 1), __ldg(wp + kb + 1));
-        }
-        bar_wg(bar_id);
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(&accf_bar[acc], acc_phase, wc));
         if (ok) {
           tc_fence_after();
           if (wg_cols > 0) {
             const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                 static_cast<uint32_t>(acc * S::ACC_COLS + half * S::HALF);
+            const float* slot = s_scale + acc * S::SLOT;
+            unsigned long long wsc[MT];
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
+              const uint32_t w = __float_as_uint(slot[NT + m]);
+              wsc[m] = pack2(w, w);
+            }
+            // steps of XC fragments of one sub-tile, both 16-lane halves; the next step's TMEM loads are in flight
+            // while this step's products are added
+            constexpr int XC = X < 4 ? X : 4;
+            constexpr int STEPS = X / XC * MT;
+            uint32_t r[2][2][4 * XC];
+            unsigned long long asc[XC];
+            auto issue = [&](int st) {
+              const uint32_t at = tb + static_cast<uint32_t>((st % MT) * NT + (st / MT) * XC * 8);
+              tmem_ld_16x256b<XC>(at, r[st & 1][0]);
+              tmem_ld_16x256b<XC>(at + (16u << 16), r[st & 1][1]);
+            };
+            issue(0);
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                uint32_t r[4 * X];
-                tmem_ld_16x256b<X>(tb + (static_cast<uint32_t>(h * 16) << 16) + static_cast<uint32_t>(m * NT), r);
-                tmem_ld_wait();
-                reg_fence(r);
+            for (int st = 0; st < STEPS; ++st) {
+              const int m = st % MT, c = st / MT;
+              if (m == 0) {
 #pragma unroll
-                for (int i = 0; i < X; ++i) {
-                  const float2 s = *reinterpret_cast<const float2*>(sb + m * S::HALF + 8 * i + 2 * (lane & 3));
-                  v[m][h][4 * i] = fmaf(__uint_as_float(r[4 * i]), s.x, v[m][h][4 * i]);
-                  v[m][h][4 * i + 1] = fmaf(__uint_as_float(r[4 * i + 1]), s.y, v[m][h][4 * i + 1]);
-                  v[m][h][4 * i + 2] = fmaf(__uint_as_float(r[4 * i + 2]), s.x, v[m][h][4 * i + 2]);
-                  v[m][h][4 * i + 3] = fmaf(__uint_as_float(r[4 * i + 3]), s.y, v[m][h][4 * i + 3]);
-                }
+                for (int i = 0; i < XC; ++i)
+                  asc[i] = *reinterpret_cast<const unsigned long long*>(slot + half * S::HALF + 8 * (c * XC + i) +
+                                                                        2 * (lane & 3));
+              }
+              tmem_ld_wait();
+              reg_fence(r[st & 1][0]);
+              reg_fence(r[st & 1][1]);
+              if (st + 1 < STEPS) issue(st + 1);
+#pragma unroll
+              for (int i = 0; i < XC; ++i) {
+                const unsigned long long sc = mul2(asc[i], wsc[m]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    fma2(v2[m][h][2 * (c * XC + i) + e],
+                         pack2(r[st & 1][h][4 * i + 2 * e], r[st & 1][h][4 * i + 2 * e + 1]), sc);
               }
             }
           }
@@ -409,10 +508,17 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
           if (lane == 0) mbar_arrive(&acce_bar[acc]);
         }
         if (++acc == S::ACC) { acc = 0; acc_phase ^= 1u; }
-        sbuf ^= 1;
       }
+      float v[MT][2][4 * X];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4 * X; ++i) v[m][h][i] = unpack2(v2[m][h][i >> 1], i & 1);
       const long long out_row0 = static_cast<long long>(U.row0) + half * S::HALF;
       if constexpr (EPI == FP8_SWIGLU) {
+        bar_wg(bar_id);                                // the previous unit's maxima and staging have been read
         // h in place of the gate values; each column's absolute maximum over the thread's 4 rows, the warp's 32
         // (lanes that differ in lane / 4) and the 4 warps
 #pragma unroll
@@ -466,7 +572,6 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
           if (ok && t < wg_cols)
             *reinterpret_cast<uint4*>(out + static_cast<long long>(t) * p.N + 16 * (tid & 7)) =
                 *reinterpret_cast<const uint4*>(stg + t * kStageFp8 + 16 * (tid & 7));
-        // the next unit's first staging write comes after at least one warpgroup barrier
       } else {
         constexpr int CI = X < 2 ? 1 : 2;              // fragments (8 tokens each) staged at a time
         float* stf = reinterpret_cast<float*>(stg);
@@ -531,38 +636,421 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
   }
 }
 
+// ------------------------------------------------------------ CTA pairs: token rows on the M side
+//
+// The same product with the roles exchanged, for many rows: a pair of CTAs computes 256 token rows x 256 weight columns,
+// each CTA loading its own 128 rows of both operands (the MMA reads the other CTA's half of the weights from the
+// partner), so a K block costs each SM 32 KB of copies and 32 KB of operand reads for 2 x 128 x 256 x 128 products; the
+// single-CTA tile above pays 48 KB and 64 KB for the same work, and shared memory is what bounds it.  A thread holds one
+// token row, so its scale is one number per block and half, read from global memory four blocks ahead: no shared memory
+// at all on the scaling path.  Tiles are 256 rows whatever a group has, which the copies of its weights hide.
+// SwiGLU: CTA 0 loads the 128 gate rows of the block, CTA 1 the matching up rows, and every thread has both halves of
+// 64 of its row's h.
+struct Fp8PairShape {
+  static constexpr int TILE_BYTES = kWTile * kFp8Block;       // 16 KB: 128 rows x 128 e4m3
+  static constexpr int STAGE_BYTES = 2 * TILE_BYTES;          // this CTA's token rows, then its weight rows
+  static constexpr int STAGES = 6;
+  static constexpr int ACC_COLS = 256;
+  static constexpr int ACC = 2;
+  static constexpr int OSTAGE_BYTES = kEpiWarps * 32 * 64;
+  static constexpr int AMAX_BYTES = 2 * 2 * kWTile * 4;       // [unit parity][warpgroup][row]
+  static constexpr int BAR_BYTES = 256;
+  static constexpr int SMEM_BYTES =
+      1024 + STAGES * STAGE_BYTES + OSTAGE_BYTES + AMAX_BYTES + BAR_BYTES + 4 * (kMaxGroups + 1) + 12;
+  static_assert(SMEM_BYTES <= 232448, "shared memory");
+  static_assert(8 * (2 * STAGES + 2 * ACC + 1) + 16 <= BAR_BYTES, "barriers");
+};
+
+__device__ __forceinline__ void umma_fp8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// A warp's 32 rows x 64 bytes from registers (one row per lane) to global memory, 4 lanes per row: the 16-byte piece c of
+// row r sits at r * 64 + (c ^ ((r >> 1) & 3)) * 16, free of bank conflicts both ways.  Rows of a length or base that is
+// not a multiple of 16 bytes are written element by element.
+template <int ELT>
+__device__ __forceinline__ void store_rows64(uint8_t* stage, const uint32_t (&v)[16], uint8_t* out, long long ld_bytes,
+                                             int rows_valid, long long bytes_valid, bool vec) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<uint4*>(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+        make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+  __syncwarp();
+  const int c = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2);
+    const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+    if (r < rows_valid && c * 16 < bytes_valid) {
+      uint8_t* d = out + r * ld_bytes + c * 16;
+      if (vec) {
+        *reinterpret_cast<uint4*>(d) = w;
+      } else {
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 16 / ELT; ++e) {
+          if (c * 16 + e * ELT < bytes_valid) {
+            if (ELT == 4) *reinterpret_cast<uint32_t*>(d + 4 * e) = x[e];
+            else *reinterpret_cast<uint16_t*>(d + 2 * e) = static_cast<uint16_t>(x[e >> 1] >> (16 * (e & 1)));
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+}
+
+template <int EPI>
+__global__ void __launch_bounds__(kFp8Threads, 1)
+    fp8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
+                    const Fp8Params p) {
+  using S = Fp8PairShape;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* ostage = ring + S::STAGES * S::STAGE_BYTES;
+  float* s_amax = reinterpret_cast<float*>(ostage + S::OSTAGE_BYTES);
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(s_amax) + S::AMAX_BYTES);
+  uint64_t* empty_bar = full_bar + S::STAGES;
+  uint64_t* accf_bar = empty_bar + S::STAGES;
+  uint64_t* acce_bar = accf_bar + S::ACC;
+  uint64_t* final_bar = acce_bar + S::ACC;
+  uint32_t* misc = reinterpret_cast<uint32_t*>(final_bar + 1);
+  uint32_t* tmem_slot = misc;
+  volatile int* s_abort = reinterpret_cast<volatile int*>(misc + 1);
+  int* s_total = reinterpret_cast<int*>(misc + 2);
+  int* s_prefix = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full_bar) + S::BAR_BYTES);   // [G + 1]
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();          // 0 = leader (issues the MMAs), 1 = follower
+  constexpr int CH = 2 * kWTile;                    // token rows of a pair unit
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::STAGES; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int a = 0; a < S::ACC; ++a) {
+      mbar_init(&accf_bar[a], 1);
+      mbar_init(&acce_bar[a], 2 * kEpiWarps);
+    }
+    mbar_init(final_bar, 1);
+    *s_abort = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmA);
+  }
+  if (warp == 1) tmem_alloc_pair(tmem_slot, S::ACC * S::ACC_COLS);
+  // everything above touches only shared memory, TMEM and the kernel parameters
+  pdl_wait();
+  pdl_trigger();
+  if (warp == 2) prefix_chunks<CH>(p, s_prefix, s_total, lane);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();     // both CTAs' barriers initialised and TMEM allocated
+  tc_fence_after();
+
+  const uint32_t tmem_base = *tmem_slot;
+  const int total_chunks = *s_total;
+  const int total_units = total_chunks * p.n_blocks;
+  const int pair = static_cast<int>(blockIdx.x) / 2, pairs = static_cast<int>(gridDim.x) / 2;
+  WaitCtl wc{s_abort, p.status, p.timeout_ns};
+  const uint32_t peer_abort = mapa_shared(smem_u32(const_cast<int*>(s_abort)), rank ^ 1u);
+
+  if (warp < kFirstEpiWarp) {
+    give_registers();
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------------- producer (both CTAs)
+      int stage = 0;
+      uint32_t phase = 0;
+      int filled_phase[S::STAGES];
+#pragma unroll
+      for (int s = 0; s < S::STAGES; ++s) filled_phase[s] = -1;
+      bool ok = true;
+      for (int u = pair; ok && u < total_units; u += pairs) {
+        const Fp8Unit U = fp8_unit<CH>(u, p, s_prefix, total_chunks);
+        const int a_row = U.row0 + static_cast<int>(rank) * kWTile;
+        const int w_row = U.g * p.w_group_rows + (EPI == FP8_SWIGLU ? U.nb * kWTile + static_cast<int>(rank) * p.N
+                                                                    : (2 * U.nb + static_cast<int>(rank)) * kWTile);
+        for (int kb = 0; kb < p.KB; ++kb) {
+          if (!mbar_wait(&empty_bar[stage], phase ^ 1u, wc)) { ok = false; break; }
+          uint8_t* st = ring + stage * S::STAGE_BYTES;
+          const uint32_t fb = mapa_shared(smem_u32(&full_bar[stage]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], 2 * S::STAGE_BYTES);   // both CTAs' copies
+          tma_load_2d_pair(st, &tmA, fb, kb * kFp8Block, a_row);
+          tma_load_2d_pair(st + S::TILE_BYTES, &tmW, fb, kb * kFp8Block, w_row);
+          filled_phase[stage] = static_cast<int>(phase);
+          if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (!ok) st_shared_remote_u32(peer_abort, 1u);
+      // the leader's full barrier counts both CTAs' copies: all of them land before either CTA exits
+      if (rank == 0) {
+        WaitCtl drain{nullptr, p.status, p.timeout_ns};
+#pragma unroll
+        for (int s = 0; s < S::STAGES; ++s)
+          if (filled_phase[s] >= 0) mbar_wait(&full_bar[s], static_cast<uint32_t>(filled_phase[s]), drain);
+      }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      // ---------------------------------------------------------- MMA issuer (leader)
+      const uint64_t adesc0 = sdesc_k_sw128(smem_u32(ring));
+      const uint64_t wdesc0 = sdesc_k_sw128(smem_u32(ring + S::TILE_BYTES));
+      const uint32_t idesc = idesc_e4m3_f32(2 * kWTile, S::ACC_COLS);
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true;
+      for (int u = pair; ok && u < total_units; u += pairs) {
+        for (int kb = 0; kb < p.KB; ++kb) {
+          if (!mbar_wait<true>(&acce_bar[acc], acc_phase ^ 1u, wc) || !mbar_wait(&full_bar[stage], phase, wc)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t so = static_cast<uint64_t>((stage * S::STAGE_BYTES) >> 4);
+          const uint32_t d = tmem_base + static_cast<uint32_t>(acc * S::ACC_COLS);
+#pragma unroll
+          for (int kk = 0; kk < kFp8Block / 32; ++kk)
+            umma_fp8_pair(d, adesc0 + so + 2u * kk, wdesc0 + so + 2u * kk, idesc, kk != 0 ? 1u : 0u);
+          umma_commit_pair(&empty_bar[stage], 0x3);
+          umma_commit_pair(&accf_bar[acc], 0x3);
+          if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
+          if (++acc == S::ACC) { acc = 0; acc_phase ^= 1u; }
+        }
+      }
+      if (!ok) {
+        *s_abort = 1;
+        st_shared_remote_u32(peer_abort, 1u);
+      }
+      // every MMA issued here has finished before the pair releases TMEM
+      umma_commit_pair(final_bar, 0x1);
+      WaitCtl drain{nullptr, p.status, p.timeout_ns};
+      mbar_wait(final_bar, 0, drain);
+    }
+  } else {
+    // ------------------------------------------------------------ scaling and epilogue (both CTAs)
+    // All eight warps walk the same units whatever happens, so the SwiGLU barrier always meets; after a wait that ran
+    // out (ok = false) a warp only keeps that barrier.
+    take_registers();
+    const int q = warp & 3;                            // TMEM lane quadrant
+    const int ew = warp - kFirstEpiWarp;
+    const int half = ew >> 2;                          // warpgroup: half of the weight columns
+    const int r_in_tile = q * 32 + lane;
+    const uint32_t acce_leader0 = mapa_shared(smem_u32(&acce_bar[0]), 0);
+    uint8_t* stg = ostage + ew * 32 * 64;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    int parity = 0;
+    bool ok = true;
+    for (int u = pair; u < total_units; u += pairs) {
+      const Fp8Unit U = fp8_unit<CH>(u, p, s_prefix, total_chunks);
+      const int first = static_cast<int>(rank) * kWTile + q * 32;            // the warp's first row of the unit
+      const int rows_valid = U.cols - first;                                 // may be <= 0: nothing to scale or store
+      const float* ap = p.a_scale + static_cast<long long>(U.row0 + min(first + lane, U.cols - 1)) * p.KB;
+      // weight scales: one block of 128 columns per warpgroup, or (SwiGLU) a gate and an up block
+      const float* wbase = p.w_scale + static_cast<long long>(U.g) * p.w_srows * p.KB;
+      const float* wp0 = wbase + static_cast<long long>(EPI == FP8_SWIGLU ? U.nb : min(2 * U.nb + half, p.w_srows - 1)) * p.KB;
+      const float* wp1 = EPI == FP8_SWIGLU ? wp0 + static_cast<long long>(p.N / kFp8Block) * p.KB : wp0;
+      unsigned long long v2[4][16];
+#pragma unroll
+      for (int st = 0; st < 4; ++st)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v2[st][i] = 0ull;
+      float4 an = load_scales(ap, 0, p), wn0 = load_scales(wp0, 0, p), wn1 = wn0;
+      if (EPI == FP8_SWIGLU) wn1 = load_scales(wp1, 0, p);
+      for (int kb0 = 0; kb0 < p.KB; kb0 += 4) {
+        const float4 ac = an, wc0 = wn0, wc1 = wn1;
+        if (kb0 + 4 < p.KB) {
+          an = load_scales(ap, kb0 + 4, p);
+          wn0 = load_scales(wp0, kb0 + 4, p);
+          if (EPI == FP8_SWIGLU) wn1 = load_scales(wp1, kb0 + 4, p);
+        }
+#pragma unroll 1
+        for (int d = 0; d < 4; ++d) {
+          if (kb0 + d >= p.KB) break;
+          const float as = d == 0 ? ac.x : d == 1 ? ac.y : d == 2 ? ac.z : ac.w;
+          const float s0 = __fmul_rn(as, d == 0 ? wc0.x : d == 1 ? wc0.y : d == 2 ? wc0.z : wc0.w);
+          const float s1 = EPI == FP8_SWIGLU ? __fmul_rn(as, d == 0 ? wc1.x : d == 1 ? wc1.y : d == 2 ? wc1.z : wc1.w) : s0;
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(&accf_bar[acc], acc_phase, wc));
+          if (ok) {
+            tc_fence_after();
+            if (rows_valid > 0) {
+              const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                                  static_cast<uint32_t>(acc * S::ACC_COLS);
+              uint32_t r[2][32];
+              // 32 columns per step: SwiGLU two steps of gate columns, then the up columns of the same h
+              auto at = [&](int st) {
+                return tb + static_cast<uint32_t>(EPI == FP8_SWIGLU ? (st >> 1) * kWTile + half * 64 + (st & 1) * 32
+                                                                    : half * kWTile + st * 32);
+              };
+              tmem_ld32(at(0), r[0]);
+#pragma unroll
+              for (int st = 0; st < 4; ++st) {
+                tmem_ld_wait();
+                tmem_reg_fence(r[st & 1]);
+                if (st < 3) tmem_ld32(at(st + 1), r[(st + 1) & 1]);
+                const uint32_t sb = __float_as_uint(st < 2 ? s0 : s1);
+                const unsigned long long s2 = pack2(sb, sb);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) fma2(v2[st][i], pack2(r[st & 1][2 * i], r[st & 1][2 * i + 1]), s2);
+              }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote_cta(acce_leader0 + static_cast<uint32_t>(acc * 8));
+          }
+          if (++acc == S::ACC) { acc = 0; acc_phase ^= 1u; }
+        }
+      }
+      const long long row0 = static_cast<long long>(U.row0) + first;
+      if constexpr (EPI == FP8_SWIGLU) {
+        float h[64];
+        float mx = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          const float g = unpack2(v2[i >> 5][(i & 31) >> 1], i & 1);
+          const float up = unpack2(v2[2 + (i >> 5)][(i & 31) >> 1], i & 1);
+          h[i] = __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), up);
+          mx = fmaxf(mx, fabsf(h[i]));
+        }
+        float* am = s_amax + parity * 2 * kWTile;
+        am[half * kWTile + r_in_tile] = mx;
+        // two buffers by unit parity: a buffer is written again only after the next unit's barrier
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        const float sc = fp8_scale(fmaxf(am[r_in_tile], am[kWTile + r_in_tile]));
+        parity ^= 1;
+        if (ok && rows_valid > 0) {
+          const float inv = __frcp_rn(sc);
+          uint32_t packed[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) packed[i] = fp8_pack4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3], inv);
+          if (half == 0 && lane < rows_valid) p.out_scale[(row0 + lane) * (p.N / kFp8Block) + U.nb] = sc;
+          store_rows64<4>(stg, packed, static_cast<uint8_t*>(p.out) + row0 * p.N + U.nb * kWTile + half * 64, p.N,
+                          rows_valid, 64, true);
+        }
+      } else if (ok && rows_valid > 0) {
+        constexpr int ELT = EPI == FP8_F32 ? 4 : 2;
+        const long long ld = static_cast<long long>(p.N) * ELT;
+        const int n0 = (2 * U.nb + half) * kWTile;
+#pragma unroll
+        for (int st = 0; st < 4; ++st) {
+          const int n = n0 + st * 32;
+          if (n >= p.N) break;
+          uint8_t* o = static_cast<uint8_t*>(p.out) + row0 * ld + static_cast<long long>(n) * ELT;
+          const long long bytes = static_cast<long long>(p.N - n) * ELT;
+          uint32_t w[16];
+          if constexpr (EPI == FP8_F32) {
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(unpack2(v2[st][8 * part + (i >> 1)], i & 1));
+              store_rows64<4>(stg, w, o + 64 * part, ld, rows_valid, bytes - 64 * part, p.vec_out != 0);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(unpack2(v2[st][i], 0), unpack2(v2[st][i], 1));
+              w[i] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            store_rows64<2>(stg, w, o, ld, rows_valid, bytes, p.vec_out != 0);
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();     // no remote arrive or multicast commit can still target this CTA
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, S::ACC * S::ACC_COLS);
+  }
+}
+
+// The register split must not ask for more than the launch holds: a kernel that waits for registers never ends.
+int check_launch_regs(const void* kernel, const char* name, std::atomic<int>& regs) {
+  int r = regs.load(std::memory_order_relaxed);
+  if (r == 0) {
+    cudaFuncAttributes fa;
+    const int rc = check_cuda(cudaFuncGetAttributes(&fa, kernel), "cudaFuncGetAttributes");
+    if (rc) return rc;
+    r = fa.numRegs;
+    regs.store(r, std::memory_order_relaxed);
+  }
+  if (r != kLaunchRegs) return set_error(INVMOE_ERR_CUDA, "%s: compiled with %d registers, not %d", name, r, kLaunchRegs);
+  return INVMOE_OK;
+}
+
+int check_units(const Fp8Call& c, int chunk, int n_blocks, long long* units) {
+  const long long chunks = c.G > 0 ? static_cast<long long>(c.rows) / chunk + (c.rows < c.G ? c.rows : c.G)
+                                   : (static_cast<long long>(c.rows) + chunk - 1) / chunk;
+  *units = chunks * n_blocks;
+  if (*units > 0x7fffffffLL) return set_error(INVMOE_ERR_UNSUPPORTED_SHAPE, "%s: too many tiles for one launch", c.name);
+  return INVMOE_OK;
+}
+
+int make_maps(const Fp8Call& c, const Fp8Params& p, int token_box, CUtensorMap* w, CUtensorMap* a) {
+  const int rc = make_tmap_fp8(w, c.w, c.K, static_cast<long long>(p.w_group_rows) * (c.G > 0 ? c.G : 1), kWTile);
+  return rc ? rc : make_tmap_fp8(a, c.a, c.K, c.rows, token_box);
+}
+
+template <int EPI>
+int launch_pair(const Fp8Call& c, Fp8Params p, cudaStream_t st) {
+  using S = Fp8PairShape;
+  const void* kernel = reinterpret_cast<const void*>(fp8_pair_kernel<EPI>);
+  p.n_blocks = EPI == FP8_SWIGLU ? c.N / kWTile : (c.N + 2 * kWTile - 1) / (2 * kWTile);
+  p.vec_out = static_cast<long long>(c.N) * (EPI == FP8_F32 ? 4 : 2) % 16 == 0;
+  long long units = 0;
+  int rc = check_units(c, 2 * kWTile, p.n_blocks, &units);
+  CUtensorMap tmW, tmA;
+  if (rc == INVMOE_OK) rc = make_maps(c, p, kWTile, &tmW, &tmA);
+  static std::atomic<uint64_t> attr_set{0};
+  static std::atomic<int> regs{0};
+  if (rc == INVMOE_OK) rc = set_smem_attr(kernel, S::SMEM_BYTES, attr_set);
+  if (rc == INVMOE_OK) rc = check_launch_regs(kernel, c.name, regs);
+  int sms = 0;
+  if (rc == INVMOE_OK) rc = device_sm_count(&sms);
+  if (rc) return rc;
+  const long long max_pairs = sms / 2;
+  const unsigned grid = 2 * static_cast<unsigned>(units < max_pairs ? units : max_pairs);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  ProfScope prof(c.name, st);
+  return check_cuda(launch_kernel_ex(fp8_pair_kernel<EPI>, dim3(grid), dim3(kFp8Threads), S::SMEM_BYTES, st, attr, 1,
+                                     tmW, tmA, p),
+                    c.name);
+}
+
 template <int MT, int NT, int EPI>
 int launch_fp8(const Fp8Call& c, Fp8Params p, cudaStream_t st) {
   using S = Fp8Shape<MT, NT>;
+  const void* kernel = reinterpret_cast<const void*>(fp8_gemm_kernel<MT, NT, EPI>);
   p.n_blocks = EPI == FP8_SWIGLU ? c.N / kWTile : (c.N + MT * kWTile - 1) / (MT * kWTile);
-  const long long max_chunks =
-      c.G > 0 ? (static_cast<long long>(c.rows) / NT + (c.rows < c.G ? c.rows : c.G)) : (c.rows + NT - 1LL) / NT;
-  if (max_chunks * p.n_blocks > 0x7fffffffLL)
-    return set_error(INVMOE_ERR_UNSUPPORTED_SHAPE, "%s: too many tiles for one launch", c.name);
+  long long units = 0;
+  int rc = check_units(c, NT, p.n_blocks, &units);
   CUtensorMap tmW, tmA;
-  int rc = make_tmap_fp8(&tmW, c.w, c.K, static_cast<long long>(p.w_group_rows) * (c.G > 0 ? c.G : 1), kWTile);
-  if (rc) return rc;
-  if ((rc = make_tmap_fp8(&tmA, c.a, c.K, c.rows, NT))) return rc;
+  if (rc == INVMOE_OK) rc = make_maps(c, p, NT, &tmW, &tmA);
   static std::atomic<uint64_t> attr_set{0};
-  if ((rc = set_smem_attr(reinterpret_cast<const void*>(fp8_gemm_kernel<MT, NT, EPI>), S::SMEM_BYTES, attr_set)))
-    return rc;
+  if (rc == INVMOE_OK) rc = set_smem_attr(kernel, S::SMEM_BYTES, attr_set);
   if constexpr (MT * NT >= 256) {
-    // the register split above must not ask for more than the launch holds: a kernel that waits for registers never ends
     static std::atomic<int> regs{0};
-    int r = regs.load(std::memory_order_relaxed);
-    if (r == 0) {
-      cudaFuncAttributes fa;
-      if ((rc = check_cuda(cudaFuncGetAttributes(&fa, reinterpret_cast<const void*>(fp8_gemm_kernel<MT, NT, EPI>)),
-                           "cudaFuncGetAttributes")))
-        return rc;
-      r = fa.numRegs;
-      regs.store(r, std::memory_order_relaxed);
-    }
-    if (r != kLaunchRegs) return set_error(INVMOE_ERR_CUDA, "%s: compiled with %d registers, not %d", c.name, r, kLaunchRegs);
+    if (rc == INVMOE_OK) rc = check_launch_regs(kernel, c.name, regs);
   }
   int sms = 0;
-  if ((rc = device_sm_count(&sms))) return rc;
-  const long long units = max_chunks * p.n_blocks;
+  if (rc == INVMOE_OK) rc = device_sm_count(&sms);
+  if (rc) return rc;
   const unsigned grid = static_cast<unsigned>(units < sms ? units : sms);
   ProfScope prof(c.name, st);
   return check_cuda(launch_kernel(fp8_gemm_kernel<MT, NT, EPI>, dim3(grid), dim3(kFp8Threads), S::SMEM_BYTES, st, tmW,
@@ -575,7 +1063,7 @@ int launch_fp8_nt(const Fp8Call& c, const Fp8Params& p, long long per_group, cud
   if (per_group <= 16) return launch_fp8<MT, 16, EPI>(c, p, st);
   if (per_group <= 32) return launch_fp8<MT, 32, EPI>(c, p, st);
   if (per_group <= 64) return launch_fp8<MT, 64, EPI>(c, p, st);
-  return launch_fp8<MT, 128, EPI>(c, p, st);
+  return launch_pair<EPI>(c, p, st);
 }
 
 }  // namespace
@@ -596,6 +1084,7 @@ int fp8_gemm_run(const Fp8Call& c, cudaStream_t st) {
   p.offsets = c.offsets;
   p.out = c.out;
   p.out_scale = c.out_scale;
+  p.vec_scale = p.KB % 4 == 0 && ((reinterpret_cast<uintptr_t>(c.a_scale) | reinterpret_cast<uintptr_t>(c.w_scale)) & 15) == 0;
   p.vec_out = c.N % 4 == 0;
   p.status = c.status;
   p.timeout_ns = kTimeoutNs;
