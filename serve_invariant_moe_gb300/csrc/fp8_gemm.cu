@@ -644,14 +644,17 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
 // single-CTA tile above pays 48 KB and 64 KB for the same work, and shared memory is what bounds it.  A thread holds one
 // token row, so its scale is one number per block and half, read from global memory four blocks ahead: no shared memory
 // at all on the scaling path.  Tiles are 256 rows whatever a group has, which the copies of its weights hide.
-// SwiGLU: CTA 0 loads the 128 gate rows of the block, CTA 1 the matching up rows, and every thread has both halves of
-// 64 of its row's h.
+// TMEM is what bounds the kernel: a block's MMAs keep it busy for 512 cycles and reading its 128 x 256 products for about
+// 340 more.  (Two MMAs of N = 128 per step, one per warpgroup with TMEM buffers of its own, so that one half is read
+// while the other is computed, measured slower: 260 us against 217 for 8192 x 4096 x 6144.)
+// SwiGLU: CTA 0 loads the 128 gate rows of the block, CTA 1 the matching up rows.  A warpgroup has columns 64 half .. + 63
+// of either CTA's 128, so that a thread holds gate and up of the same h.
 struct Fp8PairShape {
   static constexpr int TILE_BYTES = kWTile * kFp8Block;       // 16 KB: 128 rows x 128 e4m3
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;          // this CTA's token rows, then its weight rows
   static constexpr int STAGES = 6;
   static constexpr int ACC_COLS = 256;
-  static constexpr int ACC = 2;
+  static constexpr int ACC = 2;                               // TMEM buffers
   static constexpr int OSTAGE_BYTES = kEpiWarps * 32 * 64;
   static constexpr int AMAX_BYTES = 2 * 2 * kWTile * 4;       // [unit parity][warpgroup][row]
   static constexpr int BAR_BYTES = 256;
@@ -739,7 +742,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     }
     for (int a = 0; a < S::ACC; ++a) {
       mbar_init(&accf_bar[a], 1);
-      mbar_init(&acce_bar[a], 2 * kEpiWarps);
+      mbar_init(&acce_bar[a], 2 * kEpiWarps);           // the warps of both CTAs
     }
     mbar_init(final_bar, 1);
     *s_abort = 0;
@@ -820,8 +823,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
 #pragma unroll
           for (int kk = 0; kk < kFp8Block / 32; ++kk)
             umma_fp8_pair(d, adesc0 + so + 2u * kk, wdesc0 + so + 2u * kk, idesc, kk != 0 ? 1u : 0u);
-          umma_commit_pair(&empty_bar[stage], 0x3);
           umma_commit_pair(&accf_bar[acc], 0x3);
+          umma_commit_pair(&empty_bar[stage], 0x3);
           if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
           if (++acc == S::ACC) { acc = 0; acc_phase ^= 1u; }
         }
@@ -842,7 +845,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     take_registers();
     const int q = warp & 3;                            // TMEM lane quadrant
     const int ew = warp - kFirstEpiWarp;
-    const int half = ew >> 2;                          // warpgroup: half of the weight columns
+    const int half = ew >> 2;                          // warpgroup: weight rows 64 half .. + 63 of either CTA's 128
     const int r_in_tile = q * 32 + lane;
     const uint32_t acce_leader0 = mapa_shared(smem_u32(&acce_bar[0]), 0);
     uint8_t* stg = ostage + ew * 32 * 64;
@@ -855,52 +858,50 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       const int first = static_cast<int>(rank) * kWTile + q * 32;            // the warp's first row of the unit
       const int rows_valid = U.cols - first;                                 // may be <= 0: nothing to scale or store
       const float* ap = p.a_scale + static_cast<long long>(U.row0 + min(first + lane, U.cols - 1)) * p.KB;
-      // weight scales: one block of 128 columns per warpgroup, or (SwiGLU) a gate and an up block
+      // weight scales: the blocks of CTA 0's and of CTA 1's 128 weight rows (SwiGLU: gate and up)
       const float* wbase = p.w_scale + static_cast<long long>(U.g) * p.w_srows * p.KB;
-      const float* wp0 = wbase + static_cast<long long>(EPI == FP8_SWIGLU ? U.nb : min(2 * U.nb + half, p.w_srows - 1)) * p.KB;
-      const float* wp1 = EPI == FP8_SWIGLU ? wp0 + static_cast<long long>(p.N / kFp8Block) * p.KB : wp0;
-      unsigned long long v2[4][16];
+      const int sr0 = EPI == FP8_SWIGLU ? U.nb : 2 * U.nb;
+      const int sr1 = EPI == FP8_SWIGLU ? U.nb + p.N / kFp8Block : min(2 * U.nb + 1, p.w_srows - 1);
+      const float* wp0 = wbase + static_cast<long long>(sr0) * p.KB;
+      const float* wp1 = wbase + static_cast<long long>(sr1) * p.KB;
+      float v[4][32];                                  // columns 0..63 of CTA 0's rows, then 64..127 of CTA 1's
 #pragma unroll
       for (int st = 0; st < 4; ++st)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v2[st][i] = 0ull;
-      float4 an = load_scales(ap, 0, p), wn0 = load_scales(wp0, 0, p), wn1 = wn0;
-      if (EPI == FP8_SWIGLU) wn1 = load_scales(wp1, 0, p);
+        for (int i = 0; i < 32; ++i) v[st][i] = 0.0f;
+      float4 an = load_scales(ap, 0, p), wn0 = load_scales(wp0, 0, p), wn1 = load_scales(wp1, 0, p);
       for (int kb0 = 0; kb0 < p.KB; kb0 += 4) {
-        const float4 ac = an, wc0 = wn0, wc1 = wn1;
+        float4 ac = an, wc0 = wn0, wc1 = wn1;
         if (kb0 + 4 < p.KB) {
           an = load_scales(ap, kb0 + 4, p);
           wn0 = load_scales(wp0, kb0 + 4, p);
-          if (EPI == FP8_SWIGLU) wn1 = load_scales(wp1, kb0 + 4, p);
+          wn1 = load_scales(wp1, kb0 + 4, p);
         }
+        const int n_kb = min(4, p.KB - kb0);
+        // not unrolled (that measured slower): the scales of the next block move up instead
 #pragma unroll 1
-        for (int d = 0; d < 4; ++d) {
-          if (kb0 + d >= p.KB) break;
-          const float as = d == 0 ? ac.x : d == 1 ? ac.y : d == 2 ? ac.z : ac.w;
-          const float s0 = __fmul_rn(as, d == 0 ? wc0.x : d == 1 ? wc0.y : d == 2 ? wc0.z : wc0.w);
-          const float s1 = EPI == FP8_SWIGLU ? __fmul_rn(as, d == 0 ? wc1.x : d == 1 ? wc1.y : d == 2 ? wc1.z : wc1.w) : s0;
+        for (int d = 0; d < n_kb; ++d) {
+          const float s0 = __fmul_rn(ac.x, wc0.x), s1 = __fmul_rn(ac.x, wc1.x);
+          ac.x = ac.y; ac.y = ac.z; ac.z = ac.w;
+          wc0.x = wc0.y; wc0.y = wc0.z; wc0.z = wc0.w;
+          wc1.x = wc1.y; wc1.y = wc1.z; wc1.z = wc1.w;
           if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(&accf_bar[acc], acc_phase, wc));
           if (ok) {
             tc_fence_after();
             if (rows_valid > 0) {
               const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                                  static_cast<uint32_t>(acc * S::ACC_COLS);
+                                  static_cast<uint32_t>(acc * S::ACC_COLS + half * 64);
               uint32_t r[2][32];
-              // 32 columns per step: SwiGLU two steps of gate columns, then the up columns of the same h
-              auto at = [&](int st) {
-                return tb + static_cast<uint32_t>(EPI == FP8_SWIGLU ? (st >> 1) * kWTile + half * 64 + (st & 1) * 32
-                                                                    : half * kWTile + st * 32);
-              };
-              tmem_ld32(at(0), r[0]);
+              tmem_ld32(tb, r[0]);
 #pragma unroll
               for (int st = 0; st < 4; ++st) {
                 tmem_ld_wait();
                 tmem_reg_fence(r[st & 1]);
-                if (st < 3) tmem_ld32(at(st + 1), r[(st + 1) & 1]);
-                const uint32_t sb = __float_as_uint(st < 2 ? s0 : s1);
-                const unsigned long long s2 = pack2(sb, sb);
+                if (st < 3) tmem_ld32(tb + 32 * ((st + 1) & 1) + kWTile * ((st + 1) >> 1), r[(st + 1) & 1]);
+                const float sc = st < 2 ? s0 : s1;
+                // one FFMA per product: pairs in fma.rn.f32x2 measured slower here (485 -> 690 cycles a block)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) fma2(v2[st][i], pack2(r[st & 1][2 * i], r[st & 1][2 * i + 1]), s2);
+                for (int i = 0; i < 32; ++i) v[st][i] = fmaf(__uint_as_float(r[st & 1][i]), sc, v[st][i]);
               }
             }
             tc_fence_before();
@@ -916,8 +917,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
         float mx = 0.0f;
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
-          const float g = unpack2(v2[i >> 5][(i & 31) >> 1], i & 1);
-          const float up = unpack2(v2[2 + (i >> 5)][(i & 31) >> 1], i & 1);
+          const float g = v[i >> 5][i & 31], up = v[2 + (i >> 5)][i & 31];
           h[i] = __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), up);
           mx = fmaxf(mx, fabsf(h[i]));
         }
@@ -939,11 +939,10 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       } else if (ok && rows_valid > 0) {
         constexpr int ELT = EPI == FP8_F32 ? 4 : 2;
         const long long ld = static_cast<long long>(p.N) * ELT;
-        const int n0 = (2 * U.nb + half) * kWTile;
 #pragma unroll
         for (int st = 0; st < 4; ++st) {
-          const int n = n0 + st * 32;
-          if (n >= p.N) break;
+          const int n = (2 * U.nb + (st >> 1)) * kWTile + half * 64 + (st & 1) * 32;
+          if (n >= p.N) continue;
           uint8_t* o = static_cast<uint8_t*>(p.out) + row0 * ld + static_cast<long long>(n) * ELT;
           const long long bytes = static_cast<long long>(p.N - n) * ELT;
           uint32_t w[16];
@@ -951,13 +950,13 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(unpack2(v2[st][8 * part + (i >> 1)], i & 1));
+              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[st][16 * part + i]);
               store_rows64<4>(stg, w, o + 64 * part, ld, rows_valid, bytes - 64 * part, p.vec_out != 0);
             }
           } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(unpack2(v2[st][i], 0), unpack2(v2[st][i], 1));
+              const __nv_bfloat162 b = __floats2bfloat162_rn(v[st][2 * i], v[st][2 * i + 1]);
               w[i] = *reinterpret_cast<const uint32_t*>(&b);
             }
             store_rows64<2>(stg, w, o, ld, rows_valid, bytes, p.vec_out != 0);
