@@ -63,8 +63,8 @@ constexpr int kScaleWarps = 2;
 constexpr int kFirstEpiWarp = 2 + kScaleWarps;      // warp 0: producer, warp 1: MMA issuer, warps 2 and 3: scales
 constexpr int kFp8Threads = 32 * (kFirstEpiWarp + kEpiWarps);
 // Registers per thread: 168 at launch (65,536 / 384, whole units of 8).  A tile of 256 x 128 leaves 128 accumulators in
-// each of the 256 epilogue threads, so there the first warpgroup hands registers over: 56 + 2 * 224 = 3 * 168.
-constexpr int kLaunchRegs = 168, kLoaderRegs = 56, kEpiRegs = 224;
+// each of the 256 epilogue threads, so there the first warpgroup hands registers over: 72 + 2 * 216 = 3 * 168.
+constexpr int kLaunchRegs = 168, kLoaderRegs = 72, kEpiRegs = 216;
 static_assert(kLoaderRegs + 2 * kEpiRegs <= 3 * kLaunchRegs, "register split");
 constexpr int kStageF32 = kWTile + 4;               // floats per staged token row (conflict-free fragment writes)
 constexpr int kStageFp8 = kWTile + 16;              // bytes per staged token row
@@ -301,9 +301,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       // ---------------------------------------------------------- producer
       int stage = 0;
       uint32_t phase = 0;
-      int filled_phase[S::STAGES];
-#pragma unroll
-      for (int s = 0; s < S::STAGES; ++s) filled_phase[s] = -1;
+      int fills = 0;
       bool ok = true;
       for (int u = blockIdx.x; ok && u < total_units; u += gridDim.x) {
         const Fp8Unit U = fp8_unit<NT>(u, p, s_prefix, total_chunks);
@@ -319,15 +317,14 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
 #pragma unroll
           for (int m = 0; m < MT; ++m) tma_load_2d(st + m * kWBytes, &tmW, &full_bar[stage], kb * kFp8Block, wrow[m]);
           tma_load_2d(st + MT * kWBytes, &tmA, &full_bar[stage], kb * kFp8Block, U.row0);
-          filled_phase[stage] = static_cast<int>(phase);
+          ++fills;
           if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
         }
       }
       // every copy this thread issued lands before the CTA can exit
       WaitCtl drain{nullptr, p.status, p.timeout_ns};
-#pragma unroll
-      for (int s = 0; s < S::STAGES; ++s)
-        if (filled_phase[s] >= 0) mbar_wait(&full_bar[s], static_cast<uint32_t>(filled_phase[s]), drain);
+      for (int s = 0; s < S::STAGES && s < fills; ++s)   // the last of this stage's fills
+        mbar_wait(&full_bar[s], static_cast<uint32_t>((fills - 1 - s) / S::STAGES) & 1u, drain);
     } else if (warp == 1 && lane == 0) {
       // ---------------------------------------------------------- MMA issuer
       const uint64_t wdesc0 = sdesc_k_sw128(smem_u32(ring));
@@ -773,9 +770,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       // ---------------------------------------------------------- producer (both CTAs)
       int stage = 0;
       uint32_t phase = 0;
-      int filled_phase[S::STAGES];
-#pragma unroll
-      for (int s = 0; s < S::STAGES; ++s) filled_phase[s] = -1;
+      int fills = 0;
       bool ok = true;
       for (int u = pair; ok && u < total_units; u += pairs) {
         const Fp8Unit U = fp8_unit<CH>(u, p, s_prefix, total_chunks);
@@ -789,7 +784,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
           if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], 2 * S::STAGE_BYTES);   // both CTAs' copies
           tma_load_2d_pair(st, &tmA, fb, kb * kFp8Block, a_row);
           tma_load_2d_pair(st + S::TILE_BYTES, &tmW, fb, kb * kFp8Block, w_row);
-          filled_phase[stage] = static_cast<int>(phase);
+          ++fills;
           if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
         }
       }
@@ -797,9 +792,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       // the leader's full barrier counts both CTAs' copies: all of them land before either CTA exits
       if (rank == 0) {
         WaitCtl drain{nullptr, p.status, p.timeout_ns};
-#pragma unroll
-        for (int s = 0; s < S::STAGES; ++s)
-          if (filled_phase[s] >= 0) mbar_wait(&full_bar[s], static_cast<uint32_t>(filled_phase[s]), drain);
+        for (int s = 0; s < S::STAGES && s < fills; ++s)   // the last of this stage's fills
+          mbar_wait(&full_bar[s], static_cast<uint32_t>((fills - 1 - s) / S::STAGES) & 1u, drain);
       }
     } else if (warp == 1 && lane == 0 && rank == 0) {
       // ---------------------------------------------------------- MMA issuer (leader)
