@@ -161,11 +161,30 @@ __device__ __forceinline__ float unpack2(unsigned long long v, int hi) {
   return __uint_as_float(static_cast<uint32_t>(hi ? v >> 32 : v));
 }
 
+// silu(g) * u.  The hardware's exponential and reciprocal: their few units in the last place vanish against the rounding
+// to e4m3 that follows (2^-4), and the exact expf and division took a fifth of the gate/up kernel's time.  Both kernels
+// use this expression, so h does not depend on which one runs.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float swiglu(float g, float u) {
+  return __fmul_rn(__fmul_rn(g, rcp_approx(__fadd_rn(1.0f, __expf(-g)))), u);
+}
+
 // All four warps of a warpgroup execute the one instruction of its side of the split.
 __device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoaderRegs)); }
 __device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs)); }
 
 __device__ __forceinline__ void bar_wg(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+
+// mbar_wait by a whole warp, one answer for all lanes.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const WaitCtl& w) {
+  if (__all_sync(0xffffffffu, mbar_test<CLUSTER>(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait_slow<CLUSTER>(bar, parity, w));
+}
 
 // Scales of blocks kb .. kb + 3 of one row (zeros past the last).
 __device__ __forceinline__ float4 load_scales(const float* src, int kb, const Fp8Params& p) {
@@ -528,7 +547,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 float& g = v[0][h][4 * i + j + 2 * e];
-                g = __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), v[1][h][4 * i + j + 2 * e]);
+                g = swiglu(g, v[1][h][4 * i + j + 2 * e]);
                 mx = fmaxf(mx, fabsf(g));
               }
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
@@ -633,23 +652,24 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
   }
 }
 
-// ------------------------------------------------------------ CTA pairs: token rows on the M side
+// ------------------------------------------------------------ many rows: tokens on the M side
 //
-// The same product with the roles exchanged, for many rows: a pair of CTAs computes 256 token rows x 256 weight columns,
-// each CTA loading its own 128 rows of both operands (the MMA reads the other CTA's half of the weights from the
-// partner), so a K block costs each SM 32 KB of copies and 32 KB of operand reads for 2 x 128 x 256 x 128 products; the
-// single-CTA tile above pays 48 KB and 64 KB for the same work, and shared memory is what bounds it.  A thread holds one
-// token row, so its scale is one number per block and half, read from global memory four blocks ahead: no shared memory
-// at all on the scaling path.  Tiles are 256 rows whatever a group has, which the copies of its weights hide.
-// TMEM is what bounds the kernel: a block's MMAs keep it busy for 512 cycles and reading its 128 x 256 products for about
-// 340 more.  (Two MMAs of N = 128 per step, one per warpgroup with TMEM buffers of its own, so that one half is read
-// while the other is computed, measured slower: 260 us against 217 for 8192 x 4096 x 6144.)
-// SwiGLU: CTA 0 loads the 128 gate rows of the block, CTA 1 the matching up rows.  A warpgroup has columns 64 half .. + 63
-// of either CTA's 128, so that a thread holds gate and up of the same h.
-struct Fp8PairShape {
+// The same product with the roles exchanged: a CTA computes 128 token rows x 256 weight rows (one N = 256 MMA per K = 32
+// step).  A thread holds one token row, so its scale is one number per block, read from global memory four blocks ahead:
+// no shared memory on the scaling path, where the kernel above reads a scale for every column.
+// What bounds it is neither the loads nor the tensor cores (without the scaling 8192 x 4096 x 6144 takes 129 us) but the
+// handover of the products: 128 x 256 fp32 per block through TMEM and 256 FFMA issue cycles per scheduler, with two TMEM
+// buffers to hide a commit, a wait and a release behind.  So a buffer is released as soon as its last columns are in
+// registers, and the issuing warp runs converged (see umma_fp8_if).
+// Measured and not kept (8192 x 4096 x 6144, 191 us): CTA pairs with 256 x 256 tiles, 183 us, but 663 instead of 549 us
+// for 64 experts of about 256 rows, because the tiles are twice as high; four buffers of 128 columns, 260 us (an N = 128
+// MMA takes more than half the time of an N = 256 one); packed fma.rn.f32x2, 690 instead of 485 cycles a block.
+// SwiGLU: the 256 weight rows are 128 gate rows and the matching up rows.  A warpgroup has columns 64 half .. + 63 of
+// either 128, so that a thread holds gate and up of the same h.
+struct Fp8RowsShape {
   static constexpr int TILE_BYTES = kWTile * kFp8Block;       // 16 KB: 128 rows x 128 e4m3
-  static constexpr int STAGE_BYTES = 2 * TILE_BYTES;          // this CTA's token rows, then its weight rows
-  static constexpr int STAGES = 6;
+  static constexpr int STAGE_BYTES = 3 * TILE_BYTES;          // token rows, then two tiles of weight rows
+  static constexpr int STAGES = 4;
   static constexpr int ACC_COLS = 256;
   static constexpr int ACC = 2;                               // TMEM buffers
   static constexpr int OSTAGE_BYTES = kEpiWarps * 32 * 64;
@@ -661,57 +681,78 @@ struct Fp8PairShape {
   static_assert(8 * (2 * STAGES + 2 * ACC + 1) + 16 <= BAR_BYTES, "barriers");
 };
 
-__device__ __forceinline__ void umma_fp8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                              uint32_t accumulate) {
+// The MMA is predicated, not branched around: in converged code the descriptors stay in uniform registers, where the
+// instruction wants them; issued from a branch of one lane each MMA cost some 140 cycles of moves.
+__device__ __forceinline__ void umma_fp8_if(uint32_t on, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                 uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(on)
       : "memory");
 }
 
-// A warp's 32 rows x 64 bytes from registers (one row per lane) to global memory, 4 lanes per row: the 16-byte piece c of
-// row r sits at r * 64 + (c ^ ((r >> 1) & 3)) * 16, free of bank conflicts both ways.  Rows of a length or base that is
-// not a multiple of 16 bytes are written element by element.
-template <int ELT>
-__device__ __forceinline__ void store_rows64(uint8_t* stage, const uint32_t (&v)[16], uint8_t* out, long long ld_bytes,
-                                             int rows_valid, long long bytes_valid, bool vec) {
+// umma_commit of the lane whose `on` is set.
+__device__ __forceinline__ void umma_commit_if(uint32_t on, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(on)
+      : "memory");
+}
+
+// A warp's 32 rows x 16 * PIECES bytes from registers (one row per lane) to global memory, whole rows of 64 or 128 bytes
+// at a time (PIECES lanes per row), through 2 KB of shared memory: 32 rows of 64 bytes, or twice 16 rows of 128.  The
+// 16-byte piece c of row r sits at piece c ^ (r / 2 or r) of its row, free of bank conflicts both ways.  Rows whose
+// length is not a multiple of 16 bytes are written element by element.
+template <int ELT, int PIECES>
+__device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t (&v)[4 * PIECES], uint8_t* out,
+                                           long long ld_bytes, int rows_valid, long long bytes_valid, bool vec) {
+  static_assert(PIECES == 4 || PIECES == 8, "64 or 128 bytes");
+  constexpr int ROWS = 128 / PIECES;                   // rows staged at a time
   const int lane = threadIdx.x & 31;
+  auto at = [&](int r, int c) { return stage + r * (16 * PIECES) + ((c ^ (PIECES == 8 ? r & 7 : (r >> 1) & 3)) << 4); };
+  const int c = lane % PIECES;
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
-    *reinterpret_cast<uint4*>(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
-        make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-  __syncwarp();
-  const int c = lane & 3;
+  for (int r0 = 0; r0 < 32; r0 += ROWS) {
+    if (lane >= r0 && lane < r0 + ROWS) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 8 * i + (lane >> 2);
-    const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
-    if (r < rows_valid && c * 16 < bytes_valid) {
-      uint8_t* d = out + r * ld_bytes + c * 16;
-      if (vec) {
-        *reinterpret_cast<uint4*>(d) = w;
-      } else {
-        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+      for (int k = 0; k < PIECES; ++k)
+        *reinterpret_cast<uint4*>(at(lane - r0, k)) = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+    }
+    __syncwarp();
 #pragma unroll
-        for (int e = 0; e < 16 / ELT; ++e) {
-          if (c * 16 + e * ELT < bytes_valid) {
-            if (ELT == 4) *reinterpret_cast<uint32_t*>(d + 4 * e) = x[e];
-            else *reinterpret_cast<uint16_t*>(d + 2 * e) = static_cast<uint16_t>(x[e >> 1] >> (16 * (e & 1)));
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * (32 / PIECES) + lane / PIECES;
+      const uint4 w = *reinterpret_cast<const uint4*>(at(r, c));
+      if (r0 + r < rows_valid && c * 16 < bytes_valid) {
+        uint8_t* d = out + (r0 + r) * ld_bytes + c * 16;
+        if (vec) {
+          *reinterpret_cast<uint4*>(d) = w;
+        } else {
+          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 16 / ELT; ++e) {
+            if (c * 16 + e * ELT < bytes_valid) {
+              if (ELT == 4) *reinterpret_cast<uint32_t*>(d + 4 * e) = x[e];
+              else *reinterpret_cast<uint16_t*>(d + 2 * e) = static_cast<uint16_t>(x[e >> 1] >> (16 * (e & 1)));
+            }
           }
         }
       }
     }
+    __syncwarp();
   }
-  __syncwarp();
 }
 
 template <int EPI>
 __global__ void __launch_bounds__(kFp8Threads, 1)
-    fp8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
+    fp8_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
                     const Fp8Params p) {
-  using S = Fp8PairShape;
+  using S = Fp8RowsShape;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ostage = ring + S::STAGES * S::STAGE_BYTES;
@@ -729,8 +770,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();          // 0 = leader (issues the MMAs), 1 = follower
-  constexpr int CH = 2 * kWTile;                    // token rows of a pair unit
+  constexpr int CH = kWTile;                        // token rows of a unit
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::STAGES; ++s) {
@@ -739,7 +779,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     }
     for (int a = 0; a < S::ACC; ++a) {
       mbar_init(&accf_bar[a], 1);
-      mbar_init(&acce_bar[a], 2 * kEpiWarps);           // the warps of both CTAs
+      mbar_init(&acce_bar[a], kEpiWarps);
     }
     mbar_init(final_bar, 1);
     *s_abort = 0;
@@ -747,67 +787,61 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     tma_prefetch_desc(&tmW);
     tma_prefetch_desc(&tmA);
   }
-  if (warp == 1) tmem_alloc_pair(tmem_slot, S::ACC * S::ACC_COLS);
+  if (warp == 1) tmem_alloc(tmem_slot, S::ACC * S::ACC_COLS);
   // everything above touches only shared memory, TMEM and the kernel parameters
   pdl_wait();
   pdl_trigger();
   if (warp == 2) prefix_chunks<CH>(p, s_prefix, s_total, lane);
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();     // both CTAs' barriers initialised and TMEM allocated
   tc_fence_after();
 
   const uint32_t tmem_base = *tmem_slot;
   const int total_chunks = *s_total;
   const int total_units = total_chunks * p.n_blocks;
-  const int pair = static_cast<int>(blockIdx.x) / 2, pairs = static_cast<int>(gridDim.x) / 2;
   WaitCtl wc{s_abort, p.status, p.timeout_ns};
-  const uint32_t peer_abort = mapa_shared(smem_u32(const_cast<int*>(s_abort)), rank ^ 1u);
 
   if (warp < kFirstEpiWarp) {
     give_registers();
     if (warp == 0 && lane == 0) {
-      // ---------------------------------------------------------- producer (both CTAs)
+      // ---------------------------------------------------------- producer
       int stage = 0;
       uint32_t phase = 0;
       int fills = 0;
       bool ok = true;
-      for (int u = pair; ok && u < total_units; u += pairs) {
+      for (int u = blockIdx.x; ok && u < total_units; u += gridDim.x) {
         const Fp8Unit U = fp8_unit<CH>(u, p, s_prefix, total_chunks);
-        const int a_row = U.row0 + static_cast<int>(rank) * kWTile;
-        const int w_row = U.g * p.w_group_rows + (EPI == FP8_SWIGLU ? U.nb * kWTile + static_cast<int>(rank) * p.N
-                                                                    : (2 * U.nb + static_cast<int>(rank)) * kWTile);
+        const int w_row = U.g * p.w_group_rows + (EPI == FP8_SWIGLU ? 1 : 2) * U.nb * kWTile;
+        const int w_row1 = EPI == FP8_SWIGLU ? w_row + p.N : w_row + kWTile;
         for (int kb = 0; kb < p.KB; ++kb) {
           if (!mbar_wait(&empty_bar[stage], phase ^ 1u, wc)) { ok = false; break; }
           uint8_t* st = ring + stage * S::STAGE_BYTES;
-          const uint32_t fb = mapa_shared(smem_u32(&full_bar[stage]), 0);
-          if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], 2 * S::STAGE_BYTES);   // both CTAs' copies
-          tma_load_2d_pair(st, &tmA, fb, kb * kFp8Block, a_row);
-          tma_load_2d_pair(st + S::TILE_BYTES, &tmW, fb, kb * kFp8Block, w_row);
+          mbar_arrive_expect_tx(&full_bar[stage], S::STAGE_BYTES);
+          tma_load_2d(st, &tmA, &full_bar[stage], kb * kFp8Block, U.row0);
+          tma_load_2d(st + S::TILE_BYTES, &tmW, &full_bar[stage], kb * kFp8Block, w_row);
+          tma_load_2d(st + 2 * S::TILE_BYTES, &tmW, &full_bar[stage], kb * kFp8Block, w_row1);
           ++fills;
           if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
         }
       }
-      if (!ok) st_shared_remote_u32(peer_abort, 1u);
-      // the leader's full barrier counts both CTAs' copies: all of them land before either CTA exits
-      if (rank == 0) {
-        WaitCtl drain{nullptr, p.status, p.timeout_ns};
-        for (int s = 0; s < S::STAGES && s < fills; ++s)   // the last of this stage's fills
-          mbar_wait(&full_bar[s], static_cast<uint32_t>((fills - 1 - s) / S::STAGES) & 1u, drain);
-      }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
-      // ---------------------------------------------------------- MMA issuer (leader)
+      // every copy this thread issued lands before the CTA can exit
+      WaitCtl drain{nullptr, p.status, p.timeout_ns};
+      for (int s = 0; s < S::STAGES && s < fills; ++s)   // the last of this stage's fills
+        mbar_wait(&full_bar[s], static_cast<uint32_t>((fills - 1 - s) / S::STAGES) & 1u, drain);
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer: the whole warp, one lane issues
+      const uint32_t on = lane == 0 ? 1u : 0u;
       const uint64_t adesc0 = sdesc_k_sw128(smem_u32(ring));
       const uint64_t wdesc0 = sdesc_k_sw128(smem_u32(ring + S::TILE_BYTES));
-      const uint32_t idesc = idesc_e4m3_f32(2 * kWTile, S::ACC_COLS);
+      const uint32_t idesc = idesc_e4m3_f32(kWTile, S::ACC_COLS);
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true;
-      for (int u = pair; ok && u < total_units; u += pairs) {
+      for (int u = blockIdx.x; ok && u < total_units; u += gridDim.x) {
         for (int kb = 0; kb < p.KB; ++kb) {
-          if (!mbar_wait<true>(&acce_bar[acc], acc_phase ^ 1u, wc) || !mbar_wait(&full_bar[stage], phase, wc)) {
+          if (!wait_warp(&acce_bar[acc], acc_phase ^ 1u, wc) || !wait_warp(&full_bar[stage], phase, wc)) {
             ok = false;
             break;
           }
@@ -816,24 +850,21 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
           const uint32_t d = tmem_base + static_cast<uint32_t>(acc * S::ACC_COLS);
 #pragma unroll
           for (int kk = 0; kk < kFp8Block / 32; ++kk)
-            umma_fp8_pair(d, adesc0 + so + 2u * kk, wdesc0 + so + 2u * kk, idesc, kk != 0 ? 1u : 0u);
-          umma_commit_pair(&accf_bar[acc], 0x3);
-          umma_commit_pair(&empty_bar[stage], 0x3);
+            umma_fp8_if(on, d, adesc0 + so + 2u * kk, wdesc0 + so + 2u * kk, idesc, kk != 0 ? 1u : 0u);
+          umma_commit_if(on, &accf_bar[acc]);
+          umma_commit_if(on, &empty_bar[stage]);
           if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
           if (++acc == S::ACC) { acc = 0; acc_phase ^= 1u; }
         }
       }
-      if (!ok) {
-        *s_abort = 1;
-        st_shared_remote_u32(peer_abort, 1u);
-      }
-      // every MMA issued here has finished before the pair releases TMEM
-      umma_commit_pair(final_bar, 0x1);
+      if (!ok) *s_abort = 1;
+      // every MMA issued here has finished before the CTA releases TMEM
+      if (lane == 0) umma_commit(final_bar);
       WaitCtl drain{nullptr, p.status, p.timeout_ns};
       mbar_wait(final_bar, 0, drain);
     }
   } else {
-    // ------------------------------------------------------------ scaling and epilogue (both CTAs)
+    // ------------------------------------------------------------ scaling and epilogue
     // All eight warps walk the same units whatever happens, so the SwiGLU barrier always meets; after a wait that ran
     // out (ok = false) a warp only keeps that barrier.
     take_registers();
@@ -841,24 +872,24 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     const int ew = warp - kFirstEpiWarp;
     const int half = ew >> 2;                          // warpgroup: weight rows 64 half .. + 63 of either CTA's 128
     const int r_in_tile = q * 32 + lane;
-    const uint32_t acce_leader0 = mapa_shared(smem_u32(&acce_bar[0]), 0);
+    
     uint8_t* stg = ostage + ew * 32 * 64;
     int acc = 0;
     uint32_t acc_phase = 0;
     int parity = 0;
     bool ok = true;
-    for (int u = pair; u < total_units; u += pairs) {
+    for (int u = blockIdx.x; u < total_units; u += gridDim.x) {
       const Fp8Unit U = fp8_unit<CH>(u, p, s_prefix, total_chunks);
-      const int first = static_cast<int>(rank) * kWTile + q * 32;            // the warp's first row of the unit
-      const int rows_valid = U.cols - first;                                 // may be <= 0: nothing to scale or store
+      const int first = q * 32;                        // the warp's first row of the unit
+      const int rows_valid = U.cols - first;           // may be <= 0: nothing to scale or store
       const float* ap = p.a_scale + static_cast<long long>(U.row0 + min(first + lane, U.cols - 1)) * p.KB;
-      // weight scales: the blocks of CTA 0's and of CTA 1's 128 weight rows (SwiGLU: gate and up)
+      // weight scales of the two blocks of 128 weight rows (SwiGLU: gate and up)
       const float* wbase = p.w_scale + static_cast<long long>(U.g) * p.w_srows * p.KB;
       const int sr0 = EPI == FP8_SWIGLU ? U.nb : 2 * U.nb;
       const int sr1 = EPI == FP8_SWIGLU ? U.nb + p.N / kFp8Block : min(2 * U.nb + 1, p.w_srows - 1);
       const float* wp0 = wbase + static_cast<long long>(sr0) * p.KB;
       const float* wp1 = wbase + static_cast<long long>(sr1) * p.KB;
-      float v[4][32];                                  // columns 0..63 of CTA 0's rows, then 64..127 of CTA 1's
+      float v[4][32];                                  // 64 columns of the first 128 weight rows, then 64 of the second
 #pragma unroll
       for (int st = 0; st < 4; ++st)
 #pragma unroll
@@ -891,16 +922,22 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
               for (int st = 0; st < 4; ++st) {
                 tmem_ld_wait();
                 tmem_reg_fence(r[st & 1]);
-                if (st < 3) tmem_ld32(tb + 32 * ((st + 1) & 1) + kWTile * ((st + 1) >> 1), r[(st + 1) & 1]);
+                if (st < 3) {
+                  tmem_ld32(tb + 32 * ((st + 1) & 1) + kWTile * ((st + 1) >> 1), r[(st + 1) & 1]);
+                } else {
+                  // everything is in registers: the buffer is free before the last products are added
+                  tc_fence_before();
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive(&acce_bar[acc]);
+                }
                 const float sc = st < 2 ? s0 : s1;
                 // one FFMA per product: pairs in fma.rn.f32x2 measured slower here (485 -> 690 cycles a block)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[st][i] = fmaf(__uint_as_float(r[st & 1][i]), sc, v[st][i]);
               }
+            } else if (lane == 0) {
+              mbar_arrive(&acce_bar[acc]);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote_cta(acce_leader0 + static_cast<uint32_t>(acc * 8));
           }
           if (++acc == S::ACC) { acc = 0; acc_phase ^= 1u; }
         }
@@ -912,7 +949,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
           const float g = v[i >> 5][i & 31], up = v[2 + (i >> 5)][i & 31];
-          h[i] = __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), up);
+          h[i] = swiglu(g, up);
           mx = fmaxf(mx, fabsf(h[i]));
         }
         float* am = s_amax + parity * 2 * kWTile;
@@ -927,34 +964,31 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) packed[i] = fp8_pack4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3], inv);
           if (half == 0 && lane < rows_valid) p.out_scale[(row0 + lane) * (p.N / kFp8Block) + U.nb] = sc;
-          store_rows64<4>(stg, packed, static_cast<uint8_t*>(p.out) + row0 * p.N + U.nb * kWTile + half * 64, p.N,
-                          rows_valid, 64, true);
+          store_rows<4, 4>(stg, packed, static_cast<uint8_t*>(p.out) + row0 * p.N + U.nb * kWTile + half * 64, p.N,
+                           rows_valid, 64, true);
         }
       } else if (ok && rows_valid > 0) {
         constexpr int ELT = EPI == FP8_F32 ? 4 : 2;
         const long long ld = static_cast<long long>(p.N) * ELT;
+        // fp32: 32 columns, bf16: 64 columns to a row of 128 bytes
+        constexpr int COLS = 128 / ELT;
 #pragma unroll
-        for (int st = 0; st < 4; ++st) {
-          const int n = (2 * U.nb + (st >> 1)) * kWTile + half * 64 + (st & 1) * 32;
+        for (int part = 0; part < 128 / COLS; ++part) {
+          const int n = (2 * U.nb + part * COLS / 64) * kWTile + half * 64 + part * COLS % 64;
           if (n >= p.N) continue;
-          uint8_t* o = static_cast<uint8_t*>(p.out) + row0 * ld + static_cast<long long>(n) * ELT;
-          const long long bytes = static_cast<long long>(p.N - n) * ELT;
-          uint32_t w[16];
-          if constexpr (EPI == FP8_F32) {
+          uint32_t w[32];
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[st][16 * part + i]);
-              store_rows64<4>(stg, w, o + 64 * part, ld, rows_valid, bytes - 64 * part, p.vec_out != 0);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(v[st][2 * i], v[st][2 * i + 1]);
+          for (int i = 0; i < 32; ++i) {
+            if constexpr (EPI == FP8_F32) {
+              w[i] = __float_as_uint(v[part][i]);
+            } else {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * part + (i >> 4)][2 * (i & 15)],
+                                                             v[2 * part + (i >> 4)][2 * (i & 15) + 1]);
               w[i] = *reinterpret_cast<const uint32_t*>(&b);
             }
-            store_rows64<2>(stg, w, o, ld, rows_valid, bytes, p.vec_out != 0);
           }
+          store_rows<ELT, 8>(stg, w, static_cast<uint8_t*>(p.out) + row0 * ld + static_cast<long long>(n) * ELT, ld,
+                             rows_valid, static_cast<long long>(p.N - n) * ELT, p.vec_out != 0);
         }
       }
     }
@@ -962,10 +996,9 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
 
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();     // no remote arrive or multicast commit can still target this CTA
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem_base, S::ACC * S::ACC_COLS);
+    tmem_dealloc(tmem_base, S::ACC * S::ACC_COLS);
   }
 }
 
@@ -997,13 +1030,13 @@ int make_maps(const Fp8Call& c, const Fp8Params& p, int token_box, CUtensorMap* 
 }
 
 template <int EPI>
-int launch_pair(const Fp8Call& c, Fp8Params p, cudaStream_t st) {
-  using S = Fp8PairShape;
-  const void* kernel = reinterpret_cast<const void*>(fp8_pair_kernel<EPI>);
+int launch_rows(const Fp8Call& c, Fp8Params p, cudaStream_t st) {
+  using S = Fp8RowsShape;
+  const void* kernel = reinterpret_cast<const void*>(fp8_rows_kernel<EPI>);
   p.n_blocks = EPI == FP8_SWIGLU ? c.N / kWTile : (c.N + 2 * kWTile - 1) / (2 * kWTile);
   p.vec_out = static_cast<long long>(c.N) * (EPI == FP8_F32 ? 4 : 2) % 16 == 0;
   long long units = 0;
-  int rc = check_units(c, 2 * kWTile, p.n_blocks, &units);
+  int rc = check_units(c, kWTile, p.n_blocks, &units);
   CUtensorMap tmW, tmA;
   if (rc == INVMOE_OK) rc = make_maps(c, p, kWTile, &tmW, &tmA);
   static std::atomic<uint64_t> attr_set{0};
@@ -1013,15 +1046,9 @@ int launch_pair(const Fp8Call& c, Fp8Params p, cudaStream_t st) {
   int sms = 0;
   if (rc == INVMOE_OK) rc = device_sm_count(&sms);
   if (rc) return rc;
-  const long long max_pairs = sms / 2;
-  const unsigned grid = 2 * static_cast<unsigned>(units < max_pairs ? units : max_pairs);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+    const unsigned grid = static_cast<unsigned>(units < sms ? units : sms);
   ProfScope prof(c.name, st);
-  return check_cuda(launch_kernel_ex(fp8_pair_kernel<EPI>, dim3(grid), dim3(kFp8Threads), S::SMEM_BYTES, st, attr, 1,
+  return check_cuda(launch_kernel(fp8_rows_kernel<EPI>, dim3(grid), dim3(kFp8Threads), S::SMEM_BYTES, st,
                                      tmW, tmA, p),
                     c.name);
 }
@@ -1056,7 +1083,7 @@ int launch_fp8_nt(const Fp8Call& c, const Fp8Params& p, long long per_group, cud
   if (per_group <= 16) return launch_fp8<MT, 16, EPI>(c, p, st);
   if (per_group <= 32) return launch_fp8<MT, 32, EPI>(c, p, st);
   if (per_group <= 64) return launch_fp8<MT, 64, EPI>(c, p, st);
-  return launch_pair<EPI>(c, p, st);
+  return launch_rows<EPI>(c, p, st);
 }
 
 }  // namespace
