@@ -353,17 +353,20 @@ int launch_small(const GemmCall& c, cudaStream_t st) {
 
 }  // namespace
 
-// Row-major e4m3 [rows, inner] matrix; box = 128 elements (128 B, one swizzle row) x box_rows.  A last block of fewer
-// than 128 columns is filled with zeros.
-int make_tmap_fp8(CUtensorMap* m, const void* base, long long inner, long long rows, int box_rows) {
+// Row-major e4m3 [rows, inner] matrix; box = 128 elements (128 B, one swizzle row) x box_rows; a last block of fewer than
+// 128 columns is filled with zeros.  k_blocks > 0 (inner a multiple of 128): as a rank-3 tensor (128 elements, rows, inner /
+// 128 blocks) whose box holds that many consecutive blocks, one [box_rows][128] slice after another; blocks past the last
+// are zeros.
+int make_tmap_fp8(CUtensorMap* m, const void* base, long long inner, long long rows, int box_rows, int k_blocks) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return set_error(INVMOE_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(inner)};
-  cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const cuuint64_t ld = static_cast<cuuint64_t>(inner);
+  cuuint64_t dims[3] = {k_blocks > 0 ? 128 : ld, static_cast<cuuint64_t>(rows), ld / 128};
+  cuuint64_t strides[2] = {ld, 128};
+  cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(k_blocks)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, k_blocks > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return set_error(INVMOE_ERR_CUDA, "cuTensorMapEncodeTiled (e4m3) failed (%d)", (int)r);
   return INVMOE_OK;
