@@ -515,7 +515,11 @@ int launch_plain(const Fp8Call& c, const Fp8Params& p, int nt, bool small, cudaS
 }  // namespace
 
 // Which kernel and tile: by the rows of a group (all rows of a dense call; the average, half as much again for the spread
-// around it, of a grouped one).  More than 64 go to the row tiles.
+// around it, of a grouped one) and by what fills the machine.
+//   * at most 64 rows: columns, in 16, 32 or 64; 64-row tiles of the weights where 256-row tiles would not give every SM
+//     one (8 x 4096 x 6144: 14 us against 26);
+//   * more: the row tiles, unless 64-row tiles of the weights still fit in one wave (128 x 4096 x 6144: 18 us against 29
+//     on 16 row tiles; 192 x 4096 x 6144: two waves, 31 against 29).
 int fp8_gemm_run(const Fp8Call& c, cudaStream_t st) {
   if (c.rows == 0) return INVMOE_OK;
   Fp8Params p{};
@@ -541,20 +545,21 @@ int fp8_gemm_run(const Fp8Call& c, cudaStream_t st) {
     rows = (rows + c.G - 1) / c.G;
     rows += rows / 2;
   }
-  if (rows > 64) return fp8_rows_run(c, p, st);
   const int nt = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   if (swiglu) {
+    if (rows > 64) return fp8_rows_run(c, p, st);
     if (nt == 16) return launch_cols<2, 128, 16, 2, FP8_SWIGLU>(c, p, st);
     if (nt == 32) return launch_cols<2, 128, 32, 1, FP8_SWIGLU>(c, p, st);
     return launch_cols<2, 128, 64, 1, FP8_SWIGLU>(c, p, st);
   }
-  // 64-row tiles where 256-row tiles would not give every SM one
-  long long units = 0;
+  long long units256 = 0, units64 = 0;
   int sms = 0;
-  int rc = check_units(c, nt, (c.N + 2 * kWTile - 1) / (2 * kWTile), &units);
+  int rc = check_units(c, nt, (c.N + 2 * kWTile - 1) / (2 * kWTile), &units256);
+  if (rc == INVMOE_OK) rc = check_units(c, nt, (c.N + 63) / 64, &units64);
   if (rc == INVMOE_OK) rc = device_sm_count(&sms);
   if (rc) return rc;
-  const bool small = units < sms;
+  if (rows > 64 && units64 > sms) return fp8_rows_run(c, p, st);
+  const bool small = units256 < sms;
   return c.out_kind == FP8_OUT_F32 ? launch_plain<FP8_F32>(c, p, nt, small, st)
                                    : launch_plain<FP8_BF16>(c, p, nt, small, st);
 }

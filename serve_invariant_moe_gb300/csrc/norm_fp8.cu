@@ -223,30 +223,30 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const TD* __restrict__ d
   }
 }
 
-// dw[h] = sum over P partial rows: 32 columns per block, thread row y adds rows y, y + 32, ... ascending, then the 32
-// sums ascending.
-__global__ void __launch_bounds__(1024) dweight_kernel(const float* __restrict__ part, int P, int H,
-                                                       float* __restrict__ dw) {
+// dw[h] = sum over P partial rows: 16 columns per block (so that a 2048-wide row gives 128 blocks), thread row y adds
+// rows y, y + 64, ... ascending, then the 64 sums ascending.
+constexpr int kDwCols = 16, kDwRows = 64;
+__global__ void __launch_bounds__(kDwCols * kDwRows) dweight_kernel(const float* __restrict__ part, int P, int H,
+                                                                   float* __restrict__ dw) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float s[32][33];
-  const int c = blockIdx.x * 32 + threadIdx.x;
+  __shared__ float s[kDwRows][kDwCols + 1];
+  const int c = blockIdx.x * kDwCols + threadIdx.x;      // H is a multiple of 16
   float v = 0.0f;
-  if (c < H) {
-    int r = threadIdx.y;
-    for (; r + 96 < P; r += 128) {
-      const float a0 = part[static_cast<long long>(r) * H + c], a1 = part[static_cast<long long>(r + 32) * H + c];
-      const float a2 = part[static_cast<long long>(r + 64) * H + c], a3 = part[static_cast<long long>(r + 96) * H + c];
-      v = ((v + a0) + a1) + (a2 + a3);
-    }
-    for (; r < P; r += 32) v += part[static_cast<long long>(r) * H + c];
+  int r = threadIdx.y;
+  for (; r + 3 * kDwRows < P; r += 4 * kDwRows) {
+    const float* q = part + static_cast<long long>(r) * H + c;
+    const long long d = static_cast<long long>(kDwRows) * H;
+    const float a0 = q[0], a1 = q[d], a2 = q[2 * d], a3 = q[3 * d];
+    v = ((v + a0) + a1) + (a2 + a3);
   }
+  for (; r < P; r += kDwRows) v += part[static_cast<long long>(r) * H + c];
   s[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
-  if (threadIdx.y == 0 && c < H) {
+  if (threadIdx.y == 0) {
     float sum = 0.0f;
 #pragma unroll
-    for (int y = 0; y < 32; ++y) sum += s[y][threadIdx.x];
+    for (int y = 0; y < kDwRows; ++y) sum += s[y][threadIdx.x];
     dw[c] = sum;
   }
 }
@@ -425,7 +425,7 @@ int norm_bwd_launch(const void* dy, int dy_f32, const void* x, int x_f32, const 
     if (rc || dw == nullptr) return rc;
   }
   ProfScope prof("rms_norm_dweight", st);
-  return check_cuda(launch_kernel(dweight_kernel, dim3((H + 31) / 32), dim3(32, 32), 0, st,
+  return check_cuda(launch_kernel(dweight_kernel, dim3(H / kDwCols), dim3(kDwCols, kDwRows), 0, st,
                                   static_cast<const float*>(part), P, H, dw),
                     "dweight_kernel");
 }

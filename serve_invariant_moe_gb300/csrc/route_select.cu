@@ -21,15 +21,16 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kSelThreads = 256;
 
-// Larger = ranks earlier; NaN -> 0 (below every number); -0 and +0 tie.
+// Larger = ranks earlier; NaN -> 1 (below every number, whose keys start at 0x007fffff); 0 is left for "not there"; -0 and
+// +0 tie.
 __device__ __forceinline__ uint32_t order_key(float v) {
-  if (v != v) return 0u;
+  if (v != v) return 1u;
   const uint32_t b = __float_as_uint(v == 0.0f ? 0.0f : v);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
 __device__ __forceinline__ float key_value(uint32_t key) {
-  if (key == 0u) return __uint_as_float(0x7fc00000u);
+  if (key <= 1u) return __uint_as_float(0x7fc00000u);
   return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
 }
 
@@ -88,8 +89,9 @@ struct SelectParams {
   float* w;
 };
 
+// Up to E = 256 at most 32 registers a thread: a batch of 8192 tokens is then resident at once (64 warps per SM).
 template <int EPL, bool SOFTMAX, bool GROUPS>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kSelThreads, EPL <= 8 ? 8 : 1) select_kernel(const SelectParams p) {
   pdl_wait();
   pdl_trigger();
   extern __shared__ uint32_t sm_keys[];      // GROUPS: per warp E choice keys, padded by one word per 32
@@ -102,8 +104,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
   for (int i = 0; i < EPL; ++i) l[i] = i * 32 + lane < p.E ? __ldg(row + i * 32 + lane) : -INFINITY;
   SoftmaxStats st{0.0f, 1.0f};
   if (SOFTMAX) st = softmax_stats<EPL>(l, p.E, lane);
-  uint32_t key[EPL];
-  uint32_t live = 0u;                         // bit i: expert i * 32 + lane may still be chosen
+  uint32_t key[EPL];                          // 0: no such expert, taken, or its group is not kept
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = i * 32 + lane;
@@ -112,27 +113,50 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
       float c = l[i];
       if (p.bias != nullptr) c = __fadd_rn(SOFTMAX ? softmax_score(c, st) : sigmoid_f32(c), __ldg(p.bias + e));
       key[i] = order_key(c);
-      live |= 1u << i;
     }
   }
   if (GROUPS) {
     const int per = p.E / p.n_group;
-    uint32_t* sk = sm_keys + warp * (p.E + p.E / 32 + 1);
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (i * 32 + lane < p.E) sk[i * 33 + lane] = key[i];
-    __syncwarp();
-    // lane g: the two largest keys of group g
-    uint32_t gkey = 0u;
-    if (lane < p.n_group) {
+    const bool pairs = p.bias != nullptr && per > 1;
+    uint32_t gkey = 0u;                       // lane g: the value of group g
+    if (per % 32 == 0) {
+      // a group is c whole registers of the warp: its two largest keys by warp maxima
+      const int c = per / 32;
       uint32_t a = 0u, b = 0u;
-      for (int j = 0; j < per; ++j) {
-        const int e = lane * per + j;
-        const uint32_t v = sk[e + (e >> 5)];
-        b = max(b, min(a, v));
-        a = max(a, v);
+      int left = c, g = 0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        b = max(b, min(a, key[i]));
+        a = max(a, key[i]);
+        if (--left == 0 && g < p.n_group) {
+          const uint32_t t1 = __reduce_max_sync(kFull, a);
+          uint32_t v = t1;
+          if (pairs) {
+            const int first = __ffs(__ballot_sync(kFull, a == t1)) - 1;
+            v = order_key(__fadd_rn(key_value(t1), key_value(__reduce_max_sync(kFull, lane == first ? b : a))));
+          }
+          if (lane == g) gkey = v;
+          ++g;
+          left = c;
+          a = b = 0u;
+        }
       }
-      gkey = p.bias != nullptr && per > 1 ? order_key(__fadd_rn(key_value(a), key_value(b))) : a;
+    } else {
+      uint32_t* sk = sm_keys + warp * (p.E + p.E / 32 + 1);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (i * 32 + lane < p.E) sk[i * 33 + lane] = key[i];
+      __syncwarp();
+      if (lane < p.n_group) {
+        uint32_t a = 0u, b = 0u;
+        for (int j = 0; j < per; ++j) {
+          const int e = lane * per + j;
+          const uint32_t v = sk[e + (e >> 5)];
+          b = max(b, min(a, v));
+          a = max(a, v);
+        }
+        gkey = pairs ? order_key(__fadd_rn(key_value(a), key_value(b))) : a;
+      }
     }
     int rank = 0;
     for (int g = 0; g < p.n_group; ++g) {
@@ -140,26 +164,48 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
       if (o > gkey || (o == gkey && g < lane)) ++rank;
     }
     const unsigned kept = __ballot_sync(kFull, lane < p.n_group && rank < p.topk_group);
+    if (per % 32 == 0) {
+      int left = per / 32, g = 0;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = i * 32 + lane;
-      if (e < p.E && !((kept >> (e / per)) & 1u)) live &= ~(1u << i);
+      for (int i = 0; i < EPL; ++i) {
+        if (!((kept >> g) & 1u)) key[i] = 0u;
+        if (--left == 0) {
+          ++g;
+          left = per / 32;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const int e = i * 32 + lane;
+        if (e < p.E && !((kept >> (e / per)) & 1u)) key[i] = 0u;
+      }
     }
   }
-  int my_e = 0;
-  for (int j = 0; j < p.k; ++j) {
-    uint32_t best = 0u;
+  // k rounds: the warp's largest key, the lowest expert that has it; only the lane that loses its best looks again
+  uint32_t best = 0u;
+  int best_i = 0;
+  auto look = [&]() {
+    best = 0u;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if ((live >> i) & 1u) best = max(best, key[i]);
-    const uint32_t gbest = __reduce_max_sync(kFull, best);
-    uint32_t cand = 0xffffffffu;
-#pragma unroll
-    for (int i = EPL - 1; i >= 0; --i)
-      if (((live >> i) & 1u) && key[i] == gbest) cand = static_cast<uint32_t>(i * 32 + lane);
-    const int e = static_cast<int>(__reduce_min_sync(kFull, cand));
-    if ((e & 31) == lane) live &= ~(1u << (e >> 5));
+      if (key[i] > best) {
+        best = key[i];
+        best_i = i;
+      }
+  };
+  look();
+  int my_e = 0;
+  for (int j = 0; j < p.k; ++j) {
+    const uint32_t top = __reduce_max_sync(kFull, best);
+    const int e = static_cast<int>(__reduce_min_sync(kFull, best == top ? static_cast<uint32_t>(best_i * 32 + lane) : kFull));
     if (lane == j) my_e = e;
+    if ((e & 31) == lane) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (i == best_i) key[i] = 0u;
+      look();
+    }
   }
   float s = 0.0f;
   if (lane < p.k) {
@@ -223,20 +269,24 @@ __global__ void __launch_bounds__(kSelThreads)
   // value of a chosen expert's entry beyond what every expert gets
   const float mine = SOFTMAX ? __fmul_rn(d, s) : d * s * (1.0f - s);
   const float all = SOFTMAX && !renorm ? dot : 0.0f;
+  float v[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) v[i] = 0.0f;
+  for (int j = 0; j < k; ++j) {
+    const int ej = __shfl_sync(kFull, e, j);
+    const float vj = __shfl_sync(kFull, mine, j);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (ej == i * 32 + lane) v[i] += vj;
+  }
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int c = i * 32 + lane;
-    float v = 0.0f;
-    for (int j = 0; j < k; ++j) {
-      const int ej = __shfl_sync(kFull, e, j);
-      const float vj = __shfl_sync(kFull, mine, j);
-      if (ej == c) v += vj;
-    }
     if (c < E) {
       if constexpr (SOFTMAX)
-        if (!renorm) v -= __fmul_rn(all, softmax_score(l[i], st));
-      if (dl != nullptr) dl[t * E + c] = v;
-      if (dl_bf16 != nullptr) dl_bf16[t * E + c] = __float2bfloat16_rn(v);
+        if (!renorm) v[i] -= __fmul_rn(all, softmax_score(l[i], st));
+      if (dl != nullptr) dl[t * E + c] = v[i];
+      if (dl_bf16 != nullptr) dl_bf16[t * E + c] = __float2bfloat16_rn(v[i]);
     }
   }
 }
@@ -245,7 +295,7 @@ template <int EPL>
 cudaError_t select_epl(const SelectParams& p, int softmax, dim3 g, cudaStream_t st) {
   const dim3 b(kSelThreads);
   if (p.n_group > 1) {
-    const size_t smem = (kSelThreads / 32) * (static_cast<size_t>(p.E) + p.E / 32 + 1) * 4;
+    const size_t smem = p.E / p.n_group % 32 == 0 ? 0 : (kSelThreads / 32) * (static_cast<size_t>(p.E) + p.E / 32 + 1) * 4;
     return softmax ? launch_kernel(select_kernel<EPL, true, true>, g, b, smem, st, p)
                    : launch_kernel(select_kernel<EPL, false, true>, g, b, smem, st, p);
   }
