@@ -557,6 +557,11 @@ int add_rms_norm_backward(const void* dy, int dy_type, const void* x, int x_type
 int fp8_quantize(const void* x, int x_type, int banks, int rows, int cols, int block_rows, void* q, float* scale,
                  void* stream);
 
+/* xp[r] = x[row_token[r]] for every permuted row r of the plan: the bf16 rows that
+ * moe_grouped_ffn reads after moe_route_select.  x [T, H] bf16, xp [T*k, H] bf16.
+ * Shapes: H % 8 == 0, k <= 32. */
+int moe_permute_rows(const void* x, const int32_t* plan, int T, int H, int E, int k, void* xp, void* stream);
+
 /* xp[r] = q[row_token[r]] and its scales for every permuted row r of the plan.
  * q [T, H] e4m3, scale [T, ceil(H / 128)], xp [T*k, H], xp_scale [T*k, ceil(H / 128)].
  * Shapes: H % 16 == 0, H <= 32768, k <= 32. */

@@ -53,6 +53,7 @@ PROTOTYPES = {
     "rms_norm_backward_workspace_size": (_sz, [_i, _i]),
     "add_rms_norm_backward": (_i, [_vp, _i, _vp, _i, _vp, _vp, _vp, _i, _i, _vp, _vp, _vp, _sz, _vp]),
     "fp8_quantize": (_i, [_vp, _i, _i, _i, _i, _i, _vp, _vp, _vp]),
+    "moe_permute_rows": (_i, [_vp, _vp, _i, _i, _i, _i, _vp, _vp]),
     "moe_permute_fp8": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp]),
     "fp8_gemm": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _vp, _sz, _vp]),
     "moe_grouped_swiglu_fp8": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _sz, _vp]),

@@ -19,6 +19,21 @@ from . import binding
 
 
 @dataclass
+class Routing:
+    """Expert choice by scores (binding.moe_route_select); without one a layer's router is the softmax over its top-k logits."""
+    score: str = "sigmoid"                # or "softmax"
+    bias: Optional[torch.Tensor] = None   # [E] fp32, added to the scores for the choice alone
+    n_group: int = 1
+    topk_group: int = 1
+    renormalize: bool = True
+    scale: float = 1.0
+
+    def select(self, logits, k, workspace, topk_idx=None, topk_w=None, plan=True):
+        return binding.moe_route_select(logits, k, self.score, self.bias, self.n_group, self.topk_group,
+                                        self.renormalize, self.scale, topk_idx, topk_w, plan, workspace)
+
+
+@dataclass
 class MoEWeights:
     w_router: torch.Tensor            # [E, H] bf16
     w13: torch.Tensor                 # [E, 2F, H] bf16 (gate rows, then up rows)
@@ -26,6 +41,7 @@ class MoEWeights:
     k: int
     ws13: Optional[torch.Tensor] = None   # [2Fs, H] bf16 shared expert
     ws2: Optional[torch.Tensor] = None    # [H, Fs] bf16
+    routing: Optional[Routing] = None
 
     @property
     def E(self):
@@ -42,6 +58,11 @@ class MoEWeights:
     @property
     def F_shared(self):
         return 0 if self.ws13 is None else self.ws13.shape[0] // 2
+
+
+def _head(t, n):
+    """The first n rows of a buffer that may be absent."""
+    return None if t is None else t[:n]
 
 
 class MoELayer:
@@ -63,6 +84,8 @@ class MoELayer:
         w = self.w
         T = x.shape[0]
         bufs = bufs or {}
+        if w.routing is not None:
+            return self._run_routed(x, ws, bufs, out_bf16, replay_idx)
         if replay_idx is None:
             # route, experts and combine in one library call
             return binding.moe_layer_forward(x, w.w_router, w.w13, w.w2, w.k, ws, ws13=w.ws13, ws2=w.ws2,
@@ -78,6 +101,24 @@ class MoELayer:
         out = binding.moe_combine(f["y"], r["topk_w"], r["plan"], T, w.H, w.E, w.k, y_shared=f["y_shared"],
                                   out=bufs.get("out"), out_bf16=out_bf16)
         return dict(out=out, **r, **f)
+
+    def _run_routed(self, x, ws, bufs, out_bf16, replay_idx):
+        """The layer with its experts chosen by w.routing: the same calls with moe_route_topk in three parts."""
+        w = self.w
+        if replay_idx is not None:
+            raise ValueError("router replay needs the softmax top-k router (routing=None)")
+        T = x.shape[0]
+        logits = binding.moe_router_logits(x, w.w_router, ws, logits=_head(bufs.get("logits"), T))
+        plan = bufs.get("plan")
+        r = w.routing.select(logits, w.k, ws, _head(bufs.get("idx"), T), _head(bufs.get("w"), T),
+                             True if plan is None else plan)
+        xp = binding.moe_permute_rows(x, r["plan"], w.E, w.k, xp=_head(bufs.get("xp"), T * w.k))
+        f = binding.moe_grouped_ffn(xp, r["plan"], w.w13, w.w2, T, w.k, ws, h=bufs.get("h"), y=bufs.get("y"),
+                                    x_shared=x if w.ws13 is not None else None, ws13=w.ws13, ws2=w.ws2,
+                                    y_shared=_head(bufs.get("ys"), T))
+        out = binding.moe_combine(f["y"], r["topk_w"], r["plan"], T, w.H, w.E, w.k, y_shared=f["y_shared"],
+                                  out=_head(bufs.get("out"), T), out_bf16=out_bf16)
+        return dict(out=out, logits=logits, xp=xp, **r, **f)
 
     def prefill(self, x: torch.Tensor, out_bf16: Optional[torch.Tensor] = None, return_all=False,
                 replay_idx: Optional[torch.Tensor] = None):
@@ -115,8 +156,16 @@ class MoELayer:
                                              dw13=weight_grads, dw2=weight_grads,
                                              x_shared=x if w.ws13 is not None else None, ws13=w.ws13, ws2=w.ws2,
                                              dout_bf16=c["dout_bf16"], dws13=weight_grads, dws2=weight_grads)
-        r = binding.moe_route_backward(x, w.w_router, fwd["topk_idx"], fwd["topk_w"], c["dgate"], f["dxp"],
-                                       fwd["plan"], ws, dx_shared=f["dx_shared"], dw_router=weight_grads)
+        if w.routing is None:
+            r = binding.moe_route_backward(x, w.w_router, fwd["topk_idx"], fwd["topk_w"], c["dgate"], f["dxp"],
+                                           fwd["plan"], ws, dx_shared=f["dx_shared"], dw_router=weight_grads)
+        else:
+            dlogits = torch.empty_like(fwd["logits"], dtype=torch.bfloat16)
+            binding.moe_route_select_backward(fwd["logits"], fwd["topk_idx"], c["dgate"], w.routing.score,
+                                              w.routing.renormalize, w.routing.scale, dlogits=False,
+                                              dlogits_bf16=dlogits)
+            r = binding.moe_router_backward(x, w.w_router, dlogits, f["dxp"], fwd["plan"], w.k, ws,
+                                            dx_shared=f["dx_shared"], dw_router=weight_grads)
         binding.check_status(ws)
         return dict(dx=r["dx"], dw_router=r["dw_router"], dw13=f["dw13"], dw2=f["dw2"], dws13=f["dws13"],
                     dws2=f["dws2"], dgate=c["dgate"], dy=c["dy"], dxp=f["dxp"], workspace=ws)
@@ -165,6 +214,9 @@ class MoELayer:
             raise ValueError(f"x_tokens must be a contiguous [B, {w.H}] bf16 tensor on {d['device']}")
         if out_bf16 is not None:
             binding._req(out_bf16, torch.bfloat16, "out_bf16", (B, w.H))
+        if w.routing is not None:
+            bufs = {name: d[name] for name in ("logits", "idx", "w", "plan", "xp", "h", "y", "ys", "out")}
+            return self._run_routed(x_tokens, d["ws"], bufs, out_bf16, None)["out"]
         args = d["args"]
         args[0] = x_tokens.data_ptr()
         args[6] = B

@@ -721,6 +721,17 @@ def fp8_quantize(x, block_rows=1, q=None, scale=None):
     return q, scale
 
 
+def moe_permute_rows(x, plan, E, k, xp=None):
+    """The bf16 rows x [T, H] in the plan's order: xp [T*k, H]."""
+    dev = _device(x, "x")
+    T, H = _dims(x, "x")
+    xptr = _ck(x, torch.bfloat16, "x", (T, H), dev)
+    _req_plan(plan, T, E, k)
+    xp = _new(x, (T * k, H), torch.bfloat16, xp, "xp")
+    check(lib().moe_permute_rows(xptr, plan.data_ptr(), T, H, E, k, xp.data_ptr(), _raw_stream(dev)))
+    return xp
+
+
 def moe_permute_fp8(q, scale, plan, E, k, xp=None, xp_scale=None):
     """The quantised rows q [T, H] and their scales in the plan's order: (xp [T*k, H], xp_scale)."""
     dev = _device(q, "q")

@@ -190,6 +190,16 @@ int fp8_quantize(const void* x, int x_type, int banks, int rows, int cols, int b
                          static_cast<cudaStream_t>(stream));
 }
 
+int moe_permute_rows(const void* x, const int32_t* plan, int T, int H, int E, int k, void* xp, void* stream) {
+  REQUIRE(T >= 0 && H > 0 && E > 0 && k > 0 && k <= E && k <= 32, INVMOE_ERR_INVALID_ARG, "bad sizes");
+  REQUIRE(H % 8 == 0, INVMOE_ERR_UNSUPPORTED_SHAPE, "H=%d is not a multiple of 8", H);
+  if (T == 0) return INVMOE_OK;
+  REQUIRE_PTR(x); REQUIRE_PTR(plan); REQUIRE_PTR(xp);
+  REQUIRE_ALIGNED(x); REQUIRE_ALIGNED(xp);
+  return permute_launch(x, plan + 2 * E + 1 + static_cast<long long>(T) * k, T, k, H, xp,
+                        static_cast<cudaStream_t>(stream));
+}
+
 int moe_permute_fp8(const void* q, const float* scale, const int32_t* plan, int T, int H, int E, int k, void* xp,
                     float* xp_scale, void* stream) {
   REQUIRE(T >= 0 && E > 0 && k > 0 && k <= E && k <= 32, INVMOE_ERR_INVALID_ARG, "bad sizes");

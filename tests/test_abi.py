@@ -125,3 +125,38 @@ def test_binding_refuses_host_tensors_before_any_call():
         binding.rl_token_loss(torch.zeros(4), torch.zeros(4), torch.zeros(4))
     with pytest.raises(ValueError, match="CUDA tensor"):
         binding.gemm_bf16(x, wr, ws)
+
+
+def test_block_entry_points_reject_before_any_launch(lib):
+    null = None
+    assert lib.moe_route_select(null, null, 4, 8, 9, 0, 1, 1, 1, 1.0, null, null, null, null, 0, null) == -1
+    assert lib.moe_route_select(null, null, 4, 8, 2, 7, 1, 1, 1, 1.0, null, null, null, null, 0, null) == -1
+    assert lib.moe_route_select(null, null, 4, 10, 2, 0, 4, 1, 1, 1.0, null, null, null, null, 0, null) == -1
+    assert lib.moe_route_select(null, null, 4, 8, 2, 0, 1, 1, 1, 1.0, null, null, null, null, 0, null) == -1
+    assert b"logits" in lib.invmoe_last_error()
+    assert lib.add_rms_norm(null, 5, null, 0, null, 4, 64, 1e-6, null, null, null, null, null, null) == -1
+    assert lib.add_rms_norm(null, 0, null, 0, null, 4, 40, 1e-6, null, null, null, null, null, null) == -2
+    assert lib.fp8_quantize(null, 0, 1, 4, 64, 64, null, null, null) == -1
+    assert lib.fp8_gemm(null, null, null, null, 4, 64, 40, null, 0, ctypes.c_void_p(256), 4096, null) == -2
+    assert lib.fp8_gemm(null, null, null, null, 4, 64, 64, null, 0, ctypes.c_void_p(256), 8, null) == -3
+    assert lib.moe_grouped_swiglu_fp8(null, null, null, null, null, 4, 64, 2, 1, 128, null, null, ctypes.c_void_p(256),
+                                      4096, null) == -1                      # no plan for two experts
+    assert lib.moe_grouped_down_fp8(null, null, null, null, null, 4, 64, 1, 1, 96, null, ctypes.c_void_p(256), 4096,
+                                    null) == -2 and b"F=96" in lib.invmoe_last_error()
+    assert lib.rms_norm_backward_workspace_size(0, 64) == 256
+    assert lib.rms_norm_backward_workspace_size(10, 64) == 256 + 10 * 64 * 4
+
+
+def test_block_binding_refuses_host_tensors():
+    import torch
+    from serve_invariant_moe_gb300 import binding
+    x = torch.zeros(4, 64)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        binding.moe_route_select(x, 2)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        binding.add_rms_norm(x, torch.zeros(64, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        binding.fp8_quantize(x)
+    q = x.to(torch.float8_e4m3fn)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        binding.fp8_gemm(q, x, q, x, torch.zeros(256, dtype=torch.uint8))
