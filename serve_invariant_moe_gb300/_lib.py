@@ -100,6 +100,22 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_marshal = None
+
+
+def marshal():
+    """The binding's CPython helpers (csrc/marshal.cpp), loaded once with the library they call."""
+    global _marshal
+    if _marshal is None:
+        lib()
+        try:
+            from . import _marshal as module
+        except ImportError as e:
+            raise RuntimeError(f"_marshal.so is not built ({e}); run serve_invariant_moe_gb300.build.build()") from e
+        _marshal = module
+    return _marshal
+
+
 def check(rc: int):
     if rc != 0:
         raise InvmoeError(rc, lib().invmoe_last_error().decode(errors="replace"))

@@ -10,7 +10,7 @@ import math
 
 import torch
 
-from ._lib import check, lib
+from ._lib import check, lib, marshal
 
 
 def _p(t):
@@ -493,11 +493,17 @@ def moe_route_backward(x, w_router, topk_idx, topk_w, dgate, dxp, plan, workspac
 
 # ---------------------------------------------------------------------------
 # The 8-bit block: residual + norm, scored routing, e4m3 products
+#
+# These calls of a few tokens are bound by the host, so their checks, allocations and
+# argument conversions are C functions (csrc/marshal.cpp): m.check(tensor, name, type,
+# *shape) refuses as _req does, m.new(like, type, *shape) allocates, and m.<entry point>
+# takes tensors (or None) for pointers and adds the current stream.
 # ---------------------------------------------------------------------------
 
 FP8 = torch.float8_e4m3fn
 SCORES = {"sigmoid": 0, "softmax": 1}
-_TYPES = {torch.bfloat16: 0, torch.float32: 1}
+BF16_, F32_, FP8_, I32_, U8_ = range(5)              # marshal's element types
+_TYPES = {torch.bfloat16: 0, torch.float32: 1}       # INVMOE_BF16, INVMOE_F32; marshal's codes too
 
 
 def _type(t, name):
@@ -509,65 +515,48 @@ def _type(t, name):
 
 
 def _score(score):
-    if score not in SCORES:
+    code = SCORES.get(score)
+    if code is None:
         raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
-    return SCORES[score]
-
-
-def _ck(t, dtype, name, shape, dev):
-    """_req in one expression (0.3 us instead of 0.7): a call of a few tokens is bound by the host.  `dev` is the
-    current device's index; a host tensor's is -1.  Returns the address."""
-    if t is None or t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
-        _req(t, dtype, name, shape)
-    return t.data_ptr()
-
-
-def _ck_opt(t, dtype, name, shape, dev):
-    return None if t is None else _ck(t, dtype, name, shape, dev)
-
-
-def _ck_ws(t, dev):
-    if t is None or t.dtype is not torch.uint8 or t.get_device() != dev or not t.is_contiguous():
-        _req(t, torch.uint8, "workspace")
-    return t.data_ptr()
+    return code
 
 
 def _dims(t, name, n=2):
-    if t.dim() != n:
-        raise ValueError(f"{name} must have {n} dimensions, got shape {tuple(t.shape)}")
-    return t.shape
+    s = t.shape
+    if len(s) != n:
+        raise ValueError(f"{name} must have {n} dimensions, got shape {tuple(s)}")
+    return s
 
 
-def _new(like, shape, dtype, t=None, name=""):
-    """A new tensor on the device of `like`, or the caller's after the usual checks."""
-    return like.new_empty(shape, dtype=dtype) if t is None else _req(t, dtype, name, shape)
-
-
-def _device(t, name):
-    """The current device's index; a host tensor is refused before CUDA is touched."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return torch.cuda.current_device()
-
-
-def _raw_stream(dev):
-    return torch._C._cuda_getCurrentRawStream(dev)
+def _out(m, given, like, name, code, *shape):
+    """An output: a new tensor, or the caller's (None and True mean a new one) after the usual checks."""
+    if given is None or given is True:
+        return m.new(like, code, *shape)
+    m.check(given, name, code, *shape)
+    return given
 
 
 def _blocks(n):
     return (n + 127) // 128
 
 
+def _plan(m, plan, T, E, k):
+    m.check(plan, "plan", I32_)
+    if plan.numel() < 2 * E + 1 + 2 * T * k:
+        raise ValueError("plan is too small")
+    return plan
+
+
 def moe_router_logits(x, w_router, workspace, logits=None):
     """logits [T, E] fp32 = x @ w_router^T: moe_route_topk's router GEMM alone."""
-    dev = _device(x, "x")
+    m = marshal()
     T, H = _dims(x, "x")
     E = w_router.shape[0]
-    xp = _ck(x, torch.bfloat16, "x", (T, H), dev)
-    wp = _ck(w_router, torch.bfloat16, "w_router", (E, H), dev)
-    ws = _ck_ws(workspace, dev)
-    logits = _new(x, (T, E), torch.float32, logits, "logits")
-    check(lib().moe_router_logits(xp, wp, T, H, E, logits.data_ptr(), ws, workspace.numel(), _raw_stream(dev)))
+    m.check(x, "x", BF16_, T, H)
+    m.check(w_router, "w_router", BF16_, E, H)
+    m.check(workspace, "workspace", U8_)
+    logits = _out(m, logits, x, "logits", F32_, T, E)
+    check(m.moe_router_logits(x, w_router, T, H, E, logits, workspace, workspace.numel()))
     return logits
 
 
@@ -576,19 +565,21 @@ def moe_route_select(logits, k, score="sigmoid", bias=None, n_group=1, topk_grou
     """Experts by score (+ bias), limited to the best groups: topk_idx [T, k] int32, topk_w [T, k] fp32.
 
     plan: a tensor to fill, or True to allocate one (then ``workspace`` is needed): the dispatch plan."""
-    dev = _device(logits, "logits")
+    m = marshal()
     T, E = _dims(logits, "logits")
-    lp = _ck(logits, torch.float32, "logits", (T, E), dev)
-    bp = _ck_opt(bias, torch.float32, "bias", (E,), dev)
     kind = _score(score)
-    topk_idx = _new(logits, (T, k), torch.int32, topk_idx, "topk_idx")
-    topk_w = _new(logits, (T, k), torch.float32, topk_w, "topk_w")
-    pp, wp, wn = None, None, 0
+    m.check(logits, "logits", F32_, T, E)
+    if bias is not None:
+        m.check(bias, "bias", F32_, E)
+    topk_idx = _out(m, topk_idx, logits, "topk_idx", I32_, T, k)
+    topk_w = _out(m, topk_w, logits, "topk_w", F32_, T, k)
+    nbytes = 0
     if plan is not None:
-        plan = _new(logits, (plan_len(T, E, k),), torch.int32) if plan is True else _req_plan(plan, T, E, k)
-        pp, wp, wn = plan.data_ptr(), _ck_ws(workspace, dev), workspace.numel()
-    check(lib().moe_route_select(lp, bp, T, E, k, kind, n_group, topk_group, 1 if renormalize else 0, scale,
-                                 topk_idx.data_ptr(), topk_w.data_ptr(), pp, wp, wn, _raw_stream(dev)))
+        plan = m.new(logits, I32_, 2 * E + 1 + 2 * T * k) if plan is True else _plan(m, plan, T, E, k)
+        m.check(workspace, "workspace", U8_)
+        nbytes = workspace.numel()
+    check(m.moe_route_select(logits, bias, T, E, k, kind, n_group, topk_group, bool(renormalize), scale, topk_idx,
+                             topk_w, plan, workspace, nbytes))
     return {"topk_idx": topk_idx, "topk_w": topk_w, "plan": plan}
 
 
@@ -597,42 +588,38 @@ def moe_route_select_backward(logits, topk_idx, dw, score="sigmoid", renormalize
     """Gradient of moe_route_select's weights: dw [T, k] fp32 -> dlogits [T, E] fp32.
 
     dlogits: a tensor to fill, True (allocate) or False (skip); dlogits_bf16: a bf16 tensor to fill as well."""
-    dev = _device(logits, "logits")
+    m = marshal()
     T, E = _dims(logits, "logits")
     k = _dims(topk_idx, "topk_idx")[1]
-    lp = _ck(logits, torch.float32, "logits", (T, E), dev)
-    ip = _ck(topk_idx, torch.int32, "topk_idx", (T, k), dev)
-    wp = _ck(dw, torch.float32, "dw", (T, k), dev)
     kind = _score(score)
-    dp = None
-    if dlogits is False:
-        dlogits = None
-    else:
-        dlogits = _new(logits, (T, E), torch.float32, None if dlogits is True else dlogits, "dlogits")
-        dp = dlogits.data_ptr()
-    bp = _ck_opt(dlogits_bf16, torch.bfloat16, "dlogits_bf16", (T, E), dev)
-    check(lib().moe_route_select_backward(lp, ip, wp, T, E, k, kind, 1 if renormalize else 0, scale, dp, bp,
-                                          _raw_stream(dev)))
+    m.check(logits, "logits", F32_, T, E)
+    m.check(topk_idx, "topk_idx", I32_, T, k)
+    m.check(dw, "dw", F32_, T, k)
+    dlogits = None if dlogits is False else _out(m, dlogits, logits, "dlogits", F32_, T, E)
+    if dlogits_bf16 is not None:
+        m.check(dlogits_bf16, "dlogits_bf16", BF16_, T, E)
+    check(m.moe_route_select_backward(logits, topk_idx, dw, T, E, k, kind, bool(renormalize), scale, dlogits,
+                                      dlogits_bf16))
     return dlogits
 
 
 def moe_router_backward(x, w_router, dlogits_bf16, dxp, plan, k, workspace, dx_shared=None, dx=None, dw_router=True):
     """The router's part of the layer backward from dlogits_bf16 [T, E]: dx [T, H] and dw_router [E, H], fp32."""
-    dev = _device(x, "x")
+    m = marshal()
     T, H = _dims(x, "x")
     E = w_router.shape[0]
-    xp = _ck(x, torch.bfloat16, "x", (T, H), dev)
-    wp = _ck(w_router, torch.bfloat16, "w_router", (E, H), dev)
-    dlp = _ck(dlogits_bf16, torch.bfloat16, "dlogits_bf16", (T, E), dev)
-    dxpp = _ck(dxp, torch.float32, "dxp", (T * k, H), dev)
-    _req_plan(plan, T, E, k)
-    dsp = _ck_opt(dx_shared, torch.float32, "dx_shared", (T, H), dev)
-    ws = _ck_ws(workspace, dev)
-    dx = _new(x, (T, H), torch.float32, dx, "dx")
-    dw_router = None if dw_router is False else _new(x, (E, H), torch.float32,
-                                                     None if dw_router is True else dw_router, "dw_router")
-    check(lib().moe_router_backward(xp, wp, dlp, dxpp, plan.data_ptr(), dsp, T, H, E, k, dx.data_ptr(), _p(dw_router),
-                                    ws, workspace.numel(), _raw_stream(dev)))
+    m.check(x, "x", BF16_, T, H)
+    m.check(w_router, "w_router", BF16_, E, H)
+    m.check(dlogits_bf16, "dlogits_bf16", BF16_, T, E)
+    m.check(dxp, "dxp", F32_, T * k, H)
+    _plan(m, plan, T, E, k)
+    if dx_shared is not None:
+        m.check(dx_shared, "dx_shared", F32_, T, H)
+    m.check(workspace, "workspace", U8_)
+    dx = _out(m, dx, x, "dx", F32_, T, H)
+    dw_router = None if dw_router is False else _out(m, dw_router, x, "dw_router", F32_, E, H)
+    check(m.moe_router_backward(x, w_router, dlogits_bf16, dxp, plan, dx_shared, T, H, E, k, dx, dw_router, workspace,
+                                workspace.numel()))
     return dict(dx=dx, dw_router=dw_router)
 
 
@@ -643,32 +630,25 @@ def add_rms_norm(x, weight, residual=None, eps=1e-6, out=True, fp8=False, residu
     x [T, H] and residual [T, H] bf16 or fp32, weight [H] bf16.  ``out`` (bf16): a tensor to fill, True or False;
     ``fp8``: also the e4m3 row with a scale per 128 columns (into q and scale if given).  ``residual_out`` receives r
     in the residual's type (it may be ``residual`` itself; allocated if not given)."""
-    dev = _device(x, "x")
+    m = marshal()
     T, H = _dims(x, "x")
-    xt = _type(x, "x")
-    xp = _ck(x, x.dtype, "x", (T, H), dev)
-    wp = _ck(weight, torch.bfloat16, "weight", (H,), dev)
-    rt, rp, rop, op, qp, sp = 0, None, None, None, None, None
+    xt, rt = _type(x, "x"), 0
+    m.check(x, "x", xt, T, H)
+    m.check(weight, "weight", BF16_, H)
     if residual is not None:
         rt = _type(residual, "residual")
-        rp = _ck(residual, residual.dtype, "residual", (T, H), dev)
-        residual_out = _new(residual, (T, H), residual.dtype, residual_out, "residual_out")
-        rop = residual_out.data_ptr()
+        m.check(residual, "residual", rt, T, H)
+        residual_out = _out(m, residual_out, x, "residual_out", rt, T, H)
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    if out is False:
-        out = None
-    else:
-        out = _new(x, (T, H), torch.bfloat16, None if out is True else out, "out")
-        op = out.data_ptr()
+    out = None if out is False else _out(m, out, x, "out", BF16_, T, H)
     if fp8:
-        q = _new(x, (T, H), FP8, q, "q")
-        scale = _new(x, (T, _blocks(H)), torch.float32, scale, "scale")
-        qp, sp = q.data_ptr(), scale.data_ptr()
+        q = _out(m, q, x, "q", FP8_, T, H)
+        scale = _out(m, scale, x, "scale", F32_, T, _blocks(H))
     else:
         q = scale = None
-    rstd = _new(x, (T,), torch.float32, rstd, "rstd")
-    check(lib().add_rms_norm(xp, xt, rp, rt, wp, T, H, eps, rop, op, qp, sp, rstd.data_ptr(), _raw_stream(dev)))
+    rstd = _out(m, rstd, x, "rstd", F32_, T)
+    check(m.add_rms_norm(x, xt, residual, rt, weight, T, H, eps, residual_out, out, q, scale, rstd))
     return {"residual": residual_out, "out": out, "q": q, "scale": scale, "rstd": rstd}
 
 
@@ -681,25 +661,27 @@ def add_rms_norm_backward(dy, x, weight, rstd, dres=None, dx=None, dweight=True,
 
     dict(dx [T, H] in x's type: the gradient of that row, so of both summands; dweight [H] fp32 or None).
     dy bf16 or fp32; dres: the gradient that reaches the row from the residual stream; dx may be dres."""
-    dev = _device(x, "x")
+    m = marshal()
     T, H = _dims(x, "x")
     xt, dt = _type(x, "x"), _type(dy, "dy")
-    xp = _ck(x, x.dtype, "x", (T, H), dev)
-    dyp = _ck(dy, dy.dtype, "dy", (T, H), dev)
-    wp = _ck(weight, torch.bfloat16, "weight", (H,), dev)
-    rp = _ck(rstd, torch.float32, "rstd", (T,), dev)
-    drp = _ck_opt(dres, x.dtype, "dres", (T, H), dev)
-    dx = _new(x, (T, H), x.dtype, dx, "dx")
-    dwp, ws, wn = None, None, 0
+    m.check(x, "x", xt, T, H)
+    m.check(dy, "dy", dt, T, H)
+    m.check(weight, "weight", BF16_, H)
+    m.check(rstd, "rstd", F32_, T)
+    if dres is not None:
+        m.check(dres, "dres", xt, T, H)
+    dx = _out(m, dx, x, "dx", xt, T, H)
+    nbytes = 0
     if dweight is False:
         dweight = None
     else:
-        dweight = _new(x, (H,), torch.float32, None if dweight is True else dweight, "dweight")
+        dweight = _out(m, dweight, x, "dweight", F32_, H)
         if workspace is None:
-            workspace = x.new_empty(rms_norm_backward_workspace_size(T, H), dtype=torch.uint8)
-        dwp, ws, wn = dweight.data_ptr(), _ck_ws(workspace, dev), workspace.numel()
-    check(lib().add_rms_norm_backward(dyp, dt, xp, xt, wp, rp, drp, T, H, dx.data_ptr(), dwp, ws, wn,
-                                      _raw_stream(dev)))
+            workspace = m.new(x, U8_, rms_norm_backward_workspace_size(T, H))
+        else:
+            m.check(workspace, "workspace", U8_)
+        nbytes = workspace.numel()
+    check(m.add_rms_norm_backward(dy, dt, x, xt, weight, rstd, dres, T, H, dx, dweight, workspace, nbytes))
     return {"dx": dx, "dweight": dweight}
 
 
@@ -707,70 +689,68 @@ def fp8_quantize(x, block_rows=1, q=None, scale=None):
     """e4m3 of x [rows, cols] or [banks, rows, cols] (bf16 or fp32): (q, scale).
 
     block_rows 1: a scale per row and 128 columns (activations); 128: per 128 x 128 (weights)."""
-    dev = _device(x, "x")
+    m = marshal()
+    lead = tuple(x.shape[:-2])
     if x.dim() not in (2, 3):
         raise ValueError(f"x must be [rows, cols] or [banks, rows, cols], got {tuple(x.shape)}")
     xt = _type(x, "x")
-    xp = _ck(x, x.dtype, "x", x.shape, dev)
+    m.check(x, "x", xt)
     rows, cols = x.shape[-2:]
-    banks = x.shape[0] if x.dim() == 3 else 1
-    q = _new(x, tuple(x.shape), FP8, q, "q")
-    srows = rows if block_rows == 1 else _blocks(rows)
-    scale = _new(x, tuple(x.shape[:-2]) + (srows, _blocks(cols)), torch.float32, scale, "scale")
-    check(lib().fp8_quantize(xp, xt, banks, rows, cols, block_rows, q.data_ptr(), scale.data_ptr(), _raw_stream(dev)))
+    banks = x.shape[0] if lead else 1
+    q = _out(m, q, x, "q", FP8_, *x.shape)
+    scale = _out(m, scale, x, "scale", F32_, *lead, rows if block_rows == 1 else _blocks(rows), _blocks(cols))
+    check(m.fp8_quantize(x, xt, banks, rows, cols, block_rows, q, scale))
     return q, scale
 
 
 def moe_permute_rows(x, plan, E, k, xp=None):
     """The bf16 rows x [T, H] in the plan's order: xp [T*k, H]."""
-    dev = _device(x, "x")
+    m = marshal()
     T, H = _dims(x, "x")
-    xptr = _ck(x, torch.bfloat16, "x", (T, H), dev)
-    _req_plan(plan, T, E, k)
-    xp = _new(x, (T * k, H), torch.bfloat16, xp, "xp")
-    check(lib().moe_permute_rows(xptr, plan.data_ptr(), T, H, E, k, xp.data_ptr(), _raw_stream(dev)))
+    m.check(x, "x", BF16_, T, H)
+    _plan(m, plan, T, E, k)
+    xp = _out(m, xp, x, "xp", BF16_, T * k, H)
+    check(m.moe_permute_rows(x, plan, T, H, E, k, xp))
     return xp
 
 
 def moe_permute_fp8(q, scale, plan, E, k, xp=None, xp_scale=None):
     """The quantised rows q [T, H] and their scales in the plan's order: (xp [T*k, H], xp_scale)."""
-    dev = _device(q, "q")
+    m = marshal()
     T, H = _dims(q, "q")
-    qp = _ck(q, FP8, "q", (T, H), dev)
-    sp = _ck(scale, torch.float32, "scale", (T, _blocks(H)), dev)
-    _req_plan(plan, T, E, k)
-    xp = _new(q, (T * k, H), FP8, xp, "xp")
-    xp_scale = _new(q, (T * k, _blocks(H)), torch.float32, xp_scale, "xp_scale")
-    check(lib().moe_permute_fp8(qp, sp, plan.data_ptr(), T, H, E, k, xp.data_ptr(), xp_scale.data_ptr(),
-                                _raw_stream(dev)))
+    m.check(q, "q", FP8_, T, H)
+    m.check(scale, "scale", F32_, T, _blocks(H))
+    _plan(m, plan, T, E, k)
+    xp = _out(m, xp, q, "xp", FP8_, T * k, H)
+    xp_scale = _out(m, xp_scale, q, "xp_scale", F32_, T * k, _blocks(H))
+    check(m.moe_permute_fp8(q, scale, plan, T, H, E, k, xp, xp_scale))
     return xp, xp_scale
 
 
 def fp8_gemm(a, a_scale, b, b_scale, workspace, out_dtype=torch.bfloat16, out=None):
     """out [M, N] = (a * a_scale) @ (b * b_scale)^T: a [M, K] e4m3 with a scale per row and 128 columns, b [N, K]
     e4m3 with a scale per 128 x 128; out bf16 or fp32."""
-    dev = _device(a, "a")
+    m = marshal()
     M, K = _dims(a, "a")
     N = _dims(b, "b")[0]
     nb = _blocks(K)
-    ap = _ck(a, FP8, "a", (M, K), dev)
-    bp = _ck(b, FP8, "b", (N, K), dev)
-    asp = _ck(a_scale, torch.float32, "a_scale", (M, nb), dev)
-    bsp = _ck(b_scale, torch.float32, "b_scale", (_blocks(N), nb), dev)
     ot = _TYPES.get(out_dtype)
     if ot is None:
         raise ValueError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
-    ws = _ck_ws(workspace, dev)
-    out = _new(a, (M, N), out_dtype, out, "out")
-    check(lib().fp8_gemm(ap, asp, bp, bsp, M, N, K, out.data_ptr(), ot, ws, workspace.numel(), _raw_stream(dev)))
+    m.check(a, "a", FP8_, M, K)
+    m.check(b, "b", FP8_, N, K)
+    m.check(a_scale, "a_scale", F32_, M, nb)
+    m.check(b_scale, "b_scale", F32_, _blocks(N), nb)
+    m.check(workspace, "workspace", U8_)
+    out = _out(m, out, a, "out", ot, M, N)
+    check(m.fp8_gemm(a, a_scale, b, b_scale, M, N, K, out, ot, workspace, workspace.numel()))
     return out
 
 
-def _experts_plan(plan, T, E, k):
+def _experts_plan(m, plan, T, E, k):
     """The plan of a grouped call; None for one expert that takes every row."""
     if plan is not None:
-        _req_plan(plan, T, E, k)
-        return plan.data_ptr()
+        return _plan(m, plan, T, E, k)
     if E != 1 or k != 1:
         raise ValueError("plan may be None only for E = k = 1")
     return None
@@ -781,39 +761,38 @@ def moe_grouped_swiglu_fp8(xp, xp_scale, plan, w13, w13_scale, T, k, workspace, 
 
     xp [T*k, H] e4m3 in plan order, w13 [E, 2F, H] e4m3 (gate rows, then up rows), w13_scale [E, 2F/128, ceil(H/128)].
     plan None: one expert (E = k = 1) for all T rows."""
-    dev = _device(w13, "w13")
+    m = marshal()
     E, F2, H = _dims(w13, "w13", 3)
     if F2 % 2:
         raise ValueError(f"w13 must have an even number of rows (gate, then up), got {F2}")
     F, S, nb = F2 // 2, T * k, _blocks(H)
-    xpp = _ck(xp, FP8, "xp", (S, H), dev)
-    xsp = _ck(xp_scale, torch.float32, "xp_scale", (S, nb), dev)
-    wp = _ck(w13, FP8, "w13", (E, F2, H), dev)
-    wsp = _ck(w13_scale, torch.float32, "w13_scale", (E, _blocks(F2), nb), dev)
-    pp = _experts_plan(plan, T, E, k)
-    ws = _ck_ws(workspace, dev)
-    h = _new(xp, (S, F), FP8, h, "h")
-    h_scale = _new(xp, (S, _blocks(F)), torch.float32, h_scale, "h_scale")
-    check(lib().moe_grouped_swiglu_fp8(xpp, xsp, pp, wp, wsp, T, H, E, k, F, h.data_ptr(), h_scale.data_ptr(), ws,
-                                       workspace.numel(), _raw_stream(dev)))
+    m.check(xp, "xp", FP8_, S, H)
+    m.check(xp_scale, "xp_scale", F32_, S, nb)
+    m.check(w13, "w13", FP8_, E, F2, H)
+    m.check(w13_scale, "w13_scale", F32_, E, _blocks(F2), nb)
+    m.check(workspace, "workspace", U8_)
+    plan = _experts_plan(m, plan, T, E, k)
+    h = _out(m, h, xp, "h", FP8_, S, F)
+    h_scale = _out(m, h_scale, xp, "h_scale", F32_, S, _blocks(F))
+    check(m.moe_grouped_swiglu_fp8(xp, xp_scale, plan, w13, w13_scale, T, H, E, k, F, h, h_scale, workspace,
+                                   workspace.numel()))
     return {"h": h, "h_scale": h_scale}
 
 
 def moe_grouped_down_fp8(h, h_scale, plan, w2, w2_scale, T, k, workspace, y=None):
     """The experts' down product: y [T*k, H] fp32.  h [T*k, F] e4m3, w2 [E, H, F] e4m3, w2_scale
     [E, ceil(H/128), F/128]; plan None: one expert (E = k = 1) for all T rows."""
-    dev = _device(w2, "w2")
+    m = marshal()
     E, H, F = _dims(w2, "w2", 3)
     S, nb = T * k, _blocks(F)
-    hp = _ck(h, FP8, "h", (S, F), dev)
-    hsp = _ck(h_scale, torch.float32, "h_scale", (S, nb), dev)
-    wp = _ck(w2, FP8, "w2", (E, H, F), dev)
-    wsp = _ck(w2_scale, torch.float32, "w2_scale", (E, _blocks(H), nb), dev)
-    pp = _experts_plan(plan, T, E, k)
-    ws = _ck_ws(workspace, dev)
-    y = _new(h, (S, H), torch.float32, y, "y")
-    check(lib().moe_grouped_down_fp8(hp, hsp, pp, wp, wsp, T, H, E, k, F, y.data_ptr(), ws, workspace.numel(),
-                                     _raw_stream(dev)))
+    m.check(h, "h", FP8_, S, F)
+    m.check(h_scale, "h_scale", F32_, S, nb)
+    m.check(w2, "w2", FP8_, E, H, F)
+    m.check(w2_scale, "w2_scale", F32_, E, _blocks(H), nb)
+    m.check(workspace, "workspace", U8_)
+    plan = _experts_plan(m, plan, T, E, k)
+    y = _out(m, y, h, "y", F32_, S, H)
+    check(m.moe_grouped_down_fp8(h, h_scale, plan, w2, w2_scale, T, H, E, k, F, y, workspace, workspace.numel()))
     return y
 
 

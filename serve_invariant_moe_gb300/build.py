@@ -1,14 +1,17 @@
-"""Build libinvmoe.so in-tree with nvcc for sm_103a (no cmake, no torch extension machinery).
+"""Build libinvmoe.so in-tree with nvcc for sm_103a (no cmake, no torch extension machinery), and _marshal.so beside it.
 
 Each .cu translation unit is compiled in parallel into ``_build/`` and linked
-into ``serve_invariant_moe_gb300/libinvmoe.so``.  A unit is recompiled only when
-it, or a header in csrc/ or include/, is newer than its object file.
+into ``serve_invariant_moe_gb300/libinvmoe.so``; csrc/marshal.cpp (the binding's
+CPython helpers, against the installed torch's headers) becomes ``_marshal.so``.
+A unit is recompiled only when it, or a header in csrc/ or include/, is newer
+than its object file.
 """
 import concurrent.futures as cf
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -16,6 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libinvmoe.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
@@ -30,7 +34,37 @@ def nvcc() -> str:
 
 
 def _sources():
-    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
+    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cpp")))
+
+
+def _object(src):
+    return os.path.join(BUILD, os.path.splitext(os.path.basename(src))[0] + ".o")
+
+
+def _torch_dirs():
+    """Headers and libraries of the installed torch."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    return os.path.join(root, "include"), os.path.join(root, "lib"), int(torch._C._GLIBCXX_USE_CXX11_ABI)
+
+
+def _compile_command(src, obj, verbose_ptxas):
+    if src.endswith(".cu"):
+        return [nvcc()] + NVCC_FLAGS + (["-Xptxas", "-v"] if verbose_ptxas else []) + ["-c", src, "-o", obj]
+    include, _, abi = _torch_dirs()
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
+            "-isystem", include, "-isystem", cuda, "-isystem", sysconfig.get_paths()["include"], "-c", src, "-o", obj]
+
+
+def _link(cmd):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _stale(out, inputs):
+    return not os.path.exists(out) or os.path.getmtime(out) < max(os.path.getmtime(i) for i in inputs)
 
 
 def _headers_mtime():
@@ -43,11 +77,10 @@ def _headers_mtime():
 
 
 def _compile(src, verbose_ptxas=False):
-    obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
-    cmd = [nvcc()] + NVCC_FLAGS + (["-Xptxas", "-v"] if verbose_ptxas else []) + ["-c", src, "-o", obj]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    obj = _object(src)
+    r = subprocess.run(_compile_command(src, obj, verbose_ptxas), capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"compilation failed for {src}:\n{r.stdout}\n{r.stderr}")
     return obj, r.stderr
 
 
@@ -58,7 +91,7 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int = None) ->
     hdr = _headers_mtime()
     todo = []
     for s in srcs:
-        obj = os.path.join(BUILD, os.path.basename(s)[:-3] + ".o")
+        obj = _object(s)
         if force or verbose_ptxas or not os.path.exists(obj) or os.path.getmtime(obj) < max(os.path.getmtime(s), hdr):
             todo.append(s)
     logs = []
@@ -66,14 +99,18 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int = None) ->
         with cf.ThreadPoolExecutor(max_workers=jobs or min(len(todo), os.cpu_count() or 4)) as ex:
             for obj, err in ex.map(lambda s: _compile(s, verbose_ptxas), todo):
                 logs.append(err)
-    objs = [os.path.join(BUILD, os.path.basename(s)[:-3] + ".o") for s in srcs]
-    if todo or not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
-        tmp = LIB + ".tmp"
-        cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + ["-cudart", "static"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, LIB)
+    objs = [_object(s) for s in srcs if s.endswith(".cu")]
+    if todo or _stale(LIB, objs):
+        _link([nvcc()] + ARCH + ["-shared", "-o", LIB + ".tmp"] + objs + ["-cudart", "static"])
+        os.replace(LIB + ".tmp", LIB)
+    marshal = _object(os.path.join(CSRC, "marshal.cpp"))
+    if todo or _stale(MARSHAL, [marshal, LIB]):
+        torch_lib = _torch_dirs()[1]
+        # libinvmoe.so is found beside it; torch's libraries are in the process already
+        _link(["g++", "-shared", "-o", MARSHAL + ".tmp", marshal, "-L", PKG, "-l:libinvmoe.so", "-Wl,-rpath,$ORIGIN",
+               "-L", torch_lib, f"-Wl,-rpath,{torch_lib}", "-lc10", "-ltorch_cpu", "-lc10_cuda", "-ltorch_cuda",
+               "-ltorch_python"])
+        os.replace(MARSHAL + ".tmp", MARSHAL)
     if verbose_ptxas:
         sys.stderr.write("".join(logs))
     return LIB
