@@ -20,22 +20,43 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 
-// 8 consecutive elements, bf16 or fp32.
+// 8 consecutive elements, bf16 or fp32, as they are in memory.
+template <typename T>
+struct Raw8 {
+  uint4 u[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) u[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        v[4 * i] = __uint_as_float(u[i].x);
+        v[4 * i + 1] = __uint_as_float(u[i].y);
+        v[4 * i + 2] = __uint_as_float(u[i].z);
+        v[4 * i + 3] = __uint_as_float(u[i].w);
+      }
+    }
+  }
+};
+
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  } else {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  }
+  Raw8<T> r;
+  r.load(p);
+  r.get(v);
 }
 
 __device__ __forceinline__ uint32_t bf16x2_bits(float a, float b) {
@@ -88,8 +109,19 @@ __device__ __forceinline__ void quant8(const float (&y)[8], bool in, uint8_t* q,
   }
 }
 
+// Threads of a row: one vector of 8 per thread up to H = 2048, then two up to H = 8192, then four.
+struct RowShape {
+  int v, threads;
+};
+RowShape row_shape(int H) {
+  const int vecs = H / 8;
+  const int v = vecs <= 256 ? 1 : vecs <= 1024 ? 2 : 4;
+  return {v, ((vecs + v - 1) / v + 31) / 32 * 32};
+}
+constexpr int max_threads(int v) { return v == 1 ? 256 : v == 2 ? 512 : 1024; }
+
 template <int V, typename TX, typename TR>
-__global__ void __launch_bounds__(1024) norm_kernel(const TX* __restrict__ x, const TR* res,
+__global__ void __launch_bounds__(max_threads(V)) norm_kernel(const TX* __restrict__ x, const TR* res,
                                                     const __nv_bfloat16* __restrict__ weight, int H, float eps,
                                                     TR* res_out, __nv_bfloat16* __restrict__ out,
                                                     uint8_t* __restrict__ q, float* __restrict__ scale,
@@ -151,7 +183,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(const TX* __restrict__ x, co
 // rows_per_block consecutive rows and keeps its share of dw in registers; the partial rows are summed in order by
 // dweight_kernel, so no atomics and one order for a given T and H.
 template <int V, typename TX, typename TD>
-__global__ void __launch_bounds__(1024) norm_bwd_kernel(const TD* __restrict__ dy, const TX* __restrict__ x,
+__global__ void __launch_bounds__(max_threads(V)) norm_bwd_kernel(const TD* __restrict__ dy, const TX* __restrict__ x,
                                                         const __nv_bfloat16* __restrict__ weight,
                                                         const float* __restrict__ rstd, const TX* dres, int T, int H,
                                                         int rows_per_block, TX* dx, float* __restrict__ dw_part) {
@@ -169,22 +201,41 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const TD* __restrict__ d
   }
   const long long t0 = static_cast<long long>(blockIdx.x) * rows_per_block;
   const long long t1 = min(static_cast<long long>(T), t0 + rows_per_block);
-  int buf = 0;
-  for (long long t = t0; t < t1; ++t) {
-    const long long base = t * H;
-    const float rs = __ldg(rstd + t);
-    float g[V][8], n[V][8];
-    float dot = 0.0f;
+  // the next row is loaded while this one is worked on (with four vectors a thread there are no registers for that)
+  constexpr bool AHEAD = V < 4;
+  Raw8<TD> next_dy[V];
+  Raw8<TX> next_x[V], next_res[V];
+  float next_rs = 0.0f;
+  auto fetch = [&](long long t) {
+    next_rs = __ldg(rstd + t);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = (v * blockDim.x + threadIdx.x) * 8;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) g[v][i] = n[v][i] = 0.0f;
+      next_dy[v].zero();
+      next_x[v].zero();
+      next_res[v].zero();
       if (c < H) {
-        load8(dy + base + c, g[v]);
-        load8(x + base + c, n[v]);
+        next_dy[v].load(dy + t * H + c);
+        next_x[v].load(x + t * H + c);
+        if (dres != nullptr) next_res[v].load(dres + t * H + c);
       }
     }
+  };
+  if (AHEAD && t0 < t1) fetch(t0);
+  int buf = 0;
+  for (long long t = t0; t < t1; ++t) {
+    if (!AHEAD) fetch(t);
+    const float rs = next_rs;
+    float g[V][8], n[V][8];
+    Raw8<TX> res[V];
+    float dot = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      next_dy[v].get(g[v]);
+      next_x[v].get(n[v]);
+      res[v] = next_res[v];
+    }
+    if (AHEAD && t + 1 < t1) fetch(t + 1);
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -201,16 +252,11 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const TD* __restrict__ d
     for (int v = 0; v < V; ++v) {
       const int c = (v * blockDim.x + threadIdx.x) * 8;
       if (c < H) {
-        float d[8];
+        float d[8], b[8];
+        res[v].get(b);                                       // zeros without dres
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = rs * (g[v][i] - n[v][i] * mean);
-        if (dres != nullptr) {
-          float b[8];
-          load8(dres + base + c, b);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) d[i] += b[i];
-        }
-        store8(dx + base + c, d);
+        for (int i = 0; i < 8; ++i) d[i] = rs * (g[v][i] - n[v][i] * mean) + b[i];
+        store8(dx + t * H + c, d);
       }
     }
   }
@@ -223,31 +269,35 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const TD* __restrict__ d
   }
 }
 
-// dw[h] = sum over P partial rows: 16 columns per block (so that a 2048-wide row gives 128 blocks), thread row y adds
-// rows y, y + 64, ... ascending, then the 64 sums ascending.
-constexpr int kDwCols = 16, kDwRows = 64;
-__global__ void __launch_bounds__(kDwCols * kDwRows) dweight_kernel(const float* __restrict__ part, int P, int H,
-                                                                   float* __restrict__ dw) {
+// dw[h] = sum over P partial rows, 16 columns per block (so that a 2048-wide row gives 128 blocks), 4 per thread: thread row
+// y adds rows y, y + 256, ... ascending; the 8 thread rows of a warp fold by a xor butterfly; the 32 warps ascending.
+constexpr int kDwCols = 16, kDwThreads = 1024;
+__global__ void __launch_bounds__(kDwThreads) dweight_kernel(const float* __restrict__ part, int P, int H,
+                                                             float* __restrict__ dw) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float s[kDwRows][kDwCols + 1];
-  const int c = blockIdx.x * kDwCols + threadIdx.x;      // H is a multiple of 16
-  float v = 0.0f;
-  int r = threadIdx.y;
-  for (; r + 3 * kDwRows < P; r += 4 * kDwRows) {
-    const float* q = part + static_cast<long long>(r) * H + c;
-    const long long d = static_cast<long long>(kDwRows) * H;
-    const float a0 = q[0], a1 = q[d], a2 = q[2 * d], a3 = q[3 * d];
-    v = ((v + a0) + a1) + (a2 + a3);
+  __shared__ float s[32][kDwCols];
+  const int c = blockIdx.x * kDwCols + 4 * (threadIdx.x & 3);      // H is a multiple of 16
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int r = threadIdx.x >> 2; r < P; r += kDwThreads / 4) {
+    const float4 a = *reinterpret_cast<const float4*>(part + static_cast<long long>(r) * H + c);
+    v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
   }
-  for (; r < P; r += kDwRows) v += part[static_cast<long long>(r) * H + c];
-  s[threadIdx.y][threadIdx.x] = v;
+#pragma unroll
+  for (int d = 4; d <= 16; d <<= 1) {
+    v.x += __shfl_xor_sync(kFull, v.x, d);
+    v.y += __shfl_xor_sync(kFull, v.y, d);
+    v.z += __shfl_xor_sync(kFull, v.z, d);
+    v.w += __shfl_xor_sync(kFull, v.w, d);
+  }
+  if ((threadIdx.x & 31) < 4) *reinterpret_cast<float4*>(&s[threadIdx.x >> 5][4 * (threadIdx.x & 3)]) = v;
   __syncthreads();
-  if (threadIdx.y == 0) {
+  if (threadIdx.x < kDwCols) {
     float sum = 0.0f;
 #pragma unroll
-    for (int y = 0; y < kDwRows; ++y) sum += s[y][threadIdx.x];
-    dw[c] = sum;
+    for (int w = 0; w < 32; ++w) sum += s[w][threadIdx.x];
+    dw[blockIdx.x * kDwCols + threadIdx.x] = sum;
   }
 }
 
@@ -350,16 +400,6 @@ __global__ void __launch_bounds__(256) permute_fp8_kernel(const uint4* __restric
   }
 }
 
-// Threads of a row: one vector of 8 per thread up to H = 2048, then two, then four (1024 threads at H = 32768).
-struct RowShape {
-  int v, threads;
-};
-RowShape row_shape(int H) {
-  const int vecs = H / 8;
-  const int v = vecs <= 256 ? 1 : vecs <= 2048 ? 2 : 4;
-  return {v, ((vecs + v - 1) / v + 31) / 32 * 32};
-}
-
 template <typename TX, typename TR>
 cudaError_t norm_typed(const void* x, const void* res, const void* weight, int T, int H, float eps, void* res_out,
                        void* out, void* q, float* scale, float* rstd, cudaStream_t st) {
@@ -404,9 +444,10 @@ int norm_launch(const void* x, int x_f32, const void* res, int res_f32, const vo
   return check_cuda(e, "norm_kernel");
 }
 
-// Rows of one block, and so of one partial row of dw: about 4 blocks per SM for a large batch, a function of T alone
-// (not of the device), so that the order of the sum is too.
-int norm_bwd_rows(int T) { return (T + 607) / 608; }
+// Rows of one block, and so of one partial row of dw: about 2 blocks per SM for a large batch (with the next row in
+// flight that is enough, and dweight_kernel reads few partial rows), a function of T alone, not of the device, so that
+// the order of the sum is too.
+int norm_bwd_rows(int T) { return (T + 455) / 456; }
 
 int norm_bwd_launch(const void* dy, int dy_f32, const void* x, int x_f32, const void* weight, const float* rstd,
                     const void* dres, int T, int H, void* dx, float* dw, float* part, cudaStream_t st) {
@@ -425,7 +466,7 @@ int norm_bwd_launch(const void* dy, int dy_f32, const void* x, int x_f32, const 
     if (rc || dw == nullptr) return rc;
   }
   ProfScope prof("rms_norm_dweight", st);
-  return check_cuda(launch_kernel(dweight_kernel, dim3(H / kDwCols), dim3(kDwCols, kDwRows), 0, st,
+  return check_cuda(launch_kernel(dweight_kernel, dim3(H / kDwCols), dim3(kDwThreads), 0, st,
                                   static_cast<const float*>(part), P, H, dw),
                     "dweight_kernel");
 }
