@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
             if (on_w) slot[ks * S::BLOCK_SCALES + NT + j] = wv[d + ks];
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&accf_bar[acc]);
+          mbar_arrive_if(lane == 0 ? 1u : 0u, &accf_bar[acc]);
           if (++acc == S::ACC) { acc = 0; acc_phase ^= 1u; }
         }
       }
@@ -281,6 +281,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     const int half = (warp - kFirstEpiWarp) >> 2;      // warpgroup: token columns [half * HALF, +HALF)
     const int tid = q * 32 + lane;                     // thread of the warpgroup
     const int bar_id = 1 + half;
+    const uint32_t on = lane == 0 ? 1u : 0u;
     float* my_amax = s_amax + half * (4 * S::HALF);
     uint8_t* stg = staging + half * kStagingBytes;
     int acc = 0;
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
           }
           // products and scales are in registers: the buffer and its slot are free
           __syncwarp();
-          if (lane == 0) mbar_arrive(&acce_bar[acc]);
+          mbar_arrive_if(on, &acce_bar[acc]);
           if (wg_cols > 0) {
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {

@@ -12,6 +12,8 @@
 // MMA takes more than half the time of an N = 256 one); packed fma.rn.f32x2, 690 instead of 485 cycles a block.
 // SwiGLU: the 256 weight rows are 128 gate rows and the matching up rows.  A warpgroup has columns 64 half .. + 63 of
 // either 128, so that a thread holds gate and up of the same h.
+#include <type_traits>
+
 #include "fp8_gemm.cuh"
 
 namespace invmoe {
@@ -44,8 +46,7 @@ struct Fp8RowsShape {
 
 // A warp's 32 rows x 16 * PIECES bytes from registers (one row per lane) to global memory, whole rows of 64 or 128 bytes
 // at a time (PIECES lanes per row), through 2 KB of shared memory: 32 rows of 64 bytes, or twice 16 rows of 128.  The
-// 16-byte piece c of row r sits at piece c ^ (r / 2 or r) of its row, free of bank conflicts both ways.  Rows whose
-// length is not a multiple of 16 bytes are written element by element.
+// 16-byte piece c of row r sits at piece c ^ (r / 2 or r) of its row, free of bank conflicts both ways.
 template <int ELT, int PIECES>
 __device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t (&v)[4 * PIECES], uint8_t* out,
                                            long long ld_bytes, int rows_valid, long long bytes_valid, bool vec) {
@@ -53,7 +54,6 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t (&v)[4
   constexpr int ROWS = 128 / PIECES;                   // rows staged at a time
   const int lane = threadIdx.x & 31;
   auto at = [&](int r, int c) { return stage + r * (16 * PIECES) + ((c ^ (PIECES == 8 ? r & 7 : (r >> 1) & 3)) << 4); };
-  const int c = lane % PIECES;
 #pragma unroll
   for (int r0 = 0; r0 < 32; r0 += ROWS) {
     if (lane >= r0 && lane < r0 + ROWS) {
@@ -62,24 +62,23 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t (&v)[4
         *reinterpret_cast<uint4*>(at(lane - r0, k)) = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
     }
     __syncwarp();
+    if (vec) {
+      const int c = lane % PIECES;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = i * (32 / PIECES) + lane / PIECES;
-      const uint4 w = *reinterpret_cast<const uint4*>(at(r, c));
-      if (r0 + r < rows_valid && c * 16 < bytes_valid) {
-        uint8_t* d = out + (r0 + r) * ld_bytes + c * 16;
-        if (vec) {
-          *reinterpret_cast<uint4*>(d) = w;
-        } else {
-          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+      for (int i = 0; i < 4; ++i) {
+        const int r = i * (32 / PIECES) + lane / PIECES;
+        const uint4 w = *reinterpret_cast<const uint4*>(at(r, c));
+        if (r0 + r < rows_valid && c * 16 < bytes_valid) *reinterpret_cast<uint4*>(out + (r0 + r) * ld_bytes + c * 16) = w;
+      }
+    } else {
+      // rows that start anywhere: one element per lane, so that a store still covers neighbouring bytes
+      using E = std::conditional_t<ELT == 4, uint32_t, uint16_t>;
+#pragma unroll 1
+      for (int r = 0; r < ROWS && r0 + r < rows_valid; ++r) {
 #pragma unroll
-          for (int e = 0; e < 16 / ELT; ++e) {
-            if (c * 16 + e * ELT < bytes_valid) {
-              if (ELT == 4) *reinterpret_cast<uint32_t*>(d + 4 * e) = x[e];
-              else *reinterpret_cast<uint16_t*>(d + 2 * e) = static_cast<uint16_t>(x[e >> 1] >> (16 * (e & 1)));
-            }
-          }
-        }
+        for (int b = lane * ELT; b < 16 * PIECES; b += 32 * ELT)
+          if (b < bytes_valid)
+            *reinterpret_cast<E*>(out + (r0 + r) * ld_bytes + b) = *reinterpret_cast<const E*>(at(r, b >> 4) + (b & 15));
       }
     }
     __syncwarp();
@@ -223,6 +222,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     const int r_in_tile = q * 32 + lane;
     
     uint8_t* stg = ostage + ew * 32 * 64;
+    const uint32_t on = lane == 0 ? 1u : 0u;
     int acc = 0;
     uint32_t acc_phase = 0;
     int parity = 0;
@@ -259,7 +259,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
           ac.x = ac.y; ac.y = ac.z; ac.z = ac.w;
           wc0.x = wc0.y; wc0.y = wc0.z; wc0.z = wc0.w;
           wc1.x = wc1.y; wc1.y = wc1.z; wc1.z = wc1.w;
-          if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(&accf_bar[acc], acc_phase, wc));
+          if (ok && !__all_sync(0xffffffffu, mbar_test(&accf_bar[acc], acc_phase)))
+            ok = __all_sync(0xffffffffu, mbar_wait_inline(&accf_bar[acc], acc_phase, wc));
           if (ok) {
             tc_fence_after();
             if (rows_valid > 0) {
@@ -274,10 +275,9 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                 if (st < 3) {
                   tmem_ld32(tb + 32 * ((st + 1) & 1) + kWTile * ((st + 1) >> 1), r[(st + 1) & 1]);
                 } else {
-                  // everything is in registers: the buffer is free before the last products are added
-                  tc_fence_before();
-                  __syncwarp();
-                  if (lane == 0) mbar_arrive(&acce_bar[acc]);
+                  // everything is in registers: the buffer is free before the last products are added.
+                  // tcgen05.wait::ld has completed the warp's loads, so there is nothing left for a fence to order
+                  mbar_arrive_if(on, &acce_bar[acc]);
                 }
                 const float sc = st < 2 ? s0 : s1;
                 // one FFMA per product: pairs in fma.rn.f32x2 measured slower here (485 -> 690 cycles a block)
