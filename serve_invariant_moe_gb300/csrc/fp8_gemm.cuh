@@ -40,6 +40,7 @@ struct Fp8Params {
   int vec_scale;            // KB % 4 == 0 and 16-byte aligned bases: four blocks' scales in one load
   int vec_out;              // output rows are a multiple of the store vector
   int k_boxes;              // several blocks per copy (rank-3 tensor maps)
+  int bulk_out;             // whole 32-row slabs leave by bulk tensor stores
   unsigned int* status;
   unsigned long long timeout_ns;
 };

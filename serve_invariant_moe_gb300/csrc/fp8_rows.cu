@@ -35,14 +35,21 @@ struct Fp8RowsShape {
   static constexpr int STAGES = 4;
   static constexpr int ACC_COLS = 256;
   static constexpr int ACC = 2;                               // TMEM buffers
-  static constexpr int OSTAGE_BYTES = kEpiWarps * 32 * 64;
-  static constexpr int AMAX_BYTES = 2 * 2 * kWTile * 4;       // [unit parity][warpgroup][row]
+  // output staging of a warp: 32 rows of 128 bytes for bulk stores, else 2 KB (store_rows)
+  static constexpr int OSTAGE_BULK = kEpiWarps * 32 * 128;
+  static constexpr int OSTAGE_PLAIN = kEpiWarps * 32 * 64;
+  static constexpr int AMAX_BYTES = 2 * 2 * kWTile * 4;       // SwiGLU: [unit parity][warpgroup][row]
   static constexpr int BAR_BYTES = 256;
-  static constexpr int SMEM_BYTES =
-      1024 + STAGES * STAGE_BYTES + OSTAGE_BYTES + AMAX_BYTES + BAR_BYTES + 4 * (kMaxGroups + 1) + 12;
-  static_assert(SMEM_BYTES <= 232448, "shared memory");
+  static constexpr int smem_bytes(int groups, bool bulk, bool swiglu) {
+    return 1024 + STAGES * STAGE_BYTES + (bulk ? OSTAGE_BULK : OSTAGE_PLAIN) + (swiglu ? AMAX_BYTES : 0) + BAR_BYTES +
+           4 * (groups + 1) + 12;
+  }
+  static constexpr int SMEM_MAX = 232448;
   static_assert(8 * (2 * STAGES + 2 * ACC + 1) + 16 <= BAR_BYTES, "barriers");
 };
+static_assert(Fp8RowsShape::smem_bytes(kMaxGroups, false, true) <= Fp8RowsShape::SMEM_MAX &&
+                  Fp8RowsShape::smem_bytes(256, true, false) <= Fp8RowsShape::SMEM_MAX,
+              "shared memory");
 
 // A warp's 32 rows x 16 * PIECES bytes from registers (one row per lane) to global memory, whole rows of 64 or 128 bytes
 // at a time (PIECES lanes per row), through 2 KB of shared memory: 32 rows of 64 bytes, or twice 16 rows of 128.  The
@@ -88,13 +95,15 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t (&v)[4
 template <int EPI>
 __global__ void __launch_bounds__(kFp8Threads, 1)
     fp8_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
-                    const Fp8Params p) {
+                    const __grid_constant__ CUtensorMap tmO, const Fp8Params p) {
   using S = Fp8RowsShape;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ostage = ring + S::STAGES * S::STAGE_BYTES;
-  float* s_amax = reinterpret_cast<float*>(ostage + S::OSTAGE_BYTES);
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(s_amax) + S::AMAX_BYTES);
+  const bool bulk = EPI != FP8_SWIGLU && p.bulk_out != 0;
+  float* s_amax = reinterpret_cast<float*>(ostage + (bulk ? S::OSTAGE_BULK : S::OSTAGE_PLAIN));
+  uint64_t* full_bar =
+      reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(s_amax) + (EPI == FP8_SWIGLU ? S::AMAX_BYTES : 0));
   uint64_t* empty_bar = full_bar + S::STAGES;
   uint64_t* accf_bar = empty_bar + S::STAGES;
   uint64_t* acce_bar = accf_bar + S::ACC;
@@ -221,7 +230,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     const int half = ew >> 2;                          // warpgroup: weight rows 64 half .. + 63 of either CTA's 128
     const int r_in_tile = q * 32 + lane;
     
-    uint8_t* stg = ostage + ew * 32 * 64;
+    uint8_t* stg = ostage + ew * (bulk ? 32 * 128 : 32 * 64);
     const uint32_t on = lane == 0 ? 1u : 0u;
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -336,11 +345,33 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
               w[i] = *reinterpret_cast<const uint32_t*>(&b);
             }
           }
-          store_rows<ELT, 8>(stg, w, static_cast<uint8_t*>(p.out) + row0 * ld + static_cast<long long>(n) * ELT, ld,
-                             rows_valid, static_cast<long long>(p.N - n) * ELT, p.vec_out != 0);
+          if (bulk) {
+            // the previous piece has left the staging buffer
+            if (lane == 0) bulk_wait_group_read0();
+            __syncwarp();
+          }
+          if (bulk && rows_valid >= 32) {
+            // a whole slab of the group: one bulk store of 32 rows x 128 bytes, clipped at N by the map, that drains
+            // while this warp goes on
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<uint4*>(stg + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                  make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&tmO, stg, n, static_cast<int>(row0));
+              bulk_commit_group();
+            }
+          } else {
+            store_rows<ELT, 8>(stg, w, static_cast<uint8_t*>(p.out) + row0 * ld + static_cast<long long>(n) * ELT, ld,
+                               rows_valid, static_cast<long long>(p.N - n) * ELT, p.vec_out != 0);
+          }
         }
       }
     }
+    // the bulk stores this warp issued complete before the CTA exits
+    if (bulk && lane == 0) bulk_wait_group0();
   }
 
   tc_fence_before();
@@ -369,23 +400,29 @@ template <int EPI>
 int launch_rows(const Fp8Call& c, Fp8Params p, cudaStream_t st) {
   using S = Fp8RowsShape;
   const void* kernel = reinterpret_cast<const void*>(fp8_rows_kernel<EPI>);
-  p.n_blocks = EPI == FP8_SWIGLU ? c.N / kWTile : (c.N + 2 * kWTile - 1) / (2 * kWTile);
-  p.vec_out = static_cast<long long>(c.N) * (EPI == FP8_F32 ? 4 : 2) % 16 == 0;
+  constexpr int ELT = EPI == FP8_F32 ? 4 : 2;
+  constexpr bool SWIGLU = EPI == FP8_SWIGLU;
+  p.n_blocks = SWIGLU ? c.N / kWTile : (c.N + 2 * kWTile - 1) / (2 * kWTile);
+  p.vec_out = static_cast<long long>(c.N) * ELT % 16 == 0;
+  // bulk stores where a tensor map can describe the output and its staging fits beside the groups' prefix sums
+  p.bulk_out = !SWIGLU && p.vec_out && S::smem_bytes(c.G, true, false) <= S::SMEM_MAX;
+  const int smem = S::smem_bytes(c.G, p.bulk_out != 0, SWIGLU);
   long long units = 0;
   int rc = check_units(c, kWTile, p.n_blocks, &units);
-  CUtensorMap tmW, tmA;
+  CUtensorMap tmW, tmA, tmO{};
   if (rc == INVMOE_OK) rc = make_maps(c, p, kWTile, kWTile, 0, &tmW, &tmA);
+  if (rc == INVMOE_OK && p.bulk_out) rc = make_tmap_out_rows(&tmO, c.out, ELT, c.N, c.rows);
   static std::atomic<uint64_t> attr_set{0};
   static std::atomic<int> regs{0};
-  if (rc == INVMOE_OK) rc = set_smem_attr(kernel, S::SMEM_BYTES, attr_set);
+  if (rc == INVMOE_OK) rc = set_smem_attr(kernel, S::SMEM_MAX, attr_set);
   if (rc == INVMOE_OK) rc = check_launch_regs(kernel, c.name, regs);
   int sms = 0;
   if (rc == INVMOE_OK) rc = device_sm_count(&sms);
   if (rc) return rc;
-    const unsigned grid = static_cast<unsigned>(units < sms ? units : sms);
+  const unsigned grid = static_cast<unsigned>(units < sms ? units : sms);
   ProfScope prof(c.name, st);
-  return check_cuda(launch_kernel(fp8_rows_kernel<EPI>, dim3(grid), dim3(kFp8Threads), S::SMEM_BYTES, st,
-                                     tmW, tmA, p),
+  return check_cuda(launch_kernel(fp8_rows_kernel<EPI>, dim3(grid), dim3(kFp8Threads), static_cast<size_t>(smem), st, tmW,
+                                  tmA, tmO, p),
                     c.name);
 }
 

@@ -353,6 +353,22 @@ int launch_small(const GemmCall& c, cudaStream_t st) {
 
 }  // namespace
 
+// Row-major output [rows, cols] of 4- or 2-byte elements (rows a multiple of 16 bytes long) for stores of 32 rows x 128
+// bytes from 128-byte-swizzled staging.
+int make_tmap_out_rows(CUtensorMap* m, void* base, int elt, long long cols, long long rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return set_error(INVMOE_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * elt};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elt), 32};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = fn(m, elt == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(INVMOE_ERR_CUDA, "cuTensorMapEncodeTiled (output rows) failed (%d)", (int)r);
+  return INVMOE_OK;
+}
+
 // Row-major e4m3 [rows, inner] matrix; box = 128 elements (128 B, one swizzle row) x box_rows; a last block of fewer than
 // 128 columns is filled with zeros.  k_blocks > 0 (inner a multiple of 128): as a rank-3 tensor (128 elements, rows, inner /
 // 128 blocks) whose box holds that many consecutive blocks, one [box_rows][128] slice after another; blocks past the last

@@ -223,6 +223,7 @@ struct Fp8Call {
 
 int fp8_gemm_run(const Fp8Call& c, cudaStream_t st);
 int make_tmap_fp8(CUtensorMap* m, const void* base, long long inner, long long rows, int box_rows, int k_blocks);
+int make_tmap_out_rows(CUtensorMap* m, void* base, int elt, long long cols, long long rows);
 int set_smem_attr(const void* kernel, int bytes, std::atomic<uint64_t>& done);
 
 }  // namespace invmoe

@@ -34,7 +34,8 @@ __device__ __forceinline__ float key_value(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
 }
 
-__device__ __forceinline__ float sigmoid_f32(float l) { return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-l))); }
+// 1 / (1 + exp(-l)); the reciprocal is correctly rounded, so it is the division's bits for fewer instructions.
+__device__ __forceinline__ float sigmoid_f32(float l) { return __frcp_rn(__fadd_rn(1.0f, expf(-l))); }
 
 // Shift and denominator of the softmax over a row held as l[i] = logit of expert i * 32 + lane.  A row of -inf alone
 // has shift 0 and denominator 0; a row with a NaN or +inf has a NaN denominator.
