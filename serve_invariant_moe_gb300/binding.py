@@ -653,7 +653,7 @@ def add_rms_norm(x, weight, residual=None, eps=1e-6, out=True, fp8=False, residu
 
 
 def rms_norm_backward_workspace_size(T, H) -> int:
-    return int(lib().rms_norm_backward_workspace_size(T, H))
+    return marshal().rms_norm_backward_workspace_size(T, H)
 
 
 def add_rms_norm_backward(dy, x, weight, rstd, dres=None, dx=None, dweight=True, workspace=None):
@@ -677,7 +677,7 @@ def add_rms_norm_backward(dy, x, weight, rstd, dres=None, dx=None, dweight=True,
     else:
         dweight = _out(m, dweight, x, "dweight", F32_, H)
         if workspace is None:
-            workspace = m.new(x, U8_, rms_norm_backward_workspace_size(T, H))
+            workspace = m.new(x, U8_, m.rms_norm_backward_workspace_size(T, H))
         else:
             m.check(workspace, "workspace", U8_)
         nbytes = workspace.numel()

@@ -180,6 +180,17 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// rms_norm_backward_workspace_size(T, H)
+PyObject* norm_backward_bytes(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  int T = 0, H = 0;
+  if (n != 2) {
+    PyErr_SetString(PyExc_TypeError, "rms_norm_backward_workspace_size(T, H)");
+    return nullptr;
+  }
+  if (!convert(args[0], &T) || !convert(args[1], &H)) return nullptr;
+  return PyLong_FromSize_t(rms_norm_backward_workspace_size(T, H));
+}
+
 #define METHOD(name, fn) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(fn)), METH_FASTCALL, nullptr}
 #define ENTRY(name) METHOD(#name, &call<&name>)
 
@@ -192,6 +203,7 @@ PyMethodDef methods[] = {
     ENTRY(moe_router_backward),
     ENTRY(add_rms_norm),
     ENTRY(add_rms_norm_backward),
+    METHOD("rms_norm_backward_workspace_size", &norm_backward_bytes),
     ENTRY(fp8_quantize),
     ENTRY(moe_permute_rows),
     ENTRY(moe_permute_fp8),
