@@ -97,6 +97,48 @@ def test_a_rows_bits_do_not_depend_on_the_batch(M):
     assert torch.equal(part, whole[first:])
 
 
+# enough tiles for the row kernel; row lengths that its bulk stores clip, or that keep it from them, in either type
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K", [(700, 1004, 272), (700, 1000, 1040), (1301, 1003, 144), (640, 2048, 512)])
+def test_gemm_of_many_rows(M, N, K, out_dtype):
+    test_gemm_matches_64_bits(M, N, K, out_dtype)
+
+
+@pytest.mark.parametrize("M", [1, 16, 50, 128, 129, 333])
+def test_a_rows_bits_do_not_depend_on_the_kernel(M):
+    """1200 columns: 1000 rows take the row tiles, few rows the column tiles."""
+    from serve_invariant_moe_gb300 import binding
+    g = torch.Generator().manual_seed(8)
+    a, sa = rows_operand(1000, 1168, g)
+    b, sb = weight_operand(1200, 1168, g)
+    a, sa, b, sb = a.to(DEV), sa.to(DEV), b.to(DEV), sb.to(DEV)
+    for out_dtype in (torch.float32, torch.bfloat16):
+        whole = binding.fp8_gemm(a, sa, b, sb, workspace(), out_dtype=out_dtype)
+        part = binding.fp8_gemm(a[500:500 + M].contiguous(), sa[500:500 + M].contiguous(), b, sb, workspace(),
+                                out_dtype=out_dtype)
+        assert torch.equal(part, whole[500:500 + M])
+
+
+def test_outputs_of_several_streams():
+    """Calls on two streams at once, on inputs made on each: nothing is shared but read-only weights."""
+    from serve_invariant_moe_gb300 import binding
+    g = torch.Generator().manual_seed(12)
+    b, sb = (t.to(DEV) for t in weight_operand(600, 512, g))
+    inputs = [rows_operand(M, 512, g) for M in (40, 900)]
+    want = [binding.fp8_gemm(a.to(DEV), s.to(DEV), b, sb, workspace()) for a, s in inputs]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in inputs], []
+    spaces = [workspace() for _ in inputs]
+    torch.cuda.synchronize()
+    for (a, s), stream, ws in zip(inputs, streams, spaces):
+        with torch.cuda.stream(stream):
+            ad, sd = a.to(DEV), s.to(DEV)
+            got.append([binding.fp8_gemm(ad, sd, b, sb, ws) for _ in range(5)])
+    torch.cuda.synchronize()
+    for w, outs in zip(want, got):
+        assert all(torch.equal(w, o) for o in outs)
+
+
 def test_nan_and_zero_scales_stay_in_their_row():
     from serve_invariant_moe_gb300 import binding
     g = torch.Generator().manual_seed(6)
@@ -189,6 +231,23 @@ def test_grouped_down(counts, H, F):
         first += n
         W = deq_weight(w2[e], s2[e])
         assert (np.abs(y[rows] - A[rows] @ W.T) <= dot_bound(A[rows], W, F)).all()
+
+
+def test_grouped_down_of_many_experts():
+    """460 experts of 70 rows: the prefix sums of so many groups leave no room for the bulk stores' staging."""
+    from serve_invariant_moe_gb300 import binding
+    E, n, H, F = 460, 70, 64, 128
+    g = torch.Generator().manual_seed(3)
+    a, sa = rows_operand(E * n, F, g)
+    w2 = fp8_values((E, H, F), g)
+    s2 = torch.rand(E, 1, 1, generator=g) * 0.01 + 0.001
+    ws = workspace()
+    y = binding.moe_grouped_down_fp8(a.to(DEV), sa.to(DEV), plan_of([n] * E).to(DEV), w2.to(DEV), s2.to(DEV), E * n, 1, ws)
+    binding.check_status(ws)
+    A = torch.from_numpy(deq_rows(a, sa)).view(E, n, F)
+    W = w2.double() * s2.double()
+    bound = 2.0 * F * 2.0 ** -24 * torch.bmm(A.abs(), W.abs().transpose(1, 2)) + 1e-30
+    assert ((y.double().cpu().view(E, n, H) - torch.bmm(A, W.transpose(1, 2))).abs() <= bound).all()
 
 
 @pytest.mark.parametrize("T", [1, 30, 200])

@@ -92,6 +92,12 @@ def test_select(T, E, k, groups, kept, score, with_bias, renorm, scale):
     assert np.allclose(r["topk_w"].double().cpu().numpy()[ok], w[ok], rtol=5e-6, atol=1e-30)
 
 
+@pytest.mark.parametrize("score,with_bias", [("sigmoid", True), ("softmax", False)])
+@pytest.mark.parametrize("T,E,k,groups,kept", [(20, 256, 8, 4, 2), (9, 1024, 8, 4, 3), (12, 192, 6, 3, 1), (7, 320, 5, 5, 2)])
+def test_select_with_groups_of_several_warps_widths(T, E, k, groups, kept, score, with_bias):
+    test_select(T, E, k, groups, kept, score, with_bias, True, 1.0)
+
+
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 @pytest.mark.parametrize("groups,kept", [(1, 1), (4, 2)])
 def test_ties_go_to_the_lower_index(score, groups, kept):
