@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
   WaitCtl wc{s_abort, p.status, p.timeout_ns};
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       // ---------------------------------------------------------- producer
       int stage = 0;
       uint32_t phase = 0;
@@ -186,52 +186,52 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
         mbar_wait(&full_bar[s], static_cast<uint32_t>((fills - 1 - s) / S::STAGES) & 1u, drain);
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer: the whole warp, one lane issues
-    const uint32_t on = lane == 0 ? 1u : 0u;
-    const uint64_t wdesc0 = sdesc_k_sw128(smem_u32(ring));
-    const uint64_t adesc0 = sdesc_k_sw128(smem_u32(ring + KS * MT * S::W_BYTES));
-    int stage = 0;
-    uint32_t phase = 0;
-    int acc = 0;
-    uint32_t acc_phase = 0;
-    bool ok = true;
-    for (int u = blockIdx.x; ok && u < total_units; u += gridDim.x) {
-      const Fp8Unit U = fp8_unit<NT>(u, p, s_prefix, total_chunks);
-      const uint32_t idesc = idesc_e4m3_f32(WR, (U.cols + 15) & ~15);
-      for (int st = 0; st < steps; ++st) {
-        if (!probe2(&acce_bar[acc], acc_phase ^ 1u, &full_bar[stage], phase) &&
-            (!wait_warp(&acce_bar[acc], acc_phase ^ 1u, wc) || !wait_warp(&full_bar[stage], phase, wc))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint64_t so = static_cast<uint64_t>((stage * S::STAGE_BYTES) >> 4);
-        const uint32_t d0 = tmem_base + static_cast<uint32_t>(acc * S::STEP_COLS);
-        const int n = min(KS, p.KB - st * KS);
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          if (ks < n) {
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-              for (int kk = 0; kk < kFp8Block / 32; ++kk)   // K = 32 steps: 32 bytes on inside the swizzle row
-                umma_fp8_if(on, d0 + static_cast<uint32_t>((ks * MT + m) * NT),
-                            wdesc0 + so + static_cast<uint64_t>((m * KS + ks) * (S::W_BYTES >> 4)) + 2u * kk,
-                            adesc0 + so + static_cast<uint64_t>(ks * (S::A_BYTES >> 4)) + 2u * kk, idesc,
-                            kk != 0 ? 1u : 0u);
+    if (elect_one()) {
+      // ---------------------------------------------------------- MMA issuer
+      const uint64_t wdesc0 = sdesc_k_sw128(smem_u32(ring));
+      const uint64_t adesc0 = sdesc_k_sw128(smem_u32(ring + KS * MT * S::W_BYTES));
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < total_units; u += gridDim.x) {
+        const Fp8Unit U = fp8_unit<NT>(u, p, s_prefix, total_chunks);
+        const uint32_t idesc = idesc_e4m3_f32(WR, (U.cols + 15) & ~15);
+        for (int st = 0; st < steps; ++st) {
+          if (!mbar_wait(&acce_bar[acc], acc_phase ^ 1u, wc) || !mbar_wait(&full_bar[stage], phase, wc)) {
+            ok = false;
+            break;
           }
+          tc_fence_after();
+          const uint64_t so = static_cast<uint64_t>((stage * S::STAGE_BYTES) >> 4);
+          const uint32_t d0 = tmem_base + static_cast<uint32_t>(acc * S::STEP_COLS);
+          const int n = min(KS, p.KB - st * KS);
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            if (ks < n) {
+#pragma unroll
+              for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int kk = 0; kk < kFp8Block / 32; ++kk)   // K = 32 steps: 32 bytes on inside the swizzle row
+                  umma_fp8(d0 + static_cast<uint32_t>((ks * MT + m) * NT),
+                           wdesc0 + so + static_cast<uint64_t>((m * KS + ks) * (S::W_BYTES >> 4)) + 2u * kk,
+                           adesc0 + so + static_cast<uint64_t>(ks * (S::A_BYTES >> 4)) + 2u * kk, idesc,
+                           kk != 0 ? 1u : 0u);
+            }
+          }
+          umma_commit(&accf_bar[acc]);
+          umma_commit(&empty_bar[stage]);
+          if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
+          if (++acc == S::ACC) { acc = 0; acc_phase ^= 1u; }
         }
-        umma_commit_if(on, &accf_bar[acc]);
-        umma_commit_if(on, &empty_bar[stage]);
-        if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
-        if (++acc == S::ACC) { acc = 0; acc_phase ^= 1u; }
       }
+      if (!ok) *s_abort = 1;
+      // every MMA issued here has finished before the CTA releases TMEM
+      umma_commit(final_bar);
+      WaitCtl drain{nullptr, p.status, p.timeout_ns};
+      mbar_wait(final_bar, 0, drain);
     }
-    if (!ok) *s_abort = 1;
-    // every MMA issued here has finished before the CTA releases TMEM
-    umma_commit_if(on, final_bar);
-    WaitCtl drain{nullptr, p.status, p.timeout_ns};
-    wait_warp(final_bar, 0, drain);
   } else if (warp < kFirstEpiWarp) {
     // ------------------------------------------------------------ scales: thread j has token j's, threads below MT the
     // weight blocks' as well
@@ -470,6 +470,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     }
   }
 
+  __syncwarp();                                       // the elected lanes rejoin their warps
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
