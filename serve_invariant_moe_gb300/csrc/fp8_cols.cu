@@ -2,11 +2,13 @@
 //
 // Weights are the MMA's M side (MT sub-tiles of WR rows; a sub-tile lies in one scale block, so its scale is one number
 // per block of K) and tokens its N side, in multiples of 16: a group of 20 tokens costs 32 columns, not 128 rows.
-// What bounds it is reading the weights, and, for one small matrix, latency: a step of KS K blocks goes through every
-// handover at once (one copy per operand, one ring stage, one TMEM buffer, one set of scales, one wait of each role), and
-// where 256-row tiles would leave SMs without work 64-row tiles are used (8 x 4096 x 6144: 64 CTAs instead of 16).
+// What bounds it is reading the weights (64 experts of 2 x 2048 x 6144, 4 tokens: 95 us, 6.2 TB/s of DRAM), and, for one
+// small matrix, latency: a step of KS K blocks goes through every handover at once (one copy per operand, one ring stage,
+// one TMEM buffer, one set of scales, one wait of each role), and where 256-row tiles would leave SMs without work 64-row
+// tiles are used (8 x 4096 x 6144: 64 CTAs instead of 16; 8 us, of which 2 until the first block is there, 4 for twelve
+// steps and the rest launch and output; 32-row tiles on 128 CTAs: 8.5).
 //   * warp 0: one thread copies; with K % 128 == 0 the KS blocks of a box come in one rank-3 copy;
-//   * warp 1: the MMAs, 4 K = 32 steps per block and sub-tile, each block into columns of its own;
+//   * warp 1: one thread issues the MMAs, 4 K = 32 steps per block and sub-tile, each block into columns of its own;
 //   * warps 2 and 3: the scales, from global memory four blocks ahead, into the slot of the TMEM buffer they belong to
 //     (its barrier counts the MMAs' commit and these two warps);
 //   * two warpgroups, each with half of the token columns and all lanes.  TMEM is read in the 16x256b shape: a thread
@@ -504,24 +506,22 @@ int launch_cols(const Fp8Call& c, Fp8Params p, cudaStream_t st) {
 
 template <int EPI>
 int launch_plain(const Fp8Call& c, const Fp8Params& p, int nt, bool small, cudaStream_t st) {
-  if (small) {
-    if (nt == 16) return launch_cols<1, 64, 16, 4, EPI>(c, p, st);
-    if (nt == 32) return launch_cols<1, 64, 32, 4, EPI>(c, p, st);
-    return launch_cols<1, 64, 64, 2, EPI>(c, p, st);
-  }
-  if (nt == 16) return launch_cols<2, 128, 16, 2, EPI>(c, p, st);
-  if (nt == 32) return launch_cols<2, 128, 32, 1, EPI>(c, p, st);
-  return launch_cols<2, 128, 64, 1, EPI>(c, p, st);
+  if (nt == 64) return launch_cols<1, 64, 64, 2, EPI>(c, p, st);
+  if (small)
+    return nt == 16 ? launch_cols<1, 64, 16, 4, EPI>(c, p, st) : launch_cols<1, 64, 32, 4, EPI>(c, p, st);
+  return nt == 16 ? launch_cols<2, 128, 16, 2, EPI>(c, p, st) : launch_cols<2, 128, 32, 1, EPI>(c, p, st);
 }
 
 }  // namespace
 
 // Which kernel and tile: by the rows of a group (all rows of a dense call; the average, half as much again for the spread
 // around it, of a grouped one) and by what fills the machine.
-//   * at most 64 rows: columns, in 16, 32 or 64; 64-row tiles of the weights where 256-row tiles would not give every SM
-//     one (8 x 4096 x 6144: 14 us against 26);
-//   * more: the row tiles, unless 64-row tiles of the weights still fit in one wave (128 x 4096 x 6144: 18 us against 29
-//     on 16 row tiles; 192 x 4096 x 6144: two waves, 31 against 29).
+//   * at most 64 rows: columns, in 16, 32 or 64.  With 16 or 32 the tile is 256 weight rows (64 experts of 6144 x 2048, 4
+//     tokens: 49.7 us, with 64-row tiles 51.5), or 64 where that would not give every SM one (8 x 4096 x 6144: 8 us); with
+//     64, where a step holds fewer blocks of the larger tile, 64 rows (256 tokens for those experts: 143 us against 156);
+//   * more: the row tiles (512 tokens for those experts: 154 us against 210 in columns), unless the 64-row tiles are done
+//     in two waves, when 128-row tiles leave most SMs idle (128 x 4096 x 6144: 12 us against 26, 256 rows: 20 against 26,
+//     320 rows, three waves: 28 against 26).
 int fp8_gemm_run(const Fp8Call& c, cudaStream_t st) {
   if (c.rows == 0) return INVMOE_OK;
   Fp8Params p{};
@@ -560,7 +560,7 @@ int fp8_gemm_run(const Fp8Call& c, cudaStream_t st) {
   if (rc == INVMOE_OK) rc = check_units(c, nt, (c.N + 63) / 64, &units64);
   if (rc == INVMOE_OK) rc = device_sm_count(&sms);
   if (rc) return rc;
-  if (rows > 64 && units64 > sms) return fp8_rows_run(c, p, st);
+  if (rows > 64 && units64 > 2 * sms) return fp8_rows_run(c, p, st);
   const bool small = units256 < sms;
   return c.out_kind == FP8_OUT_F32 ? launch_plain<FP8_F32>(c, p, nt, small, st)
                                    : launch_plain<FP8_BF16>(c, p, nt, small, st);
