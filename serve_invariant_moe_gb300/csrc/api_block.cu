@@ -41,7 +41,7 @@ int check_grouped(int T, int H, int E, int k, int F) {
   REQUIRE(H % 16 == 0, INVMOE_ERR_UNSUPPORTED_SHAPE, "H=%d is not a multiple of 16", H);
   REQUIRE(F % 128 == 0, INVMOE_ERR_UNSUPPORTED_SHAPE, "F=%d is not a multiple of 128", F);
   REQUIRE(static_cast<long long>(T) * k <= 0x7fffffffLL, INVMOE_ERR_UNSUPPORTED_SHAPE, "T * k exceeds 2^31 - 1");
-  REQUIRE(2LL * F * E <= 0x7fffffffLL && static_cast<long long>(H) * E <= 0x7fffffffLL, INVMOE_ERR_UNSUPPORTED_SHAPE,
+  REQUIRE(2LL * F * E <= 0x7fffff00LL && static_cast<long long>(H) * E <= 0x7fffff00LL, INVMOE_ERR_UNSUPPORTED_SHAPE,
           "too many weight rows");
   return INVMOE_OK;
 }
@@ -74,6 +74,7 @@ int moe_route_select(const float* logits, const float* bias, int T, int E, int k
     REQUIRE_PTR(workspace);
     REQUIRE(ws_bytes >= kStatusBytes + route_ws(T, E), INVMOE_ERR_WORKSPACE_TOO_SMALL, "workspace too small");
     REQUIRE_ALIGNED(workspace);
+    REQUIRE(static_cast<long long>(T) * k <= 0x7fffffffLL, INVMOE_ERR_UNSUPPORTED_SHAPE, "T * k exceeds 2^31 - 1");
   }
   if (T == 0) {
     if (plan == nullptr) return INVMOE_OK;
@@ -149,7 +150,7 @@ int add_rms_norm(const void* x, int x_type, const void* residual, int residual_t
 size_t rms_norm_backward_workspace_size(int T, int H) {
   if (T <= 0 || H <= 0) return kStatusBytes;
   const int rows = norm_bwd_rows(T);
-  return kStatusBytes + align_up(static_cast<size_t>((T + rows - 1) / rows) * H * sizeof(float), 256);
+  return kStatusBytes + align_up(static_cast<size_t>((T - 1) / rows + 1) * H * sizeof(float), 256);
 }
 
 int add_rms_norm_backward(const void* dy, int dy_type, const void* x, int x_type, const void* weight,
@@ -218,7 +219,7 @@ int fp8_gemm(const void* a, const float* a_scale, const void* b, const float* b_
   if (rc) return rc;
   REQUIRE(M >= 0 && N > 0 && K > 0, INVMOE_ERR_INVALID_ARG, "need M >= 0, N, K > 0");
   REQUIRE(K % 16 == 0, INVMOE_ERR_UNSUPPORTED_SHAPE, "K=%d is not a multiple of 16", K);
-  REQUIRE(N <= 0x7fffff00, INVMOE_ERR_UNSUPPORTED_SHAPE, "N=%d is too large", N);
+  REQUIRE(N <= 0x7fffff00 && K <= 0x7fffff00, INVMOE_ERR_UNSUPPORTED_SHAPE, "N=%d or K=%d is too large", N, K);
   REQUIRE_PTR(workspace);
   REQUIRE(ws_bytes >= kStatusBytes, INVMOE_ERR_WORKSPACE_TOO_SMALL, "workspace too small");
   if (M == 0) return INVMOE_OK;

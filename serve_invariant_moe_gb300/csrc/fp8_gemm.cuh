@@ -160,14 +160,15 @@ __device__ __forceinline__ Fp8Unit fp8_unit(int u, const Fp8Params& p, const int
 template <int CH>
 __device__ __forceinline__ void prefix_chunks(const Fp8Params& p, int* prefix, int* total, int lane) {
   if (p.G == 0) {
-    if (lane == 0) *total = (p.M + CH - 1) / CH;
+    if (lane == 0) *total = (p.M - 1) / CH + 1;
     return;
   }
+  auto chunks = [](int n) { return n / CH + (n % CH != 0); };
   const int per = (p.G + 31) / 32;
   const int g0 = lane * per;
   int local = 0;
   for (int i = 0; i < per; ++i)
-    if (g0 + i < p.G) local += (__ldg(p.counts + g0 + i) + CH - 1) / CH;
+    if (g0 + i < p.G) local += chunks(__ldg(p.counts + g0 + i));
   int incl = local;
   for (int d = 1; d < 32; d <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, incl, d);
@@ -177,7 +178,7 @@ __device__ __forceinline__ void prefix_chunks(const Fp8Params& p, int* prefix, i
   for (int i = 0; i < per; ++i)
     if (g0 + i < p.G) {
       prefix[g0 + i] = run;
-      run += (__ldg(p.counts + g0 + i) + CH - 1) / CH;
+      run += chunks(__ldg(p.counts + g0 + i));
     }
   if (lane == 31) {
     prefix[p.G] = incl;
@@ -190,7 +191,8 @@ inline int check_units(const Fp8Call& c, int chunk, int n_blocks, long long* uni
   const long long chunks = c.G > 0 ? static_cast<long long>(c.rows) / chunk + (c.rows < c.G ? c.rows : c.G)
                                    : (static_cast<long long>(c.rows) + chunk - 1) / chunk;
   *units = chunks * n_blocks;
-  if (*units > 0x7fffffffLL) return set_error(INVMOE_ERR_UNSUPPORTED_SHAPE, "%s: too many tiles for one launch", c.name);
+  // below 2^31 by more than a grid, so that a CTA's unit index cannot pass it either
+  if (*units > 0x7fff0000LL) return set_error(INVMOE_ERR_UNSUPPORTED_SHAPE, "%s: too many tiles for one launch", c.name);
   return INVMOE_OK;
 }
 

@@ -447,11 +447,11 @@ int norm_launch(const void* x, int x_f32, const void* res, int res_f32, const vo
 // Rows of one block, and so of one partial row of dw: about 2 blocks per SM for a large batch (with the next row in
 // flight that is enough, and dweight_kernel reads few partial rows), a function of T alone, not of the device, so that
 // the order of the sum is too.
-int norm_bwd_rows(int T) { return (T + 455) / 456; }
+int norm_bwd_rows(int T) { return (T - 1) / 456 + 1; }
 
 int norm_bwd_launch(const void* dy, int dy_f32, const void* x, int x_f32, const void* weight, const float* rstd,
                     const void* dres, int T, int H, void* dx, float* dw, float* part, cudaStream_t st) {
-  const int rows = norm_bwd_rows(T), P = (T + rows - 1) / rows;
+  const int rows = norm_bwd_rows(T), P = (T - 1) / rows + 1;
   {
     ProfScope prof("rms_norm_bwd", st);
     cudaError_t e;
@@ -489,7 +489,7 @@ int quantize_launch(const void* x, int x_f32, long long banks, int rows, int col
                                             static_cast<const __nv_bfloat16*>(x), total, cols, nb, qq, scale),
                       "quant_rows_kernel");
   }
-  const int rb = (rows + kFp8Block - 1) / kFp8Block;
+  const int rb = (rows - 1) / kFp8Block + 1;
   const long long blocks = banks * rb * nb;
   if (blocks > 0x7fffffffLL) return set_error(INVMOE_ERR_UNSUPPORTED_SHAPE, "too many blocks for one launch");
   const dim3 g(static_cast<unsigned>(blocks));

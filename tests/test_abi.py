@@ -160,3 +160,14 @@ def test_block_binding_refuses_host_tensors():
     q = x.to(torch.float8_e4m3fn)
     with pytest.raises(ValueError, match="CUDA tensor"):
         binding.fp8_gemm(q, x, q, x, torch.zeros(256, dtype=torch.uint8))
+
+
+def test_block_sizes_near_2_31_do_not_wrap():
+    import ctypes
+    from serve_invariant_moe_gb300 import _lib
+    lib, null, ws, big = _lib.lib(), None, ctypes.c_void_p(256), 2 ** 31 - 1
+    # 456 partial rows for any number of tokens
+    assert lib.rms_norm_backward_workspace_size(big, 64) == 256 + 456 * 64 * 4
+    assert lib.fp8_gemm(null, null, null, null, 4, 64, 2 ** 31 - 16, null, 0, ws, 4096, null) == -2
+    assert lib.moe_grouped_down_fp8(null, null, null, null, null, 4, 2 ** 31 - 16, 1, 1, 128, null, ws, 4096, null) == -2
+    assert lib.moe_route_select(null, null, big, 8, 2, 0, 1, 1, 1, 1.0, null, null, ws, ws, 2 ** 62, null) == -2
