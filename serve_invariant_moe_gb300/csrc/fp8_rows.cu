@@ -3,13 +3,14 @@
 // Tokens are the MMA's M side: a CTA computes 128 token rows x 256 weight rows (one N = 256 MMA per K = 32
 // step).  A thread holds one token row, so its scale is one number per block, read from global memory four blocks ahead:
 // no shared memory on the scaling path, where the kernel of few tokens reads a scale for every column.
-// What bounds it is neither the loads nor the tensor cores (without the scaling 8192 x 4096 x 6144 takes 129 us) but the
-// handover of the products: 128 x 256 fp32 per block through TMEM and 256 FFMA issue cycles per scheduler, with two TMEM
-// buffers to hide a commit, a wait and a release behind.  So a buffer is released as soon as its last columns are in
-// registers, and the issuing warp runs converged (see umma_fp8_if).
-// Measured and not kept (8192 x 4096 x 6144, 191 us): CTA pairs with 256 x 256 tiles, 183 us, but 663 instead of 549 us
-// for 64 experts of about 256 rows, because the tiles are twice as high; four buffers of 128 columns, 260 us (an N = 128
-// MMA takes more than half the time of an N = 256 one); packed fma.rn.f32x2, 690 instead of 485 cycles a block.
+// 8192 x 4096 x 6144 takes 169 us (2.44 PFLOP/s), 64 experts' gate and up of 2048 x 6144 with about 256 rows each 425 us.
+// What bounds it is the handover of the products, 128 x 256 fp32 per block through two TMEM buffers: with the waits and
+// arrives alone the dense product takes 134 us (a block is then 769 cycles, what its 96 KB of copies and operand reads take
+// of shared memory), with the loads from TMEM 147, with the 256 FFMA issue cycles per scheduler 169.  So a buffer is
+// released as soon as its last columns are in registers, arrives are predicated, and one elected thread issues.
+// Measured and not kept: CTA pairs with 256 x 256 tiles, 167 us, but 483 for those 64 experts, because the tiles are twice
+// as high; loads of 16 columns, 175, or two loads of 32 at once, no change; blocks unrolled by two, 188; the last columns
+// added behind the next block's wait, which spills, 229; packed fma.rn.f32x2, 690 instead of 485 cycles a block.
 // SwiGLU: the 256 weight rows are 128 gate rows and the matching up rows.  A warpgroup has columns 64 half .. + 63 of
 // either 128, so that a thread holds gate and up of the same h.
 #include <type_traits>
