@@ -6,10 +6,11 @@
 //   * without a bias the choice is by logit (both scores increase with it), so no score is computed for the losers;
 //   * with a bias the choice is by score + bias, one fp32 addition; a group's value is the sum of its two largest;
 //   * the softmax denominator is summed in fixed point (steps of 2^-42, integers), exact whatever the order.
-// What bounds it for many tokens is instruction issue, not the row it reads (65536 x 256 in 8 groups, top 4 and 8: 86 us,
-// 0.8 TB/s): a sigmoid per expert (8 per lane), the groups' maxima (two warp reductions each) and the k rounds.  8192
-// tokens take 16 us with groups, 11.5 without; 4096 x 128 softmax 9, where half is launch.  A warp per token, not a
-// thread: the row comes in whole lines, and every reduction is one instruction.
+// What bounds it for many tokens is instruction issue, not the row it reads (65536 x 256 in 8 groups, top 4 and 8: 76 us,
+// 0.9 TB/s): a sigmoid per expert (8 per lane), the groups' maxima (two warp reductions each) and the k rounds, of which
+// the searches were half (looking through the lane's experts every time one is lost: 86 us).  8192 tokens take 14.5 us
+// with groups, 10.6 without; 4096 x 128 softmax 9, where half is launch.  A warp per token, not a thread: the row comes in
+// whole lines, and every reduction is one instruction.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -41,13 +42,13 @@ __device__ __forceinline__ float key_value(uint32_t key) {
 // 1 / (1 + exp(-l)); the reciprocal is correctly rounded, so it is the division's bits for fewer instructions.
 __device__ __forceinline__ float sigmoid_f32(float l) { return __frcp_rn(__fadd_rn(1.0f, expf(-l))); }
 
-// Shift and denominator of the softmax over a row held as l[i] = logit of expert i * 32 + lane.  A row of -inf alone
-// has shift 0 and denominator 0; a row with a NaN or +inf has a NaN denominator.
+// Shift and denominator of the softmax over a row held as l[i] = logit of expert i * 32 + lane; KEEP: l[i] becomes
+// exp(logit - shift).  A row of -inf alone has shift 0 and denominator 0; a row with a NaN or +inf has a NaN denominator.
 struct SoftmaxStats {
   float shift, total;
 };
-template <int EPL>
-__device__ __forceinline__ SoftmaxStats softmax_stats(const float (&l)[EPL], int E, int lane) {
+template <int EPL, bool KEEP>
+__device__ __forceinline__ SoftmaxStats softmax_stats(float (&l)[EPL], int E, int lane) {
   uint32_t best = 0u;
 #pragma unroll
   for (int i = 0; i < EPL; ++i)
@@ -62,6 +63,7 @@ __device__ __forceinline__ SoftmaxStats softmax_stats(const float (&l)[EPL], int
   for (int i = 0; i < EPL; ++i) {
     if (i * 32 + lane < E) {
       const float e = expf(__fsub_rn(l[i], s.shift));
+      if (KEEP) l[i] = e;
       if (e <= 1.0f) {
         const float t = __fmul_rn(e, 2097152.0f);
         const unsigned h = static_cast<unsigned>(t);
@@ -80,9 +82,12 @@ __device__ __forceinline__ SoftmaxStats softmax_stats(const float (&l)[EPL], int
   return s;
 }
 
-// p = exp(l - shift) / total; an empty row's scores are 0.
+// p = exp(l - shift) / total of an e = exp(l - shift); an empty row's scores are 0.
+__device__ __forceinline__ float softmax_share(float e, const SoftmaxStats& s) {
+  return s.total == 0.0f ? 0.0f : __fdiv_rn(e, s.total);
+}
 __device__ __forceinline__ float softmax_score(float l, const SoftmaxStats& s) {
-  return s.total == 0.0f ? 0.0f : __fdiv_rn(expf(__fsub_rn(l, s.shift)), s.total);
+  return softmax_share(expf(__fsub_rn(l, s.shift)), s);
 }
 
 struct SelectParams {
@@ -94,9 +99,13 @@ struct SelectParams {
   float* w;
 };
 
-// Up to E = 256 at most 32 registers a thread: a batch of 8192 tokens is then resident at once (64 warps per SM).
+// Blocks per SM that the registers must leave room for: up to E = 256 at most 32 registers a thread, so that a batch of
+// 8192 tokens is resident at once (64 warps per SM); above, 64 (8192 x 1024: 51 us with the 83 to 111 the compiler would
+// take, 38.5 with 64).
+constexpr int select_blocks(int epl) { return epl <= 8 ? 8 : 4; }
+
 template <int EPL, bool SOFTMAX, bool GROUPS>
-__global__ void __launch_bounds__(kSelThreads, EPL <= 8 ? 8 : 1) select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kSelThreads, select_blocks(EPL)) select_kernel(const SelectParams p) {
   pdl_wait();
   pdl_trigger();
   extern __shared__ uint32_t sm_keys[];      // GROUPS: per warp E choice keys, padded by one word per 32
@@ -108,14 +117,15 @@ __global__ void __launch_bounds__(kSelThreads, EPL <= 8 ? 8 : 1) select_kernel(c
 #pragma unroll
   for (int i = 0; i < EPL; ++i) l[i] = i * 32 + lane < p.E ? __ldg(row + i * 32 + lane) : -INFINITY;
   SoftmaxStats st{0.0f, 1.0f};
-  if (SOFTMAX) st = softmax_stats<EPL>(l, p.E, lane);
-  uint32_t key[EPL];                          // 0: no such expert, taken, or its group is not kept
+  if (SOFTMAX) st = softmax_stats<EPL, false>(l, p.E, lane);
+  uint32_t key[EPL];                          // 0: no such expert, or its group is not kept
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = i * 32 + lane;
     key[i] = 0u;
     if (e < p.E) {
       float c = l[i];
+      // (a second exp, not one kept from the statistics: with 1024 experts those registers would spill)
       if (p.bias != nullptr) c = __fadd_rn(SOFTMAX ? softmax_score(c, st) : sigmoid_f32(c), __ldg(p.bias + e));
       key[i] = order_key(c);
     }
@@ -189,29 +199,55 @@ __global__ void __launch_bounds__(kSelThreads, EPL <= 8 ? 8 : 1) select_kernel(c
       }
     }
   }
-  // k rounds: the warp's largest key, the lowest expert that has it; only the lane that loses its best looks again
-  uint32_t best = 0u;
-  int best_i = 0;
-  auto look = [&]() {
-    best = 0u;
+  // k rounds: the warp's largest key, the lowest expert that has it.  A lane keeps its two largest keys at hand and looks
+  // through its experts again only when it has lost both (with 8 choices over 32 lanes about once a token; the vote makes
+  // that a branch of the warp).  What it has lost are the first of its keys in the order (largest, lowest expert), so a look
+  // begins behind the last of them.
+  uint32_t best = 0u, second = 0u;
+  int best_i = 0, second_i = 0;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        best_i = i;
-      }
-  };
-  look();
+  for (int i = 0; i < EPL; ++i) {
+    if (key[i] > best) {
+      second = best;
+      second_i = best_i;
+      best = key[i];
+      best_i = i;
+    } else if (key[i] > second) {
+      second = key[i];
+      second_i = i;
+    }
+  }
+  bool spare = true;                          // `second` is still there
   int my_e = 0;
   for (int j = 0; j < p.k; ++j) {
     const uint32_t top = __reduce_max_sync(kFull, best);
     const int e = static_cast<int>(__reduce_min_sync(kFull, best == top ? static_cast<uint32_t>(best_i * 32 + lane) : kFull));
     if (lane == j) my_e = e;
-    if ((e & 31) == lane) {
+    const bool mine = (e & 31) == lane;
+    if (__any_sync(kFull, mine && !spare)) {
+      if (mine) {
+        const uint32_t lost = best;
+        const int lost_i = best_i;
+        best = second = 0u;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (i == best_i) key[i] = 0u;
-      look();
+        for (int i = 0; i < EPL; ++i) {
+          const uint32_t v = key[i] < lost || (key[i] == lost && i > lost_i) ? key[i] : 0u;
+          if (v > best) {
+            second = best;
+            second_i = best_i;
+            best = v;
+            best_i = i;
+          } else if (v > second) {
+            second = v;
+            second_i = i;
+          }
+        }
+        spare = true;
+      }
+    } else if (mine) {
+      best = second;
+      best_i = second_i;
+      spare = false;
     }
   }
   float s = 0.0f;
@@ -236,10 +272,12 @@ __global__ void __launch_bounds__(kSelThreads, EPL <= 8 ? 8 : 1) select_kernel(c
 //   sigmoid           dl_j = ds_j s_j (1 - s_j), other experts 0
 //   softmax           dl_e = p_e (ds_e - sum_j ds_j p_j), ds_e = 0 for experts not chosen; renormalised, the sum is 0
 //                     and only the chosen experts have a gradient
-// One warp per token; an entry of topk_idx outside [0, E) takes no part.  Bound by writing the row (8192 x 256: 8.4 MB,
-// 5.2 us a call, about the launch's cost): each lane walks the k choices once and keeps those that fall to its columns.
+// One warp per token; an entry of topk_idx outside [0, E) takes no part.  Bound by writing the row, which is written as if
+// nothing were chosen and then corrected at the k chosen entries (8192 x 1024: 7.8 us for 34 MB, 11.5 when every column was
+// compared with every choice; 8192 x 256: about the cost of a launch); the plain softmax by its exponentials and
+// divisions (8192 x 1024: 25 us).
 template <int EPL, bool SOFTMAX>
-__global__ void __launch_bounds__(kSelThreads)
+__global__ void __launch_bounds__(kSelThreads, EPL <= 8 ? 5 : 4)
     select_bwd_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx, const float* __restrict__ dw,
                       int T, int E, int k, int renorm, float scale, float* __restrict__ dl,
                       __nv_bfloat16* __restrict__ dl_bf16) {
@@ -249,12 +287,13 @@ __global__ void __launch_bounds__(kSelThreads)
   const long long t = static_cast<long long>(blockIdx.x) * (kSelThreads / 32) + (threadIdx.x >> 5);
   if (t >= T) return;
   const float* row = logits + t * E;
+  // only a softmax that is not renormalised has a gradient for the experts not chosen, and needs every score in it
   SoftmaxStats st{0.0f, 1.0f};
   float l[SOFTMAX ? EPL : 1];
   if constexpr (SOFTMAX) {
 #pragma unroll
     for (int i = 0; i < EPL; ++i) l[i] = i * 32 + lane < E ? __ldg(row + i * 32 + lane) : -INFINITY;
-    st = softmax_stats<EPL>(l, E, lane);
+    st = softmax_stats<EPL, true>(l, E, lane);
   }
   int e = -1;
   float s = 0.0f, d = 0.0f;
@@ -274,28 +313,35 @@ __global__ void __launch_bounds__(kSelThreads)
     dot = fmaf(__shfl_sync(kFull, d, j), sj, dot);
   }
   if (renorm) d = sum == 0.0f ? 0.0f : __fdiv_rn(d - __fdiv_rn(dot, sum), sum);
-  // value of a chosen expert's entry beyond what every expert gets
+  // value of a chosen expert's entry beyond what every expert gets; an expert chosen twice gets both
   const float mine = SOFTMAX ? __fmul_rn(d, s) : d * s * (1.0f - s);
   const float all = SOFTMAX && !renorm ? dot : 0.0f;
-  float v[EPL];
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) v[i] = 0.0f;
+  float v = 0.0f;
   for (int j = 0; j < k; ++j) {
     const int ej = __shfl_sync(kFull, e, j);
     const float vj = __shfl_sync(kFull, mine, j);
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (ej == i * 32 + lane) v[i] += vj;
+    if (ej == e) v += vj;
   }
+  if constexpr (SOFTMAX)
+    if (!renorm) v -= __fmul_rn(all, s);
+  // the row as if nothing were chosen, then the chosen entries: the warp's stores to one address are in this order
+  float* out = dl != nullptr ? dl + t * E : nullptr;
+  __nv_bfloat16* out_bf16 = dl_bf16 != nullptr ? dl_bf16 + t * E : nullptr;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int c = i * 32 + lane;
     if (c < E) {
+      float g = 0.0f;
       if constexpr (SOFTMAX)
-        if (!renorm) v[i] -= __fmul_rn(all, softmax_score(l[i], st));
-      if (dl != nullptr) dl[t * E + c] = v[i];
-      if (dl_bf16 != nullptr) dl_bf16[t * E + c] = __float2bfloat16_rn(v[i]);
+        if (!renorm) g = __fsub_rn(0.0f, __fmul_rn(all, softmax_share(l[i], st)));
+      if (out != nullptr) out[c] = g;
+      if (out_bf16 != nullptr) out_bf16[c] = __float2bfloat16_rn(g);
     }
+  }
+  __syncwarp();
+  if (e >= 0) {
+    if (out != nullptr) out[e] = v;
+    if (out_bf16 != nullptr) out_bf16[e] = __float2bfloat16_rn(v);
   }
 }
 
