@@ -496,8 +496,9 @@ def moe_route_backward(x, w_router, topk_idx, topk_w, dgate, dxp, plan, workspac
 #
 # These calls of a few tokens are bound by the host, so their checks, allocations and
 # argument conversions are C functions (csrc/marshal.cpp): m.check(tensor, name, type,
-# *shape) refuses as _req does, m.new(like, type, *shape) allocates, and m.<entry point>
-# takes tensors (or None) for pointers and adds the current stream.
+# *shape) refuses as _req does, m.new(like, type, *shape) allocates, m.<entry point>
+# takes tensors (or None) for pointers and adds the current stream, and the norm's functions
+# are there as a whole.
 # ---------------------------------------------------------------------------
 
 FP8 = torch.float8_e4m3fn
@@ -630,26 +631,8 @@ def add_rms_norm(x, weight, residual=None, eps=1e-6, out=True, fp8=False, residu
     x [T, H] and residual [T, H] bf16 or fp32, weight [H] bf16.  ``out`` (bf16): a tensor to fill, True or False;
     ``fp8``: also the e4m3 row with a scale per 128 columns (into q and scale if given).  ``residual_out`` receives r
     in the residual's type (it may be ``residual`` itself; allocated if not given)."""
-    m = marshal()
-    T, H = _dims(x, "x")
-    xt, rt = _type(x, "x"), 0
-    m.check(x, "x", xt, T, H)
-    m.check(weight, "weight", BF16_, H)
-    if residual is not None:
-        rt = _type(residual, "residual")
-        m.check(residual, "residual", rt, T, H)
-        residual_out = _out(m, residual_out, x, "residual_out", rt, T, H)
-    elif residual_out is not None:
-        raise ValueError("residual_out needs a residual")
-    out = None if out is False else _out(m, out, x, "out", BF16_, T, H)
-    if fp8:
-        q = _out(m, q, x, "q", FP8_, T, H)
-        scale = _out(m, scale, x, "scale", F32_, T, _blocks(H))
-    else:
-        q = scale = None
-    rstd = _out(m, rstd, x, "rstd", F32_, T)
-    check(m.add_rms_norm(x, xt, residual, rt, weight, T, H, eps, residual_out, out, q, scale, rstd))
-    return {"residual": residual_out, "out": out, "q": q, "scale": scale, "rstd": rstd}
+    r = marshal().norm(x, weight, residual, eps, out, fp8, residual_out, q, scale, rstd)
+    return r if r.__class__ is dict else check(r)
 
 
 def rms_norm_backward_workspace_size(T, H) -> int:
@@ -661,28 +644,8 @@ def add_rms_norm_backward(dy, x, weight, rstd, dres=None, dx=None, dweight=True,
 
     dict(dx [T, H] in x's type: the gradient of that row, so of both summands; dweight [H] fp32 or None).
     dy bf16 or fp32; dres: the gradient that reaches the row from the residual stream; dx may be dres."""
-    m = marshal()
-    T, H = _dims(x, "x")
-    xt, dt = _type(x, "x"), _type(dy, "dy")
-    m.check(x, "x", xt, T, H)
-    m.check(dy, "dy", dt, T, H)
-    m.check(weight, "weight", BF16_, H)
-    m.check(rstd, "rstd", F32_, T)
-    if dres is not None:
-        m.check(dres, "dres", xt, T, H)
-    dx = _out(m, dx, x, "dx", xt, T, H)
-    nbytes = 0
-    if dweight is False:
-        dweight = None
-    else:
-        dweight = _out(m, dweight, x, "dweight", F32_, H)
-        if workspace is None:
-            workspace = m.new(x, U8_, m.rms_norm_backward_workspace_size(T, H))
-        else:
-            m.check(workspace, "workspace", U8_)
-        nbytes = workspace.numel()
-    check(m.add_rms_norm_backward(dy, dt, x, xt, weight, rstd, dres, T, H, dx, dweight, workspace, nbytes))
-    return {"dx": dx, "dweight": dweight}
+    r = marshal().norm_backward(dy, x, weight, rstd, dres, dx, dweight, workspace)
+    return r if r.__class__ is dict else check(r)
 
 
 def fp8_quantize(x, block_rows=1, q=None, scale=None):
