@@ -245,6 +245,24 @@ def test_backward_of_masked_rows_and_bad_indices():
             assert torch.equal(d[1:2], one)
 
 
+@pytest.mark.parametrize("score,renorm", [("sigmoid", False), ("softmax", False), ("softmax", True)])
+def test_backward_of_an_expert_chosen_twice(score, renorm):
+    """Its entry is the sum of both gradients.  With equal dw the renormalised ones are 0 up to rounding, the others
+    dw (2 ds/dl): the bound is 16 roundings of the sum of the absolute terms, which are at most 2."""
+    from serve_invariant_moe_gb300 import binding
+    l = torch.randn(5, 40, generator=torch.Generator().manual_seed(6))
+    idx = torch.tensor([[3, 3], [0, 39], [33, 33], [7, 8], [1, 1]], dtype=torch.int32)
+    dw = torch.ones(5, 2)
+    got = binding.moe_route_select_backward(l.to(DEV), idx.to(DEV), dw.to(DEV), score, renorm).double().cpu()
+    x = l.double().requires_grad_(True)
+    sc = torch.sigmoid(x) if score == "sigmoid" else torch.softmax(x, 1)
+    w = sc.gather(1, idx.long())
+    if renorm:
+        w = w / w.sum(1, keepdim=True)
+    w.sum().backward()
+    assert (got - x.grad).abs().max() <= 16 * 2 * 2.0 ** -24
+
+
 def test_refusals():
     from serve_invariant_moe_gb300 import binding
     from serve_invariant_moe_gb300._lib import InvmoeError
