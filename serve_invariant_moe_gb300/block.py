@@ -120,7 +120,8 @@ class Fp8MoEBlock:
     def decode(self, x, residual, out_bf16=None):
         """One token per request: as prefill, for a bf16 residual, on buffers kept for the largest batch so far.
 
-        Returns views of those buffers: (out [B, H] fp32, residual [B, H] bf16), valid until the next call."""
+        Returns views of those buffers: (out [B, H] fp32, residual [B, H] bf16), valid until the next call.  The calls
+        share the buffers, so they belong on one stream."""
         B = x.shape[0]
         if self._bufs is None or self._bufs["T"] < B:
             self._bufs = self._alloc(max(B, 1), True)
