@@ -149,7 +149,7 @@ int add_rms_norm(const void* x, int x_type, const void* residual, int residual_t
 
 size_t rms_norm_backward_workspace_size(int T, int H) {
   if (T <= 0 || H <= 0) return kStatusBytes;
-  const int rows = norm_bwd_rows(T);
+  const int rows = norm_bwd_rows(T, H);
   return kStatusBytes + align_up(static_cast<size_t>((T - 1) / rows + 1) * H * sizeof(float), 256);
 }
 

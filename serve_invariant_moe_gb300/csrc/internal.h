@@ -195,7 +195,7 @@ int select_bwd_launch(const float* logits, const int32_t* idx, const float* dw, 
 // ---------------------------------------------------------------- norm and e4m3
 int norm_launch(const void* x, int x_f32, const void* res, int res_f32, const void* weight, int T, int H, float eps,
                 void* res_out, void* out, void* q, float* scale, float* rstd, cudaStream_t st);
-int norm_bwd_rows(int T);
+int norm_bwd_rows(int T, int H);
 int norm_bwd_launch(const void* dy, int dy_f32, const void* x, int x_f32, const void* weight, const float* rstd,
                     const void* dres, int T, int H, void* dx, float* dw, float* part, cudaStream_t st);
 int quantize_launch(const void* x, int x_f32, long long banks, int rows, int cols, int block_rows, void* q,

@@ -193,72 +193,123 @@ __global__ void __launch_bounds__(max_threads(V)) norm_bwd_kernel(const TD* __re
   pdl_trigger();
   __shared__ float s_part[2][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
-  float w[V][8], dw[V][8];
+  // Up to two vectors a thread keeps the row in registers and loads the next one while this one is worked on.  With four
+  // (H > 8192, 1024 threads of 64 registers) only dw stays there and the row is read a second time, from L1 or L2.
+  constexpr bool KEEP = V < 4;
+  float w[KEEP ? V : 1][8], dw[V][8];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = (v * blockDim.x + threadIdx.x) * 8;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[v][i] = dw[v][i] = 0.0f;
-    if (c < H) load8(weight + c, w[v]);
+    for (int i = 0; i < 8; ++i) dw[v][i] = 0.0f;
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[v][i] = 0.0f;
+      if (c < H) load8(weight + c, w[v]);
+    }
   }
   const long long t0 = static_cast<long long>(blockIdx.x) * rows_per_block;
   const long long t1 = min(static_cast<long long>(T), t0 + rows_per_block);
-  // the next row is loaded while this one is worked on (with four vectors a thread there are no registers for that)
-  constexpr bool AHEAD = V < 4;
-  Raw8<TD> next_dy[V];
-  Raw8<TX> next_x[V], next_res[V];
-  float next_rs = 0.0f;
-  auto fetch = [&](long long t) {
-    next_rs = __ldg(rstd + t);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (v * blockDim.x + threadIdx.x) * 8;
-      next_dy[v].zero();
-      next_x[v].zero();
-      next_res[v].zero();
-      if (c < H) {
-        next_dy[v].load(dy + t * H + c);
-        next_x[v].load(x + t * H + c);
-        if (dres != nullptr) next_res[v].load(dres + t * H + c);
-      }
-    }
-  };
-  if (AHEAD && t0 < t1) fetch(t0);
   int buf = 0;
-  for (long long t = t0; t < t1; ++t) {
-    if (!AHEAD) fetch(t);
-    const float rs = next_rs;
-    float g[V][8], n[V][8];
-    Raw8<TX> res[V];
-    float dot = 0.0f;
+  if constexpr (KEEP) {
+    Raw8<TD> next_dy[V];
+    Raw8<TX> next_x[V], next_res[V];
+    float next_rs = 0.0f;
+    auto fetch = [&](long long t) {
+      next_rs = __ldg(rstd + t);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      next_dy[v].get(g[v]);
-      next_x[v].get(n[v]);
-      res[v] = next_res[v];
-    }
-    if (AHEAD && t + 1 < t1) fetch(t + 1);
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        n[v][i] *= rs;
-        dw[v][i] = fmaf(g[v][i], n[v][i], dw[v][i]);
-        g[v][i] *= w[v][i];
-        dot = fmaf(g[v][i], n[v][i], dot);
+      for (int v = 0; v < V; ++v) {
+        const int c = (v * blockDim.x + threadIdx.x) * 8;
+        next_dy[v].zero();
+        next_x[v].zero();
+        next_res[v].zero();
+        if (c < H) {
+          next_dy[v].load(dy + t * H + c);
+          next_x[v].load(x + t * H + c);
+          if (dres != nullptr) next_res[v].load(dres + t * H + c);
+        }
       }
-    dot = block_sum(dot, s_part[buf], warp, lane, nwarps);   // two buffers: one barrier per row
-    buf ^= 1;
-    const float mean = __fdiv_rn(dot, static_cast<float>(H));
+    };
+    if (t0 < t1) fetch(t0);
+    for (long long t = t0; t < t1; ++t) {
+      const float rs = next_rs;
+      float g[V][8], n[V][8];
+      Raw8<TX> res[V];
+      float dot = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (v * blockDim.x + threadIdx.x) * 8;
-      if (c < H) {
-        float d[8], b[8];
-        res[v].get(b);                                       // zeros without dres
+      for (int v = 0; v < V; ++v) {
+        next_dy[v].get(g[v]);
+        next_x[v].get(n[v]);
+        res[v] = next_res[v];
+      }
+      if (t + 1 < t1) fetch(t + 1);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = rs * (g[v][i] - n[v][i] * mean) + b[i];
-        store8(dx + t * H + c, d);
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          n[v][i] *= rs;
+          dw[v][i] = fmaf(g[v][i], n[v][i], dw[v][i]);
+          g[v][i] *= w[v][i];
+          dot = fmaf(g[v][i], n[v][i], dot);
+        }
+      dot = block_sum(dot, s_part[buf], warp, lane, nwarps);   // two buffers: one barrier per row
+      buf ^= 1;
+      const float mean = __fdiv_rn(dot, static_cast<float>(H));
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int c = (v * blockDim.x + threadIdx.x) * 8;
+        if (c < H) {
+          float d[8], b[8];
+          res[v].get(b);                                       // zeros without dres
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d[i] = rs * (g[v][i] - n[v][i] * mean) + b[i];
+          store8(dx + t * H + c, d);
+        }
+      }
+    }
+  } else {
+    for (long long t = t0; t < t1; ++t) {
+      const float rs = __ldg(rstd + t);
+      float dot = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int c = (v * blockDim.x + threadIdx.x) * 8;
+        if (c < H) {
+          float g[8], n[8], wv[8];
+          load8(dy + t * H + c, g);
+          load8(x + t * H + c, n);
+          load8(weight + c, wv);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            n[i] *= rs;
+            dw[v][i] = fmaf(g[i], n[i], dw[v][i]);
+            g[i] *= wv[i];
+            dot = fmaf(g[i], n[i], dot);
+          }
+        }
+      }
+      dot = block_sum(dot, s_part[buf], warp, lane, nwarps);
+      buf ^= 1;
+      const float mean = __fdiv_rn(dot, static_cast<float>(H));
+#pragma unroll 1
+      for (int v = 0; v < V; ++v) {
+        const int c = (v * blockDim.x + threadIdx.x) * 8;
+        if (c < H) {
+          float d[8], b[8], n[8], wv[8];
+          load8(dy + t * H + c, d);
+          load8(x + t * H + c, n);
+          load8(weight + c, wv);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) b[i] = 0.0f;
+          if (dres != nullptr) load8(dres + t * H + c, b);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            n[i] *= rs;
+            d[i] *= wv[i];
+            d[i] = rs * (d[i] - n[i] * mean) + b[i];
+          }
+          store8(dx + t * H + c, d);
+        }
       }
     }
   }
@@ -446,14 +497,20 @@ int norm_launch(const void* x, int x_f32, const void* res, int res_f32, const vo
   return check_cuda(e, "norm_kernel");
 }
 
-// Rows of one block, and so of one partial row of dw: about 2 blocks per SM for a large batch (with the next row in
-// flight that is enough, and dweight_kernel reads few partial rows), a function of T alone, not of the device, so that
-// the order of the sum is too.
-int norm_bwd_rows(int T) { return (T - 1) / 456 + 1; }
+// Rows of one block, and so of one partial row of dw: as many blocks as are resident at once, three of at most 256 threads
+// to an SM, two where a thread has two vectors, one of more threads.  More blocks write more partial rows and leave a
+// partly filled wave (1000 x 6144: 18 us with 456 blocks, 12.6 with 152), fewer leave registers idle (4096 x 2048: 13 us
+// with 456, 17 with 304; 8192 x 4096: 56 with 456, 48 with 304, 66 with 152).  A function of T and H alone, not of the
+// device, so that the order of the sum is too.
+int norm_bwd_rows(int T, int H) {
+  const RowShape s = row_shape(H);
+  const int blocks = s.v == 1 ? 456 : s.threads <= 256 ? 304 : 152;
+  return (T - 1) / blocks + 1;
+}
 
 int norm_bwd_launch(const void* dy, int dy_f32, const void* x, int x_f32, const void* weight, const float* rstd,
                     const void* dres, int T, int H, void* dx, float* dw, float* part, cudaStream_t st) {
-  const int rows = norm_bwd_rows(T), P = (T - 1) / rows + 1;
+  const int rows = norm_bwd_rows(T, H), P = (T - 1) / rows + 1;
   {
     ProfScope prof("rms_norm_bwd", st);
     cudaError_t e;

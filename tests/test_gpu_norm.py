@@ -166,6 +166,13 @@ def test_norm_backward(T, H, x_dtype, dy_dtype, with_dres):
     assert only["dweight"] is None and torch.equal(only["dx"], got["dx"])
 
 
+@pytest.mark.parametrize("x_dtype,dy_dtype", [(torch.bfloat16, torch.float32), (torch.float32, torch.bfloat16)])
+@pytest.mark.parametrize("T,H", [(400, 10256), (333, 4112), (160, 8192)])
+def test_norm_backward_of_wide_rows(T, H, x_dtype, dy_dtype):
+    """Several rows a block where a row needs two or four vectors a thread."""
+    test_norm_backward(T, H, x_dtype, dy_dtype, True)
+
+
 def test_backward_without_rows_clears_dweight():
     from serve_invariant_moe_gb300 import binding
     z = torch.empty(0, 64, device=DEV)
