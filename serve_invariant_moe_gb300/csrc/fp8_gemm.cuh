@@ -109,14 +109,18 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const 
   return __all_sync(0xffffffffu, mbar_wait_slow(bar, parity, w));
 }
 
-// Scales of blocks kb .. kb + 3 of one row (zeros past the last).
+// Scales of blocks kb .. kb + 3 of one row (past the last: the last one's, which nothing uses); VEC: p.vec_scale.
+template <bool VEC>
+__device__ __forceinline__ float4 load_scales_as(const float* src, int kb, const Fp8Params& p) {
+  if (VEC) return __ldg(reinterpret_cast<const float4*>(src + kb));
+  const int last = p.KB - 1;
+  return make_float4(__ldg(src + kb), __ldg(src + min(kb + 1, last)), __ldg(src + min(kb + 2, last)),
+                     __ldg(src + min(kb + 3, last)));
+}
+
+// Which of the two at run time, for a kernel that loads few.
 __device__ __forceinline__ float4 load_scales(const float* src, int kb, const Fp8Params& p) {
-  if (p.vec_scale) return __ldg(reinterpret_cast<const float4*>(src + kb));
-  float4 v = make_float4(__ldg(src + kb), 0.0f, 0.0f, 0.0f);
-  if (kb + 1 < p.KB) v.y = __ldg(src + kb + 1);
-  if (kb + 2 < p.KB) v.z = __ldg(src + kb + 2);
-  if (kb + 3 < p.KB) v.w = __ldg(src + kb + 3);
-  return v;
+  return p.vec_scale ? load_scales_as<true>(src, kb, p) : load_scales_as<false>(src, kb, p);
 }
 
 struct Fp8Unit {

@@ -3,11 +3,13 @@
 // Tokens are the MMA's M side: a CTA computes 128 token rows x 256 weight rows (one N = 256 MMA per K = 32
 // step).  A thread holds one token row, so its scale is one number per block, read from global memory four blocks ahead:
 // no shared memory on the scaling path, where the kernel of few tokens reads a scale for every column.
-// 8192 x 4096 x 6144 takes 169 us (2.44 PFLOP/s), 64 experts' gate and up of 2048 x 6144 with about 256 rows each 425 us.
+// 8192 x 4096 x 6144 takes 166 us (2.48 PFLOP/s), 64 experts' gate and up of 2048 x 6144 with about 256 rows each 425 us.
 // What bounds it is the handover of the products, 128 x 256 fp32 per block through two TMEM buffers: with the waits and
-// arrives alone the dense product takes 134 us (a block is then 769 cycles, what its 96 KB of copies and operand reads take
-// of shared memory), with the loads from TMEM 147, with the 256 FFMA issue cycles per scheduler 169.  So a buffer is
-// released as soon as its last columns are in registers, arrives are predicated, and one elected thread issues.
+// arrives alone the dense product takes 134 us (a block is then 769 cycles, what its 48 KB take from L2 at 64 bytes a cycle
+// and SM), with the loads from TMEM 147, with the 256 FFMA issue cycles per scheduler 169.  So a buffer is released as soon
+// as its last columns are in registers, arrives are predicated, one elected thread issues, and how scales are loaded is
+// known at compile time (169 -> 166).  Rows that do not start on 128 bytes (K % 128 != 0) cost a quarter more, since a
+// box's rows then touch five sectors instead of four (4000 x 4096: K = 6144 95 us, 6160 120).
 // Measured and not kept: CTA pairs with 256 x 256 tiles, 167 us, but 483 for those 64 experts, because the tiles are twice
 // as high; loads of 16 columns, 175, or two loads of 32 at once, no change; blocks unrolled by two, 188; the last columns
 // added behind the next block's wait, which spills, 229; packed fma.rn.f32x2, 690 instead of 485 cycles a block.
@@ -93,7 +95,8 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t (&v)[4
   }
 }
 
-template <int EPI>
+// VEC: scales in vectors of four blocks (p.vec_scale).
+template <int EPI, bool VEC>
 __global__ void __launch_bounds__(kFp8Threads, 1)
     fp8_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
                     const __grid_constant__ CUtensorMap tmO, const Fp8Params p) {
@@ -179,7 +182,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       // ---------------------------------------------------------- MMA issuer
       // To this thread all units are one stream of blocks.  It shares its scheduler with two epilogue warps, and what it
       // does between two blocks' MMAs the tensor cores wait for: the loop is unrolled over the ring, so that stages,
-      // buffers, descriptors and barriers are constants (8192 x 4096 x 6144: 169 us, a plain loop 174).
+      // buffers, descriptors and barriers are constants (8192 x 4096 x 6144: a plain loop takes 5 us more).
       static_assert(S::STAGES == 4 && S::ACC == 2, "the unrolled stream");
       const uint64_t adesc0 = sdesc_k_sw128(smem_u32(ring));
       const uint64_t wdesc0 = sdesc_k_sw128(smem_u32(ring + S::TILE_BYTES));
@@ -250,13 +253,13 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       for (int st = 0; st < 4; ++st)
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[st][i] = 0.0f;
-      float4 an = load_scales(ap, 0, p), wn0 = load_scales(wp0, 0, p), wn1 = load_scales(wp1, 0, p);
+      float4 an = load_scales_as<VEC>(ap, 0, p), wn0 = load_scales_as<VEC>(wp0, 0, p), wn1 = load_scales_as<VEC>(wp1, 0, p);
       for (int kb0 = 0; kb0 < p.KB; kb0 += 4) {
         float4 ac = an, wc0 = wn0, wc1 = wn1;
         if (kb0 + 4 < p.KB) {
-          an = load_scales(ap, kb0 + 4, p);
-          wn0 = load_scales(wp0, kb0 + 4, p);
-          wn1 = load_scales(wp1, kb0 + 4, p);
+          an = load_scales_as<VEC>(ap, kb0 + 4, p);
+          wn0 = load_scales_as<VEC>(wp0, kb0 + 4, p);
+          wn1 = load_scales_as<VEC>(wp1, kb0 + 4, p);
         }
         const int n_kb = min(4, p.KB - kb0);
         // not unrolled (that measured slower): the scales of the next block move up instead
@@ -395,10 +398,10 @@ int check_launch_regs(const void* kernel, const char* name, std::atomic<int>& re
   return INVMOE_OK;
 }
 
-template <int EPI>
+template <int EPI, bool VEC>
 int launch_rows(const Fp8Call& c, Fp8Params p, cudaStream_t st) {
   using S = Fp8RowsShape;
-  const void* kernel = reinterpret_cast<const void*>(fp8_rows_kernel<EPI>);
+  const void* kernel = reinterpret_cast<const void*>(fp8_rows_kernel<EPI, VEC>);
   constexpr int ELT = EPI == FP8_F32 ? 4 : 2;
   constexpr bool SWIGLU = EPI == FP8_SWIGLU;
   p.n_blocks = SWIGLU ? c.N / kWTile : (c.N + 2 * kWTile - 1) / (2 * kWTile);
@@ -420,7 +423,7 @@ int launch_rows(const Fp8Call& c, Fp8Params p, cudaStream_t st) {
   if (rc) return rc;
   const unsigned grid = static_cast<unsigned>(units < sms ? units : sms);
   ProfScope prof(c.name, st);
-  return check_cuda(launch_kernel(fp8_rows_kernel<EPI>, dim3(grid), dim3(kFp8Threads), static_cast<size_t>(smem), st, tmW,
+  return check_cuda(launch_kernel(fp8_rows_kernel<EPI, VEC>, dim3(grid), dim3(kFp8Threads), static_cast<size_t>(smem), st, tmW,
                                   tmA, tmO, p),
                     c.name);
 }
@@ -428,9 +431,9 @@ int launch_rows(const Fp8Call& c, Fp8Params p, cudaStream_t st) {
 }  // namespace
 
 int fp8_rows_run(const Fp8Call& c, const Fp8Params& p, cudaStream_t st) {
-  if (c.out_kind == FP8_OUT_SWIGLU) return launch_rows<FP8_SWIGLU>(c, p, st);
-  if (c.out_kind == FP8_OUT_F32) return launch_rows<FP8_F32>(c, p, st);
-  return launch_rows<FP8_BF16>(c, p, st);
+  if (c.out_kind == FP8_OUT_SWIGLU) return p.vec_scale ? launch_rows<FP8_SWIGLU, true>(c, p, st) : launch_rows<FP8_SWIGLU, false>(c, p, st);
+  if (c.out_kind == FP8_OUT_F32) return p.vec_scale ? launch_rows<FP8_F32, true>(c, p, st) : launch_rows<FP8_F32, false>(c, p, st);
+  return p.vec_scale ? launch_rows<FP8_BF16, true>(c, p, st) : launch_rows<FP8_BF16, false>(c, p, st);
 }
 
 }  // namespace invmoe
