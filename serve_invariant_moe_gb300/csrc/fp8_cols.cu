@@ -2,7 +2,7 @@
 //
 // Weights are the MMA's M side (MT sub-tiles of WR rows; a sub-tile lies in one scale block, so its scale is one number
 // per block of K) and tokens its N side, in multiples of 16: a group of 20 tokens costs 32 columns, not 128 rows.
-// What bounds it is reading the weights (64 experts of 2 x 2048 x 6144, 4 tokens: 95 us, 6.2 TB/s of DRAM), and, for one
+// What bounds it is reading the weights (64 experts of 2 x 2048 x 6144, 4 tokens: 95 us, 6.3 TB/s of DRAM), and, for one
 // small matrix, latency: a step of KS K blocks goes through every handover at once (one copy per operand, one ring stage,
 // one TMEM buffer, one set of scales, one wait of each role), and where 256-row tiles would leave SMs without work 64-row
 // tiles are used (8 x 4096 x 6144: 64 CTAs instead of 16; 8 us, of which 2 until the first block is there, 4 for twelve
