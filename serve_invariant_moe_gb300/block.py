@@ -138,10 +138,13 @@ class Fp8MoEBlock:
 class Fp8DecodeGraph:
     """A decode step of B requests as one CUDA graph: fill x and residual, replay, read out and residual_out.
 
-    The captured kernels are those of Fp8MoEBlock.decode, so the bits are the same."""
+    The captured kernels are those of Fp8MoEBlock.decode, so the bits are the same.  They read the weights that the block
+    has now: a graph keeps those alive, and is made anew for others."""
 
     def __init__(self, block: Fp8MoEBlock, B: int, x_dtype=torch.bfloat16):
         w, dev = block.w, block.w.w13.device
+        # captured kernels hold addresses: the tensors live as long as the graph, whatever becomes of block and weights
+        self._held = [*vars(w).values(), w.routing.bias]
         self.x = torch.zeros((B, w.H), dtype=x_dtype, device=dev)
         self.residual = torch.zeros((B, w.H), dtype=torch.bfloat16, device=dev)
         bufs = block._alloc(B, True)

@@ -1,0 +1,127 @@
+"""Host side of the 8-bit block on CPU: what its objects keep alive and which status words its check reads.
+
+The library's calls are replaced by fakes on CPU tensors, CUDA graphs and streams by objects that do nothing."""
+import contextlib
+import gc
+import types
+import weakref
+
+import pytest
+import torch
+
+from serve_invariant_moe_gb300 import api, block
+
+
+class FakeBinding:
+    """The binding's functions that the block calls; `fail` names one whose kernel gives up a wait."""
+    FP8 = torch.float8_e4m3fn
+
+    def __init__(self):
+        self.fail = None
+        self.stream = 0
+
+    def _call(self, name, workspace):
+        if name == self.fail:
+            workspace[0] = 1
+
+    def plan_len(self, T, E, k):
+        return 2 * E + 1 + 2 * T * k
+
+    def workspace_size(self, T, H, E, k):
+        return 256 + 4 * T * E
+
+    def new_workspace(self, nbytes, device):
+        return torch.zeros(max(nbytes, 256), dtype=torch.uint8)
+
+    def check_status(self, workspace):
+        if workspace[0]:
+            workspace[0] = 0
+            raise RuntimeError("timeout")
+
+    def _stream(self):
+        return self.stream
+
+    def add_rms_norm(self, x, w, residual, eps, out, fp8, residual_out, q, scale, rstd):
+        return dict(out=out, q=q, scale=scale, rstd=rstd, residual=residual_out)
+
+    def moe_router_logits(self, x, w, ws, logits):
+        self._call("moe_router_logits", ws)
+        return logits
+
+    def moe_route_select(self, logits, k, score, bias, n_group, topk_group, renormalize, scale, idx, w, plan, ws):
+        assert ws.numel() >= self.workspace_size(logits.shape[0], 0, logits.shape[1], k)
+        return dict(topk_idx=idx, topk_w=w, plan=plan)
+
+    def moe_permute_fp8(self, q, scale, plan, E, k, xp, xs):
+        return xp, xs
+
+    def moe_grouped_swiglu_fp8(self, xp, xs, plan, w13, s13, T, k, ws, h, hs):
+        self._call("moe_grouped_swiglu_fp8", ws)
+        return dict(h=h, h_scale=hs)
+
+    def moe_grouped_down_fp8(self, h, hs, plan, w2, s2, T, k, ws, y):
+        self._call("moe_grouped_down_fp8", ws)
+        return y
+
+    def moe_combine(self, y, w, plan, T, H, E, k, y_shared, out, out_bf16):
+        return torch.zeros(T, H) if out is None else out
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    f = FakeBinding()
+    monkeypatch.setattr(block, "binding", f)
+    monkeypatch.setattr(api, "binding", f)
+    stream = types.SimpleNamespace(wait_stream=lambda other: None)
+    monkeypatch.setattr(torch.cuda, "Stream", lambda **kw: stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: stream)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "graph", lambda g: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "CUDAGraph", lambda: types.SimpleNamespace(replay=lambda: None))
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda *a: None)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    return f
+
+
+def weights(E=4, H=128, F=128, Fs=128):
+    e = lambda *s, dtype=torch.float8_e4m3fn: torch.empty(*s, dtype=dtype)   # noqa: E731
+    f = lambda *s: torch.empty(*s)                                           # noqa: E731
+    bf16 = torch.bfloat16
+    return block.Fp8MoEWeights(e(H, dtype=bf16), e(E, H, dtype=bf16), e(E, 2 * F, H), f(E, 2 * F // 128, H // 128),
+                               e(E, H, F), f(E, H // 128, F // 128), 2, api.Routing(bias=f(E)), e(1, 2 * Fs, H),
+                               f(1, 2 * Fs // 128, H // 128), e(1, H, Fs), f(1, H // 128, Fs // 128))
+
+
+def memory(w):
+    """A weak reference to the memory of every tensor that a step reads."""
+    tensors = [t for t in [*vars(w).values(), w.routing.bias] if isinstance(t, torch.Tensor)]
+    assert len(tensors) == 11
+    return [weakref.ref(t) for t in tensors]
+
+
+def test_a_graph_keeps_what_its_kernels_read(fake):
+    """Captured kernels hold addresses: the weights must outlive the caller's last reference to the block."""
+    w = weights()
+    refs = memory(w)
+    g = block.Fp8DecodeGraph(block.Fp8MoEBlock(w), 3)
+    del w
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    del g
+    gc.collect()
+    assert all(r() is None for r in refs)
+
+
+def test_a_graph_keeps_what_its_kernels_read_when_the_weights_are_exchanged(fake):
+    w = weights()
+    refs = memory(w)
+    b = block.Fp8MoEBlock(w)
+    g = block.Fp8DecodeGraph(b, 3)
+    new = weights()
+    for name, t in vars(new).items():
+        setattr(w, name, t)
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    del g
+    gc.collect()
+    assert all(r() is None for r in refs)
