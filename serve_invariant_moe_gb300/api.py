@@ -278,7 +278,8 @@ class DecodeGraphs:
     smaller than a bucket are padded with zero tokens, which changes no other
     row's bits (every row is computed on its own).  The captured kernels are the
     same as the eager ones, so a replayed step gives the same bits as
-    MoELayer.decode on the same tokens.
+    MoELayer.decode on the same tokens.  They read the weights that the layer has
+    now and write the buffers it decodes in now: both are kept alive here.
     """
 
     def __init__(self, layer: MoELayer, buckets=(1, 2, 4, 8, 16, 32, 64, 128)):
@@ -287,6 +288,8 @@ class DecodeGraphs:
         w = layer.w
         dev = w.w13.device
         layer.alloc_decode(self.buckets[-1])
+        # captured kernels hold addresses: a larger batch gives the layer new buffers, these stay the graphs'
+        self._held = [layer._decode, *vars(w).values(), w.routing and w.routing.bias]
         self.inp = {B: torch.zeros((B, w.H), dtype=torch.bfloat16, device=dev) for B in self.buckets}
         self.out = {}
         self.graphs = {}

@@ -1,4 +1,5 @@
-"""Host side of the 8-bit block on CPU: what its objects keep alive and which status words its check reads.
+"""Host side of the 8-bit block and of the decode graphs on CPU: what the objects keep alive and which status words the
+block's check reads.
 
 The library's calls are replaced by fakes on CPU tensors, CUDA graphs and streams by objects that do nothing."""
 import contextlib
@@ -27,7 +28,7 @@ class FakeBinding:
     def plan_len(self, T, E, k):
         return 2 * E + 1 + 2 * T * k
 
-    def workspace_size(self, T, H, E, k):
+    def workspace_size(self, T, H, E, k, *more):
         return 256 + 4 * T * E
 
     def new_workspace(self, nbytes, device):
@@ -63,6 +64,12 @@ class FakeBinding:
         self._call("moe_grouped_down_fp8", ws)
         return y
 
+    def lib(self):
+        return types.SimpleNamespace(moe_layer_forward=lambda *args: 0)
+
+    def check(self, rc):
+        assert rc == 0
+
     def moe_combine(self, y, w, plan, T, H, E, k, y_shared, out, out_bf16):
         return torch.zeros(T, H) if out is None else out
 
@@ -72,7 +79,7 @@ def fake(monkeypatch):
     f = FakeBinding()
     monkeypatch.setattr(block, "binding", f)
     monkeypatch.setattr(api, "binding", f)
-    stream = types.SimpleNamespace(wait_stream=lambda other: None)
+    stream = types.SimpleNamespace(wait_stream=lambda other: None, cuda_stream=0)
     monkeypatch.setattr(torch.cuda, "Stream", lambda **kw: stream)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: stream)
     monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
@@ -125,3 +132,22 @@ def test_a_graph_keeps_what_its_kernels_read_when_the_weights_are_exchanged(fake
     del g
     gc.collect()
     assert all(r() is None for r in refs)
+
+
+def test_decode_graphs_keep_their_buffers_and_weights(fake):
+    """A larger batch, decoded or prefilled, gives the layer new buffers; the captured steps still write the old ones."""
+    bf16 = lambda *s: torch.empty(*s, dtype=torch.bfloat16)   # noqa: E731
+    w = api.MoEWeights(bf16(4, 64), bf16(4, 256, 64), bf16(4, 64, 128), 2)
+    layer = api.MoELayer(w)
+    graphs = api.DecodeGraphs(layer, buckets=(1, 4))
+    buffers = {name: weakref.ref(t) for name, t in layer._decode.items() if isinstance(t, torch.Tensor)}
+    read = [weakref.ref(t) for t in (w.w_router, w.w13, w.w2)]
+    assert {"logits", "plan", "xp", "h", "y", "out", "ws"} <= set(buffers)
+    layer.decode(bf16(9, 64))
+    w.w_router, w.w13, w.w2 = bf16(4, 64), bf16(4, 256, 64), bf16(4, 64, 128)
+    gc.collect()
+    assert [name for name, r in buffers.items() if r() is None] == []
+    assert all(r() is not None for r in read)
+    del graphs
+    gc.collect()
+    assert all(r() is None for r in [*buffers.values(), *read])
