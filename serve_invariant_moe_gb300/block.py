@@ -12,6 +12,7 @@ per 128 x 128 weights and per row and 128 activations):
 Every step is per token with one reduction order, so a token's bits do not depend on its batch, on prefill or decode, or
 on the kernel that a batch size selects.
 """
+import threading
 from dataclasses import dataclass
 from typing import Optional
 
@@ -68,7 +69,25 @@ class Fp8MoEBlock:
 
     def __init__(self, weights: Fp8MoEWeights):
         self.w = weights
-        self._bufs = None
+        self._bufs = None                       # decode's
+        self._ws = {}                           # prefill's workspaces, one per thread and stream
+        self._unread, self._captured = [], []   # others with a status that check() reads: replaced ones, graphs'
+
+    def _workspace(self, T):
+        """prefill's workspace: this thread's own on the current stream (calls of two threads interleave their launches), kept
+        for its status; a captured call's belongs to its graph."""
+        w = self.w
+        need = binding.workspace_size(T, w.H, w.E, w.k)
+        if torch.cuda.is_current_stream_capturing():
+            self._captured.append(binding.new_workspace(need, w.w13.device))
+            return self._captured[-1]
+        key = threading.get_ident(), binding._stream()
+        ws = self._ws.get(key)
+        if ws is None or ws.numel() < need:
+            if ws is not None:
+                self._unread.append(ws)
+            ws = self._ws[key] = binding.new_workspace(need, w.w13.device)
+        return ws
 
     def _alloc(self, T, kept):
         """The intermediates of a batch of T tokens."""
@@ -79,11 +98,14 @@ class Fp8MoEBlock:
                  logits=e((T, w.E)), topk_idx=e((T, w.k), torch.int32), topk_w=e((T, w.k)),
                  plan=e(binding.plan_len(T, w.E, w.k), torch.int32), xp=e((S, w.H), binding.FP8), xp_scale=e((S, nb)),
                  h=e((S, w.F), binding.FP8), h_scale=e((S, w.F // 128)), y=e((S, w.H)),
-                 ws=binding.new_workspace(binding.workspace_size(T, w.H, w.E, w.k), dev), residual=None, out=None)
+                 residual=None, out=None)
         if w.F_shared:
             b.update(hs=e((T, w.F_shared), binding.FP8), hs_scale=e((T, w.F_shared // 128)), ys=e((T, w.H)))
         if kept:
-            b.update(residual=e((T, w.H), torch.bfloat16), out=e((T, w.H)))
+            b.update(residual=e((T, w.H), torch.bfloat16), out=e((T, w.H)),
+                     ws=binding.new_workspace(binding.workspace_size(T, w.H, w.E, w.k), dev))
+        else:
+            b["ws"] = self._workspace(T)
         return b
 
     def _run(self, x, residual, b, residual_out, out, out_bf16):
@@ -124,15 +146,29 @@ class Fp8MoEBlock:
         share the buffers, so they belong on one stream."""
         B = x.shape[0]
         if self._bufs is None or self._bufs["T"] < B:
+            if self._bufs is not None:
+                self._unread.append(self._bufs["ws"])
             self._bufs = self._alloc(max(B, 1), True)
         b = self._bufs
         res = self._run(x, residual, b, b["residual"][:B], b["out"][:B], out_bf16)
         return res["out"], res["residual"]
 
     def check(self):
-        """Raise if a kernel of the decode buffers' calls gave up waiting (synchronises)."""
+        """Raise if a kernel of a prefill or decode call since the last check gave up waiting: what it should have written
+        is then not there.  Waits for the device."""
+        torch.cuda.synchronize(self.w.w13.device)
+        spaces = [*self._ws.values(), *self._unread, *self._captured]
         if self._bufs is not None:
-            binding.check_status(self._bufs["ws"])
+            spaces.append(self._bufs["ws"])
+        self._unread = []
+        failed = None
+        for ws in spaces:                       # all of them, so that each time-out is reported once
+            try:
+                binding.check_status(ws)
+            except RuntimeError as e:
+                failed = e
+        if failed is not None:
+            raise failed
 
 
 class Fp8DecodeGraph:
@@ -163,3 +199,8 @@ class Fp8DecodeGraph:
     def replay(self):
         self.graph.replay()
         return self.out, self.residual_out
+
+    def check(self):
+        """As Fp8MoEBlock.check, for the replays."""
+        torch.cuda.synchronize(self.x.device)
+        binding.check_status(self._bufs["ws"])

@@ -4,6 +4,7 @@ block's check reads.
 The library's calls are replaced by fakes on CPU tensors, CUDA graphs and streams by objects that do nothing."""
 import contextlib
 import gc
+import threading
 import types
 import weakref
 
@@ -151,3 +152,75 @@ def test_decode_graphs_keep_their_buffers_and_weights(fake):
     del graphs
     gc.collect()
     assert all(r() is None for r in [*buffers.values(), *read])
+
+
+FAILING = ["moe_router_logits", "moe_grouped_swiglu_fp8", "moe_grouped_down_fp8"]
+
+
+@pytest.mark.parametrize("fail", FAILING)
+def test_check_covers_prefill(fake, fail):
+    """On every stream, also of calls before a larger batch, and each time-out is reported once."""
+    b = block.Fp8MoEBlock(weights())
+    b.check()
+    for stream, T in [(0, 8), (1, 3), (0, 3)]:
+        fake.stream, fake.fail = stream, fail
+        b.prefill(torch.empty(T, 128))
+        fake.fail = None
+        b.prefill(torch.empty(5 * T, 128))          # needs a larger workspace
+        with pytest.raises(RuntimeError, match="timeout"):
+            b.check()
+        b.check()
+
+
+def test_streams_and_threads_do_not_share_a_workspace(fake):
+    b = block.Fp8MoEBlock(weights())
+    spaces = []
+
+    def run():
+        spaces.append(b.prefill(torch.empty(4, 128), return_all=True)["workspace"])
+    for stream in (0, 1, 0):
+        fake.stream = stream
+        run()
+    t = threading.Thread(target=run)
+    t.start()
+    t.join()
+    assert spaces[0] is spaces[2] and spaces[0] is not spaces[1] and spaces[3] is not spaces[0]
+
+
+@pytest.mark.parametrize("fail", FAILING)
+def test_check_covers_replaced_decode_buffers(fake, fail):
+    b = block.Fp8MoEBlock(weights())
+    x, res = torch.empty(9, 128), torch.empty(9, 128, dtype=torch.bfloat16)
+    fake.fail = fail
+    b.decode(x[:2], res[:2])
+    fake.fail = None
+    b.decode(x, res)
+    with pytest.raises(RuntimeError, match="timeout"):
+        b.check()
+    b.check()
+
+
+@pytest.mark.parametrize("fail", FAILING)
+def test_check_covers_graphs(fake, fail):
+    b = block.Fp8MoEBlock(weights())
+    g = block.Fp8DecodeGraph(b, 2)
+    g.check()
+    fake.fail = fail
+    fake._call(fail, g._bufs["ws"])                 # what a replayed kernel does
+    with pytest.raises(RuntimeError, match="timeout"):
+        g.check()
+    g.check()
+
+
+def test_check_covers_a_prefill_that_a_caller_captures(fake, monkeypatch):
+    """Its workspace belongs to the captured graph: no other call uses it, and every replay's status is read."""
+    b = block.Fp8MoEBlock(weights())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    ws = b.prefill(torch.empty(4, 128), return_all=True)["workspace"]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    assert b.prefill(torch.empty(4, 128), return_all=True)["workspace"] is not ws
+    for _ in range(2):
+        ws[0] = 1
+        with pytest.raises(RuntimeError, match="timeout"):
+            b.check()
+        b.check()
