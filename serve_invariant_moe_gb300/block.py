@@ -142,14 +142,18 @@ class Fp8MoEBlock:
     def decode(self, x, residual, out_bf16=None):
         """One token per request: as prefill, for a bf16 residual, on buffers kept for the largest batch so far.
 
-        Returns views of those buffers: (out [B, H] fp32, residual [B, H] bf16), valid until the next call.  The calls
-        share the buffers, so they belong on one stream."""
+        Returns views of those buffers: (out [B, H] fp32, residual [B, H] bf16), valid until the next call, which may be
+        given them or rows of them.  The calls share the buffers, so they belong on one stream."""
         B = x.shape[0]
         if self._bufs is None or self._bufs["T"] < B:
             if self._bufs is not None:
                 self._unread.append(self._bufs["ws"])
             self._bufs = self._alloc(max(B, 1), True)
         b = self._bufs
+        # rows of the last step's residual at other places than they go to: a block would write what another one reads
+        if (residual is not None and residual.data_ptr() != b["residual"].data_ptr()
+                and residual.untyped_storage().data_ptr() == b["residual"].untyped_storage().data_ptr()):
+            residual = residual.clone()
         res = self._run(x, residual, b, b["residual"][:B], b["out"][:B], out_bf16)
         return res["out"], res["residual"]
 
