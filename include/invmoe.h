@@ -528,7 +528,7 @@ int moe_router_backward(const void* x, const void* w_router, const void* dlogits
                         float* dw_router, void* workspace, size_t ws_bytes, void* stream);
 
 /* r = x + residual (fp32 sum, rounded to the residual's type and stored in residual_out, which
- * may be residual itself; without a residual r = x and residual_out is NULL);
+ * may be residual itself but not overlap it otherwise; without a residual r = x and residual_out is NULL);
  * rstd = 1 / sqrt(mean(r^2) + eps) in fp32; y = (r * rstd) * weight;
  * out [T, H] bf16 (nullable) = y; q [T, H] e4m3 with scale [T, ceil(H / 128)] (nullable,
  * together) = y quantised from fp32; rstd [T] fp32 (nullable).  One of out and q is given.
@@ -546,7 +546,8 @@ size_t rms_norm_backward_workspace_size(int T, int H);
  *                                                  both x and residual
  *   dweight = sum_t dy * n                        [H] fp32 (nullable), rows in a fixed order
  * dy [T, H] of dy_type; dres [T, H] of x's type (nullable): the gradient that reaches r from
- * the residual stream; dx may be dres.  workspace is used for dweight alone. */
+ * the residual stream; dx may be dres but not overlap it otherwise.  workspace is used for
+ * dweight alone. */
 int add_rms_norm_backward(const void* dy, int dy_type, const void* x, int x_type, const void* weight,
                           const float* rstd, const void* dres, int T, int H, void* dx, float* dweight, void* workspace,
                           size_t ws_bytes, void* stream);

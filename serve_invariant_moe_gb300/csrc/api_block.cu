@@ -29,6 +29,8 @@ int check_type(int type, const char* what) {
   return INVMOE_OK;
 }
 
+size_t matrix_bytes(int T, int H, int type) { return static_cast<size_t>(T) * H * (type == INVMOE_F32 ? 4 : 2); }
+
 int check_width(int H) {
   REQUIRE(H > 0, INVMOE_ERR_INVALID_ARG, "need H > 0");
   REQUIRE(H % 16 == 0 && H <= 32768, INVMOE_ERR_UNSUPPORTED_SHAPE, "H=%d is not a multiple of 16 up to 32768", H);
@@ -143,6 +145,8 @@ int add_rms_norm(const void* x, int x_type, const void* residual, int residual_t
   REQUIRE_PTR(x); REQUIRE_PTR(weight);
   REQUIRE_ALIGNED(x); REQUIRE_ALIGNED(weight); REQUIRE_ALIGNED(residual); REQUIRE_ALIGNED(residual_out);
   REQUIRE_ALIGNED(out); REQUIRE_ALIGNED(q);
+  REQUIRE(same_or_apart(residual_out, residual, matrix_bytes(T, H, residual_type)), INVMOE_ERR_INVALID_ARG,
+          "residual_out overlaps residual without being it");
   return norm_launch(x, x_type == INVMOE_F32, residual, residual != nullptr && residual_type == INVMOE_F32, weight, T,
                      H, eps, residual_out, out, q, scale, rstd, static_cast<cudaStream_t>(stream));
 }
@@ -173,6 +177,7 @@ int add_rms_norm_backward(const void* dy, int dy_type, const void* x, int x_type
   }
   REQUIRE_PTR(dy); REQUIRE_PTR(x); REQUIRE_PTR(weight); REQUIRE_PTR(rstd); REQUIRE_PTR(dx);
   REQUIRE_ALIGNED(dy); REQUIRE_ALIGNED(x); REQUIRE_ALIGNED(weight); REQUIRE_ALIGNED(dx); REQUIRE_ALIGNED(dres);
+  REQUIRE(same_or_apart(dx, dres, matrix_bytes(T, H, x_type)), INVMOE_ERR_INVALID_ARG, "dx overlaps dres without being it");
   return norm_bwd_launch(dy, dy_type == INVMOE_F32, x, x_type == INVMOE_F32, weight, rstd, dres, T, H, dx, dweight,
                          dweight != nullptr ? reinterpret_cast<float*>(scratch(workspace)) : nullptr, st);
 }

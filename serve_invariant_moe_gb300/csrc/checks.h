@@ -10,6 +10,12 @@ namespace invmoe {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// The first of two arrays of n bytes is the second, or they have no byte in common (or one is absent).
+inline bool same_or_apart(const void* a, const void* b, size_t n) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a == nullptr || b == nullptr || (x > y ? x - y : y - x) >= n || x == y;
+}
+
 inline size_t route_ws(int T, int E) {
   const size_t NC = (static_cast<size_t>(T) + kDispatchChunk - 1) / kDispatchChunk;
   return align_up(NC * static_cast<size_t>(E) * sizeof(int32_t), 256);

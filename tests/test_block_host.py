@@ -242,3 +242,19 @@ def test_decode_of_some_of_the_last_step_s_requests(fake):
     assert torch.equal(r, res[1:4])
     _, r = b.decode(x[2:3], r[2:])
     assert torch.equal(r, res[3:4])
+
+
+def test_the_norm_refuses_partly_overlapping_rows():
+    """Before anything is launched: the addresses are never read."""
+    import ctypes
+    from serve_invariant_moe_gb300 import _lib, build
+    build.build()
+    lib, p, null = _lib.lib(), ctypes.c_void_p, None
+    T, H, at = 3, 64, 1 << 20
+    for shift in (-T * H * 2 + 16, -128, 16, 128, T * H * 2 - 16):
+        assert lib.add_rms_norm(p(4096), 0, p(at), 0, p(8192), T, H, 1e-6, p(at + shift), p(16384), null, null, null,
+                                null) == -1
+        assert b"overlaps" in lib.invmoe_last_error()
+        assert lib.add_rms_norm_backward(p(4096), 0, p(8192), 0, p(8192), p(8192), p(at), T, H, p(at + shift), null, null,
+                                         0, null) == -1
+        assert b"overlaps" in lib.invmoe_last_error()
