@@ -296,13 +296,14 @@ __global__ void __launch_bounds__(kSelThreads, EPL <= 8 ? 5 : 4)
     st = softmax_stats<EPL, true>(l, E, lane);
   }
   int e = -1;
-  float s = 0.0f, d = 0.0f;
+  float s = 0.0f, d = 0.0f, comp = 1.0f;         // comp: ds / dl = s * comp
   if (lane < k) {
     e = __ldg(idx + t * k + lane);
     if (e < 0 || e >= E) e = -1;
     if (e >= 0) {
       const float lj = __ldg(row + e);
       s = SOFTMAX ? softmax_score(lj, st) : sigmoid_f32(lj);
+      if (!SOFTMAX) comp = sigmoid_f32(-lj);     // 1 - s of the rounded s has lost its bits where s is near 1
       d = __fmul_rn(__ldg(dw + t * k + lane), scale);
     }
   }
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(kSelThreads, EPL <= 8 ? 5 : 4)
   }
   if (renorm) d = sum == 0.0f ? 0.0f : __fdiv_rn(d - __fdiv_rn(dot, sum), sum);
   // value of a chosen expert's entry beyond what every expert gets; an expert chosen twice gets both
-  const float mine = SOFTMAX ? __fmul_rn(d, s) : d * s * (1.0f - s);
+  const float mine = d * s * comp;
   const float all = SOFTMAX && !renorm ? dot : 0.0f;
   float v = 0.0f;
   for (int j = 0; j < k; ++j) {
