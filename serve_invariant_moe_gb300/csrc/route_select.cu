@@ -266,12 +266,14 @@ __global__ void __launch_bounds__(kSelThreads, select_blocks(EPL)) select_kernel
   }
 }
 
-// Gradient of the weights: with s_j the chosen scores, S = sum_j s_j, d_j = scale * dw_j,
-//   renormalised      ds_j = (d_j - sum_i d_i s_i / S) / S        (0 where S = 0)
+// Gradient of the weights: with s_j the chosen scores, S = sum_j s_j, d_j = dw_j, all times scale,
+//   renormalised      ds_j s_j = w_j sum_i w_i (d_j - d_i),  w_j = s_j / S        (0 where S = 0)
 //   otherwise         ds_j = d_j
 //   sigmoid           dl_j = ds_j s_j (1 - s_j), other experts 0
 //   softmax           dl_e = p_e (ds_e - sum_j ds_j p_j), ds_e = 0 for experts not chosen; renormalised, the sum is 0
 //                     and only the chosen experts have a gradient
+// Renormalised, the sum over differences keeps what d_j - sum_i w_i d_i leaves to rounding where one w_j is near 1, and has
+// no quotient that tiny scores could make overflow.
 // One warp per token; an entry of topk_idx outside [0, E) takes no part.  Bound by writing the row, which is written as if
 // nothing were chosen and then corrected at the k chosen entries (8192 x 1024: 7.8 us for 34 MB, 11.5 when every column was
 // compared with every choice; 8192 x 256: about the cost of a launch); the plain softmax by its exponentials and
@@ -304,25 +306,31 @@ __global__ void __launch_bounds__(kSelThreads, EPL <= 8 ? 5 : 4)
       const float lj = __ldg(row + e);
       s = SOFTMAX ? softmax_score(lj, st) : sigmoid_f32(lj);
       if (!SOFTMAX) comp = sigmoid_f32(-lj);     // 1 - s of the rounded s has lost its bits where s is near 1
-      d = __fmul_rn(__ldg(dw + t * k + lane), scale);
+      d = __ldg(dw + t * k + lane);
     }
   }
-  float sum = 0.0f, dot = 0.0f;
-  for (int j = 0; j < k; ++j) {
-    const float sj = __shfl_sync(kFull, s, j);
-    sum += sj;
-    dot = fmaf(__shfl_sync(kFull, d, j), sj, dot);
-  }
-  if (renorm) d = sum == 0.0f ? 0.0f : __fdiv_rn(d - __fdiv_rn(dot, sum), sum);
   // value of a chosen expert's entry beyond what every expert gets; an expert chosen twice gets both
-  const float mine = d * s * comp;
-  const float all = SOFTMAX && !renorm ? dot : 0.0f;
+  float mine, dot = 0.0f;
+  if (renorm) {
+    float sum = 0.0f;
+    for (int j = 0; j < k; ++j) sum += __shfl_sync(kFull, s, j);
+    const float w = sum == 0.0f ? 0.0f : __fdiv_rn(s, sum);
+    float acc = 0.0f;
+    for (int j = 0; j < k; ++j)
+      acc = fmaf(__shfl_sync(kFull, w, j), __fsub_rn(d, __shfl_sync(kFull, d, j)), acc);
+    mine = w * comp * acc;
+  } else {
+    for (int j = 0; j < k; ++j) dot = fmaf(__shfl_sync(kFull, d, j), __shfl_sync(kFull, s, j), dot);
+    mine = d * s * comp;
+  }
+  const float all = SOFTMAX && !renorm ? __fmul_rn(dot, scale) : 0.0f;
   float v = 0.0f;
   for (int j = 0; j < k; ++j) {
     const int ej = __shfl_sync(kFull, e, j);
     const float vj = __shfl_sync(kFull, mine, j);
     if (ej == e) v += vj;
   }
+  v = __fmul_rn(v, scale);
   if constexpr (SOFTMAX)
     if (!renorm) v -= __fmul_rn(all, s);
   // the row as if nothing were chosen, then the chosen entries: the warp's stores to one address are in this order

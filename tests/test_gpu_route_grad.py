@@ -99,3 +99,33 @@ def check(l, idx, dw, score, renorm, scale=2.5):
 @pytest.mark.parametrize("z", GAPS)
 def test_sigmoid(T, E, k, z):
     check(*confident(T, E, k, z, 2), "sigmoid", False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("T,E,k", SIZES)
+@pytest.mark.parametrize("z", GAPS)
+def test_renormalised(T, E, k, z, score):
+    check(*confident(T, E, k, z, 3), score, True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_renormalised_over_one_expert_is_constant(score):
+    from serve_invariant_moe_gb300 import binding
+    l, idx, dw = confident(50, 40, 1, 0.0, 4)
+    got = binding.moe_route_select_backward(l.to(DEV), idx.to(DEV), dw.to(DEV), score, True)
+    assert (got == 0).all()
+
+
+@pytest.mark.gpu
+def test_renormalised_over_tiny_scores():
+    """Scores near the smallest normal number, where a score has lost up to two bits (2^-22 of it): no overflow."""
+    from serve_invariant_moe_gb300 import binding
+    g = torch.Generator().manual_seed(5)
+    l = -87.0 - 0.7 * torch.rand(20, 16, generator=g)
+    idx = torch.rand(20, 16, generator=g).topk(4, dim=1).indices.to(torch.int32)
+    dw = torch.randn(20, 4, generator=g) * 1e3
+    got = binding.moe_route_select_backward(l.to(DEV), idx.to(DEV), dw.to(DEV), "sigmoid", True, 2.5)
+    ref, size = gradient(l, idx, dw, "sigmoid", True, 2.5)
+    assert (np.abs(got.double().cpu().numpy() - ref) <= (64 + 6 * 4 + 16) * 2.0 ** -24 * size).all()
