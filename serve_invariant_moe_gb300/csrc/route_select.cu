@@ -266,14 +266,15 @@ __global__ void __launch_bounds__(kSelThreads, select_blocks(EPL)) select_kernel
   }
 }
 
-// Gradient of the weights: with s_j the chosen scores, S = sum_j s_j, d_j = dw_j, all times scale,
-//   renormalised      ds_j s_j = w_j sum_i w_i (d_j - d_i),  w_j = s_j / S        (0 where S = 0)
-//   otherwise         ds_j = d_j
-//   sigmoid           dl_j = ds_j s_j (1 - s_j), other experts 0
-//   softmax           dl_e = p_e (ds_e - sum_j ds_j p_j), ds_e = 0 for experts not chosen; renormalised, the sum is 0
-//                     and only the chosen experts have a gradient
-// Renormalised, the sum over differences keeps what d_j - sum_i w_i d_i leaves to rounding where one w_j is near 1, and has
-// no quotient that tiny scores could make overflow.
+// Gradient of the weights: with s_j the chosen scores, w_j = s_j / sum_i s_i (0 where the sum is 0), d_j = dw_j, times scale:
+//   sigmoid, plain          dl_j = d_j s_j (1 - s_j), other experts 0
+//   sigmoid, renormalised   dl_j = w_j (1 - s_j) sum_i w_i (d_j - d_i)
+//   softmax, renormalised   dl_j = w_j sum_i w_i (d_j - d_i)
+//   softmax, plain          dl_e = -p_e sum_i d_i p_i for the experts not chosen,
+//                           dl_j = p_j (sum_i p_i (d_j - d_i) + d_j r),  r = the share of the experts not chosen
+// In this form nothing cancels but what dw itself cancels: 1 - s_j is sigmoid(-l_j), and the sum over the chosen goes over
+// differences instead of d_j less the mean, which of a confident expert (w_j or p_j near 1) leaves rounding errors alone.
+// No quotient of a score but w_j either, so tiny scores do not overflow.
 // One warp per token; an entry of topk_idx outside [0, E) takes no part.  Bound by writing the row, which is written as if
 // nothing were chosen and then corrected at the k chosen entries (8192 x 1024: 7.8 us for 34 MB, 11.5 when every column was
 // compared with every choice; 8192 x 256: about the cost of a launch); the plain softmax by its exponentials and
@@ -290,6 +291,7 @@ __global__ void __launch_bounds__(kSelThreads, EPL <= 8 ? 5 : 4)
   if (t >= T) return;
   const float* row = logits + t * E;
   // only a softmax that is not renormalised has a gradient for the experts not chosen, and needs every score in it
+  const bool dense = SOFTMAX && !renorm;
   SoftmaxStats st{0.0f, 1.0f};
   float l[SOFTMAX ? EPL : 1];
   if constexpr (SOFTMAX) {
@@ -305,12 +307,11 @@ __global__ void __launch_bounds__(kSelThreads, EPL <= 8 ? 5 : 4)
     if (e >= 0) {
       const float lj = __ldg(row + e);
       s = SOFTMAX ? softmax_score(lj, st) : sigmoid_f32(lj);
-      if (!SOFTMAX) comp = sigmoid_f32(-lj);     // 1 - s of the rounded s has lost its bits where s is near 1
+      if (!SOFTMAX) comp = sigmoid_f32(-lj);
       d = __ldg(dw + t * k + lane);
     }
   }
-  // value of a chosen expert's entry beyond what every expert gets; an expert chosen twice gets both
-  float mine, dot = 0.0f;
+  float v = 0.0f, all = 0.0f;                    // of the chosen expert's entry, and of every other one's, before scale
   if (renorm) {
     float sum = 0.0f;
     for (int j = 0; j < k; ++j) sum += __shfl_sync(kFull, s, j);
@@ -318,21 +319,50 @@ __global__ void __launch_bounds__(kSelThreads, EPL <= 8 ? 5 : 4)
     float acc = 0.0f;
     for (int j = 0; j < k; ++j)
       acc = fmaf(__shfl_sync(kFull, w, j), __fsub_rn(d, __shfl_sync(kFull, d, j)), acc);
-    mine = w * comp * acc;
+    v = w * comp * acc;
   } else {
-    for (int j = 0; j < k; ++j) dot = fmaf(__shfl_sync(kFull, d, j), __shfl_sync(kFull, s, j), dot);
-    mine = d * s * comp;
+    v = d * s * comp;
   }
-  const float all = SOFTMAX && !renorm ? __fmul_rn(dot, scale) : 0.0f;
-  float v = 0.0f;
-  for (int j = 0; j < k; ++j) {
-    const int ej = __shfl_sync(kFull, e, j);
-    const float vj = __shfl_sync(kFull, mine, j);
-    if (ej == e) v += vj;
+  if constexpr (SOFTMAX) {
+    if (dense) {
+      // D: the sum of the slots that chose the expert; `first`: the first of them, which stands for it below
+      float D = 0.0f, rest = 0.0f;
+      bool first = e >= 0;
+      unsigned mine = 0u;                        // bit i: expert i * 32 + lane is chosen
+      for (int j = 0; j < k; ++j) {
+        const int ej = __shfl_sync(kFull, e, j);
+        const float dj = __shfl_sync(kFull, d, j);
+        all = fmaf(dj, __shfl_sync(kFull, s, j), all);
+        if (ej == e) {
+          D += dj;
+          if (j < lane) first = false;
+        }
+        if (ej >= 0 && (ej & 31) == lane) mine |= 1u << (ej >> 5);
+      }
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (i * 32 + lane < E && !((mine >> i) & 1u)) rest += l[i];
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) rest += __shfl_xor_sync(kFull, rest, o);
+      const float once = first ? s : 0.0f;
+      float acc = __fmul_rn(D, softmax_share(rest, st));
+      for (int j = 0; j < k; ++j)
+        acc = fmaf(__shfl_sync(kFull, once, j), __fsub_rn(D, __shfl_sync(kFull, D, j)), acc);
+      v = s * acc;
+    }
+  }
+  if (!dense) {
+    // an expert chosen twice gets both
+    float both = 0.0f;
+    for (int j = 0; j < k; ++j) {
+      const int ej = __shfl_sync(kFull, e, j);
+      const float vj = __shfl_sync(kFull, v, j);
+      if (ej == e) both += vj;
+    }
+    v = both;
   }
   v = __fmul_rn(v, scale);
-  if constexpr (SOFTMAX)
-    if (!renorm) v -= __fmul_rn(all, s);
+  all = __fmul_rn(all, scale);
   // the row as if nothing were chosen, then the chosen entries: the warp's stores to one address are in this order
   float* out = dl != nullptr ? dl + t * E : nullptr;
   __nv_bfloat16* out_bf16 = dl_bf16 != nullptr ? dl_bf16 + t * E : nullptr;
@@ -342,7 +372,7 @@ __global__ void __launch_bounds__(kSelThreads, EPL <= 8 ? 5 : 4)
     if (c < E) {
       float g = 0.0f;
       if constexpr (SOFTMAX)
-        if (!renorm) g = __fsub_rn(0.0f, __fmul_rn(all, softmax_share(l[i], st)));
+        if (dense) g = __fsub_rn(0.0f, __fmul_rn(all, softmax_share(l[i], st)));
       if (out != nullptr) out[c] = g;
       if (out_bf16 != nullptr) out_bf16[c] = __float2bfloat16_rn(g);
     }

@@ -129,3 +129,20 @@ def test_renormalised_over_tiny_scores():
     got = binding.moe_route_select_backward(l.to(DEV), idx.to(DEV), dw.to(DEV), "sigmoid", True, 2.5)
     ref, size = gradient(l, idx, dw, "sigmoid", True, 2.5)
     assert (np.abs(got.double().cpu().numpy() - ref) <= (64 + 6 * 4 + 16) * 2.0 ** -24 * size).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,k", SIZES)
+@pytest.mark.parametrize("z", GAPS)
+def test_softmax(T, E, k, z):
+    check(*confident(T, E, k, z, 6), "softmax", False)
+
+
+@pytest.mark.gpu
+def test_softmax_over_every_expert():
+    """All chosen: no share is left over, and equal dw have no gradient."""
+    from serve_invariant_moe_gb300 import binding
+    l = torch.randn(7, 30, generator=torch.Generator().manual_seed(7))
+    idx = torch.arange(30, dtype=torch.int32).expand(7, 30).contiguous()
+    got = binding.moe_route_select_backward(l.to(DEV), idx.to(DEV), torch.ones(7, 30, device=DEV), "softmax", False)
+    assert (got == 0).all()
