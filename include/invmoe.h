@@ -579,7 +579,8 @@ int fp8_gemm(const void* a, const float* a_scale, const void* b, const float* b_
 
 /* The experts' gate/up product, SwiGLU and re-quantisation: for every expert e and its rows r,
  *   g, u = fp8_gemm of xp[r] with w13[e] (gate rows 0..F-1, up rows F..2F-1), not stored
- *   h[r] = g / (1 + exp(-g)) * u in fp32, quantised per 128 columns: h [T*k, F] e4m3 with
+ *   h[r] = g / (1 + exp(-g)) * u in fp32 (the quotient a product with a reciprocal, within two
+ *          units in the last place), quantised per 128 columns: h [T*k, F] e4m3 with
  *          h_scale [T*k, F / 128]
  * w13 [E, 2F, H] e4m3, w13_scale [E, 2F / 128, ceil(H / 128)].  plan as moe_grouped_ffn's;
  * NULL with E = k = 1: one expert for all T rows (a shared expert).
