@@ -4,14 +4,17 @@
 // one token, its kernel 3: five outputs at 1.5 us each, four checks, fourteen argument conversions.  Here a check, an
 // allocation and a whole call each are one C function: checks read the tensor directly, outputs come from the caching
 // allocator without the dispatcher, and a call converts its arguments by the C prototype and adds the current stream.  The
-// norm's functions, which have most outputs, are C as a whole (one token 9.5 -> 6.3 us, of which five allocations are 3.4
+// norm's functions, which have most outputs, are C as a whole (one token 9.5 -> 6.4 us, of which five allocations are 3.5
 // and the launch 2.1; 2.9 with the caller's outputs; routing, with two outputs, would gain 0.3 of 4.7).
 // The entry points called are those of include/invmoe.h; nothing is computed here.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <ATen/Context.h>
 #include <ATen/EmptyTensor.h>
 #include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -108,8 +111,12 @@ PyObject* check(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// On the current device, which is that of every input checked before: no device guard, 0.13 us less of 0.8.
+// On the current device, which is that of every input checked before: no device guard, 0.13 us less of 0.8.  Where a
+// dispatch mode is on, or uninitialised memory is to be filled, by the dispatcher, as torch.empty would.
 PyObject* new_output(long code, at::IntArrayRef dims) {
+  const at::Context& ctx = at::globalContext();
+  if (c10::impl::dispatch_mode_enabled() || (ctx.deterministicAlgorithms() && ctx.deterministicFillUninitializedMemory()))
+    return THPVariable_Wrap(at::empty(dims, at::TensorOptions().dtype(kTypes[code]).device(at::kCUDA)));
   return THPVariable_Wrap(at::Tensor(at::detail::empty_generic(dims, c10::cuda::CUDACachingAllocator::get(),
                                                                c10::DispatchKeySet(c10::DispatchKey::CUDA), kTypes[code],
                                                                std::nullopt)));
