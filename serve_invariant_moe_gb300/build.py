@@ -4,7 +4,7 @@ Each .cu translation unit is compiled in parallel into ``_build/`` and linked
 into ``serve_invariant_moe_gb300/libinvmoe.so``; csrc/marshal.cpp (the binding's
 CPython helpers, against the installed torch's headers) becomes ``_marshal.so``.
 A unit is recompiled only when it, or a header in csrc/ or include/, is newer
-than its object file.
+than its object file, the helpers also when torch or Python is another one.
 """
 import concurrent.futures as cf
 import os
@@ -46,6 +46,12 @@ def _torch_dirs():
     import torch
     root = os.path.dirname(torch.__file__)
     return os.path.join(root, "include"), os.path.join(root, "lib"), int(torch._C._GLIBCXX_USE_CXX11_ABI)
+
+
+def _host():
+    """What the helpers' object was compiled against: torch's C++ interface and Python's change with their versions."""
+    import torch
+    return "\n".join([torch.__version__, torch.__file__, sys.version])
 
 
 def _compile_command(src, obj, verbose_ptxas):
@@ -90,9 +96,12 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int = None) ->
     srcs = _sources()
     hdr = _headers_mtime()
     todo = []
+    marshal_src, stamp, host = os.path.join(CSRC, "marshal.cpp"), os.path.join(BUILD, "marshal.host"), _host()
+    same_host = os.path.exists(stamp) and open(stamp).read() == host
     for s in srcs:
         obj = _object(s)
-        if force or verbose_ptxas or not os.path.exists(obj) or os.path.getmtime(obj) < max(os.path.getmtime(s), hdr):
+        if (force or verbose_ptxas or not os.path.exists(obj) or os.path.getmtime(obj) < max(os.path.getmtime(s), hdr)
+                or (s == marshal_src and not same_host)):
             todo.append(s)
     logs = []
     if todo:
@@ -103,7 +112,7 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int = None) ->
     if todo or _stale(LIB, objs):
         _link([nvcc()] + ARCH + ["-shared", "-o", LIB + ".tmp"] + objs + ["-cudart", "static"])
         os.replace(LIB + ".tmp", LIB)
-    marshal = _object(os.path.join(CSRC, "marshal.cpp"))
+    marshal = _object(marshal_src)
     if todo or _stale(MARSHAL, [marshal, LIB]):
         torch_lib = _torch_dirs()[1]
         # libinvmoe.so is found beside it; torch's libraries are in the process already
@@ -111,6 +120,9 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int = None) ->
                "-L", torch_lib, f"-Wl,-rpath,{torch_lib}", "-lc10", "-ltorch_cpu", "-lc10_cuda", "-ltorch_cuda",
                "-ltorch_python"])
         os.replace(MARSHAL + ".tmp", MARSHAL)
+    if not same_host:
+        with open(stamp, "w") as f:
+            f.write(host)
     if verbose_ptxas:
         sys.stderr.write("".join(logs))
     return LIB
