@@ -366,15 +366,6 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// Arrive on an mbarrier of the pair (possibly the peer CTA's) with CTA-scope release: for an
-// epilogue warp that frees TMEM columns.  The arrive follows tcgen05.wait::ld, so the columns' loads
-// are complete; it hands over no global or shared data, and a cluster-scope release would first wait
-// for the warp's earlier global stores to become visible cluster-wide (same-box A/B: fp32 down
-// projection in token columns 153 -> 141 us on the Qwen-like layer, GLM-scale -1 %).
-__device__ __forceinline__ void mbar_arrive_remote_cta(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
 __device__ __forceinline__ void st_shared_remote_u32(uint32_t cluster_addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }

@@ -77,6 +77,15 @@ __device__ __forceinline__ void tma_load_5d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+// Arrive on an mbarrier of the pair (possibly the peer CTA's) with CTA-scope release: for an
+// epilogue warp that frees TMEM columns.  The arrive follows tcgen05.wait::ld, so the columns' loads
+// are complete; it hands over no global or shared data, and a cluster-scope release would first wait
+// for the warp's earlier global stores to become visible cluster-wide (same-box A/B: fp32 down
+// projection in token columns 153 -> 141 us on the Qwen-like layer, GLM-scale -1 %).
+__device__ __forceinline__ void mbar_arrive_remote_cta(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 constexpr int kTokChunk = 320;     // most tokens (TMEM columns) of one unit
 constexpr int kTokBoxRows = 32;    // token rows per TMA box: 32, 64 or 128 (a CTA's share of one MMA) ...
 constexpr int kTokMidRows = 64;
