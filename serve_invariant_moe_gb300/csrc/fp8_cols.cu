@@ -2,11 +2,11 @@
 //
 // Weights are the MMA's M side (MT sub-tiles of WR rows; a sub-tile lies in one scale block, so its scale is one number
 // per block of K) and tokens its N side, in multiples of 16: a group of 20 tokens costs 32 columns, not 128 rows.
-// What bounds it is reading the weights (64 experts of 2 x 2048 x 6144, 4 tokens: 95 us, 6.3 TB/s of DRAM), and, for one
-// small matrix, latency: a step of KS K blocks goes through every handover at once (one copy per operand, one ring stage,
-// one TMEM buffer, one set of scales, one wait of each role), and where 256-row tiles would leave SMs without work 64-row
-// tiles are used (8 x 4096 x 6144: 64 CTAs instead of 16; 8 us, of which 2 until the first block is there, 4 for twelve
-// steps and the rest launch and output; 32-row tiles on 128 CTAs: 8.5).
+// What bounds it is reading the weights (4 tokens that reach 24 of 64 experts of 2 x 2048 x 6144, 604 MB: 95 us, 6.3 TB/s of
+// DRAM), and, for one small matrix, latency: a step of KS K blocks goes through every handover at once (one copy per operand,
+// one ring stage, one TMEM buffer, one set of scales, one wait of each role), and where 256-row tiles would leave SMs without
+// work 64-row tiles are used (8 x 4096 x 6144: 64 CTAs instead of 16; 8 us, of which 2 until the first block is there, 4 for
+// twelve steps and the rest launch and output; 32-row tiles on 128 CTAs: 8.5).
 //   * warp 0: one thread copies; with K % 128 == 0 the KS blocks of a box come in one rank-3 copy;
 //   * warp 1: one thread issues the MMAs, 4 K = 32 steps per block and sub-tile, each block into columns of its own;
 //   * warps 2 and 3: the scales, from global memory four blocks ahead, into the slot of the TMEM buffer they belong to
@@ -506,10 +506,10 @@ int launch_plain(const Fp8Call& c, const Fp8Params& p, int nt, bool small, cudaS
 
 // Which kernel and tile: by the rows of a group (all rows of a dense call; the average, half as much again for the spread
 // around it, of a grouped one) and by what fills the machine.
-//   * at most 64 rows: columns, in 16, 32 or 64.  With 16 or 32 the tile is 256 weight rows (64 experts of 6144 x 2048, 4
-//     tokens: 49.7 us, with 64-row tiles 51.5), or 64 where that would not give every SM one (8 x 4096 x 6144: 8 us); with
-//     64, where a step holds fewer blocks of the larger tile, 64 rows (256 tokens for those experts: 143 us against 156);
-//   * more: the row tiles (512 tokens for those experts: 154 us against 210 in columns), unless the 64-row tiles are done
+//   * at most 64 rows: columns, in 16, 32 or 64.  With 16 or 32 the tile is 256 weight rows (4 tokens that reach 24 of
+//     64 experts of 6144 x 2048, 302 MB: 49.7 us, with 64-row tiles 51.5), or 64 where that would not give every SM one (8 x 4096 x 6144: 8 us); with
+//     64, where a step holds fewer blocks of the larger tile, 64 rows (256 tokens, all 64 experts: 143 us against 156);
+//   * more: the row tiles (512 tokens, the same experts: 154 us against 210 in columns), unless the 64-row tiles are done
 //     in two waves, when 128-row tiles leave most SMs idle (128 x 4096 x 6144: 12 us against 26, 256 rows: 20 against 26,
 //     320 rows, three waves: 28 against 26).
 int fp8_gemm_run(const Fp8Call& c, cudaStream_t st) {

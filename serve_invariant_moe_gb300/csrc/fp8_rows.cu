@@ -3,13 +3,15 @@
 // Tokens are the MMA's M side: a CTA computes 128 token rows x 256 weight rows (one N = 256 MMA per K = 32
 // step).  A thread holds one token row, so its scale is one number per block, read from global memory four blocks ahead:
 // no shared memory on the scaling path, where the kernel of few tokens reads a scale for every column.
-// 8192 x 4096 x 6144 takes 166 us (2.48 PFLOP/s), 64 experts' gate and up of 2048 x 6144 with about 256 rows each 425 us.
+// Ten calls in a row on the same inputs: 8192 x 4096 x 6144 takes 166 us (2.48 PFLOP/s), 64 experts' gate and up of 2048 x
+// 6144 with about 256 rows each 435 us; in a long run, under the power limit, the dense product takes 180.
 // What bounds it is the handover of the products, 128 x 256 fp32 per block through two TMEM buffers: with the waits and
-// arrives alone the dense product takes 134 us (a block is then 769 cycles, what its 48 KB take from L2 at 64 bytes a cycle
-// and SM), with the loads from TMEM 147, with the 256 FFMA issue cycles per scheduler 169.  So a buffer is released as soon
-// as its last columns are in registers, arrives are predicated, one elected thread issues, and how scales are loaded is
-// known at compile time (169 -> 166).  Rows that do not start on 128 bytes (K % 128 != 0) cost a quarter more, since a
-// box's rows then touch five sectors instead of four (4000 x 4096: K = 6144 95 us, 6160 120).
+// arrives alone the dense product takes 134 us (a block is then 769 cycles: its 48 KB are written to shared memory and read
+// from it, 768 cycles at 128 bytes; taking them from L2 at 64 bytes a cycle and SM would cost the same, and no measurement
+// tells the two apart), with the loads from TMEM 147, with the 256 FFMA issue cycles per scheduler 169.  So a buffer is
+// released as soon as its last columns are in registers, arrives are predicated, one elected thread issues, and how scales
+// are loaded is known at compile time (169 -> 166).  Rows that do not start on 128 bytes (K % 128 != 0) cost a quarter more,
+// since a box's rows then touch five sectors instead of four (4000 x 4096: K = 6144 95 us, 6160 121).
 // Measured and not kept: CTA pairs with 256 x 256 tiles, 167 us, but 483 for those 64 experts, because the tiles are twice
 // as high; loads of 16 columns, 175, or two loads of 32 at once, no change; blocks unrolled by two, 188; the last columns
 // added behind the next block's wait, which spills, 229; packed fma.rn.f32x2, 690 instead of 485 cycles a block.
@@ -229,7 +231,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     take_registers();
     const int q = warp & 3;                            // TMEM lane quadrant
     const int ew = warp - kFirstEpiWarp;
-    const int half = ew >> 2;                          // warpgroup: weight rows 64 half .. + 63 of either CTA's 128
+    const int half = ew >> 2;                          // warpgroup: weight rows 64 half .. + 63 of either 128
     const int r_in_tile = q * 32 + lane;
     uint8_t* stg = ostage + ew * (bulk ? 32 * 128 : 32 * 64);
     const uint32_t on = lane == 0 ? 1u : 0u;

@@ -4,8 +4,9 @@
 // one token, its kernel 3: five outputs at 1.5 us each, four checks, fourteen argument conversions.  Here a check, an
 // allocation and a whole call each are one C function: checks read the tensor directly, outputs come from the caching
 // allocator (through the dispatcher only where torch has something to do there), and a call converts its arguments by the C
-// prototype and adds the current stream.  The norm's functions, which have most outputs, are C as a whole (one token 9.5 -> 6.4 us, of which five allocations are 3.5
-// and the launch 2.1; 2.9 with the caller's outputs; routing, with two outputs, would gain 0.3 of 4.7).
+// prototype and adds the current stream.  The norm's functions, which have most outputs, are C as a whole (one token 9.5 ->
+// 6.4 us, of which five allocations are 3.5 and the launch 2.1; 2.9 with the caller's outputs; routing, with two outputs,
+// would gain 0.3 of 4.7).
 // The entry points called are those of include/invmoe.h; nothing is computed here.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>

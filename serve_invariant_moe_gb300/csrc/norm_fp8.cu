@@ -182,8 +182,10 @@ __global__ void __launch_bounds__(max_threads(V)) norm_kernel(const TX* __restri
 
 // Backward: g = dy * w, n = r * rstd, dr = rstd * (g - n * mean(g n)) + dres; dw = sum_t dy n.  A block walks
 // rows_per_block consecutive rows and keeps its share of dw in registers; the partial rows are summed in order by
-// dweight_kernel, so no atomics and one order for a given T and H.  4096 x 2048, fp32 dy, bf16 x: 16.5 us on the device for
-// 84 MB, 5.1 TB/s; what is left over a copy is the start (nine rows a block) and the second kernel.
+// dweight_kernel, so no atomics and one order for a given T and H.  4096 x 2048, fp32 dy, bf16 x and dres: 18.8 us a
+// call for 84 MB, 4.5 TB/s, of which this kernel takes 13 and dweight_kernel 4; what is left over a copy is the start (nine
+// rows a block) and the second kernel.  Narrow rows leave a block one or two warps and one row in flight, so they are bound
+// by latency, not by memory (cold, 8192 rows of 128: 21 us, 0.4 TB/s; of 512: 23 us, 1.5 TB/s).
 template <int V, typename TX, typename TD>
 __global__ void __launch_bounds__(max_threads(V)) norm_bwd_kernel(const TD* __restrict__ dy, const TX* __restrict__ x,
                                                         const __nv_bfloat16* __restrict__ weight,
@@ -497,9 +499,10 @@ int norm_launch(const void* x, int x_f32, const void* res, int res_f32, const vo
   return check_cuda(e, "norm_kernel");
 }
 
-// Rows of one block, and so of one partial row of dw: as many blocks as are resident at once, three of at most 256 threads
-// to an SM, two where a thread has two vectors, one of more threads.  More blocks write more partial rows and leave a
-// partly filled wave (1000 x 6144: 18 us with 456 blocks, 12.6 with 152), fewer leave registers idle (4096 x 2048: 13 us
+// Rows of one block, and so of one partial row of dw: as many blocks as are resident at once for rows of 2048 and more,
+// three of 256 threads to an SM, two where a thread has two vectors, one of more threads (narrower rows, of which more
+// blocks would fit, take the 456 too).  More blocks write more partial rows and leave a partly filled wave (1000 x 6144,
+// both kernels: 18 us with 456 blocks, 12.6 with 152), fewer leave registers idle (4096 x 2048, norm_bwd_kernel alone: 13 us
 // with 456, 17 with 304; 8192 x 4096: 56 with 456, 48 with 304, 66 with 152).  A function of T and H alone, not of the
 // device, so that the order of the sum is too.
 int norm_bwd_rows(int T, int H) {

@@ -276,9 +276,9 @@ __global__ void __launch_bounds__(kSelThreads, select_blocks(EPL)) select_kernel
 // differences instead of d_j less the mean, which of a confident expert (w_j or p_j near 1) leaves rounding errors alone.
 // No quotient of a score but w_j either, so tiny scores do not overflow.
 // One warp per token; an entry of topk_idx outside [0, E) takes no part.  Bound by writing the row, which is written as if
-// nothing were chosen and then corrected at the k chosen entries (8192 x 1024: 7.8 us for 34 MB, 11.5 when every column was
-// compared with every choice; 8192 x 256: about the cost of a launch); the plain softmax by its exponentials and
-// divisions (8192 x 1024: 25 us).
+// nothing were chosen and then corrected at the k chosen entries (8192 x 1024, renormalised sigmoid: 8.6 us for 34 MB, half
+// as much again when every column was compared with every choice; 8192 x 256: 5.4 us); the plain softmax by its exponentials
+// and divisions (8192 x 1024: 28 us, of which the sum over the experts not chosen is 2).
 template <int EPL, bool SOFTMAX>
 __global__ void __launch_bounds__(kSelThreads, EPL <= 8 ? 5 : 4)
     select_bwd_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx, const float* __restrict__ dw,
