@@ -74,6 +74,11 @@ extern "C" {
 #define INVMOE_SCORE_SIGMOID 0
 #define INVMOE_SCORE_SOFTMAX 1
 
+/* Gates (sandwich_norm). */
+#define INVMOE_GATE_NONE    0
+#define INVMOE_GATE_CHANNEL 1
+#define INVMOE_GATE_TOKEN   2
+
 /* Library version (major*10000 + minor*100 + patch). */
 int invmoe_version(void);
 
@@ -594,6 +599,77 @@ int moe_grouped_swiglu_fp8(const void* xp, const float* xp_scale, const int32_t*
 int moe_grouped_down_fp8(const void* h, const float* h_scale, const int32_t* plan, const void* w2,
                          const float* w2_scale, int T, int H, int E, int k, int F, float* y, void* workspace,
                          size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * A drafted decode step: norms around a block, verification of drafted tokens
+ * ------------------------------------------------------------------------- */
+
+/* The norms after and before a block, of the block's output x and the residual stream:
+ *   n = (x * rstd_post) * w_post,  rstd_post = 1 / sqrt(mean(x^2) + eps)
+ *   r' = residual_scale * residual + n * (branch_scale * gate)
+ *        (fp32, rounded to the residual's type and stored in residual_out, which may be
+ *        residual itself; no other two arrays may overlap)
+ *   y = (r' * rstd) * w_next,  rstd = 1 / sqrt(mean(r'^2) + eps), of the row as stored
+ * out [T, H] bf16 = y and/or q [T, H] e4m3 with scale [T, ceil(H / 128)] = y quantised from
+ * fp32.  w_next NULL: no second norm, out, q, scale and rstd are NULL.  rstd_post and rstd
+ * [T] fp32 (nullable).  x, residual [T, H]: INVMOE_BF16 or INVMOE_F32; w_post, w_next [H]
+ * bf16; gate: NULL, [H] bf16 (INVMOE_GATE_CHANNEL) or [T] fp32 (INVMOE_GATE_TOKEN, 4-byte
+ * aligned).  Shapes: H % 16 == 0, H <= 32768. */
+int sandwich_norm(const void* x, int x_type, const void* w_post, const void* residual, int residual_type, const void* gate,
+                  int gate_kind, const void* w_next, int T, int H, float residual_scale, float branch_scale, float eps,
+                  void* residual_out, void* out, void* q, float* scale, float* rstd_post, float* rstd, void* stream);
+
+/* Workspace of sandwich_norm_backward. */
+size_t sandwich_norm_backward_workspace_size(int T, int H);
+
+/* Backward of sandwich_norm at its input x, its stored row r' (residual here) and its two
+ * rstd; rounding and quantisation are passed straight through:
+ *   d = dres + rstd * (dy * w_next - r^ * mean(dy * w_next * r^)),  r^ = r' * rstd
+ *   dresidual = residual_scale * d                     [T, H], the residual's type
+ *   dx = rstd_post * (u - n^ * mean(u * n^))           [T, H], x's type, with
+ *        n^ = x * rstd_post, u = branch_scale * gate * d * w_post
+ *   dw_next [H] = sum_t dy * r^
+ *   dw_post [H] = branch_scale * sum_t gate * d * n^
+ *   dgate [H] = branch_scale * sum_t d * w_post * n^   (a channel's gate)
+ *   dgate [T] = branch_scale * sum_h d * w_post * n^   (a token's gate)
+ * dy [T, H] of dy_type, with w_next and rstd, or all three NULL (no second norm: dres is
+ * then required and residual is not read); dres [T, H] of the residual's type (nullable).
+ * dw_post, dw_next, dgate: fp32, rows summed in a fixed order; each nullable, but dw_next
+ * and a channel's dgate come with dw_post.  dx and dresidual overlap nothing. */
+int sandwich_norm_backward(const void* dy, int dy_type, const void* dres, const void* x, int x_type, const void* w_post,
+                           const float* rstd_post, const void* residual, int residual_type, const void* w_next,
+                           const float* rstd, const void* gate, int gate_kind, int T, int H, float residual_scale,
+                           float branch_scale, void* dx, void* dresidual, float* dw_post, float* dw_next, float* dgate,
+                           void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace of verify_drafts; need not be zero. */
+size_t verify_workspace_size(int B, int D, int V);
+
+/* Drafted tokens of B requests against the target's probabilities.  logits [B, D + 1, V]: a
+ * request's row i is the target's distribution of its i-th new token; draft_tokens [B, D]
+ * int32 and draft_logits [B, D, V] (nullable: the drafter put all its mass on its token) are
+ * what was drafted; both logits INVMOE_BF16 or INVMOE_F32.  With p_i, q_i the softmax of row i
+ * over tau:
+ *   accept   draft i = 0, 1, ... while accept_u[i] * q_i(x_i) < p_i(x_i), accept_u [B, D] fp32
+ *            in [0, 1); a draft token outside [0, V) is not accepted
+ *   draw     the token after the n accepted ones: the j with the largest w_j / noise[j], noise
+ *            [B, V] fp32 drawn from the exponential distribution, w = max(p_n - q_n, 0) after
+ *            a rejection, p_n where every draft was accepted or that is zero everywhere; an
+ *            equal score goes to the lower index, a noise that is negative or NaN takes no part
+ * tau: temperature [B] fp32, or the scalar tau where that is NULL.  0 (and, of a request's
+ * own, anything not positive): drafts are accepted while they are the target row's largest
+ * logit (lowest index of equal ones), which is also the next token; accept_u and noise are not
+ * used.  n_draft [B] int32 (nullable: D): drafts of a request, the rest of its rows is not read.
+ * A NaN logit counts as -inf, +inf as the largest finite number; a target row of -inf alone
+ * accepts nothing and gives token -1.
+ * Outputs: tokens [B, D + 1] int32 = the n accepted drafts, the drawn token, then -1;
+ * n_accepted [B] int32; logp [B, D + 1] fp32 = log p_i of the emitted tokens (at temperature 1
+ * where tau is 0; -inf for token -1), then 0.  noise is read also for D = 0: plain sampling.
+ * Every request's bits are its own.  Shapes: D <= 32, any V. */
+int verify_drafts(const void* logits, int logits_type, const void* draft_logits, const int32_t* draft_tokens,
+                  const float* accept_u, const float* noise, const int32_t* n_draft, const float* temperature, float tau,
+                  int B, int D, int V, int32_t* tokens, int32_t* n_accepted, float* logp, void* workspace, size_t ws_bytes,
+                  void* stream);
 
 /* ---------------------------------------------------------------------------
  * rl_token_loss -- IcePop-masked clipped policy loss and DIS weights per token

@@ -759,6 +759,128 @@ def moe_grouped_down_fp8(h, h_scale, plan, w2, w2_scale, T, k, workspace, y=None
     return y
 
 
+# ---------------------------------------------------------------------------
+# A drafted decode step: norms around a block, verification of drafted tokens
+# ---------------------------------------------------------------------------
+
+def _gate(m, gate, T, H):
+    """The gate's kind by its type and shape: None, [H] bf16 (per channel) or [T] fp32 (per token)."""
+    if gate is None:
+        return 0
+    if gate.dtype == torch.bfloat16:
+        m.check(gate, "gate", BF16_, H)
+        return 1
+    if gate.dtype == torch.float32:
+        m.check(gate, "gate", F32_, T)
+        return 2
+    raise ValueError(f"gate must be [H] torch.bfloat16 or [T] torch.float32, got {gate.dtype}")
+
+
+def sandwich_norm(x, w_post, residual, w_next=None, gate=None, residual_scale=1.0, branch_scale=1.0, eps=1e-6, out=True,
+                  fp8=False, residual_out=None, q=None, scale=None, rstd_post=None, rstd=None):
+    """The norms after and before a block: dict(residual, out, q, scale, rstd_post, rstd).
+
+    residual = residual_scale * residual + branch_scale * gate * rms_norm(x) * w_post, stored in the residual's type (into
+    ``residual_out``, which may be ``residual`` itself); out = rms_norm(residual) * w_next in bf16 (a tensor to fill, True or
+    False), with ``fp8`` also as the e4m3 row with a scale per 128 columns.  Without w_next there is no second norm.
+    x, residual [T, H] bf16 or fp32; weights [H] bf16; gate None, [H] bf16 (a channel's) or [T] fp32 (a token's)."""
+    r = marshal().sandwich(x, w_post, residual, w_next, gate, residual_scale, branch_scale, eps, out, fp8, residual_out, q,
+                           scale, rstd_post, rstd)
+    return r if r.__class__ is dict else check(r)
+
+
+def sandwich_norm_backward_workspace_size(T, H) -> int:
+    return int(lib().sandwich_norm_backward_workspace_size(T, H))
+
+
+def sandwich_norm_backward(dy, dres, x, w_post, rstd_post, residual, w_next=None, rstd=None, gate=None, residual_scale=1.0,
+                           branch_scale=1.0, dx=None, dresidual=None, dweights=True, workspace=None):
+    """Backward of sandwich_norm at its x, its stored row (``residual`` here: its ``residual`` output) and its rstd_post and
+    rstd: dict(dx, dresidual, dw_post, dw_next, dgate).
+
+    dy [T, H] bf16 or fp32: the gradient of ``out`` (None without w_next); dres [T, H] in the residual's type: the gradient
+    that reaches the stored row from the residual stream (None: none).  dx has x's type, dresidual the residual's; the
+    weights' gradients are fp32 [H] (skipped with dweights=False), dgate [H] or [T] fp32 as the gate.  ``workspace``:
+    sandwich_norm_backward_workspace_size bytes (allocated if not given)."""
+    m = marshal()
+    T, H = _dims(x, "x")
+    xt, rt = _type(x, "x"), _type(residual, "residual")
+    m.check(x, "x", xt, T, H)
+    m.check(residual, "residual", rt, T, H)
+    m.check(w_post, "w_post", BF16_, H)
+    m.check(rstd_post, "rstd_post", F32_, T)
+    if (dy is None) != (w_next is None) or (dy is None) != (rstd is None):
+        raise ValueError("dy, w_next and rstd go together")
+    yt = 0
+    if dy is not None:
+        yt = _type(dy, "dy")
+        m.check(dy, "dy", yt, T, H)
+        m.check(w_next, "w_next", BF16_, H)
+        m.check(rstd, "rstd", F32_, T)
+    if dres is not None:
+        m.check(dres, "dres", rt, T, H)
+    kind = _gate(m, gate, T, H)
+    dx = _out(m, dx, x, "dx", xt, T, H)
+    dresidual = _out(m, dresidual, x, "dresidual", rt, T, H)
+    dw_post = m.new(x, F32_, H) if dweights else None
+    dw_next = m.new(x, F32_, H) if dweights and dy is not None else None
+    dgate = m.new(x, F32_, T) if kind == 2 else m.new(x, F32_, H) if kind == 1 and dweights else None
+    if workspace is None:
+        workspace = m.new(x, U8_, sandwich_norm_backward_workspace_size(T, H))
+    m.check(workspace, "workspace", U8_)
+    check(m.sandwich_norm_backward(dy, yt, dres, x, xt, w_post, rstd_post, residual, rt, w_next, rstd, gate, kind, T, H,
+                                   residual_scale, branch_scale, dx, dresidual, dw_post, dw_next, dgate, workspace,
+                                   workspace.numel()))
+    return dict(dx=dx, dresidual=dresidual, dw_post=dw_post, dw_next=dw_next, dgate=dgate)
+
+
+def verify_workspace_size(B, D, V) -> int:
+    return int(lib().verify_workspace_size(B, D, V))
+
+
+def verify_drafts(logits, noise, workspace, draft_tokens=None, draft_logits=None, accept_u=None, n_draft=None,
+                  temperature=1.0, tokens=None, n_accepted=None, logp=None):
+    """Accept each request's drafts against the target's probabilities and draw the token that follows:
+    dict(tokens [B, D+1] int32, n_accepted [B] int32, logp [B, D+1] fp32).
+
+    logits [B, D+1, V] bf16 or fp32 of the target; draft_tokens [B, D] int32 with their draft_logits [B, D, V] (None: a
+    drafter without probabilities) and accept_u [B, D] fp32 uniform in [0, 1); n_draft [B] int32: how many of the D count
+    (None: all); noise [B, V] fp32 exponential.  temperature: a number or [B] fp32, 0 for greedy.  Without draft_tokens one
+    token per request is drawn.  tokens: the accepted drafts, the drawn token, -1 behind it; logp: of those tokens, 0 behind.
+    workspace: at least verify_workspace_size(B, D, V) bytes, any content."""
+    m = marshal()
+    B, rows, V = _dims(logits, "logits", 3)
+    D = rows - 1
+    if D < 0:
+        raise ValueError("logits must have at least one row per request")
+    lt = _type(logits, "logits")
+    m.check(logits, "logits", lt, B, D + 1, V)
+    m.check(noise, "noise", F32_, B, V)
+    if D == 0:
+        if draft_tokens is not None or draft_logits is not None or accept_u is not None or n_draft is not None:
+            raise ValueError("logits of one row per request leave no room for drafts")
+    else:
+        m.check(draft_tokens, "draft_tokens", I32_, B, D)
+        m.check(accept_u, "accept_u", F32_, B, D)
+        if draft_logits is not None:
+            m.check(draft_logits, "draft_logits", lt, B, D, V)
+        if n_draft is not None:
+            m.check(n_draft, "n_draft", I32_, B)
+    tau, each = 1.0, None
+    if isinstance(temperature, torch.Tensor):
+        m.check(temperature, "temperature", F32_, B)
+        each = temperature
+    else:
+        tau = temperature
+    m.check(workspace, "workspace", U8_)
+    tokens = _out(m, tokens, logits, "tokens", I32_, B, D + 1)
+    n_accepted = _out(m, n_accepted, logits, "n_accepted", I32_, B)
+    logp = _out(m, logp, logits, "logp", F32_, B, D + 1)
+    check(m.verify_drafts(logits, lt, draft_logits, draft_tokens, accept_u, noise, n_draft, each, tau, B, D, V, tokens,
+                          n_accepted, logp, workspace, workspace.numel()))
+    return {"tokens": tokens, "n_accepted": n_accepted, "logp": logp}
+
+
 def gemm_bf16(a, b, workspace, variant=0, out=None):
     """Diagnostic: the dense tcgen05 GEMM engine alone, d = a @ b^T in fp32.
 

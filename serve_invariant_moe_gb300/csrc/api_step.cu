@@ -1,0 +1,152 @@
+// api_step.cu -- the extern "C" entry points of a drafted decode step: norms around a block, drafted tokens.
+#include <cuda_runtime.h>
+
+#include "checks.h"
+#include "internal.h"
+
+using namespace invmoe;
+
+namespace {
+
+int check_rows(int T, int H, int x_type, int residual_type, const void* gate, int gate_kind, float residual_scale,
+               float branch_scale) {
+  REQUIRE(x_type == INVMOE_BF16 || x_type == INVMOE_F32, INVMOE_ERR_INVALID_ARG, "x_type must be INVMOE_BF16 or INVMOE_F32");
+  REQUIRE(residual_type == INVMOE_BF16 || residual_type == INVMOE_F32, INVMOE_ERR_INVALID_ARG,
+          "residual_type must be INVMOE_BF16 or INVMOE_F32");
+  REQUIRE(T >= 0 && H > 0, INVMOE_ERR_INVALID_ARG, "need T >= 0, H > 0");
+  REQUIRE(H % 16 == 0 && H <= 32768, INVMOE_ERR_UNSUPPORTED_SHAPE, "H=%d is not a multiple of 16 up to 32768", H);
+  REQUIRE(gate_kind == INVMOE_GATE_NONE || gate_kind == INVMOE_GATE_CHANNEL || gate_kind == INVMOE_GATE_TOKEN,
+          INVMOE_ERR_INVALID_ARG, "gate_kind must be INVMOE_GATE_NONE, INVMOE_GATE_CHANNEL or INVMOE_GATE_TOKEN");
+  REQUIRE((gate == nullptr) == (gate_kind == INVMOE_GATE_NONE) || T == 0, INVMOE_ERR_INVALID_ARG,
+          "gate and gate_kind do not go together");
+  REQUIRE(residual_scale == residual_scale && branch_scale == branch_scale, INVMOE_ERR_INVALID_ARG, "a scale is NaN");
+  return INVMOE_OK;
+}
+
+size_t matrix_bytes(int T, int H, int type) { return static_cast<size_t>(T) * H * (type == INVMOE_F32 ? 4 : 2); }
+
+// Two arrays have no byte in common (or one is absent).
+bool apart(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a == nullptr || b == nullptr || x + na <= y || y + nb <= x;
+}
+
+}  // namespace
+
+extern "C" {
+
+int sandwich_norm(const void* x, int x_type, const void* w_post, const void* residual, int residual_type, const void* gate,
+                  int gate_kind, const void* w_next, int T, int H, float residual_scale, float branch_scale, float eps,
+                  void* residual_out, void* out, void* q, float* scale, float* rstd_post, float* rstd, void* stream) {
+  const int rc = check_rows(T, H, x_type, residual_type, gate, gate_kind, residual_scale, branch_scale);
+  if (rc) return rc;
+  REQUIRE(eps >= 0.0f, INVMOE_ERR_INVALID_ARG, "need eps >= 0");
+  REQUIRE((q == nullptr) == (scale == nullptr), INVMOE_ERR_INVALID_ARG, "q and scale go together");
+  if (T == 0) return INVMOE_OK;
+  REQUIRE((w_next != nullptr) == (out != nullptr || q != nullptr), INVMOE_ERR_INVALID_ARG,
+          "w_next goes with an output of the second norm (out, q)");
+  REQUIRE(w_next != nullptr || rstd == nullptr, INVMOE_ERR_INVALID_ARG, "rstd without w_next");
+  REQUIRE_PTR(x); REQUIRE_PTR(w_post); REQUIRE_PTR(residual); REQUIRE_PTR(residual_out);
+  REQUIRE_ALIGNED(x); REQUIRE_ALIGNED(w_post); REQUIRE_ALIGNED(residual); REQUIRE_ALIGNED(residual_out);
+  REQUIRE_ALIGNED(w_next); REQUIRE_ALIGNED(out); REQUIRE_ALIGNED(q);
+  if (gate_kind == INVMOE_GATE_CHANNEL) REQUIRE_ALIGNED(gate);
+  const size_t xn = matrix_bytes(T, H, x_type), rn = matrix_bytes(T, H, residual_type), on = matrix_bytes(T, H, INVMOE_BF16);
+  REQUIRE(same_or_apart(residual_out, residual, rn), INVMOE_ERR_INVALID_ARG,
+          "residual_out overlaps residual without being it");
+  REQUIRE(apart(residual_out, rn, x, xn) && apart(out, on, x, xn) && apart(out, on, residual, rn) &&
+              apart(out, on, residual_out, rn) && apart(q, on / 2, x, xn) && apart(q, on / 2, residual, rn) &&
+              apart(q, on / 2, residual_out, rn) && apart(q, on / 2, out, on),
+          INVMOE_ERR_INVALID_ARG, "an output overlaps another one or an input");
+  return sandwich_launch({x, x_type == INVMOE_F32, w_post, residual, residual_type == INVMOE_F32, gate, gate_kind, w_next, T,
+                          H, residual_scale, branch_scale, eps, residual_out, out, q, scale, rstd_post, rstd},
+                         static_cast<cudaStream_t>(stream));
+}
+
+size_t sandwich_norm_backward_workspace_size(int T, int H) {
+  if (T <= 0 || H <= 0) return kStatusBytes;
+  return kStatusBytes + align_up(T, 64) * sizeof(float) +
+         align_up(static_cast<size_t>(sandwich_bwd_plan(T, H).parts) * 2 * H * sizeof(float), 256);
+}
+
+int sandwich_norm_backward(const void* dy, int dy_type, const void* dres, const void* x, int x_type, const void* w_post,
+                           const float* rstd_post, const void* residual, int residual_type, const void* w_next,
+                           const float* rstd, const void* gate, int gate_kind, int T, int H, float residual_scale,
+                           float branch_scale, void* dx, void* dresidual, float* dw_post, float* dw_next, float* dgate,
+                           void* workspace, size_t ws_bytes, void* stream) {
+  const int rc = check_rows(T, H, x_type, residual_type, gate, gate_kind, residual_scale, branch_scale);
+  if (rc) return rc;
+  REQUIRE(dy_type == INVMOE_BF16 || dy_type == INVMOE_F32, INVMOE_ERR_INVALID_ARG,
+          "dy_type must be INVMOE_BF16 or INVMOE_F32");
+  const bool channel = gate_kind == INVMOE_GATE_CHANNEL;
+  REQUIRE(dw_post != nullptr || (dw_next == nullptr && (dgate == nullptr || !channel)), INVMOE_ERR_INVALID_ARG,
+          "dw_next and a channel gate's dgate come with dw_post");
+  REQUIRE(dw_next == nullptr || w_next != nullptr || T == 0, INVMOE_ERR_INVALID_ARG, "dw_next without w_next");
+  REQUIRE(dgate == nullptr || gate_kind != INVMOE_GATE_NONE, INVMOE_ERR_INVALID_ARG, "dgate without a gate");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    for (float* g : {dw_post, dw_next, channel ? dgate : nullptr}) {
+      if (g == nullptr) continue;
+      const int e = check_cuda(cudaMemsetAsync(g, 0, static_cast<size_t>(H) * sizeof(float), st), "cudaMemsetAsync");
+      if (e) return e;
+    }
+    return INVMOE_OK;
+  }
+  REQUIRE_PTR(workspace);
+  REQUIRE(ws_bytes >= sandwich_norm_backward_workspace_size(T, H), INVMOE_ERR_WORKSPACE_TOO_SMALL, "workspace too small");
+  REQUIRE((dy != nullptr) == (w_next != nullptr) && (dy != nullptr) == (rstd != nullptr), INVMOE_ERR_INVALID_ARG,
+          "dy, w_next and rstd go together");
+  REQUIRE(dy != nullptr || dres != nullptr, INVMOE_ERR_INVALID_ARG, "dy and dres are both NULL");
+  REQUIRE(dy == nullptr || residual != nullptr, INVMOE_ERR_INVALID_ARG, "residual is NULL");
+  REQUIRE_PTR(x); REQUIRE_PTR(w_post); REQUIRE_PTR(rstd_post); REQUIRE_PTR(dx); REQUIRE_PTR(dresidual);
+  REQUIRE_ALIGNED(dy); REQUIRE_ALIGNED(dres); REQUIRE_ALIGNED(x); REQUIRE_ALIGNED(w_post); REQUIRE_ALIGNED(residual);
+  REQUIRE_ALIGNED(w_next); REQUIRE_ALIGNED(dx); REQUIRE_ALIGNED(dresidual); REQUIRE_ALIGNED(workspace);
+  if (channel) REQUIRE_ALIGNED(gate);
+  const size_t xn = matrix_bytes(T, H, x_type), rn = matrix_bytes(T, H, residual_type), yn = matrix_bytes(T, H, dy_type);
+  REQUIRE(apart(dx, xn, dresidual, rn) && apart(dx, xn, x, xn) && apart(dx, xn, dy, yn) && apart(dx, xn, dres, rn) &&
+              apart(dx, xn, residual, rn) && apart(dresidual, rn, x, xn) && apart(dresidual, rn, dy, yn) &&
+              apart(dresidual, rn, dres, rn) && apart(dresidual, rn, residual, rn),
+          INVMOE_ERR_INVALID_ARG, "dx or dresidual overlaps the other or an input");
+  return sandwich_bwd_launch(
+      {dy, dy_type == INVMOE_F32, dres, x, x_type == INVMOE_F32, w_post, rstd_post, residual, residual_type == INVMOE_F32,
+       w_next, rstd, gate, gate_kind, T, H, residual_scale, branch_scale, dx, dresidual, dw_post, dw_next, dgate,
+       reinterpret_cast<float*>(scratch(workspace)), status_word(workspace)},
+      st);
+}
+
+size_t verify_workspace_size(int B, int D, int V) {
+  if (B <= 0 || D < 0 || V <= 0) return kStatusBytes;
+  const size_t chunks = verify_chunks(V);
+  return kStatusBytes + align_up(static_cast<size_t>(B) * sizeof(int32_t), 256) +
+         static_cast<size_t>(B) * (2 * static_cast<size_t>(D) + 2) * chunks * 16;
+}
+
+int verify_drafts(const void* logits, int logits_type, const void* draft_logits, const int32_t* draft_tokens,
+                  const float* accept_u, const float* noise, const int32_t* n_draft, const float* temperature, float tau,
+                  int B, int D, int V, int32_t* tokens, int32_t* n_accepted, float* logp, void* workspace, size_t ws_bytes,
+                  void* stream) {
+  REQUIRE(logits_type == INVMOE_BF16 || logits_type == INVMOE_F32, INVMOE_ERR_INVALID_ARG,
+          "logits_type must be INVMOE_BF16 or INVMOE_F32");
+  REQUIRE(B >= 0 && D >= 0 && V > 0, INVMOE_ERR_INVALID_ARG, "need B, D >= 0 and V > 0");
+  REQUIRE(D <= kVerifyMaxDrafts, INVMOE_ERR_UNSUPPORTED_SHAPE, "D=%d > %d", D, kVerifyMaxDrafts);
+  REQUIRE(temperature != nullptr || tau >= 0.0f, INVMOE_ERR_INVALID_ARG, "need a temperature >= 0");
+  const int chunks = verify_chunks(V), rows = D + 1 + (draft_logits != nullptr ? D : 0);
+  REQUIRE(static_cast<long long>(B) * rows <= 0x7fffffffLL / chunks, INVMOE_ERR_UNSUPPORTED_SHAPE,
+          "too many rows for one launch");
+  REQUIRE_PTR(workspace);
+  REQUIRE(ws_bytes >= verify_workspace_size(B, D, V), INVMOE_ERR_WORKSPACE_TOO_SMALL, "workspace too small");
+  REQUIRE_ALIGNED(workspace);
+  if (B == 0) return INVMOE_OK;
+  REQUIRE_PTR(logits); REQUIRE_PTR(noise); REQUIRE_PTR(tokens); REQUIRE_PTR(n_accepted); REQUIRE_PTR(logp);
+  REQUIRE(D > 0 || draft_logits == nullptr, INVMOE_ERR_INVALID_ARG, "draft_logits without drafts");
+  if (D > 0) { REQUIRE_PTR(draft_tokens); REQUIRE_PTR(accept_u); }
+  REQUIRE_ALIGNED(logits); REQUIRE_ALIGNED(draft_logits); REQUIRE_ALIGNED(noise);
+  uint8_t* s = scratch(workspace);
+  VerifyCall c{logits, draft_logits, draft_tokens, accept_u, noise, n_draft, temperature, tau, B, D, V, rows, chunks,
+               tokens, n_accepted, logp, reinterpret_cast<int32_t*>(s), nullptr, nullptr};
+  s += align_up(static_cast<size_t>(B) * sizeof(int32_t), 256);
+  c.racers = s;
+  c.stats = s + static_cast<size_t>(B) * chunks * 16;
+  return verify_launch(c, logits_type == INVMOE_F32, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -198,10 +198,86 @@ int norm_launch(const void* x, int x_f32, const void* res, int res_f32, const vo
 int norm_bwd_rows(int T, int H);
 int norm_bwd_launch(const void* dy, int dy_f32, const void* x, int x_f32, const void* weight, const float* rstd,
                     const void* dres, int T, int H, void* dx, float* dw, float* part, cudaStream_t st);
+
+struct SandwichCall {
+  const void* x;
+  bool x_f32;
+  const void* w_post;
+  const void* residual;
+  bool res_f32;
+  const void* gate;
+  int gate_kind;
+  const void* w_next;
+  int T, H;
+  float res_scale, branch_scale, eps;
+  void* residual_out;
+  void* out;
+  void* q;
+  float* scale;
+  float* rstd_post;
+  float* rstd;
+};
+int sandwich_launch(const SandwichCall& c, cudaStream_t st);
+
+struct SandwichPlan {
+  int rows, parts;        // rows summed into a partial row, number of partial rows
+};
+SandwichPlan sandwich_bwd_plan(int T, int H);
+
+struct SandwichBwdCall {
+  const void* dy;
+  bool dy_f32;
+  const void* dres;
+  const void* x;
+  bool x_f32;
+  const void* w_post;
+  const float* rstd_post;
+  const void* r;
+  bool res_f32;
+  const void* w_next;
+  const float* rstd;
+  const void* gate;
+  int gate_kind;
+  int T, H;
+  float res_scale, branch_scale;
+  void* dx;
+  void* dresidual;
+  float* dw_post;
+  float* dw_next;
+  float* dgate;
+  float* scratch;         // with dw_post: T floats (rounded up to 64), then the partial rows
+  unsigned int* status;
+};
+int sandwich_bwd_launch(const SandwichBwdCall& c, cudaStream_t st);
+
 int quantize_launch(const void* x, int x_f32, long long banks, int rows, int cols, int block_rows, void* q,
                     float* scale, cudaStream_t st);
 int permute_fp8_launch(const void* q, const float* scale, const int32_t* slot_row, int T, int k, int H, void* xp,
                        float* xp_scale, cudaStream_t st);
+
+// ---------------------------------------------------------------- drafted tokens
+constexpr int kVerifyMaxDrafts = 32;
+struct VerifyCall {
+  const void* logits;          // [B, D + 1, V]
+  const void* draft_logits;    // [B, D, V] or null
+  const int32_t* draft_tokens; // [B, D]
+  const float* accept_u;       // [B, D]
+  const float* noise;          // [B, V]
+  const int32_t* n_draft;      // [B] or null: D
+  const float* temperature;    // [B] or null: tau
+  float tau;
+  int B, D, V;
+  int rows;                    // of a request that have statistics: D + 1, and D with draft logits
+  int chunks;
+  int32_t* tokens;             // [B, D + 1]
+  int32_t* n_accepted;         // [B]
+  float* logp;                 // [B, D + 1]
+  int32_t* done;               // scratch: [B] chunks finished
+  void* stats;                 // scratch: 16 bytes per request, row and chunk
+  void* racers;                // scratch: 16 bytes per request and chunk
+};
+int verify_chunks(int V);
+int verify_launch(const VerifyCall& c, bool f32, cudaStream_t st);
 
 enum Fp8Out : int { FP8_OUT_F32 = 0, FP8_OUT_BF16 = 1, FP8_OUT_SWIGLU = 2 };
 

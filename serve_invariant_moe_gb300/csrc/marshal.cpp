@@ -1,4 +1,5 @@
-// marshal.cpp -- CPython helpers of the binding: argument checks, output allocation and the calls of the 8-bit block.
+// marshal.cpp -- CPython helpers of the binding: argument checks, output allocation and the calls of the 8-bit block and of a
+// drafted decode step.
 //
 // A call of a few tokens is bound by the host.  Through ctypes and the Python-level checks add_rms_norm took 20-26 us for
 // one token, its kernel 3: five outputs at 1.5 us each, four checks, fourteen argument conversions.  Here a check, an
@@ -360,6 +361,74 @@ PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// sandwich(x, w_post, residual, w_next, gate, residual_scale, branch_scale, eps, out, fp8, residual_out, q, scale, rstd_post,
+// rstd): likewise, of sandwich_norm.
+PyObject* sandwich(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 15) {
+    PyErr_SetString(PyExc_TypeError, "sandwich takes 15 arguments");
+    return nullptr;
+  }
+  int T, H, xt, rT, rH, rt;
+  if (!matrix(a[0], "x", &T, &H, &xt) || !matrix(a[2], "residual", &rT, &rH, &rt)) return nullptr;
+  const int64_t rows[] = {T}, row[] = {H}, full[] = {T, H}, blocks[] = {T, (static_cast<int64_t>(H) + 127) / 128};
+  const bool next = a[3] != Py_None;
+  float number[3];                                    // residual_scale, branch_scale, eps
+  for (int i = 0; i < 3; ++i)
+    if (!convert(a[5 + i], &number[i])) return nullptr;
+  const int fp8 = PyObject_IsTrue(a[9]);
+  if (fp8 < 0) return nullptr;
+  if (!check_tensor(a[0], "x", xt, full) || !check_tensor(a[1], "w_post", 0, row) ||
+      !check_tensor(a[2], "residual", rt, full) || (next && !check_tensor(a[3], "w_next", 0, row)))
+    return nullptr;
+  int kind = INVMOE_GATE_NONE;
+  const void* gate = nullptr;
+  if (a[4] != Py_None) {
+    if (!THPVariable_Check(a[4])) {
+      refuse("gate", "must be a tensor");
+      return nullptr;
+    }
+    const at::Tensor& g = THPVariable_Unpack(a[4]);
+    kind = g.scalar_type() == kTypes[0] ? INVMOE_GATE_CHANNEL : INVMOE_GATE_TOKEN;
+    if (kind == INVMOE_GATE_CHANNEL ? !check_tensor(a[4], "gate", 0, row) : !check_tensor(a[4], "gate", 1, rows))
+      return nullptr;
+    gate = g.data_ptr();
+  }
+  Ref res_out, out, q, scale, rstd_post, rstd;
+  if (!output(a[10], "residual_out", rt, full, &res_out) || !output(a[13], "rstd_post", 1, rows, &rstd_post)) return nullptr;
+  if (!next) {
+    if (given(a[8]) == kTaken || fp8 || given(a[11]) == kTaken || given(a[12]) == kTaken || given(a[14]) == kTaken) {
+      refuse("w_next", "is required for out, fp8 and rstd");
+      return nullptr;
+    }
+    for (Ref* r : {&out, &q, &scale, &rstd}) none(r);
+  } else {
+    if (given(a[8]) == kSkip) none(&out);
+    else if (!output(a[8], "out", 0, full, &out)) return nullptr;
+    if (!fp8) {
+      none(&q);
+      none(&scale);
+    } else if (!output(a[11], "q", 2, full, &q) || !output(a[12], "scale", 1, blocks, &scale)) {
+      return nullptr;
+    }
+    if (!output(a[14], "rstd", 1, rows, &rstd)) return nullptr;
+  }
+  const void* x = THPVariable_Unpack(a[0]).data_ptr();
+  const void* w_post = THPVariable_Unpack(a[1]).data_ptr();
+  const void* residual = THPVariable_Unpack(a[2]).data_ptr();
+  const void* w_next = next ? THPVariable_Unpack(a[3]).data_ptr() : nullptr;
+  void* stream = c10::cuda::getCurrentCUDAStream().stream();
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = sandwich_norm(x, xt, w_post, residual, rt, gate, kind, w_next, T, H, number[0], number[1], number[2], res_out.data(),
+                     out.data(), q.data(), static_cast<float*>(scale.data()), static_cast<float*>(rstd_post.data()),
+                     static_cast<float*>(rstd.data()), stream);
+  Py_END_ALLOW_THREADS
+  if (rc != 0) return PyLong_FromLong(rc);
+  return dict_of({"residual", "out", "q", "scale", "rstd_post", "rstd"}, {&res_out, &out, &q, &scale, &rstd_post, &rstd});
+  END_HANDLE_TH_ERRORS
+}
+
 #define METHOD(name, fn) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(fn)), METH_FASTCALL, nullptr}
 #define ENTRY(name) METHOD(#name, &call<&name>)
 
@@ -379,6 +448,9 @@ PyMethodDef methods[] = {
     ENTRY(fp8_gemm),
     ENTRY(moe_grouped_swiglu_fp8),
     ENTRY(moe_grouped_down_fp8),
+    METHOD("sandwich", &sandwich),
+    ENTRY(sandwich_norm_backward),
+    ENTRY(verify_drafts),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

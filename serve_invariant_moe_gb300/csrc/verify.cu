@@ -1,0 +1,346 @@
+// verify.cu -- drafted tokens checked against the target's probabilities, from given random numbers.
+//
+// With p_i = softmax(z_i / tau) of a request's target rows and q_i of its draft rows, draft token x_i is accepted while
+// u_i q_i(x_i) < p_i(x_i).  The token after the n accepted ones is drawn by a race of exponential noise e: the largest
+// w_j / e_j, where w = max(p_n - q_n, 0) after a rejection and p_n otherwise, which draws j with probability w_j / sum w.  So
+// every emitted token has the target's distribution, and which one it is follows from the logits and the given numbers alone.
+//
+// Two kernels: the statistics (maximum, sum of exponentials) of every row that counts, a block per chunk of kChunk logits;
+// then acceptance and the race on the one row that is left, a block per chunk again, the last one of a request to finish
+// joining the chunks.  Bound by reading the logits once (the race reads one row more per request, mostly from L2).  Chunks
+// and the order in which they are joined follow from V alone, so a request's bits do not depend on the batch.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cfloat>
+#include <cstdint>
+
+#include "internal.h"
+#include "ptx.cuh"
+#include "row_ops.cuh"
+
+namespace invmoe {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPer = 32;                          // logits of a thread
+constexpr int kChunk = kThreads * kPer;
+
+// NaN counts as no logit at all; +inf as the largest finite number, so that it takes all the mass.
+__device__ __forceinline__ float usable(float z) { return z != z ? -INFINITY : fminf(z, FLT_MAX); }
+
+struct Scale {
+  bool greedy;
+  float inv;                                      // 1 / tau; 1 for a greedy request
+};
+__device__ __forceinline__ Scale scale_of(const VerifyCall& p, int b) {
+  const float tau = p.temperature != nullptr ? __ldg(p.temperature + b) : p.tau;
+  if (!(tau > 0.0f)) return {true, 1.0f};
+  return {false, fminf(__frcp_rn(tau), FLT_MAX)};
+}
+
+// exp((z - m) / tau), 0 for a logit of -inf.
+__device__ __forceinline__ float weight(float z, float m, float inv) {
+  return z == -INFINITY ? 0.0f : expf(__fmul_rn(__fsub_rn(z, m), inv));
+}
+
+__device__ __forceinline__ int drafts_of(const VerifyCall& p, int b) {
+  return p.n_draft != nullptr ? max(0, min(p.D, __ldg(p.n_draft + b))) : p.D;
+}
+
+// Element of the i-th of a thread's kPer: vectors of 8 or, where rows do not start on 16 bytes, single ones.
+template <bool VEC>
+__device__ __forceinline__ int place(int i) {
+  return VEC ? ((i >> 3) * kThreads + static_cast<int>(threadIdx.x)) * 8 + (i & 7)
+             : i * kThreads + static_cast<int>(threadIdx.x);
+}
+
+// This thread's elements of a row from `first` on; `fill` behind the row's end.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_chunk(const T* row, int first, int V, float fill, float (&z)[kPer]) {
+  if constexpr (VEC) {
+#pragma unroll
+    for (int v = 0; v < kPer / 8; ++v) {
+      const int c = first + (v * kThreads + static_cast<int>(threadIdx.x)) * 8;
+      float t[8];
+      if (c + 8 <= V) {
+        load8(row + c, t);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = c + i < V ? static_cast<float>(row[c + i]) : fill;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[v * 8 + i] = t[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int c = first + i * kThreads + static_cast<int>(threadIdx.x);
+      z[i] = c < V ? static_cast<float>(row[c]) : fill;
+    }
+  }
+}
+
+__device__ __forceinline__ float block_max(float v, float* s_part, int warp, int lane) {
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, d));
+  if (lane == 0) s_part[warp] = v;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) v = fmaxf(v, s_part[w]);
+  return v;
+}
+
+struct Stats {
+  float max, sum;
+  int arg, pad;                                   // lowest index of the maximum (greedy requests)
+};
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads) verify_stats_kernel(const VerifyCall p) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float s_max[kThreads / 32], s_sum[kThreads / 32];
+  __shared__ int s_arg[kThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int chunk = static_cast<int>(blockIdx.x % p.chunks);
+  const long long row = blockIdx.x / p.chunks;    // a request's target rows, then its draft rows
+  const int b = static_cast<int>(row / p.rows), i = static_cast<int>(row - static_cast<long long>(b) * p.rows);
+  if (chunk == 0 && i == 0 && threadIdx.x == 0) p.done[b] = 0;
+  const int n = drafts_of(p, b);
+  const Scale sc = scale_of(p, b);
+  const bool target = i <= p.D;
+  if (target ? i > n : i - (p.D + 1) >= n || sc.greedy) return;
+  const T* z_row = target ? static_cast<const T*>(p.logits) + (static_cast<long long>(b) * (p.D + 1) + i) * p.V
+                          : static_cast<const T*>(p.draft_logits) + (static_cast<long long>(b) * p.D + i - (p.D + 1)) * p.V;
+  float z[kPer];
+  load_chunk<T, VEC>(z_row, chunk * kChunk, p.V, -INFINITY, z);
+  float m = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    z[j] = usable(z[j]);
+    m = fmaxf(m, z[j]);
+  }
+  m = block_max(m, s_max, warp, lane);
+  float s = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) s += weight(z[j], m, sc.inv);
+  s = block_sum(s, s_sum, warp, lane, kThreads / 32);
+  int arg = 0x7fffffff;
+  if (sc.greedy) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (z[j] == m) arg = min(arg, place<VEC>(j));
+    arg = __reduce_min_sync(kFull, arg);
+    if (lane == 0) s_arg[warp] = arg;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) arg = min(arg, s_arg[w]);
+    arg += chunk * kChunk;
+  }
+  if (threadIdx.x == 0) static_cast<Stats*>(p.stats)[row * p.chunks + chunk] = Stats{m, s, arg, 0};
+}
+
+// A row's statistics from its chunks': lane l joins chunks l, l + 32, ... ascending, then a xor butterfly.
+__device__ __forceinline__ Stats row_stats(const Stats* part, int chunks, float inv, int lane) {
+  float m = -INFINITY;
+  for (int c = lane; c < chunks; c += 32) m = fmaxf(m, part[c].max);
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+  float s = 0.0f;
+  int arg = 0x7fffffff;
+  for (int c = lane; c < chunks; c += 32) {
+    const Stats t = part[c];
+    s += t.sum * weight(t.max, m, inv);
+    if (t.max == m) arg = min(arg, t.arg);
+  }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
+  return Stats{m, s, static_cast<int>(__reduce_min_sync(kFull, arg)), 0};
+}
+
+// A racer: the larger score wins, then the lower index.  0 is nobody.
+__device__ __forceinline__ unsigned long long racer(float w, float e, int j) {
+  const float score = __fdiv_rn(w, e);
+  if (!(w > 0.0f) || !(score >= 0.0f) || __float_as_uint(score) == 0x80000000u) return 0ull;
+  return (static_cast<unsigned long long>(__float_as_uint(score)) << 32) | (0xffffffffu - static_cast<unsigned>(j));
+}
+__device__ __forceinline__ unsigned long long warp_best(unsigned long long v) {
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) v = max(v, __shfl_xor_sync(kFull, v, d));
+  return v;
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads) verify_choose_kernel(const VerifyCall p) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ Stats s_row[2 * kVerifyMaxDrafts + 1];
+  __shared__ unsigned long long s_best[2][kThreads / 32];
+  __shared__ int s_n, s_last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int b = static_cast<int>(blockIdx.x / p.chunks), chunk = static_cast<int>(blockIdx.x % p.chunks);
+  const int D = p.D, V = p.V;
+  const int n_draft = drafts_of(p, b);
+  const Scale sc = scale_of(p, b);
+  if (sc.greedy && chunk != 0) return;            // nothing to draw: one block reads the maxima
+  const Stats* part = static_cast<const Stats*>(p.stats) + static_cast<long long>(b) * p.rows * p.chunks;
+  const T* logits = static_cast<const T*>(p.logits) + static_cast<long long>(b) * (D + 1) * V;
+  const T* drafts = static_cast<const T*>(p.draft_logits) + static_cast<long long>(b) * D * V;
+  const bool has_q = p.draft_logits != nullptr;
+  for (int r = warp; r < p.rows; r += kThreads / 32) {
+    if (r <= D ? r > n_draft : r - (D + 1) >= n_draft || sc.greedy) continue;
+    const Stats t = row_stats(part + static_cast<long long>(r) * p.chunks, p.chunks, sc.inv, lane);
+    if (lane == 0) s_row[r] = t;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    bool ok = false;
+    if (lane < n_draft) {
+      const int x = __ldg(p.draft_tokens + static_cast<long long>(b) * D + lane);
+      const Stats t = s_row[lane];
+      if (x >= 0 && x < V && t.max > -INFINITY) {
+        if (sc.greedy) {
+          ok = x == t.arg;
+        } else {
+          // u q < p over the common denominators: u e_q S_p < e_p S_q
+          const float ep = weight(usable(static_cast<float>(logits[static_cast<long long>(lane) * V + x])), t.max, sc.inv);
+          float eq = 1.0f, sq = 1.0f;
+          if (has_q) {
+            const Stats d = s_row[D + 1 + lane];
+            eq = d.max > -INFINITY ? weight(usable(static_cast<float>(drafts[static_cast<long long>(lane) * V + x])), d.max, sc.inv)
+                                   : 0.0f;
+            sq = d.max > -INFINITY ? d.sum : 1.0f;
+          }
+          const float u = __ldg(p.accept_u + static_cast<long long>(b) * D + lane);
+          ok = static_cast<double>(u) * eq * t.sum < static_cast<double>(ep) * sq;
+        }
+      }
+    }
+    const unsigned no = ~__ballot_sync(kFull, ok);
+    if (lane == 0) s_n = no == 0u ? 32 : __ffs(no) - 1;
+  }
+  __syncthreads();
+  const int n = s_n;                              // accepted; row n gives the next token
+  const Stats t = s_row[n];
+  const bool rejected = n < n_draft;
+  unsigned long long best = 0ull, other = 0ull;   // of the weights, and of p alone in case they are all zero
+  if (!sc.greedy && t.max > -INFINITY) {
+    const float inv_p = __frcp_rn(t.sum);
+    float z[kPer], e[kPer];
+    load_chunk<T, VEC>(logits + static_cast<long long>(n) * V, chunk * kChunk, V, -INFINITY, z);
+    load_chunk<float, VEC>(p.noise + static_cast<long long>(b) * V, chunk * kChunk, V, 1.0f, e);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) z[j] = __fmul_rn(weight(usable(z[j]), t.max, sc.inv), inv_p);
+    if (!rejected) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) best = max(best, racer(z[j], e[j], chunk * kChunk + place<VEC>(j)));
+    } else if (has_q) {
+      const Stats d = s_row[D + 1 + n];
+      const float inv_q = d.max > -INFINITY ? __frcp_rn(d.sum) : 0.0f;
+      float q[kPer];
+      load_chunk<T, VEC>(drafts + static_cast<long long>(n) * V, chunk * kChunk, V, -INFINITY, q);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int at = chunk * kChunk + place<VEC>(j);
+        const float qj = inv_q == 0.0f ? 0.0f : __fmul_rn(weight(usable(q[j]), d.max, sc.inv), inv_q);
+        best = max(best, racer(__fsub_rn(z[j], qj), e[j], at));
+        other = max(other, racer(z[j], e[j], at));
+      }
+    } else {
+      const int x = __ldg(p.draft_tokens + static_cast<long long>(b) * D + n);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int at = chunk * kChunk + place<VEC>(j);
+        const unsigned long long v = racer(z[j], e[j], at);
+        other = max(other, v);
+        if (at != x) best = max(best, v);
+      }
+    }
+  }
+  best = warp_best(best);
+  other = warp_best(other);
+  if (lane == 0) {
+    s_best[0][warp] = best;
+    s_best[1][warp] = other;
+  }
+  __syncthreads();
+  ulonglong2* racers = static_cast<ulonglong2*>(p.racers) + static_cast<long long>(b) * p.chunks;
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      best = max(best, s_best[0][w]);
+      other = max(other, s_best[1][w]);
+    }
+    s_last = 1;
+    if (!sc.greedy && p.chunks > 1) {
+      racers[chunk] = make_ulonglong2(best, other);
+      __threadfence();
+      s_last = atomicAdd(p.done + b, 1) == p.chunks - 1;
+      __threadfence();
+    }
+  }
+  __syncthreads();
+  if (!s_last || warp != 0) return;
+  int token = t.max > -INFINITY ? t.arg : -1;
+  if (!sc.greedy) {
+    if (p.chunks > 1) {
+      best = other = 0ull;
+      for (int c = lane; c < p.chunks; c += 32) {
+        const ulonglong2 v = __ldcg(racers + c);
+        best = max(best, v.x);
+        other = max(other, v.y);
+      }
+      best = warp_best(best);
+      other = warp_best(other);
+    }
+    best = __shfl_sync(kFull, best, 0);
+    other = __shfl_sync(kFull, other, 0);
+    if (best == 0ull) best = other;
+    token = best == 0ull ? -1 : static_cast<int>(0xffffffffu - static_cast<unsigned>(best));
+  }
+  if (lane == 0) p.n_accepted[b] = n;
+  for (int i = lane; i <= D; i += 32) {
+    int x = -1;
+    float lp = 0.0f;
+    if (i <= n) {
+      x = i < n ? __ldg(p.draft_tokens + static_cast<long long>(b) * D + i) : token;
+      const Stats r = s_row[i];
+      lp = x < 0 ? -INFINITY
+                 : __fsub_rn(__fmul_rn(__fsub_rn(usable(static_cast<float>(logits[static_cast<long long>(i) * V + x])), r.max),
+                                       sc.inv),
+                             logf(r.sum));
+    }
+    p.tokens[static_cast<long long>(b) * (D + 1) + i] = x;
+    p.logp[static_cast<long long>(b) * (D + 1) + i] = lp;
+  }
+}
+
+}  // namespace
+
+int verify_chunks(int V) { return (V - 1) / kChunk + 1; }
+
+int verify_launch(const VerifyCall& c, bool f32, cudaStream_t st) {
+  const bool vec = c.V % (f32 ? 4 : 8) == 0;
+  const dim3 g1(static_cast<unsigned>(static_cast<long long>(c.B) * c.rows * c.chunks)), g2(c.B * c.chunks);
+  {
+    ProfScope prof("verify_stats", st);
+    const cudaError_t e =
+        f32 ? vec ? launch_kernel(verify_stats_kernel<float, true>, g1, dim3(kThreads), 0, st, c)
+                  : launch_kernel(verify_stats_kernel<float, false>, g1, dim3(kThreads), 0, st, c)
+        : vec ? launch_kernel(verify_stats_kernel<__nv_bfloat16, true>, g1, dim3(kThreads), 0, st, c)
+              : launch_kernel(verify_stats_kernel<__nv_bfloat16, false>, g1, dim3(kThreads), 0, st, c);
+    const int rc = check_cuda(e, "verify_stats_kernel");
+    if (rc) return rc;
+  }
+  ProfScope prof("verify_choose", st);
+  const cudaError_t e =
+      f32 ? vec ? launch_kernel(verify_choose_kernel<float, true>, g2, dim3(kThreads), 0, st, c)
+                : launch_kernel(verify_choose_kernel<float, false>, g2, dim3(kThreads), 0, st, c)
+      : vec ? launch_kernel(verify_choose_kernel<__nv_bfloat16, true>, g2, dim3(kThreads), 0, st, c)
+            : launch_kernel(verify_choose_kernel<__nv_bfloat16, false>, g2, dim3(kThreads), 0, st, c);
+  return check_cuda(e, "verify_choose_kernel");
+}
+
+}  // namespace invmoe

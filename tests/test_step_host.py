@@ -1,0 +1,83 @@
+"""CPU-side checks of a drafted decode step's entry points: host-side validation, sizes, refusal of host tensors."""
+import ctypes
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from serve_invariant_moe_gb300 import build, _lib
+    build.build()
+    return _lib.lib()
+
+
+N = None
+P = ctypes.c_void_p(4096)          # never read: every call below is refused on the host
+
+
+def test_sandwich_norm_rejects_before_any_launch(lib):
+    f = lib.sandwich_norm
+    tail = (1.0, 1.0, 1e-6, P, P, N, N, N, N, N)
+    assert f(P, 5, P, P, 0, N, 0, P, 4, 64, *tail) == -1
+    assert f(P, 0, P, P, 7, N, 0, P, 4, 64, *tail) == -1
+    assert f(P, 0, P, P, 0, N, 0, P, 4, 40, *tail) == -2
+    assert f(P, 0, P, P, 0, N, 0, P, 4, 32784, *tail) == -2
+    assert f(P, 0, P, P, 0, N, 0, P, -1, 64, *tail) == -1
+    assert f(P, 0, P, P, 0, N, 1, P, 4, 64, *tail) == -1 and b"gate" in lib.invmoe_last_error()
+    assert f(P, 0, P, P, 0, P, 3, P, 4, 64, *tail) == -1
+    assert f(P, 0, P, P, 0, N, 0, N, 4, 64, *tail) == -1 and b"w_next" in lib.invmoe_last_error()
+    assert f(P, 0, P, P, 0, N, 0, P, 4, 64, 1.0, 1.0, -1.0, P, P, N, N, N, N, N) == -1
+    assert f(P, 0, P, P, 0, N, 0, P, 4, 64, float("nan"), 1.0, 1e-6, P, P, N, N, N, N, N) == -1
+    assert f(P, 0, P, P, 0, N, 0, P, 4, 64, 1.0, 1.0, 1e-6, P, P, P, N, N, N, N) == -1 and b"q and scale" in lib.invmoe_last_error()
+    assert f(ctypes.c_void_p(4100), 0, P, P, 0, N, 0, P, 4, 64, *tail) == -4
+    assert f(P, 0, P, P, 0, N, 0, P, 0, 64, *tail) == 0                     # no rows
+
+
+def test_sandwich_norm_backward_rejects_before_any_launch(lib):
+    f, need = lib.sandwich_norm_backward, lib.sandwich_norm_backward_workspace_size
+    a, b, c, d, e = (ctypes.c_void_p(1 << (20 + i)) for i in range(5))
+    tail = (1.0, 1.0, a, b, P, P, N, P, need(4, 64), N)
+    assert f(c, 5, d, e, 0, P, P, P, 0, P, P, N, 0, 4, 64, *tail) == -1
+    assert f(c, 0, d, e, 0, P, P, P, 0, N, N, N, 0, 4, 64, *tail) == -1       # dy without w_next
+    assert f(c, 0, d, e, 0, P, P, P, 0, P, P, N, 0, 4, 40, *tail) == -2
+    assert f(c, 0, d, e, 0, P, P, P, 0, P, P, N, 0, 4, 64, 1.0, 1.0, a, b, P, P, P, P, need(4, 64), N) == -1   # dgate without gate
+    assert f(c, 0, d, e, 0, P, P, P, 0, P, P, N, 0, 4, 64, 1.0, 1.0, a, b, N, P, N, P, need(4, 64), N) == -1   # dw_next without dw_post
+    assert f(c, 0, d, e, 0, P, P, P, 0, P, P, N, 0, 4, 64, 1.0, 1.0, a, b, P, P, N, P, need(4, 64) - 1, N) == -3
+    assert f(N, 0, N, e, 0, P, P, P, 0, N, N, N, 0, 4, 64, 1.0, 1.0, a, b, P, N, N, P, need(4, 64), N) == -1   # no gradient at all
+    assert f(c, 0, d, e, 0, P, P, P, 0, P, P, N, 0, 4, 64, 1.0, 1.0, a, a, P, P, N, P, need(4, 64), N) == -1   # dx is dresidual
+    assert b"overlaps" in lib.invmoe_last_error()
+    assert need(0, 64) == 256
+    assert need(2 ** 31 - 1, 64) > 2 ** 33                                      # counted without wrapping
+
+
+def test_verify_drafts_rejects_before_any_launch(lib):
+    f, need = lib.verify_drafts, lib.verify_workspace_size
+    out = (P, P, P)
+    ok = need(2, 3, 100)
+    assert f(P, 9, N, P, P, P, N, N, 1.0, 2, 3, 100, *out, P, ok, N) == -1
+    assert f(P, 1, N, P, P, P, N, N, -0.5, 2, 3, 100, *out, P, ok, N) == -1
+    assert f(P, 1, N, P, P, P, N, N, 1.0, 2, 33, 100, *out, P, 1 << 30, N) == -2
+    assert f(P, 1, N, P, P, P, N, N, 1.0, 2, 3, 0, *out, P, ok, N) == -1
+    assert f(P, 1, N, P, P, P, N, N, 1.0, 2, 3, 100, *out, P, ok - 1, N) == -3
+    assert f(P, 1, N, N, P, P, N, N, 1.0, 2, 3, 100, *out, P, ok, N) == -1 and b"draft_tokens" in lib.invmoe_last_error()
+    assert f(P, 1, P, N, N, P, N, N, 1.0, 2, 0, 100, *out, P, ok, N) == -1
+    assert f(ctypes.c_void_p(4097), 1, N, P, P, P, N, N, 1.0, 2, 3, 100, *out, P, ok, N) == -4
+    assert f(P, 1, N, P, P, P, N, N, 1.0, 2 ** 31 - 1, 3, 151552, *out, P, 2 ** 62, N) == -2
+    assert f(P, 1, N, P, P, P, N, N, 1.0, 0, 3, 100, *out, P, ok, N) == 0
+    assert need(0, 3, 100) == 256 and need(2 ** 31 - 1, 32, 2 ** 31 - 1) > 2 ** 45
+
+
+def test_binding_refuses_host_tensors():
+    from serve_invariant_moe_gb300 import binding
+    x, w = torch.zeros(4, 64), torch.zeros(64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        binding.sandwich_norm(x, w, x, w)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        binding.sandwich_norm_backward(x, x, x, w, torch.zeros(4), x, w, torch.zeros(4))
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        binding.verify_drafts(torch.zeros(2, 1, 8), torch.zeros(2, 8), torch.zeros(256, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="2 dimensions"):
+        binding.sandwich_norm(x[0], w, x, w)
+    with pytest.raises(ValueError, match="3 dimensions"):
+        binding.verify_drafts(torch.zeros(2, 8), torch.zeros(2, 8), torch.zeros(256, dtype=torch.uint8))
