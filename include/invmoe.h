@@ -73,6 +73,7 @@ extern "C" {
 /* Expert scores (moe_route_select). */
 #define INVMOE_SCORE_SIGMOID 0
 #define INVMOE_SCORE_SOFTMAX 1
+#define INVMOE_SCORE_TOPK    2  /* moe_layer_decode: the softmax over the k largest logits */
 
 /* Gates (sandwich_norm). */
 #define INVMOE_GATE_NONE    0
@@ -601,8 +602,28 @@ int moe_grouped_down_fp8(const void* h, const float* h_scale, const int32_t* pla
                          size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
- * A drafted decode step: norms around a block, verification of drafted tokens
+ * A drafted decode step: the layer of a few tokens in one kernel, norms around a
+ * block, verification of drafted tokens
  * ------------------------------------------------------------------------- */
+
+/* Workspace of moe_layer_decode.  Its first 256 bytes are zero before the first call, as in
+ * every workspace; the rest may have any content. */
+size_t moe_decode_workspace_size(int T, int H, int E, int k, int F, int F_shared);
+
+/* moe_layer_forward for at most 16 tokens in one kernel, with the same bits: router, choice,
+ * gate/up, SwiGLU, down, shared expert (F_shared > 0: ws13, ws2) and combine.  score
+ * INVMOE_SCORE_TOPK chooses as moe_route_topk (bias NULL, n_group = topk_group = 1, scale 1,
+ * renormalize 1), INVMOE_SCORE_SIGMOID and _SOFTMAX as moe_route_select.  out [T, H] fp32 and
+ * out_bf16 [T, H]: at least one; logits [T, E], topk_idx [T, k], topk_w [T, k]: each
+ * nullable.  Weights as for moe_layer_forward.  x is read until the end: no output may
+ * overlap it.  The kernel's blocks wait for one another, so it is launched cooperatively and
+ * starts when all of them fit on the device; calls that may run at the same time need
+ * workspaces of their own.
+ * Shapes: T <= 16, E <= 512, k <= 32, H % 64 == 0, H <= 32768, F % 64 == 0, F_shared % 64 == 0. */
+int moe_layer_decode(const void* x, const void* w_router, const void* w13, const void* w2, const void* ws13, const void* ws2,
+                     int T, int H, int E, int k, int F, int F_shared, int score, const float* bias, int n_group,
+                     int topk_group, int renormalize, float scale, float* out, void* out_bf16, float* logits,
+                     int32_t* topk_idx, float* topk_w, void* workspace, size_t ws_bytes, void* stream);
 
 /* The norms after and before a block, of the block's output x and the residual stream:
  *   n = (x * rstd_post) * w_post,  rstd_post = 1 / sqrt(mean(x^2) + eps)

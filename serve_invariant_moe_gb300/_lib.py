@@ -58,6 +58,9 @@ PROTOTYPES = {
     "fp8_gemm": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _vp, _sz, _vp]),
     "moe_grouped_swiglu_fp8": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _sz, _vp]),
     "moe_grouped_down_fp8": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _sz, _vp]),
+    "moe_decode_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "moe_layer_decode": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _i, _i, _i, _f, _vp, _vp, _vp,
+                              _vp, _vp, _vp, _sz, _vp]),
     "sandwich_norm": (_i, [_vp, _i, _vp, _vp, _i, _vp, _i, _vp, _i, _i, _f, _f, _f, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "sandwich_norm_backward_workspace_size": (_sz, [_i, _i]),
     "sandwich_norm_backward": (_i, [_vp, _i, _vp, _vp, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _f, _f, _vp,

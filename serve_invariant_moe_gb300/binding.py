@@ -760,8 +760,49 @@ def moe_grouped_down_fp8(h, h_scale, plan, w2, w2_scale, T, k, workspace, y=None
 
 
 # ---------------------------------------------------------------------------
-# A drafted decode step: norms around a block, verification of drafted tokens
+# A drafted decode step: the layer of a few tokens in one kernel, norms around a block, verification of drafted tokens
 # ---------------------------------------------------------------------------
+
+DECODE_MAX_TOKENS, DECODE_MAX_EXPERTS = 16, 512      # of moe_layer_decode
+
+
+def moe_decode_workspace_size(T, H, E, k, F, F_shared=0) -> int:
+    return int(lib().moe_decode_workspace_size(T, H, E, k, F, F_shared))
+
+
+def moe_layer_decode(x, w_router, w13, w2, k, workspace, ws13=None, ws2=None, score=None, bias=None, n_group=1, topk_group=1,
+                     renormalize=True, scale=1.0, out=True, out_bf16=None, logits=None, topk_idx=None, topk_w=None):
+    """The whole layer of at most 16 tokens in one kernel, with moe_layer_forward's bits:
+    dict(out, out_bf16, logits, topk_idx, topk_w).
+
+    score None: the softmax over the k largest logits; "sigmoid" or "softmax": the choice of moe_route_select, with its
+    arguments.  out [T, H] fp32 and out_bf16: a tensor to fill, True, or False / None to skip it (not both).
+    workspace: at least moe_decode_workspace_size bytes from new_workspace."""
+    m = marshal()
+    T, H = _dims(x, "x")
+    E, F2, _ = _dims(w13, "w13", 3)
+    F, Fs = F2 // 2, 0
+    kind = 2 if score is None else _score(score)
+    m.check(x, "x", BF16_, T, H)
+    m.check(w_router, "w_router", BF16_, E, H)
+    m.check(w13, "w13", BF16_, E, 2 * F, H)
+    m.check(w2, "w2", BF16_, E, H, F)
+    if ws13 is not None:
+        Fs = ws13.shape[0] // 2
+        m.check(ws13, "ws13", BF16_, 2 * Fs, H)
+        m.check(ws2, "ws2", BF16_, H, Fs)
+    if bias is not None:
+        m.check(bias, "bias", F32_, E)
+    m.check(workspace, "workspace", U8_)
+    out = None if out is False else _out(m, out, x, "out", F32_, T, H)
+    out_bf16 = None if out_bf16 is None or out_bf16 is False else _out(m, out_bf16, x, "out_bf16", BF16_, T, H)
+    logits = _out(m, logits, x, "logits", F32_, T, E)
+    topk_idx = _out(m, topk_idx, x, "topk_idx", I32_, T, k)
+    topk_w = _out(m, topk_w, x, "topk_w", F32_, T, k)
+    check(m.moe_layer_decode(x, w_router, w13, w2, ws13, ws2, T, H, E, k, F, Fs, kind, bias, n_group, topk_group,
+                             bool(renormalize), scale, out, out_bf16, logits, topk_idx, topk_w, workspace,
+                             workspace.numel()))
+    return {"out": out, "out_bf16": out_bf16, "logits": logits, "topk_idx": topk_idx, "topk_w": topk_w}
 
 def _gate(m, gate, T, H):
     """The gate's kind by its type and shape: None, [H] bf16 (per channel) or [T] fp32 (per token)."""

@@ -1,4 +1,5 @@
-// api_step.cu -- the extern "C" entry points of a drafted decode step: norms around a block, drafted tokens.
+// api_step.cu -- the extern "C" entry points of a drafted decode step: the layer of a few tokens, norms around a
+// block, drafted tokens.
 #include <cuda_runtime.h>
 
 #include "checks.h"
@@ -29,6 +30,22 @@ size_t matrix_bytes(int T, int H, int type) { return static_cast<size_t>(T) * H 
 bool apart(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return a == nullptr || b == nullptr || x + na <= y || y + nb <= x;
+}
+
+// moe_layer_decode's part of the workspace behind the status block: offsets of its arrays.
+struct DecodeScratch {
+  size_t logits, h, hs, y, ys, total;
+};
+DecodeScratch decode_scratch(int T, int H, int E, int k, int F, int F_shared) {
+  DecodeScratch s{};
+  const size_t rows = static_cast<size_t>(T) * k;
+  s.logits = align_up(kDecodeFlags * sizeof(int), 256);
+  s.h = s.logits + align_up(static_cast<size_t>(T) * E * 4, 256);
+  s.hs = s.h + align_up(rows * F * 2, 256);
+  s.y = s.hs + align_up(static_cast<size_t>(T) * F_shared * 2, 256);
+  s.ys = s.y + align_up(rows * H * 4, 256);
+  s.total = s.ys + (F_shared > 0 ? align_up(static_cast<size_t>(T) * H * 4, 256) : 0);
+  return s;
 }
 
 }  // namespace
@@ -111,6 +128,81 @@ int sandwich_norm_backward(const void* dy, int dy_type, const void* dres, const 
        w_next, rstd, gate, gate_kind, T, H, residual_scale, branch_scale, dx, dresidual, dw_post, dw_next, dgate,
        reinterpret_cast<float*>(scratch(workspace)), status_word(workspace)},
       st);
+}
+
+size_t moe_decode_workspace_size(int T, int H, int E, int k, int F, int F_shared) {
+  if (T <= 0 || T > kDecodeMaxTokens || H <= 0 || E <= 0 || k <= 0 || k > 32 || F <= 0 || F_shared < 0) return kStatusBytes;
+  return kStatusBytes + decode_scratch(T, H, E, k, F, F_shared).total;
+}
+
+int moe_layer_decode(const void* x, const void* w_router, const void* w13, const void* w2, const void* ws13, const void* ws2,
+                     int T, int H, int E, int k, int F, int F_shared, int score, const float* bias, int n_group,
+                     int topk_group, int renormalize, float scale, float* out, void* out_bf16, float* logits,
+                     int32_t* topk_idx, float* topk_w, void* workspace, size_t ws_bytes, void* stream) {
+  REQUIRE(T >= 0 && H > 0 && E > 0 && k > 0 && F > 0 && F_shared >= 0, INVMOE_ERR_INVALID_ARG,
+          "need T, F_shared >= 0 and H, E, k, F > 0");
+  REQUIRE(T <= kDecodeMaxTokens, INVMOE_ERR_UNSUPPORTED_SHAPE, "T=%d > %d", T, kDecodeMaxTokens);
+  REQUIRE(E <= kDecodeMaxExperts, INVMOE_ERR_UNSUPPORTED_SHAPE, "E=%d > %d", E, kDecodeMaxExperts);
+  REQUIRE(k <= E, INVMOE_ERR_INVALID_ARG, "k=%d must satisfy 1 <= k <= E=%d", k, E);
+  REQUIRE(k <= 32, INVMOE_ERR_UNSUPPORTED_SHAPE, "k=%d > 32", k);
+  REQUIRE(H % 64 == 0 && H <= 128 * kDecodeMaxBlocks, INVMOE_ERR_UNSUPPORTED_SHAPE, "H=%d is not a multiple of 64 up to %d", H,
+          128 * kDecodeMaxBlocks);
+  REQUIRE(F % 64 == 0 && F <= 1 << 20, INVMOE_ERR_UNSUPPORTED_SHAPE, "F=%d is not a multiple of 64 up to 2^20", F);
+  REQUIRE(F_shared % 64 == 0 && F_shared <= 1 << 20, INVMOE_ERR_UNSUPPORTED_SHAPE,
+          "F_shared=%d is not a multiple of 64 up to 2^20", F_shared);
+  REQUIRE(score == INVMOE_SCORE_TOPK || score == INVMOE_SCORE_SIGMOID || score == INVMOE_SCORE_SOFTMAX,
+          INVMOE_ERR_INVALID_ARG, "score must be INVMOE_SCORE_TOPK, INVMOE_SCORE_SIGMOID or INVMOE_SCORE_SOFTMAX");
+  if (score == INVMOE_SCORE_TOPK) {
+    REQUIRE(bias == nullptr && n_group == 1 && topk_group == 1 && scale == 1.0f && renormalize, INVMOE_ERR_INVALID_ARG,
+            "bias, groups, scale and plain weights need a score");
+  } else {
+    REQUIRE(n_group >= 1 && n_group <= 32 && E % n_group == 0, INVMOE_ERR_INVALID_ARG,
+            "n_group=%d must be 1..32 and divide E=%d", n_group, E);
+    REQUIRE(topk_group >= 1 && topk_group <= n_group, INVMOE_ERR_INVALID_ARG, "topk_group=%d must be 1..n_group=%d",
+            topk_group, n_group);
+    REQUIRE(k <= E / n_group * topk_group, INVMOE_ERR_INVALID_ARG, "k=%d exceeds the %d experts of %d groups", k,
+            E / n_group * topk_group, topk_group);
+  }
+  if (T == 0) return INVMOE_OK;
+  REQUIRE_PTR(workspace);
+  REQUIRE(ws_bytes >= moe_decode_workspace_size(T, H, E, k, F, F_shared), INVMOE_ERR_WORKSPACE_TOO_SMALL,
+          "workspace too small");
+  REQUIRE_PTR(x); REQUIRE_PTR(w_router); REQUIRE_PTR(w13); REQUIRE_PTR(w2);
+  REQUIRE(out != nullptr || out_bf16 != nullptr, INVMOE_ERR_INVALID_ARG, "out and out_bf16 are both NULL");
+  REQUIRE_ALIGNED(x); REQUIRE_ALIGNED(w_router); REQUIRE_ALIGNED(w13); REQUIRE_ALIGNED(w2);
+  REQUIRE_ALIGNED(out); REQUIRE_ALIGNED(out_bf16); REQUIRE_ALIGNED(workspace);
+  if (F_shared > 0) {
+    REQUIRE_PTR(ws13); REQUIRE_PTR(ws2);
+    REQUIRE_ALIGNED(ws13); REQUIRE_ALIGNED(ws2);
+  }
+  // columns of x are read until the last block is done with its gate/up units, long after others have written outputs
+  const size_t xn = matrix_bytes(T, H, INVMOE_BF16);
+  REQUIRE(apart(x, xn, out, 2 * xn) && apart(x, xn, out_bf16, xn) && apart(out, 2 * xn, out_bf16, xn),
+          INVMOE_ERR_INVALID_ARG, "an output overlaps x or the other one");
+  const DecodeScratch s = decode_scratch(T, H, E, k, F, F_shared);
+  uint8_t* base = scratch(workspace);
+  DecodeParams p{};
+  p.T = T; p.H = H; p.E = E; p.k = k; p.F = F; p.Fs = F_shared;
+  p.score = score == INVMOE_SCORE_TOPK ? kDecodeTopk : score == INVMOE_SCORE_SIGMOID ? kDecodeSigmoid : kDecodeSoftmax;
+  p.bias = bias;
+  p.n_group = n_group;
+  p.topk_group = topk_group;
+  p.renorm = renormalize != 0;
+  p.scale = scale;
+  p.logits = logits != nullptr ? logits : reinterpret_cast<float*>(base + s.logits);
+  p.topk_idx = topk_idx;
+  p.topk_w = topk_w;
+  p.h = reinterpret_cast<__nv_bfloat16*>(base + s.h);
+  p.hs = reinterpret_cast<__nv_bfloat16*>(base + s.hs);
+  p.y = reinterpret_cast<float*>(base + s.y);
+  p.ys = reinterpret_cast<float*>(base + s.ys);
+  p.out = out;
+  p.out_bf16 = static_cast<__nv_bfloat16*>(out_bf16);
+  p.status = status_word(workspace);
+  p.ctl = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + 192);
+  p.flags = reinterpret_cast<int*>(base);
+  p.timeout_ns = kTimeoutNs;
+  return moe_decode_launch({x, w_router, w13, w2, ws13, ws2}, p, static_cast<cudaStream_t>(stream));
 }
 
 size_t verify_workspace_size(int B, int D, int V) {

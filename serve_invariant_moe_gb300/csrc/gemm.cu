@@ -369,6 +369,25 @@ int make_tmap_out_rows(CUtensorMap* m, void* base, int elt, long long cols, long
   return INVMOE_OK;
 }
 
+int make_tmap_bf16(CUtensorMap* m, const void* base, int rank, const unsigned long long* dims,
+                   const unsigned long long* strides, const unsigned* box) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return set_error(INVMOE_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cuuint64_t d[5], s[4];
+  cuuint32_t b[5], one[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    one[i] = 1;
+    if (i + 1 < rank) s[i] = strides[i];
+  }
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, s, b, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(INVMOE_ERR_CUDA, "cuTensorMapEncodeTiled (rank %d) failed (%d)", rank, (int)r);
+  return INVMOE_OK;
+}
+
 // Row-major e4m3 [rows, inner] matrix; box = 128 elements (128 B, one swizzle row) x box_rows; a last block of fewer than
 // 128 columns is filled with zeros.  k_blocks > 0 (inner a multiple of 128): as a rank-3 tensor (128 elements, rows, inner /
 // 128 blocks) whose box holds that many consecutive blocks, one [box_rows][128] slice after another; blocks past the last

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <atomic>
 #include <cstddef>
@@ -278,6 +279,44 @@ struct VerifyCall {
 };
 int verify_chunks(int V);
 int verify_launch(const VerifyCall& c, bool f32, cudaStream_t st);
+
+// ---------------------------------------------------------------- the layer of a few tokens in one kernel
+constexpr int kDecodeMaxTokens = 16, kDecodeMaxPairs = 512, kDecodeMaxExperts = 512;
+constexpr int kDecodeMaxBlocks = 256;                 // of 128 outputs: H <= 32768
+constexpr int kDecodeFlags = 1 + kDecodeMaxBlocks + kDecodeMaxPairs + 1;
+enum DecodeScore : int { kDecodeTopk, kDecodeSigmoid, kDecodeSoftmax };
+struct DecodeCall {
+  const void* x;
+  const void* w_router;
+  const void* w13;
+  const void* w2;
+  const void* ws13;
+  const void* ws2;
+};
+struct DecodeParams {
+  int T, H, E, k, F, Fs;
+  int score;                   // DecodeScore; the rest of the line for scores alone
+  const float* bias;
+  int n_group, topk_group, renorm;
+  float scale;
+  float* logits;               // [T, E]
+  int32_t* topk_idx;           // [T, k] or null
+  float* topk_w;               // [T, k] or null
+  __nv_bfloat16* h;            // [T * k, F]
+  __nv_bfloat16* hs;           // [T, Fs]
+  float* y;                    // [T * k, H]
+  float* ys;                   // [T, H]
+  float* out;                  // [T, H] or null
+  __nv_bfloat16* out_bf16;     // [T, H] or null
+  unsigned int* status;
+  int* ctl;                    // unit counter, blocks done, go; zero between calls
+  int* flags;                  // kDecodeFlags counters, any content
+  unsigned long long timeout_ns;
+};
+int moe_decode_launch(const DecodeCall& c, const DecodeParams& p, cudaStream_t st);
+// Row-major bf16 tensor, 128-byte swizzle; strides in bytes of the dimensions after the first.
+int make_tmap_bf16(CUtensorMap* m, const void* base, int rank, const unsigned long long* dims,
+                   const unsigned long long* strides, const unsigned* box);
 
 enum Fp8Out : int { FP8_OUT_F32 = 0, FP8_OUT_BF16 = 1, FP8_OUT_SWIGLU = 2 };
 

@@ -448,6 +448,7 @@ PyMethodDef methods[] = {
     ENTRY(fp8_gemm),
     ENTRY(moe_grouped_swiglu_fp8),
     ENTRY(moe_grouped_down_fp8),
+    ENTRY(moe_layer_decode),
     METHOD("sandwich", &sandwich),
     ENTRY(sandwich_norm_backward),
     ENTRY(verify_drafts),

@@ -11,72 +11,11 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "route_token.cuh"
 
 namespace invmoe {
 
 namespace {
-
-constexpr unsigned kFull = 0xffffffffu;
-
-// Total order key: larger = ranks earlier.  NaN -> 0 (below every number,
-// including -inf); -0.0 and +0.0 map to the same key (a tie).
-__device__ __forceinline__ uint32_t order_key(float v) {
-  if (v != v) return 0u;
-  uint32_t b = __float_as_uint(v == 0.0f ? 0.0f : v);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-
-__device__ __forceinline__ float key_value(uint32_t key) {
-  if (key == 0u) return __uint_as_float(0x7fc00000u);
-  return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
-}
-
-// One warp per token.  Lane l holds experts l, l+32, ... (EPL of them).  Each of
-// the k rounds takes the warp-wide maximum of the order keys still in play
-// (redux.sync max), then the lowest expert index holding that key (redux.sync
-// min): a larger logit wins, an exact tie goes to the lower expert index, and a
-// NaN (key 0) is taken only after every number, lowest index first.  The gate
-// softmax is taken over the k selected logits in rank order, in fp32.  Lane j < k
-// returns the j-th ranked expert and its gate.  Both routing kernels below call
-// this one function, so they take the same decisions and compute the same gate bits.
-template <int EPL>
-__device__ __forceinline__ void topk_token(const float* __restrict__ row, int E, int k, int lane, int& out_e,
-                                           float& out_w) {
-  uint32_t key[EPL];
-  uint32_t live = 0u;   // bit i: expert i*32 + lane exists and has not been taken yet
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = i * 32 + lane;
-    key[i] = (e < E) ? order_key(row[e]) : 0u;
-    if (e < E) live |= 1u << i;
-  }
-  int my_e = 0;
-  float my_v = 0.0f;
-  for (int j = 0; j < k; ++j) {
-    uint32_t best = 0u;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (((live >> i) & 1u) && key[i] > best) best = key[i];
-    const uint32_t gbest = __reduce_max_sync(kFull, best);
-    uint32_t cand = 0xffffffffu;
-#pragma unroll
-    for (int i = EPL - 1; i >= 0; --i)
-      if (((live >> i) & 1u) && key[i] == gbest) cand = static_cast<uint32_t>(i * 32 + lane);
-    const int e = static_cast<int>(__reduce_min_sync(kFull, cand));
-    if ((e & 31) == lane) live &= ~(1u << (e >> 5));
-    if (lane == j) {
-      my_e = e;
-      my_v = key_value(gbest);
-    }
-  }
-  // gates: w_j = exp(v_j - v_0) / sum_{i<k} exp(v_i - v_0), the sum in rank order
-  const float v0 = __shfl_sync(kFull, my_v, 0);
-  const float ex = (lane < k) ? expf(my_v - v0) : 0.0f;
-  float s = 0.0f;
-  for (int j = 0; j < k; ++j) s = __fadd_rn(s, __shfl_sync(kFull, ex, j));
-  out_e = my_e;
-  out_w = __fdiv_rn(ex, s);
-}
 
 // Blocks of kTopkThreads; up to E = 256 at most 32 registers a thread, so that a whole batch of
 // 8192 tokens (one warp each) is resident at once (64 warps per SM on 152 SMs) instead of a
@@ -93,7 +32,7 @@ __global__ void __launch_bounds__(kTopkThreads, EPL <= 8 ? 8 : 1)
   if (t >= T) return;
   int e;
   float wt;
-  topk_token<EPL>(logits + static_cast<long long>(t) * E, E, k, lane, e, wt);
+  topk_token<EPL>(logits + static_cast<long long>(t) * E, LoadPlain{}, E, k, lane, e, wt);
   if (lane < k) {
     idx[static_cast<long long>(t) * k + lane] = e;
     w[static_cast<long long>(t) * k + lane] = wt;
@@ -153,7 +92,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   for (int t = warp; t < T; t += 32) {
     int e;
     float wt;
-    topk_token<EPL>(lrow0 + static_cast<long long>(t) * E, E, k, lane, e, wt);
+    topk_token<EPL>(lrow0 + static_cast<long long>(t) * E, LoadPlain{}, E, k, lane, e, wt);
     if (lane < k) {
       idx[t * k + lane] = e;
       w[t * k + lane] = wt;

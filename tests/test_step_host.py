@@ -68,6 +68,26 @@ def test_verify_drafts_rejects_before_any_launch(lib):
     assert need(0, 3, 100) == 256 and need(2 ** 31 - 1, 32, 2 ** 31 - 1) > 2 ** 45
 
 
+def test_moe_layer_decode_rejects_before_any_launch(lib):
+    f, need = lib.moe_layer_decode, lib.moe_decode_workspace_size
+    x, o, b, ws = (ctypes.c_void_p(1 << (20 + i)) for i in range(4))
+
+    def call(T=4, H=256, E=8, k=2, F=128, Fs=0, score=2, bias=N, groups=1, kept=1, renorm=1, scale=1.0, x=x, out=o, n=None):
+        n = need(T, H, E, k, F, Fs) if n is None else n
+        return f(x, P, P, P, N, N, T, H, E, k, F, Fs, score, bias, groups, kept, renorm, scale, out, N, N, N, N, ws, n, N)
+    assert call(T=17, n=1 << 30) == -2 and b"T=17" in lib.invmoe_last_error()
+    assert call(E=513) == -2 and call(H=100) == -2 and call(F=96) == -2 and call(Fs=32) == -2 and call(H=32832) == -2
+    assert call(k=9) == -1 and call(E=64, k=33) == -2 and call(T=-1) == -1
+    assert call(score=3) == -1 and call(bias=b) == -1 and call(scale=2.0) == -1 and call(renorm=0) == -1
+    assert call(score=0, groups=3) == -1 and call(score=0, groups=4, kept=5) == -1 and call(score=0, groups=8, kept=1) == -1
+    assert call(n=need(4, 256, 8, 2, 128, 0) - 1) == -3
+    assert call(out=N) == -1 and call(Fs=64) == -1                    # no output; no shared weights
+    assert call(x=ctypes.c_void_p(4100)) == -4
+    assert call(x=o) == -1 and b"overlaps" in lib.invmoe_last_error()
+    assert call(T=0) == 0
+    assert need(17, 256, 8, 2, 128, 0) == 256 and need(16, 32768, 512, 32, 1 << 20, 1 << 20) > 2 ** 30
+
+
 def test_binding_refuses_host_tensors():
     from serve_invariant_moe_gb300 import binding
     x, w = torch.zeros(4, 64), torch.zeros(64, dtype=torch.bfloat16)
@@ -77,6 +97,9 @@ def test_binding_refuses_host_tensors():
         binding.sandwich_norm_backward(x, x, x, w, torch.zeros(4), x, w, torch.zeros(4))
     with pytest.raises(ValueError, match="CUDA tensor"):
         binding.verify_drafts(torch.zeros(2, 1, 8), torch.zeros(2, 8), torch.zeros(256, dtype=torch.uint8))
+    h = w.view(1, 64)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        binding.moe_layer_decode(h, h, h.view(1, 1, 64).expand(1, 2, 64), h.view(1, 64, 1), 1, torch.zeros(256, dtype=torch.uint8))
     with pytest.raises(ValueError, match="2 dimensions"):
         binding.sandwich_norm(x[0], w, x, w)
     with pytest.raises(ValueError, match="3 dimensions"):
