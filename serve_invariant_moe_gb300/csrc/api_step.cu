@@ -145,8 +145,8 @@ int moe_layer_decode(const void* x, const void* w_router, const void* w13, const
   REQUIRE(E <= kDecodeMaxExperts, INVMOE_ERR_UNSUPPORTED_SHAPE, "E=%d > %d", E, kDecodeMaxExperts);
   REQUIRE(k <= E, INVMOE_ERR_INVALID_ARG, "k=%d must satisfy 1 <= k <= E=%d", k, E);
   REQUIRE(k <= 32, INVMOE_ERR_UNSUPPORTED_SHAPE, "k=%d > 32", k);
-  REQUIRE(H % 64 == 0 && H <= 128 * kDecodeMaxBlocks, INVMOE_ERR_UNSUPPORTED_SHAPE, "H=%d is not a multiple of 64 up to %d", H,
-          128 * kDecodeMaxBlocks);
+  REQUIRE(H % 64 == 0 && H <= 64 * kDecodeMaxBlocks, INVMOE_ERR_UNSUPPORTED_SHAPE, "H=%d is not a multiple of 64 up to %d", H,
+          64 * kDecodeMaxBlocks);
   REQUIRE(F % 64 == 0 && F <= 1 << 20, INVMOE_ERR_UNSUPPORTED_SHAPE, "F=%d is not a multiple of 64 up to 2^20", F);
   REQUIRE(F_shared % 64 == 0 && F_shared <= 1 << 20, INVMOE_ERR_UNSUPPORTED_SHAPE,
           "F_shared=%d is not a multiple of 64 up to 2^20", F_shared);

@@ -282,8 +282,8 @@ int verify_launch(const VerifyCall& c, bool f32, cudaStream_t st);
 
 // ---------------------------------------------------------------- the layer of a few tokens in one kernel
 constexpr int kDecodeMaxTokens = 16, kDecodeMaxPairs = 512, kDecodeMaxExperts = 512;
-constexpr int kDecodeMaxBlocks = 256;                 // of 128 outputs: H <= 32768
-constexpr int kDecodeFlags = 1 + kDecodeMaxBlocks + kDecodeMaxPairs + 1;
+constexpr int kDecodeMaxBlocks = 512;                 // of 64 outputs: H <= 32768
+constexpr int kDecodeFlags = 2 + 2 * kDecodeMaxBlocks + kDecodeMaxPairs;
 enum DecodeScore : int { kDecodeTopk, kDecodeSigmoid, kDecodeSoftmax };
 struct DecodeCall {
   const void* x;
@@ -312,6 +312,7 @@ struct DecodeParams {
   int* ctl;                    // unit counter, blocks done, go; zero between calls
   int* flags;                  // kDecodeFlags counters, any content
   unsigned long long timeout_ns;
+  int up_rows, shared_rows, down_rows;   // rows of the units, set by the launch
 };
 int moe_decode_launch(const DecodeCall& c, const DecodeParams& p, cudaStream_t st);
 // Row-major bf16 tensor, 128-byte swizzle; strides in bytes of the dimensions after the first.

@@ -22,6 +22,13 @@ struct LoadL2 {
   __device__ __forceinline__ float operator()(const float* p) const { return __ldcg(p); }
 };
 
+// l[i] = logit of expert i * 32 + lane (past the last: that one's), every load on its way before the first is used.
+template <int EPL, typename LOAD>
+__device__ __forceinline__ void load_row(const float* row, LOAD ld, int E, int lane, float (&l)[EPL]) {
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) l[i] = ld(row + min(i * 32 + lane, E - 1));
+}
+
 // Total order key: larger = ranks earlier.  NaN -> 0 (below every number,
 // including -inf); -0.0 and +0.0 map to the same key (a tie).
 __device__ __forceinline__ uint32_t topk_key(float v) {
@@ -43,18 +50,18 @@ __device__ __forceinline__ float topk_key_value(uint32_t key) {
 // softmax is taken over the k selected logits in rank order, in fp32.  Lane j < k
 // returns the j-th ranked expert and its gate.  Every routing kernel calls
 // this one function, so they take the same decisions and compute the same gate bits.
-template <int EPL, typename LOAD>
-__device__ __forceinline__ void topk_token(const float* row, LOAD ld, int E, int k, int lane, int& out_e, float& out_w) {
+template <int EPL>
+__device__ __forceinline__ void topk_choose(const float (&l)[EPL], int E, int k, int lane, int& my_e, float& my_v) {
   uint32_t key[EPL];
   uint32_t live = 0u;   // bit i: expert i*32 + lane exists and has not been taken yet
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = i * 32 + lane;
-    key[i] = (e < E) ? topk_key(ld(row + e)) : 0u;
+    key[i] = (e < E) ? topk_key(l[i]) : 0u;
     if (e < E) live |= 1u << i;
   }
-  int my_e = 0;
-  float my_v = 0.0f;
+  my_e = 0;
+  my_v = 0.0f;
   for (int j = 0; j < k; ++j) {
     uint32_t best = 0u;
 #pragma unroll
@@ -72,13 +79,24 @@ __device__ __forceinline__ void topk_token(const float* row, LOAD ld, int E, int
       my_v = topk_key_value(gbest);
     }
   }
-  // gates: w_j = exp(v_j - v_0) / sum_{i<k} exp(v_i - v_0), the sum in rank order
+}
+
+// Lane j < k's gate, of the j-th logit that topk_choose left it.
+__device__ __forceinline__ float topk_gate(float my_v, int k, int lane) {
+  // w_j = exp(v_j - v_0) / sum_{i<k} exp(v_i - v_0), the sum in rank order
   const float v0 = __shfl_sync(kFull, my_v, 0);
   const float ex = (lane < k) ? expf(my_v - v0) : 0.0f;
   float s = 0.0f;
   for (int j = 0; j < k; ++j) s = __fadd_rn(s, __shfl_sync(kFull, ex, j));
-  out_e = my_e;
-  out_w = __fdiv_rn(ex, s);
+  return __fdiv_rn(ex, s);
+}
+
+template <int EPL, typename LOAD>
+__device__ __forceinline__ void topk_token(const float* row, LOAD ld, int E, int k, int lane, int& out_e, float& out_w) {
+  float l[EPL], v;
+  load_row(row, ld, E, lane, l);
+  topk_choose(l, E, k, lane, out_e, v);
+  out_w = topk_gate(v, k, lane);
 }
 
 // Larger = ranks earlier; NaN -> 1 (below every number, whose keys start at 0x007fffff); 0 is left for "not there"; -0 and
@@ -154,15 +172,15 @@ struct SelectParams {
   float* w;
 };
 
-// One warp's choice for one token: lane j < k returns the j-th ranked expert and its weight.  GROUPS: sk is the warp's own
+// One warp's choice for one token: lane j < k returns the j-th ranked expert; st: the row's statistics (SOFTMAX).  GROUPS: sk is the warp's own
 // shared memory, E words and one per 32.
-template <int EPL, bool SOFTMAX, bool GROUPS, typename LOAD>
-__device__ __forceinline__ void select_token(const float* row, LOAD ld, const SelectParams& p, uint32_t* sk, int lane,
-                                             int& out_e, float& out_w) {
+template <int EPL, bool SOFTMAX, bool GROUPS>
+__device__ __forceinline__ void select_choose(const float (&row_l)[EPL], const SelectParams& p, uint32_t* sk, int lane,
+                                              int& my_e, SoftmaxStats& st) {
   float l[EPL];
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) l[i] = i * 32 + lane < p.E ? ld(row + i * 32 + lane) : -INFINITY;
-  SoftmaxStats st{0.0f, 1.0f};
+  for (int i = 0; i < EPL; ++i) l[i] = i * 32 + lane < p.E ? row_l[i] : -INFINITY;
+  st = SoftmaxStats{0.0f, 1.0f};
   if (SOFTMAX) st = softmax_stats<EPL, false>(l, p.E, lane);
   uint32_t key[EPL];                          // 0: no such expert, or its group is not kept
 #pragma unroll
@@ -263,7 +281,7 @@ __device__ __forceinline__ void select_token(const float* row, LOAD ld, const Se
     }
   }
   bool spare = true;                          // `second` is still there
-  int my_e = 0;
+  my_e = 0;
   for (int j = 0; j < p.k; ++j) {
     const uint32_t top = __reduce_max_sync(kFull, best);
     const int e = static_cast<int>(__reduce_min_sync(kFull, best == top ? static_cast<uint32_t>(best_i * 32 + lane) : kFull));
@@ -295,6 +313,12 @@ __device__ __forceinline__ void select_token(const float* row, LOAD ld, const Se
       spare = false;
     }
   }
+}
+
+// Lane j < k's weight of expert my_e, the j-th ranked.
+template <bool SOFTMAX, typename LOAD>
+__device__ __forceinline__ float select_weight(const float* row, LOAD ld, const SelectParams& p, int my_e, const SoftmaxStats& st,
+                                               int lane) {
   float s = 0.0f;
   if (lane < p.k) {
     const float lj = ld(row + my_e);
@@ -305,8 +329,17 @@ __device__ __forceinline__ void select_token(const float* row, LOAD ld, const Se
     for (int j = 0; j < p.k; ++j) sum = __fadd_rn(sum, __shfl_sync(kFull, s, j));
     s = sum == 0.0f ? 0.0f : __fdiv_rn(s, sum);
   }
-  out_e = my_e;
-  out_w = __fmul_rn(s, p.scale);
+  return __fmul_rn(s, p.scale);
+}
+
+template <int EPL, bool SOFTMAX, bool GROUPS, typename LOAD>
+__device__ __forceinline__ void select_token(const float* row, LOAD ld, const SelectParams& p, uint32_t* sk, int lane,
+                                             int& out_e, float& out_w) {
+  float l[EPL];
+  SoftmaxStats st;
+  load_row(row, ld, p.E, lane, l);
+  select_choose<EPL, SOFTMAX, GROUPS>(l, p, sk, lane, out_e, st);
+  out_w = select_weight<SOFTMAX>(row, ld, p, out_e, st, lane);
 }
 
 }  // namespace
