@@ -5,6 +5,8 @@
 // with rstd_p = 1 / sqrt(mean(x^2) + eps) of the block's output x, rstd likewise of the stored row r', a and b scalars and
 // the gate g one number per channel or per token (or absent).  Bound by memory: per element the forward reads x and r and
 // writes r' and y.  One block holds one row in registers across both sums; the reduction orders depend on H alone.
+// 8192 x 6144, fp32 x, bf16 residual, a channel's gate: 78.6 us for 503 MB, 6.4 TB/s (82.5 with 51 registers, where 40 leave
+// room for another block, 80.0 with the warps' sums read one by one); 8 rows: 7 us, the host's call.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -43,15 +45,35 @@ __device__ __forceinline__ float inv_rms(float ss, int H, float eps) {
   return __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(ss, static_cast<float>(H)), eps)));
 }
 
+// block_sum with the same order of additions, four of the warps' sums to a load.
+__device__ __forceinline__ float block_sum4(float v, float* s_part, int warp, int lane, int nwarps) {
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+  if (nwarps == 1) return v;
+  if (lane == 0) s_part[warp] = v;
+  __syncthreads();
+  float s = 0.0f;
+  int w = 0;
+  for (; w + 4 <= nwarps; w += 4) {
+    const float4 t = *reinterpret_cast<const float4*>(s_part + w);
+    s += t.x;
+    s += t.y;
+    s += t.z;
+    s += t.w;
+  }
+  for (; w < nwarps; ++w) s += s_part[w];
+  return s;
+}
+
 template <int V, typename TX, typename TR>
-__global__ void __launch_bounds__(max_threads(V))
+__global__ void __launch_bounds__(max_threads(V), V == 2 ? 3 : 1)
     sandwich_kernel(const TX* __restrict__ x, const __nv_bfloat16* __restrict__ w_post, const TR* res, const Gate gate,
                     const __nv_bfloat16* __restrict__ w_next, int H, float res_scale, float branch_scale, float eps,
                     TR* res_out, __nv_bfloat16* __restrict__ out, uint8_t* __restrict__ q, float* __restrict__ scale,
                     float* __restrict__ rstd_post, float* __restrict__ rstd_out) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float s_part[2][32];
+  __shared__ __align__(16) float s_part[2][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
   const long long t = blockIdx.x;
   const long long base = t * H;
@@ -73,7 +95,7 @@ __global__ void __launch_bounds__(max_threads(V))
   for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int i = 0; i < 8; ++i) ss = fmaf(r[v][i], r[v][i], ss);
-  const float rstd_p = inv_rms(block_sum(ss, s_part[0], warp, lane, nwarps), H, eps);
+  const float rstd_p = inv_rms(block_sum4(ss, s_part[0], warp, lane, nwarps), H, eps);
   const float token = token_factor(gate, branch_scale, t);
   ss = 0.0f;
 #pragma unroll
@@ -95,7 +117,7 @@ __global__ void __launch_bounds__(max_threads(V))
   }
   if (rstd_post != nullptr && threadIdx.x == 0) rstd_post[t] = rstd_p;
   if (w_next == nullptr) return;
-  const float rstd = inv_rms(block_sum(ss, s_part[1], warp, lane, nwarps), H, eps);
+  const float rstd = inv_rms(block_sum4(ss, s_part[1], warp, lane, nwarps), H, eps);
   if (rstd_out != nullptr && threadIdx.x == 0) rstd_out[t] = rstd;
   const int nb = (H + kFp8Block - 1) / kFp8Block;
 #pragma unroll
@@ -136,8 +158,227 @@ struct BwdParams {
   float* mean;                    // [T] mean(e r^)
   float* part;                    // [P][2][H]: partial rows of dw_n and S
   int rows;                       // rows of a partial row
+  unsigned int* status;
+  unsigned long long timeout_ns;
 };
 
+// Rows of at most 8192: a block walks p.rows consecutive rows with its share of both channel sums in registers.  Rows come by
+// bulk copies into a ring of shared memory, as many rows ahead as fit, in two groups with a barrier each: dy and r', which the
+// first sum needs, and dres and x.  A group's place is free again once the block's sum after its last use is through, so the
+// block's two barriers per row are also what the next copies wait for.
+// 8192 x 6144, fp32 x, the rest bf16, a channel's gate: 137 us with the sums' kernel for 805 MB, 5.9 TB/s; 4096 x 2048, all
+// fp32: 38.5 us, 5.2 TB/s, of which the start (14 rows a block) and the second kernel are what a copy does not have.  Two
+// vectors a thread from 2064 columns on, so that a row is few warps and its sums few additions: 768 threads of one vector took
+// 183 us, and 157 with the warps' sums read one by one and a division per mean.  At 8192 columns two rows fill the ring
+// and 128 registers are not quite enough: 4.4 TB/s.
+constexpr int kBwdMaxDepth = 8, kBwdMaxWidth = 8192;
+constexpr int kBwdBlocks = 2;                  // on a multiprocessor, of rows up to 2048
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// Bytes of a ring place: the four rows, absent ones left out.
+struct BwdShape {
+  uint32_t dy, r, dres, x, row;                // offsets of a place's rows; bytes of a place
+  int depth;
+};
+
+// Sum over a block of at most THREADS threads, the same in each: xor butterfly per warp, then the warps' sums, four chains of
+// them.  s_part: a float per warp, 0 behind the last.  Every call is a barrier.
+template <int THREADS>
+__device__ __forceinline__ float row_sum(float v, float* s_part, int warp, int lane) {
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+  if (lane == 0) s_part[warp] = v;
+  __syncthreads();
+  float4 s = *reinterpret_cast<const float4*>(s_part);
+#pragma unroll
+  for (int w = 1; w < THREADS / 128; ++w) {
+    const float4 t = reinterpret_cast<const float4*>(s_part)[w];
+    s.x += t.x; s.y += t.y; s.z += t.z; s.w += t.w;
+  }
+  return (s.x + s.y) + (s.z + s.w);
+}
+
+// V vectors of a thread, at most THREADS threads, BLOCKS of them on a multiprocessor.
+template <int V, int THREADS, int BLOCKS, typename TX, typename TR, typename TD>
+__global__ void __launch_bounds__(THREADS, BLOCKS) sandwich_bwd_kernel(const BwdParams p, const BwdShape sh) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ __align__(16) float s_part[2][2][32];
+  __shared__ uint64_t bars[2][kBwdMaxDepth];
+  __shared__ volatile int s_abort;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool next = p.w_next != nullptr, has_dres = p.dres != nullptr;
+  for (int i = threadIdx.x; i < 128; i += blockDim.x) (&s_part[0][0][0])[i] = 0.0f;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < sh.depth; ++i) {
+      mbar_init(&bars[0][i], 1);
+      mbar_init(&bars[1][i], 1);
+    }
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+  const WaitCtl wc{&s_abort, p.status, p.timeout_ns};
+  const long long t0 = static_cast<long long>(blockIdx.x) * p.rows;
+  const int n = static_cast<int>(min(static_cast<long long>(p.T), t0 + p.rows) - t0);
+  const uint32_t bx = p.H * sizeof(TX), br = p.H * sizeof(TR), bd = p.H * sizeof(TD);
+  const float inv_h = 1.0f / static_cast<float>(p.H);
+  auto load = [&](int i, int at_place, int group) {   // thread 0: a group of this block's row i
+    uint8_t* place = ring + at_place * sh.row;
+    uint64_t* bar = &bars[group][at_place];
+    const long long at = (t0 + i) * p.H;
+    if (group == 0) {
+      mbar_arrive_expect_tx(bar, bd + br);
+      bulk_load(place + sh.dy, static_cast<const TD*>(p.dy) + at, bd, bar);
+      bulk_load(place + sh.r, static_cast<const TR*>(p.r) + at, br, bar);
+    } else {
+      mbar_arrive_expect_tx(bar, bx + (has_dres ? br : 0));
+      if (has_dres) bulk_load(place + sh.dres, static_cast<const TR*>(p.dres) + at, br, bar);
+      bulk_load(place + sh.x, static_cast<const TX*>(p.x) + at, bx, bar);
+    }
+  };
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < sh.depth && i < n; ++i) {
+      if (next) load(i, i, 0);
+      load(i, i, 1);
+    }
+  }
+  Raw8<__nv_bfloat16> wn[V];
+  float wp[V][8];                              // w_p, times b and the gate of a channel
+  float dwn[V][8], s[V][8];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = (v * blockDim.x + threadIdx.x) * 8;
+    wn[v].zero();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) wp[v][i] = 0.0f;
+    if (c < p.H) {
+      if (next) wn[v].load(p.w_next + c);
+      load8(p.w_post + c, wp[v]);
+      if (p.gate.channel != nullptr) {
+        float f[8];
+        branch_factor(p.gate, p.branch_scale, 0.0f, c, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) wp[v][i] *= f[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dwn[v][i] = s[v][i] = 0.0f;
+  }
+  bool ok = true;
+  float next_p = 0.0f, next_r = 0.0f, next_g = 1.0f;           // the row's numbers, a row ahead
+  auto fetch = [&](int i) {
+    next_p = __ldg(p.rstd_post + t0 + i);
+    if (next) next_r = __ldg(p.rstd + t0 + i);
+    if (p.gate.token != nullptr) next_g = __ldg(p.gate.token + t0 + i);
+  };
+  if (n > 0) fetch(0);
+  int at_place = 0;
+  uint32_t phase = 0;
+  for (int i = 0; i < n; ++i) {
+    const long long t = t0 + i;
+    const uint8_t* place = ring + at_place * sh.row;
+    const float rstd_p = next_p, rstd = next_r, g = next_g;
+    if (i + 1 < n) fetch(i + 1);
+    float d[V][8];                             // e
+    float n_r[V][8];
+    float mean = 0.0f;
+    if (next) {
+      ok = ok && mbar_wait(&bars[0][at_place], phase, wc);
+      float dot = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int c = (v * blockDim.x + threadIdx.x) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[v][j] = n_r[v][j] = 0.0f;
+        if (c < p.H) {
+          float w[8];
+          load8(reinterpret_cast<const TD*>(place + sh.dy) + c, d[v]);
+          load8(reinterpret_cast<const TR*>(place + sh.r) + c, n_r[v]);
+          wn[v].get(w);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            n_r[v][j] *= rstd;
+            dwn[v][j] = fmaf(d[v][j], n_r[v][j], dwn[v][j]);
+            d[v][j] *= w[j];
+            dot = fmaf(d[v][j], n_r[v][j], dot);
+          }
+        }
+      }
+      mean = row_sum<THREADS>(dot, s_part[0][i & 1], warp, lane) * inv_h;
+      if (threadIdx.x == 0 && i + sh.depth < n) load(i + sh.depth, at_place, 0);
+    }
+    ok = ok && mbar_wait(&bars[1][at_place], phase, wc);
+    float u[V][8], n_x[V][8];                  // u: d w_p, times the channel's gate
+    float dot = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * blockDim.x + threadIdx.x) * 8;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[v][j] = n_x[v][j] = 0.0f;
+      if (c < p.H) {
+        float b[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) b[j] = 0.0f;
+        if (has_dres) load8(reinterpret_cast<const TR*>(place + sh.dres) + c, b);
+        load8(reinterpret_cast<const TX*>(place + sh.x) + c, n_x[v]);
+        if (next) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) b[j] = fmaf(rstd, fmaf(-n_r[v][j], mean, d[v][j]), b[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          n_x[v][j] *= rstd_p;
+          s[v][j] = fmaf(b[j] * g, n_x[v][j], s[v][j]);
+          u[v][j] = b[j] * wp[v][j];
+          dot = fmaf(u[v][j], n_x[v][j], dot);
+          b[j] *= p.res_scale;
+        }
+        store8(static_cast<TR*>(p.dresidual) + t * p.H + c, b);
+      }
+    }
+    dot = row_sum<THREADS>(dot, s_part[1][i & 1], warp, lane);
+    if (threadIdx.x == 0) {
+      if (i + sh.depth < n) load(i + sh.depth, at_place, 1);
+      if (p.dgate_token != nullptr) p.dgate_token[t] = p.branch_scale * dot;
+    }
+    const float k = p.gate.channel != nullptr ? rstd_p : rstd_p * __fmul_rn(g, p.branch_scale);   // what u still lacks
+    const float m = dot * inv_h;
+    if (++at_place == sh.depth) {
+      at_place = 0;
+      phase ^= 1u;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * blockDim.x + threadIdx.x) * 8;
+      if (c < p.H) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) n_x[v][j] = k * fmaf(-n_x[v][j], m, u[v][j]);
+        store8(static_cast<TX*>(p.dx) + t * p.H + c, n_x[v]);
+      }
+    }
+  }
+  if (p.part != nullptr) {
+    float* row = p.part + static_cast<long long>(blockIdx.x) * 2 * p.H;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * blockDim.x + threadIdx.x) * 8;
+      if (c < p.H) {
+        store8(row + c, dwn[v]);
+        store8(row + p.H + c, s[v]);
+      }
+    }
+  }
+}
+
+// Rows above 8192, whose sums do not fit a block's registers: the rows by one kernel, the channel sums by another, which reads
+// everything again (8192 x 6144 took 406 us that way, 4096 x 2048 144).
 // d of 8 elements, from the row's mean(e r^).
 template <typename TR, typename TD>
 __device__ __forceinline__ void stream_grad(const BwdParams& p, long long at, int c, float rstd, float mean, float (&d)[8]) {
@@ -352,12 +593,76 @@ int sandwich_launch(const SandwichCall& c, cudaStream_t st) {
   return check_cuda(e, "sandwich_kernel");
 }
 
-// Partial rows: a function of T and H alone, so that the order of the sums is too.
+// Partial rows: a function of T and H alone, so that the order of the sums is too.  Up to 8192 columns as many blocks as are
+// resident at once, with the registers and the ring that they take: two of at most 256 threads for rows up to 2048 (three:
+// 42 us instead of 38.5 for 4096 x 2048), one for wider ones.
 SandwichPlan sandwich_bwd_plan(int T, int H) {
-  (void)H;
-  const int rows = (T - 1) / 64 + 1;
+  const int blocks = H <= 2048 ? 152 * kBwdBlocks : H <= kBwdMaxWidth ? 152 : 64;
+  const int rows = (T - 1) / blocks + 1;
   return {rows, (T - 1) / rows + 1};
 }
+
+namespace {
+
+template <int V, int THREADS, int BLOCKS, typename TX, typename TR, typename TD>
+int launch_bwd(const BwdParams& p, int threads, int parts, cudaStream_t st) {
+  BwdShape sh{};
+  const uint32_t bx = p.H * sizeof(TX), br = p.H * sizeof(TR), bd = p.H * sizeof(TD);   // multiples of 32
+  if (p.w_next != nullptr) {
+    sh.dy = 0;
+    sh.r = bd;
+    sh.row = bd + br;
+  }
+  sh.dres = sh.row;
+  if (p.dres != nullptr) sh.row += br;
+  sh.x = sh.row;
+  sh.row += bx;
+  constexpr uint32_t room = 216 * 1024 / BLOCKS;
+  sh.depth = static_cast<int>(room / sh.row);
+  if (sh.depth > kBwdMaxDepth) sh.depth = kBwdMaxDepth;
+  if (sh.depth > p.rows) sh.depth = p.rows;
+  const auto kernel = sandwich_bwd_kernel<V, THREADS, BLOCKS, TX, TR, TD>;
+  static std::atomic<uint64_t> attr_set{0};
+  const int rc = set_smem_attr(reinterpret_cast<const void*>(kernel), static_cast<int>(room), attr_set);
+  if (rc) return rc;
+  return check_cuda(launch_kernel(kernel, dim3(parts), dim3(threads), sh.depth * sh.row, st, p, sh), "sandwich_bwd_kernel");
+}
+
+template <typename TX, typename TR, typename TD>
+int launch_bwd_typed(const BwdParams& p, int parts, cudaStream_t st) {
+  const int vecs = p.H / 8;
+  if (vecs <= 256) return launch_bwd<1, 256, kBwdBlocks, TX, TR, TD>(p, (vecs + 31) / 32 * 32, parts, st);
+  const int threads = (vecs + 63) / 64 * 32;
+  if (vecs <= 512) return launch_bwd<2, 256, 1, TX, TR, TD>(p, threads, parts, st);
+  if (vecs <= 768) return launch_bwd<2, 384, 1, TX, TR, TD>(p, threads, parts, st);
+  return launch_bwd<2, 512, 1, TX, TR, TD>(p, threads, parts, st);
+}
+
+int launch_wide(const BwdParams& p, const SandwichBwdCall& c, int parts, cudaStream_t st) {
+  {
+    ProfScope prof("sandwich_bwd_rows", st);
+    const int threads = row_shape(p.H).threads;
+    const cudaError_t e = by_types(c.x_f32, c.res_f32, [&](auto tx, auto tr) {
+      using TX = decltype(tx);
+      using TR = decltype(tr);
+      return c.dy_f32 ? launch_kernel(sandwich_bwd_rows_kernel<4, TX, TR, float>, dim3(p.T), dim3(threads), 0, st, p)
+                      : launch_kernel(sandwich_bwd_rows_kernel<4, TX, TR, __nv_bfloat16>, dim3(p.T), dim3(threads), 0, st, p);
+    });
+    const int rc = check_cuda(e, "sandwich_bwd_rows_kernel");
+    if (rc || p.part == nullptr) return rc;
+  }
+  ProfScope prof("sandwich_bwd_cols", st);
+  const dim3 grid((p.H + 2047) / 2048, parts);
+  const cudaError_t e = by_types(c.x_f32, c.res_f32, [&](auto tx, auto tr) {
+    using TX = decltype(tx);
+    using TR = decltype(tr);
+    return c.dy_f32 ? launch_kernel(sandwich_bwd_cols_kernel<TX, TR, float>, grid, dim3(256), 0, st, p)
+                    : launch_kernel(sandwich_bwd_cols_kernel<TX, TR, __nv_bfloat16>, grid, dim3(256), 0, st, p);
+  });
+  return check_cuda(e, "sandwich_bwd_cols_kernel");
+}
+
+}  // namespace
 
 int sandwich_bwd_launch(const SandwichBwdCall& c, cudaStream_t st) {
   const SandwichPlan plan = sandwich_bwd_plan(c.T, c.H);
@@ -379,35 +684,26 @@ int sandwich_bwd_launch(const SandwichBwdCall& c, cudaStream_t st) {
   p.dresidual = c.dresidual;
   p.dgate_token = c.gate_kind == INVMOE_GATE_TOKEN ? c.dgate : nullptr;
   p.rows = plan.rows;
+  p.status = c.status;
+  p.timeout_ns = kTimeoutNs;
   if (c.dw_post != nullptr) {
     p.mean = c.scratch;
     p.part = c.scratch + align_up(c.T, 64);
   }
-  {
-    ProfScope prof("sandwich_bwd_rows", st);
-    const cudaError_t e = by_types(c.x_f32, c.res_f32, [&](auto tx, auto tr) {
+  if (c.H <= kBwdMaxWidth) {
+    ProfScope prof("sandwich_bwd", st);
+    int rc = INVMOE_OK;
+    by_types(c.x_f32, c.res_f32, [&](auto tx, auto tr) {
       using TX = decltype(tx);
       using TR = decltype(tr);
-      return by_width(c.H, [&](auto v, int threads) {
-        return c.dy_f32 ? launch_kernel(sandwich_bwd_rows_kernel<v.value, TX, TR, float>, dim3(c.T), dim3(threads), 0, st, p)
-                        : launch_kernel(sandwich_bwd_rows_kernel<v.value, TX, TR, __nv_bfloat16>, dim3(c.T), dim3(threads),
-                                        0, st, p);
-      });
+      rc = c.dy_f32 ? launch_bwd_typed<TX, TR, float>(p, plan.parts, st)
+                    : launch_bwd_typed<TX, TR, __nv_bfloat16>(p, plan.parts, st);
+      return cudaSuccess;
     });
-    const int rc = check_cuda(e, "sandwich_bwd_rows_kernel");
     if (rc || c.dw_post == nullptr) return rc;
-  }
-  {
-    ProfScope prof("sandwich_bwd_cols", st);
-    const dim3 grid((c.H + 2047) / 2048, plan.parts);
-    const cudaError_t e = by_types(c.x_f32, c.res_f32, [&](auto tx, auto tr) {
-      using TX = decltype(tx);
-      using TR = decltype(tr);
-      return c.dy_f32 ? launch_kernel(sandwich_bwd_cols_kernel<TX, TR, float>, grid, dim3(256), 0, st, p)
-                      : launch_kernel(sandwich_bwd_cols_kernel<TX, TR, __nv_bfloat16>, grid, dim3(256), 0, st, p);
-    });
-    const int rc = check_cuda(e, "sandwich_bwd_cols_kernel");
-    if (rc) return rc;
+  } else {
+    const int rc = launch_wide(p, c, plan.parts, st);
+    if (rc || c.dw_post == nullptr) return rc;
   }
   ProfScope prof("sandwich_bwd_sum", st);
   return check_cuda(launch_kernel(sandwich_sum_kernel, dim3(c.H / kSumCols, 2), dim3(kSumThreads), 0, st,
