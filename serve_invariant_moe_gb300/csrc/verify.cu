@@ -28,22 +28,38 @@ constexpr int kPer = 32;                          // logits of a thread
 constexpr int kChunk = kThreads * kPer;
 
 // NaN counts as no logit at all; +inf as the largest finite number, so that it takes all the mass.
-__device__ __forceinline__ float usable(float z) { return z != z ? -INFINITY : fminf(z, FLT_MAX); }
+__device__ __forceinline__ float usable(float z) { return fminf(fmaxf(z, -INFINITY), FLT_MAX); }
 
 struct Scale {
   bool greedy;
   float inv;                                      // 1 / tau; 1 for a greedy request
+  float inv2;                                     // log2(e) / tau
 };
 __device__ __forceinline__ Scale scale_of(const VerifyCall& p, int b) {
   const float tau = p.temperature != nullptr ? __ldg(p.temperature + b) : p.tau;
-  if (!(tau > 0.0f)) return {true, 1.0f};
-  return {false, fminf(__frcp_rn(tau), FLT_MAX)};
+  const bool greedy = !(tau > 0.0f);
+  const float inv = greedy ? 1.0f : fminf(__frcp_rn(tau), FLT_MAX);
+  return {greedy, inv, fminf(__fmul_rn(inv, 1.4426950408889634f), FLT_MAX)};
 }
 
-// exp((z - m) / tau), 0 for a logit of -inf.
-__device__ __forceinline__ float weight(float z, float m, float inv) {
-  return z == -INFINITY ? 0.0f : expf(__fmul_rn(__fsub_rn(z, m), inv));
+// 2^x within 2^-22, 0 below the normal numbers.  A weight is one subtraction, one product and one of these: with expf and
+// its cases the statistics kernel was bound by instructions (64 requests, 152 thousand tokens: 56 us).
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// exp((z - m) / tau) for a finite m; 0 for a logit of -inf.
+__device__ __forceinline__ float weight(float z, float m, float inv2) {
+  return exp2_approx(__fmul_rn(__fsub_rn(z, m), inv2));
+}
+// What to subtract from a chunk's logits: its maximum, or 0 where it has none.
+__device__ __forceinline__ float shift_of(float m) { return m == -INFINITY ? 0.0f : m; }
 
 __device__ __forceinline__ int drafts_of(const VerifyCall& p, int b) {
   return p.n_draft != nullptr ? max(0, min(p.D, __ldg(p.n_draft + b))) : p.D;
@@ -124,8 +140,9 @@ __global__ void __launch_bounds__(kThreads) verify_stats_kernel(const VerifyCall
   }
   m = block_max(m, s_max, warp, lane);
   float s = 0.0f;
+  const float shift = shift_of(m);
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) s += weight(z[j], m, sc.inv);
+  for (int j = 0; j < kPer; ++j) s += weight(z[j], shift, sc.inv2);
   s = block_sum(s, s_sum, warp, lane, kThreads / 32);
   int arg = 0x7fffffff;
   if (sc.greedy) {
@@ -142,17 +159,19 @@ __global__ void __launch_bounds__(kThreads) verify_stats_kernel(const VerifyCall
   if (threadIdx.x == 0) static_cast<Stats*>(p.stats)[row * p.chunks + chunk] = Stats{m, s, arg, 0};
 }
 
-// A row's statistics from its chunks': lane l joins chunks l, l + 32, ... ascending, then a xor butterfly.
-__device__ __forceinline__ Stats row_stats(const Stats* part, int chunks, float inv, int lane) {
-  float m = -INFINITY;
-  for (int c = lane; c < chunks; c += 32) m = fmaxf(m, part[c].max);
+// A row's statistics from its chunks': lane l joins chunks l, l + 32, ... ascending, then a xor butterfly.  `first`: the
+// lane's first chunk, loaded by the caller.
+__device__ __forceinline__ Stats join(const Stats& first, const Stats* part, int chunks, float inv2, int lane) {
+  float m = first.max;
+  for (int c = lane + 32; c < chunks; c += 32) m = fmaxf(m, part[c].max);
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
-  float s = 0.0f;
-  int arg = 0x7fffffff;
-  for (int c = lane; c < chunks; c += 32) {
+  const float shift = shift_of(m);
+  float s = first.sum * weight(first.max, shift, inv2);
+  int arg = first.max == m ? first.arg : 0x7fffffff;
+  for (int c = lane + 32; c < chunks; c += 32) {
     const Stats t = part[c];
-    s += t.sum * weight(t.max, m, inv);
+    s += t.sum * weight(t.max, shift, inv2);
     if (t.max == m) arg = min(arg, t.arg);
   }
 #pragma unroll
@@ -160,12 +179,23 @@ __device__ __forceinline__ Stats row_stats(const Stats* part, int chunks, float 
   return Stats{m, s, static_cast<int>(__reduce_min_sync(kFull, arg)), 0};
 }
 
-// A racer: the larger score wins, then the lower index.  0 is nobody.
-__device__ __forceinline__ unsigned long long racer(float w, float e, int j) {
-  const float score = __fdiv_rn(w, e);
-  if (!(w > 0.0f) || !(score >= 0.0f) || __float_as_uint(score) == 0x80000000u) return 0ull;
-  return (static_cast<unsigned long long>(__float_as_uint(score)) << 32) | (0xffffffffu - static_cast<unsigned>(j));
-}
+// A thread's best racer so far, its places ascending: the larger w / e wins, then the lower place.
+struct Racer {
+  float score = -1.0f;
+  int at = 0;
+  __device__ __forceinline__ void take(float w, float e_inv, int j) {
+    const float v = __fmul_rn(w, e_inv);
+    if (w > 0.0f && v > score && v >= 0.0f) {      // (a noise that is negative, -0 or NaN takes no part)
+      score = v;
+      at = j;
+    }
+  }
+  // Comparable over threads; 0 is nobody.
+  __device__ __forceinline__ unsigned long long key() const {
+    if (score < 0.0f) return 0ull;
+    return (static_cast<unsigned long long>(__float_as_uint(score)) << 32) | (0xffffffffu - static_cast<unsigned>(at));
+  }
+};
 __device__ __forceinline__ unsigned long long warp_best(unsigned long long v) {
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) v = max(v, __shfl_xor_sync(kFull, v, d));
@@ -177,6 +207,8 @@ __global__ void __launch_bounds__(kThreads) verify_choose_kernel(const VerifyCal
   pdl_wait();
   pdl_trigger();
   __shared__ Stats s_row[2 * kVerifyMaxDrafts + 1];
+  __shared__ float s_z[2 * kVerifyMaxDrafts + 1];  // the row's logit of its draft token
+  __shared__ int s_x[kVerifyMaxDrafts];
   __shared__ unsigned long long s_best[2][kThreads / 32];
   __shared__ int s_n, s_last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -189,28 +221,56 @@ __global__ void __launch_bounds__(kThreads) verify_choose_kernel(const VerifyCal
   const T* logits = static_cast<const T*>(p.logits) + static_cast<long long>(b) * (D + 1) * V;
   const T* drafts = static_cast<const T*>(p.draft_logits) + static_cast<long long>(b) * D * V;
   const bool has_q = p.draft_logits != nullptr;
-  for (int r = warp; r < p.rows; r += kThreads / 32) {
-    if (r <= D ? r > n_draft : r - (D + 1) >= n_draft || sc.greedy) continue;
-    const Stats t = row_stats(part + static_cast<long long>(r) * p.chunks, p.chunks, sc.inv, lane);
-    if (lane == 0) s_row[r] = t;
+  // what needs no decision is on its way first: the noise, every row's chunks, the draft tokens and their logits
+  float e[kPer];
+  if (!sc.greedy) load_chunk<float, VEC>(p.noise + static_cast<long long>(b) * V, chunk * kChunk, V, 1.0f, e);
+  for (int r0 = warp; r0 < p.rows; r0 += 2 * (kThreads / 32)) {
+    Stats first[2];
+    int x[2];
+    float z[2];
+    bool counts[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = r0 + h * (kThreads / 32), i = r <= D ? r : r - (D + 1);
+      counts[h] = r < p.rows && (r <= D ? r <= n_draft : i < n_draft && !sc.greedy);
+      first[h] = Stats{-INFINITY, 0.0f, 0x7fffffff, 0};
+      if (counts[h] && lane < p.chunks) first[h] = part[static_cast<long long>(r) * p.chunks + lane];
+      x[h] = counts[h] && i < n_draft ? __ldg(p.draft_tokens + static_cast<long long>(b) * D + i) : -1;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = r0 + h * (kThreads / 32), i = r <= D ? r : r - (D + 1);
+      z[h] = -INFINITY;
+      if (x[h] >= 0 && x[h] < V) z[h] = static_cast<float>((r <= D ? logits : drafts)[static_cast<long long>(i) * V + x[h]]);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = r0 + h * (kThreads / 32);
+      if (!counts[h]) continue;
+      const Stats t = join(first[h], part + static_cast<long long>(r) * p.chunks, p.chunks, sc.inv2, lane);
+      if (lane == 0) {
+        s_row[r] = t;
+        s_z[r] = usable(z[h]);
+        if (r < n_draft) s_x[r] = x[h];
+      }
+    }
   }
   __syncthreads();
   if (warp == 0) {
     bool ok = false;
     if (lane < n_draft) {
-      const int x = __ldg(p.draft_tokens + static_cast<long long>(b) * D + lane);
+      const int x = s_x[lane];
       const Stats t = s_row[lane];
       if (x >= 0 && x < V && t.max > -INFINITY) {
         if (sc.greedy) {
           ok = x == t.arg;
         } else {
           // u q < p over the common denominators: u e_q S_p < e_p S_q
-          const float ep = weight(usable(static_cast<float>(logits[static_cast<long long>(lane) * V + x])), t.max, sc.inv);
+          const float ep = weight(s_z[lane], t.max, sc.inv2);
           float eq = 1.0f, sq = 1.0f;
           if (has_q) {
             const Stats d = s_row[D + 1 + lane];
-            eq = d.max > -INFINITY ? weight(usable(static_cast<float>(drafts[static_cast<long long>(lane) * V + x])), d.max, sc.inv)
-                                   : 0.0f;
+            eq = d.max > -INFINITY ? weight(s_z[D + 1 + lane], d.max, sc.inv2) : 0.0f;
             sq = d.max > -INFINITY ? d.sum : 1.0f;
           }
           const float u = __ldg(p.accept_u + static_cast<long long>(b) * D + lane);
@@ -225,57 +285,58 @@ __global__ void __launch_bounds__(kThreads) verify_choose_kernel(const VerifyCal
   const int n = s_n;                              // accepted; row n gives the next token
   const Stats t = s_row[n];
   const bool rejected = n < n_draft;
-  unsigned long long best = 0ull, other = 0ull;   // of the weights, and of p alone in case they are all zero
+  Racer best, other;                              // of the weights, and of p alone in case they are all zero
   if (!sc.greedy && t.max > -INFINITY) {
     const float inv_p = __frcp_rn(t.sum);
-    float z[kPer], e[kPer];
+    float z[kPer];
     load_chunk<T, VEC>(logits + static_cast<long long>(n) * V, chunk * kChunk, V, -INFINITY, z);
-    load_chunk<float, VEC>(p.noise + static_cast<long long>(b) * V, chunk * kChunk, V, 1.0f, e);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) z[j] = __fmul_rn(weight(usable(z[j]), t.max, sc.inv), inv_p);
+    for (int j = 0; j < kPer; ++j) e[j] = rcp_approx(e[j]);
     if (!rejected) {
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) best = max(best, racer(z[j], e[j], chunk * kChunk + place<VEC>(j)));
+      for (int j = 0; j < kPer; ++j)
+        best.take(__fmul_rn(weight(usable(z[j]), t.max, sc.inv2), inv_p), e[j], chunk * kChunk + place<VEC>(j));
     } else if (has_q) {
       const Stats d = s_row[D + 1 + n];
-      const float inv_q = d.max > -INFINITY ? __frcp_rn(d.sum) : 0.0f;
+      const bool some = d.max > -INFINITY;
+      const float inv_q = some ? __frcp_rn(d.sum) : 0.0f, shift = shift_of(d.max);
       float q[kPer];
       load_chunk<T, VEC>(drafts + static_cast<long long>(n) * V, chunk * kChunk, V, -INFINITY, q);
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const int at = chunk * kChunk + place<VEC>(j);
-        const float qj = inv_q == 0.0f ? 0.0f : __fmul_rn(weight(usable(q[j]), d.max, sc.inv), inv_q);
-        best = max(best, racer(__fsub_rn(z[j], qj), e[j], at));
-        other = max(other, racer(z[j], e[j], at));
+        const float pj = __fmul_rn(weight(usable(z[j]), t.max, sc.inv2), inv_p);
+        const float qj = some ? __fmul_rn(weight(usable(q[j]), shift, sc.inv2), inv_q) : 0.0f;
+        best.take(__fsub_rn(pj, qj), e[j], at);
+        other.take(pj, e[j], at);
       }
     } else {
-      const int x = __ldg(p.draft_tokens + static_cast<long long>(b) * D + n);
+      const int x = s_x[n];
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const int at = chunk * kChunk + place<VEC>(j);
-        const unsigned long long v = racer(z[j], e[j], at);
-        other = max(other, v);
-        if (at != x) best = max(best, v);
+        const float pj = __fmul_rn(weight(usable(z[j]), t.max, sc.inv2), inv_p);
+        if (at != x) best.take(pj, e[j], at);
+        other.take(pj, e[j], at);
       }
     }
   }
-  best = warp_best(best);
-  other = warp_best(other);
+  unsigned long long first = warp_best(best.key()), second = rejected ? warp_best(other.key()) : 0ull;
   if (lane == 0) {
-    s_best[0][warp] = best;
-    s_best[1][warp] = other;
+    s_best[0][warp] = first;
+    s_best[1][warp] = second;
   }
   __syncthreads();
   ulonglong2* racers = static_cast<ulonglong2*>(p.racers) + static_cast<long long>(b) * p.chunks;
   if (threadIdx.x == 0) {
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
-      best = max(best, s_best[0][w]);
-      other = max(other, s_best[1][w]);
+      first = max(first, s_best[0][w]);
+      second = max(second, s_best[1][w]);
     }
     s_last = 1;
     if (!sc.greedy && p.chunks > 1) {
-      racers[chunk] = make_ulonglong2(best, other);
+      racers[chunk] = make_ulonglong2(first, second);
       __threadfence();
       s_last = atomicAdd(p.done + b, 1) == p.chunks - 1;
       __threadfence();
@@ -286,31 +347,29 @@ __global__ void __launch_bounds__(kThreads) verify_choose_kernel(const VerifyCal
   int token = t.max > -INFINITY ? t.arg : -1;
   if (!sc.greedy) {
     if (p.chunks > 1) {
-      best = other = 0ull;
+      first = second = 0ull;
       for (int c = lane; c < p.chunks; c += 32) {
         const ulonglong2 v = __ldcg(racers + c);
-        best = max(best, v.x);
-        other = max(other, v.y);
+        first = max(first, v.x);
+        second = max(second, v.y);
       }
-      best = warp_best(best);
-      other = warp_best(other);
+      first = warp_best(first);
+      second = warp_best(second);
     }
-    best = __shfl_sync(kFull, best, 0);
-    other = __shfl_sync(kFull, other, 0);
-    if (best == 0ull) best = other;
-    token = best == 0ull ? -1 : static_cast<int>(0xffffffffu - static_cast<unsigned>(best));
+    first = __shfl_sync(kFull, first, 0);
+    second = __shfl_sync(kFull, second, 0);
+    if (first == 0ull) first = second;
+    token = first == 0ull ? -1 : static_cast<int>(0xffffffffu - static_cast<unsigned>(first));
   }
   if (lane == 0) p.n_accepted[b] = n;
   for (int i = lane; i <= D; i += 32) {
     int x = -1;
     float lp = 0.0f;
     if (i <= n) {
-      x = i < n ? __ldg(p.draft_tokens + static_cast<long long>(b) * D + i) : token;
+      x = i < n ? s_x[i] : token;
       const Stats r = s_row[i];
-      lp = x < 0 ? -INFINITY
-                 : __fsub_rn(__fmul_rn(__fsub_rn(usable(static_cast<float>(logits[static_cast<long long>(i) * V + x])), r.max),
-                                       sc.inv),
-                             logf(r.sum));
+      const float z = i < n ? s_z[i] : x < 0 ? 0.0f : usable(static_cast<float>(logits[static_cast<long long>(i) * V + x]));
+      lp = x < 0 ? -INFINITY : __fsub_rn(__fmul_rn(__fsub_rn(z, r.max), sc.inv), logf(r.sum));
     }
     p.tokens[static_cast<long long>(b) * (D + 1) + i] = x;
     p.logp[static_cast<long long>(b) * (D + 1) + i] = lp;

@@ -1,8 +1,9 @@
 """Verification of drafted tokens on the GPU against a request-by-request oracle in 64 bits.
 
-Tolerance.  exp((z - m) / tau) in fp32: two roundings of an argument of at most 104 (beyond it the weight is 0 in fp32) move it
-by 2 * 104 * 2^-24, expf adds 2 units of 2^-23 and a sum of at most 32 + 13 + (V / 8192 / 32 + 5) terms in a row 60 * 2^-24:
-REL = 4e-5 of a probability covers it, with the reciprocal of the sum.  A decision has to be the oracle's except where its two
+Tolerance.  exp((z - m) / tau) in fp32: three roundings (the difference, log2(e) / tau, their product) of an argument of at most
+104 (beyond it the weight is 0 in fp32) move it by 3 * 104 * 2^-24, the exponential adds 2^-22, the reciprocals of the sum and of
+the noise 2^-22 each, and a sum of at most 32 + 13 + (V / 8192 / 32 + 5) terms in a row 60 * 2^-24: REL = 4e-5 of a probability
+covers it.  A decision has to be the oracle's except where its two
 sides are within that of one another, and a drawn token's score has to be within that of the largest.  The logarithm of a
 probability is within REL + 2^-23 of its value.
 """
