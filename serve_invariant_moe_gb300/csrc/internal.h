@@ -276,9 +276,10 @@ struct VerifyCall {
   int32_t* done;               // scratch: [B] chunks finished
   void* stats;                 // scratch: 16 bytes per request, row and chunk
   void* racers;                // scratch: 16 bytes per request and chunk
+  int racing;                  // blocks of a request in the race, set by the launch
 };
 int verify_chunks(int V);
-int verify_launch(const VerifyCall& c, bool f32, cudaStream_t st);
+int verify_launch(VerifyCall c, bool f32, cudaStream_t st);
 
 // ---------------------------------------------------------------- the layer of a few tokens in one kernel
 constexpr int kDecodeMaxTokens = 16, kDecodeMaxPairs = 512, kDecodeMaxExperts = 512;

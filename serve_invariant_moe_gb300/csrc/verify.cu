@@ -98,16 +98,6 @@ __device__ __forceinline__ void load_chunk(const T* row, int first, int V, float
   }
 }
 
-__device__ __forceinline__ float block_max(float v, float* s_part, int warp, int lane) {
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, d));
-  if (lane == 0) s_part[warp] = v;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) v = fmaxf(v, s_part[w]);
-  return v;
-}
-
 struct Stats {
   float max, sum;
   int arg, pad;                                   // lowest index of the maximum (greedy requests)
@@ -117,8 +107,7 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) verify_stats_kernel(const VerifyCall p) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float s_max[kThreads / 32], s_sum[kThreads / 32];
-  __shared__ int s_arg[kThreads / 32];
+  __shared__ Stats s_warp[kThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int chunk = static_cast<int>(blockIdx.x % p.chunks);
   const long long row = blockIdx.x / p.chunks;    // a request's target rows, then its draft rows
@@ -138,25 +127,35 @@ __global__ void __launch_bounds__(kThreads) verify_stats_kernel(const VerifyCall
     z[j] = usable(z[j]);
     m = fmaxf(m, z[j]);
   }
-  m = block_max(m, s_max, warp, lane);
-  float s = 0.0f;
+  // a warp's own maximum and sum first, so that the block meets once
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
   const float shift = shift_of(m);
+  float s = 0.0f;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) s += weight(z[j], shift, sc.inv2);
-  s = block_sum(s, s_sum, warp, lane, kThreads / 32);
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
   int arg = 0x7fffffff;
   if (sc.greedy) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
       if (z[j] == m) arg = min(arg, place<VEC>(j));
     arg = __reduce_min_sync(kFull, arg);
-    if (lane == 0) s_arg[warp] = arg;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) arg = min(arg, s_arg[w]);
-    arg += chunk * kChunk;
   }
-  if (threadIdx.x == 0) static_cast<Stats*>(p.stats)[row * p.chunks + chunk] = Stats{m, s, arg, 0};
+  if (lane == 0) s_warp[warp] = Stats{m, s, arg, 0};
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+#pragma unroll
+  for (int w = 1; w < kThreads / 32; ++w) m = fmaxf(m, s_warp[w].max);
+  s = 0.0f;
+  arg = 0x7fffffff;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    s += s_warp[w].sum * weight(s_warp[w].max, shift_of(m), sc.inv2);
+    if (s_warp[w].max == m) arg = min(arg, s_warp[w].arg);
+  }
+  static_cast<Stats*>(p.stats)[row * p.chunks + chunk] = Stats{m, s, chunk * kChunk + arg, 0};
 }
 
 // A row's statistics from its chunks': lane l joins chunks l, l + 32, ... ascending, then a xor butterfly.  `first`: the
@@ -212,18 +211,18 @@ __global__ void __launch_bounds__(kThreads) verify_choose_kernel(const VerifyCal
   __shared__ unsigned long long s_best[2][kThreads / 32];
   __shared__ int s_n, s_last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = static_cast<int>(blockIdx.x / p.chunks), chunk = static_cast<int>(blockIdx.x % p.chunks);
+  const int b = static_cast<int>(blockIdx.x / p.racing), first_chunk = static_cast<int>(blockIdx.x % p.racing);
   const int D = p.D, V = p.V;
   const int n_draft = drafts_of(p, b);
   const Scale sc = scale_of(p, b);
-  if (sc.greedy && chunk != 0) return;            // nothing to draw: one block reads the maxima
+  if (sc.greedy && first_chunk != 0) return;            // nothing to draw: one block reads the maxima
   const Stats* part = static_cast<const Stats*>(p.stats) + static_cast<long long>(b) * p.rows * p.chunks;
   const T* logits = static_cast<const T*>(p.logits) + static_cast<long long>(b) * (D + 1) * V;
   const T* drafts = static_cast<const T*>(p.draft_logits) + static_cast<long long>(b) * D * V;
   const bool has_q = p.draft_logits != nullptr;
   // what needs no decision is on its way first: the noise, every row's chunks, the draft tokens and their logits
   float e[kPer];
-  if (!sc.greedy) load_chunk<float, VEC>(p.noise + static_cast<long long>(b) * V, chunk * kChunk, V, 1.0f, e);
+  if (!sc.greedy) load_chunk<float, VEC>(p.noise + static_cast<long long>(b) * V, first_chunk * kChunk, V, 1.0f, e);
   for (int r0 = warp; r0 < p.rows; r0 += 2 * (kThreads / 32)) {
     Stats first[2];
     int x[2];
@@ -288,36 +287,35 @@ __global__ void __launch_bounds__(kThreads) verify_choose_kernel(const VerifyCal
   Racer best, other;                              // of the weights, and of p alone in case they are all zero
   if (!sc.greedy && t.max > -INFINITY) {
     const float inv_p = __frcp_rn(t.sum);
-    float z[kPer];
-    load_chunk<T, VEC>(logits + static_cast<long long>(n) * V, chunk * kChunk, V, -INFINITY, z);
+    const T* z_row = logits + static_cast<long long>(n) * V;
+    const T* q_row = drafts + static_cast<long long>(n) * V;
+    const Stats d = rejected && has_q ? s_row[D + 1 + n] : Stats{-INFINITY, 0.0f, 0, 0};
+    const bool some_q = d.max > -INFINITY;
+    const float inv_q = some_q ? __frcp_rn(d.sum) : 0.0f;
+    const int x = rejected && !has_q ? s_x[n] : -1;              // what a drafter without probabilities drew
+    for (int chunk = first_chunk; chunk < p.chunks; chunk += p.racing) {
+      float z[kPer];
+      if (chunk != first_chunk) load_chunk<float, VEC>(p.noise + static_cast<long long>(b) * V, chunk * kChunk, V, 1.0f, e);
+      load_chunk<T, VEC>(z_row, chunk * kChunk, V, -INFINITY, z);
+      if (some_q) {
+        float q[kPer];
+        load_chunk<T, VEC>(q_row, chunk * kChunk, V, -INFINITY, q);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) e[j] = rcp_approx(e[j]);
-    if (!rejected) {
+        for (int j = 0; j < kPer; ++j) {
+          const int at = chunk * kChunk + place<VEC>(j);
+          const float pj = __fmul_rn(weight(usable(z[j]), t.max, sc.inv2), inv_p);
+          const float qj = __fmul_rn(weight(usable(q[j]), d.max, sc.inv2), inv_q), r = rcp_approx(e[j]);
+          best.take(__fsub_rn(pj, qj), r, at);
+          other.take(pj, r, at);
+        }
+      } else {
 #pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        best.take(__fmul_rn(weight(usable(z[j]), t.max, sc.inv2), inv_p), e[j], chunk * kChunk + place<VEC>(j));
-    } else if (has_q) {
-      const Stats d = s_row[D + 1 + n];
-      const bool some = d.max > -INFINITY;
-      const float inv_q = some ? __frcp_rn(d.sum) : 0.0f, shift = shift_of(d.max);
-      float q[kPer];
-      load_chunk<T, VEC>(drafts + static_cast<long long>(n) * V, chunk * kChunk, V, -INFINITY, q);
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int at = chunk * kChunk + place<VEC>(j);
-        const float pj = __fmul_rn(weight(usable(z[j]), t.max, sc.inv2), inv_p);
-        const float qj = some ? __fmul_rn(weight(usable(q[j]), shift, sc.inv2), inv_q) : 0.0f;
-        best.take(__fsub_rn(pj, qj), e[j], at);
-        other.take(pj, e[j], at);
-      }
-    } else {
-      const int x = s_x[n];
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int at = chunk * kChunk + place<VEC>(j);
-        const float pj = __fmul_rn(weight(usable(z[j]), t.max, sc.inv2), inv_p);
-        if (at != x) best.take(pj, e[j], at);
-        other.take(pj, e[j], at);
+        for (int j = 0; j < kPer; ++j) {
+          const int at = chunk * kChunk + place<VEC>(j);
+          const float pj = __fmul_rn(weight(usable(z[j]), t.max, sc.inv2), inv_p), r = rcp_approx(e[j]);
+          if (at != x) best.take(pj, r, at);
+          if (x >= 0 && at == x) other.take(pj, r, at);
+        }
       }
     }
   }
@@ -335,10 +333,10 @@ __global__ void __launch_bounds__(kThreads) verify_choose_kernel(const VerifyCal
       second = max(second, s_best[1][w]);
     }
     s_last = 1;
-    if (!sc.greedy && p.chunks > 1) {
-      racers[chunk] = make_ulonglong2(first, second);
+    if (!sc.greedy && p.racing > 1) {
+      racers[first_chunk] = make_ulonglong2(first, second);
       __threadfence();
-      s_last = atomicAdd(p.done + b, 1) == p.chunks - 1;
+      s_last = atomicAdd(p.done + b, 1) == p.racing - 1;
       __threadfence();
     }
   }
@@ -346,9 +344,9 @@ __global__ void __launch_bounds__(kThreads) verify_choose_kernel(const VerifyCal
   if (!s_last || warp != 0) return;
   int token = t.max > -INFINITY ? t.arg : -1;
   if (!sc.greedy) {
-    if (p.chunks > 1) {
+    if (p.racing > 1) {
       first = second = 0ull;
-      for (int c = lane; c < p.chunks; c += 32) {
+      for (int c = lane; c < p.racing; c += 32) {
         const ulonglong2 v = __ldcg(racers + c);
         first = max(first, v.x);
         second = max(second, v.y);
@@ -380,9 +378,17 @@ __global__ void __launch_bounds__(kThreads) verify_choose_kernel(const VerifyCal
 
 int verify_chunks(int V) { return (V - 1) / kChunk + 1; }
 
-int verify_launch(const VerifyCall& c, bool f32, cudaStream_t st) {
+int verify_launch(VerifyCall c, bool f32, cudaStream_t st) {
   const bool vec = c.V % (f32 ? 4 : 8) == 0;
-  const dim3 g1(static_cast<unsigned>(static_cast<long long>(c.B) * c.rows * c.chunks)), g2(c.B * c.chunks);
+  int sms = 0;
+  const int rc = device_sm_count(&sms);
+  if (rc) return rc;
+  // Every racing block decides for itself, so no more of them than two to a multiprocessor where a chunk each would be more
+  // (64 requests of 19 chunks: 1216 blocks of one chunk took 33 us).  The largest score is the same however the chunks are
+  // shared out.
+  c.racing = (2 * sms - 1) / c.B + 1;
+  if (c.racing > c.chunks) c.racing = c.chunks;
+  const dim3 g1(static_cast<unsigned>(static_cast<long long>(c.B) * c.rows * c.chunks)), g2(c.B * c.racing);
   {
     ProfScope prof("verify_stats", st);
     const cudaError_t e =
