@@ -66,10 +66,15 @@ def _head(t, n):
 
 
 class MoELayer:
-    """Batch-invariant MoE layer forward on one GPU."""
+    """Batch-invariant MoE layer forward on one GPU.
 
-    def __init__(self, weights: MoEWeights):
+    fused: decode (and prefill without its intermediates) of at most 16 tokens runs the layer in one kernel
+    (binding.moe_layer_decode, at most 512 experts), with the same bits; the decode buffers of its intermediates
+    (xp, h, y, ys, plan) are then not written."""
+
+    def __init__(self, weights: MoEWeights, fused: bool = False):
         self.w = weights
+        self.fused = fused
         self._ws = None
         self._decode = None
 
@@ -120,6 +125,26 @@ class MoELayer:
                                   out=_head(bufs.get("out"), T), out_bf16=out_bf16)
         return dict(out=out, logits=logits, xp=xp, **r, **f)
 
+    def _run_fused(self, x, d, out, out_bf16):
+        """At most 16 tokens in one kernel; logits and choice into the decode buffers."""
+        w, B = self.w, x.shape[0]
+        r = w.routing
+        chosen = {} if r is None else dict(score=r.score, bias=r.bias, n_group=r.n_group, topk_group=r.topk_group,
+                                           renormalize=r.renormalize, scale=r.scale)
+        return binding.moe_layer_decode(x, w.w_router, w.w13, w.w2, w.k, d["fused_ws"], w.ws13, w.ws2, out=out,
+                                        out_bf16=out_bf16, logits=d["logits"][:B], topk_idx=d["idx"][:B],
+                                        topk_w=d["w"][:B], **chosen)["out"]
+
+    def check(self):
+        """Raise if a kernel of a decode call since the last check gave up waiting: what it should have written is then not
+        there.  Waits for the device."""
+        d = self._decode
+        if d is not None:
+            torch.cuda.synchronize(d["device"])
+            for name in ("ws", "fused_ws"):
+                if name in d:
+                    binding.check_status(d[name])
+
     def prefill(self, x: torch.Tensor, out_bf16: Optional[torch.Tensor] = None, return_all=False,
                 replay_idx: Optional[torch.Tensor] = None):
         """x [T, H] bf16 -> out [T, H] fp32 (optionally also a bf16 copy).  With replay_idx [T, k]
@@ -133,6 +158,8 @@ class MoELayer:
             if self._decode is None or self._decode["B"] < T:
                 self.alloc_decode(max(T, 1))
             d = self._decode
+            if self.fused and T <= binding.DECODE_MAX_TOKENS:
+                return self._run_fused(x, d, None, out_bf16)
             bufs = {k: d[k] for k in ("logits", "idx", "w", "plan", "xp", "h", "y", "ys")}
             return self._run(x, d["ws"], bufs, out_bf16=out_bf16)["out"]
         res = self._run(x, self._workspace(T), out_bf16=out_bf16, replay_idx=replay_idx)
@@ -189,6 +216,10 @@ class MoELayer:
             ws=binding.new_workspace(binding.workspace_size(B, w.H, w.E, w.k, w.F, w.F_shared, 0), dev),
         )
         d = self._decode
+        if self.fused:
+            few = min(B, binding.DECODE_MAX_TOKENS)
+            d["fused_ws"] = binding.new_workspace(
+                binding.moe_decode_workspace_size(few, w.H, w.E, w.k, w.F, w.F_shared), dev)
         d["device"] = torch.device(dev)
         p = lambda t: None if t is None else t.data_ptr()   # noqa: E731
         # moe_layer_forward's arguments; decode() fills in x (0), B (6), out_bf16 (21) and the stream (24)
@@ -214,6 +245,8 @@ class MoELayer:
             raise ValueError(f"x_tokens must be a contiguous [B, {w.H}] bf16 tensor on {d['device']}")
         if out_bf16 is not None:
             binding._req(out_bf16, torch.bfloat16, "out_bf16", (B, w.H))
+        if self.fused and 0 < B <= binding.DECODE_MAX_TOKENS:
+            return self._run_fused(x_tokens, d, d["out"][:B], out_bf16)
         if w.routing is not None:
             bufs = {name: d[name] for name in ("logits", "idx", "w", "plan", "xp", "h", "y", "ys", "out")}
             return self._run_routed(x_tokens, d["ws"], bufs, out_bf16, None)["out"]
@@ -322,6 +355,29 @@ def moe_prefill(layer: MoELayer, x: torch.Tensor) -> torch.Tensor:
 
 def moe_decode(layer: MoELayer, x_tokens: torch.Tensor) -> torch.Tensor:
     return layer.decode(x_tokens)
+
+
+def head_verify_drafts(hidden, w_vocab, noise, draft_tokens=None, draft_logits=None, accept_u=None, n_draft=None,
+                       temperature=1.0, logits=None, workspace=None):
+    """The end of a drafted decode step: the head's logits of B requests' D + 1 rows each, then binding.verify_drafts on them.
+
+    hidden [B * (D + 1), H] bf16, request by request, row i of a request the state behind its i-th drafted token (row 0:
+    behind its last emitted one); noise [B, V].  Returns verify_drafts' dict and the logits [B, D + 1, V] fp32 (into
+    ``logits`` if given)."""
+    T, H = hidden.shape
+    B, V = noise.shape
+    D = 0 if draft_tokens is None else draft_tokens.shape[1]
+    if T != B * (D + 1) or w_vocab.shape[0] != V:
+        raise ValueError(f"hidden must have {B} * {D + 1} rows and w_vocab {V}, got {T} and {w_vocab.shape[0]}")
+    need = max(binding.workspace_size(T, H, V=V), binding.verify_workspace_size(B, D, V))
+    if workspace is None:
+        workspace = binding.new_workspace(need, hidden.device)
+    target = torch.zeros(T, dtype=torch.int32, device=hidden.device)     # the head's own logprob is not used
+    logits = None if logits is None else logits.view(T, V)
+    z = binding.lm_logprob_kl(hidden, w_vocab, target, workspace, logits=logits, write_logits=True)["logits"]
+    z = z.view(B, D + 1, V)
+    got = binding.verify_drafts(z, noise, workspace, draft_tokens, draft_logits, accept_u, n_draft, temperature)
+    return {**got, "logits": z}
 
 
 def head_logprob_kl(hidden, w_vocab, target, rollout_logp=None, beta=2.0, workspace=None, logits=None,

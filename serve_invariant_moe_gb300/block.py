@@ -1,4 +1,4 @@
-"""The 8-bit MoE block: residual + norm, scored routing, e4m3 experts, combine.
+"""MoE blocks.  The 8-bit one: residual + norm, scored routing, e4m3 experts, combine.
 
 What one block of a transformer does around its MoE layer, with the experts' weights and activations in e4m3 (a scale
 per 128 x 128 weights and per row and 128 activations):
@@ -11,6 +11,8 @@ per 128 x 128 weights and per row and 128 activations):
 
 Every step is per token with one reduction order, so a token's bits do not depend on its batch, on prefill or decode, or
 on the kernel that a batch size selects.
+
+MoEBlock is the bf16 block with norms before and after its layer, its gate and residual scale; forward and backward.
 """
 import threading
 from dataclasses import dataclass
@@ -19,7 +21,7 @@ from typing import Optional
 import torch
 
 from . import binding
-from .api import Routing
+from .api import MoELayer, MoEWeights, Routing
 
 
 @dataclass
@@ -208,3 +210,67 @@ class Fp8DecodeGraph:
         """As Fp8MoEBlock.check, for the replays."""
         torch.cuda.synchronize(self.x.device)
         binding.check_status(self._bufs["ws"])
+
+
+@dataclass
+class MoEBlockWeights:
+    layer: MoEWeights
+    w_post: torch.Tensor                    # [H] bf16: the norm of the layer's output
+    w_next: Optional[torch.Tensor] = None   # [H] bf16: the next block's norm; None behind the last block
+    gate: Optional[torch.Tensor] = None     # [H] bf16, a channel's
+    residual_scale: float = 1.0
+    branch_scale: float = 1.0
+    eps: float = 1e-6
+
+
+class MoEBlock:
+    """One bf16 MoE block with norms before and after its layer, from one normalised row to the next block's:
+
+        m   = MoE layer of n                                               (api.MoELayer)
+        r'  = residual_scale r + branch_scale gate rms_norm(m) w_post      the residual stream
+        n'  = rms_norm(r') w_next                                          bf16, the next block's n
+
+    The norms, gate and scales are one call (binding.sandwich_norm).  The first block's n is add_rms_norm's of the embedded
+    row.  Every step is per token with one reduction order, so prefill and decode give the same bits."""
+
+    def __init__(self, weights: MoEBlockWeights, fused: bool = True):
+        """fused: decode of at most 16 rows runs the layer in one kernel (MoELayer)."""
+        self.w = weights
+        self.layer = MoELayer(weights.layer, fused=fused)
+
+    def _after(self, m, residual, gate, residual_out=None):
+        w = self.w
+        return binding.sandwich_norm(m, w.w_post, residual, w.w_next, w.gate if gate is None else gate, w.residual_scale,
+                                     w.branch_scale, w.eps, residual_out=residual_out)
+
+    def prefill(self, n, residual, gate=None, residual_out=None, return_all=False):
+        """n [T, H] bf16 and residual [T, H] (bf16 or fp32) -> (n' or None, the new residual).
+
+        gate [T] fp32: one per token, in the place of the weights'.  return_all: the dict that backward takes."""
+        m = self.layer.prefill(n, return_all=return_all)
+        s = self._after(m["out"] if return_all else m, residual, gate, residual_out)
+        if return_all:
+            return {**s, "layer": m, "n": n, "gate": self.w.gate if gate is None else gate}
+        return s["out"], s["residual"]
+
+    def decode(self, n, residual, gate=None, residual_out=None):
+        """One row per request (or per drafted token): as prefill, the layer on buffers kept for the largest batch so far.
+        The calls share those buffers, so they belong on one stream."""
+        s = self._after(self.layer.decode(n), residual, gate, residual_out)
+        return s["out"], s["residual"]
+
+    def backward(self, fwd, dnext, dres=None, weight_grads=True):
+        """fwd: prefill(..., return_all=True)'s dict; dnext [T, H]: the gradient of n' (None behind the last block); dres: the
+        gradient that reaches the new residual from the stream, in its type.
+
+        Returns the gradients dn (of n, fp32), dresidual, dw_post, dw_next, dgate and the layer's (``layer``)."""
+        w = self.w
+        s = binding.sandwich_norm_backward(dnext, dres, fwd["layer"]["out"], w.w_post, fwd["rstd_post"], fwd["residual"],
+                                           w.w_next if dnext is not None else None, fwd["rstd"] if dnext is not None else None,
+                                           fwd["gate"], w.residual_scale, w.branch_scale, dweights=weight_grads)
+        g = self.layer.backward(fwd["n"], fwd["layer"], s["dx"], weight_grads)
+        return dict(dn=g["dx"], dresidual=s["dresidual"], dw_post=s["dw_post"], dw_next=s["dw_next"], dgate=s["dgate"], layer=g)
+
+    def check(self):
+        """MoELayer.check, for decode."""
+        self.layer.check()

@@ -209,7 +209,7 @@ size_t verify_workspace_size(int B, int D, int V) {
   if (B <= 0 || D < 0 || V <= 0) return kStatusBytes;
   const size_t chunks = verify_chunks(V);
   return kStatusBytes + align_up(static_cast<size_t>(B) * sizeof(int32_t), 256) +
-         static_cast<size_t>(B) * (2 * static_cast<size_t>(D) + 2) * chunks * 16;
+         static_cast<size_t>(B) * ((2 * static_cast<size_t>(D) + 1) * chunks + verify_race_chunks(V)) * 16;
 }
 
 int verify_drafts(const void* logits, int logits_type, const void* draft_logits, const int32_t* draft_tokens,
@@ -222,7 +222,8 @@ int verify_drafts(const void* logits, int logits_type, const void* draft_logits,
   REQUIRE(D <= kVerifyMaxDrafts, INVMOE_ERR_UNSUPPORTED_SHAPE, "D=%d > %d", D, kVerifyMaxDrafts);
   REQUIRE(temperature != nullptr || tau >= 0.0f, INVMOE_ERR_INVALID_ARG, "need a temperature >= 0");
   const int chunks = verify_chunks(V), rows = D + 1 + (draft_logits != nullptr ? D : 0);
-  REQUIRE(static_cast<long long>(B) * rows <= 0x7fffffffLL / chunks, INVMOE_ERR_UNSUPPORTED_SHAPE,
+  REQUIRE(static_cast<long long>(B) * rows <= 0x7fffffffLL / chunks && B <= 0x3fffffff / verify_race_chunks(V),
+          INVMOE_ERR_UNSUPPORTED_SHAPE,
           "too many rows for one launch");
   REQUIRE_PTR(workspace);
   REQUIRE(ws_bytes >= verify_workspace_size(B, D, V), INVMOE_ERR_WORKSPACE_TOO_SMALL, "workspace too small");
@@ -237,7 +238,7 @@ int verify_drafts(const void* logits, int logits_type, const void* draft_logits,
                tokens, n_accepted, logp, reinterpret_cast<int32_t*>(s), nullptr, nullptr};
   s += align_up(static_cast<size_t>(B) * sizeof(int32_t), 256);
   c.racers = s;
-  c.stats = s + static_cast<size_t>(B) * chunks * 16;
+  c.stats = s + static_cast<size_t>(B) * verify_race_chunks(V) * 16;
   return verify_launch(c, logits_type == INVMOE_F32, static_cast<cudaStream_t>(stream));
 }
 

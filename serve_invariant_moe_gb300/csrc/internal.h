@@ -275,10 +275,11 @@ struct VerifyCall {
   float* logp;                 // [B, D + 1]
   int32_t* done;               // scratch: [B] chunks finished
   void* stats;                 // scratch: 16 bytes per request, row and chunk
-  void* racers;                // scratch: 16 bytes per request and chunk
+  void* racers;                // scratch: 16 bytes per request and block of the race
   int racing;                  // blocks of a request in the race, set by the launch
 };
-int verify_chunks(int V);
+int verify_chunks(int V);        // of a row's statistics
+int verify_race_chunks(int V);   // of the race: at most so many blocks of a request
 int verify_launch(VerifyCall c, bool f32, cudaStream_t st);
 
 // ---------------------------------------------------------------- the layer of a few tokens in one kernel

@@ -6,9 +6,13 @@
 // every emitted token has the target's distribution, and which one it is follows from the logits and the given numbers alone.
 //
 // Two kernels: the statistics (maximum, sum of exponentials) of every row that counts, a block per chunk of kChunk logits;
-// then acceptance and the race on the one row that is left, a block per chunk again, the last one of a request to finish
-// joining the chunks.  Bound by reading the logits once (the race reads one row more per request, mostly from L2).  Chunks
-// and the order in which they are joined follow from V alone, so a request's bits do not depend on the batch.
+// then acceptance and the race on the one row that is left, by as many blocks of a request as are resident, the last one to
+// finish joining them.  Bound by reading the logits once and, for the row that is drawn from, once more, with the noise.
+// The chunks and the order in which they are joined follow from V alone, and the largest score is the same however the race
+// is shared out, so a request's bits do not depend on the batch.
+// 64 requests of at most 4 drafts, 151552 tokens, fp32: 49 us (statistics 34, 5.3 TB/s; choice 21), 99 at first: expf and its
+// special cases kept the statistics at 56 us, and a racing block per chunk, each with the whole decision to take, the choice
+// at 50.  One request: 10 us, two launches and the decision's chain of loads (chunks, draft tokens, their logits).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -24,8 +28,10 @@ namespace invmoe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPer = 32;                          // logits of a thread
+constexpr int kPer = 32;                          // logits of a thread of the statistics
 constexpr int kChunk = kThreads * kPer;
+constexpr int kRacePer = 16;                      // of the race, which holds two rows and the noise
+constexpr int kRaceChunk = kThreads * kRacePer;
 
 // NaN counts as no logit at all; +inf as the largest finite number, so that it takes all the mass.
 __device__ __forceinline__ float usable(float z) { return fminf(fmaxf(z, -INFINITY), FLT_MAX); }
@@ -43,7 +49,7 @@ __device__ __forceinline__ Scale scale_of(const VerifyCall& p, int b) {
 }
 
 // 2^x within 2^-22, 0 below the normal numbers.  A weight is one subtraction, one product and one of these: with expf and
-// its cases the statistics kernel was bound by instructions (64 requests, 152 thousand tokens: 56 us).
+// its cases the statistics kernel was bound by instructions.
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -65,7 +71,7 @@ __device__ __forceinline__ int drafts_of(const VerifyCall& p, int b) {
   return p.n_draft != nullptr ? max(0, min(p.D, __ldg(p.n_draft + b))) : p.D;
 }
 
-// Element of the i-th of a thread's kPer: vectors of 8 or, where rows do not start on 16 bytes, single ones.
+// Place of the i-th of a thread's logits in its chunk: vectors of 8 or, where rows do not start on 16 bytes, single ones.
 template <bool VEC>
 __device__ __forceinline__ int place(int i) {
   return VEC ? ((i >> 3) * kThreads + static_cast<int>(threadIdx.x)) * 8 + (i & 7)
@@ -73,11 +79,11 @@ __device__ __forceinline__ int place(int i) {
 }
 
 // This thread's elements of a row from `first` on; `fill` behind the row's end.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_chunk(const T* row, int first, int V, float fill, float (&z)[kPer]) {
+template <typename T, bool VEC, int PER>
+__device__ __forceinline__ void load_chunk(const T* row, int first, int V, float fill, float (&z)[PER]) {
   if constexpr (VEC) {
 #pragma unroll
-    for (int v = 0; v < kPer / 8; ++v) {
+    for (int v = 0; v < PER / 8; ++v) {
       const int c = first + (v * kThreads + static_cast<int>(threadIdx.x)) * 8;
       float t[8];
       if (c + 8 <= V) {
@@ -91,7 +97,7 @@ __device__ __forceinline__ void load_chunk(const T* row, int first, int V, float
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
       const int c = first + i * kThreads + static_cast<int>(threadIdx.x);
       z[i] = c < V ? static_cast<float>(row[c]) : fill;
     }
@@ -202,7 +208,7 @@ __device__ __forceinline__ unsigned long long warp_best(unsigned long long v) {
 }
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) verify_choose_kernel(const VerifyCall p) {
+__global__ void __launch_bounds__(kThreads, 4) verify_choose_kernel(const VerifyCall p) {
   pdl_wait();
   pdl_trigger();
   __shared__ Stats s_row[2 * kVerifyMaxDrafts + 1];
@@ -221,8 +227,8 @@ __global__ void __launch_bounds__(kThreads) verify_choose_kernel(const VerifyCal
   const T* drafts = static_cast<const T*>(p.draft_logits) + static_cast<long long>(b) * D * V;
   const bool has_q = p.draft_logits != nullptr;
   // what needs no decision is on its way first: the noise, every row's chunks, the draft tokens and their logits
-  float e[kPer];
-  if (!sc.greedy) load_chunk<float, VEC>(p.noise + static_cast<long long>(b) * V, first_chunk * kChunk, V, 1.0f, e);
+  float e[kRacePer];
+  if (!sc.greedy) load_chunk<float, VEC>(p.noise + static_cast<long long>(b) * V, first_chunk * kRaceChunk, V, 1.0f, e);
   for (int r0 = warp; r0 < p.rows; r0 += 2 * (kThreads / 32)) {
     Stats first[2];
     int x[2];
@@ -293,16 +299,17 @@ __global__ void __launch_bounds__(kThreads) verify_choose_kernel(const VerifyCal
     const bool some_q = d.max > -INFINITY;
     const float inv_q = some_q ? __frcp_rn(d.sum) : 0.0f;
     const int x = rejected && !has_q ? s_x[n] : -1;              // what a drafter without probabilities drew
-    for (int chunk = first_chunk; chunk < p.chunks; chunk += p.racing) {
-      float z[kPer];
-      if (chunk != first_chunk) load_chunk<float, VEC>(p.noise + static_cast<long long>(b) * V, chunk * kChunk, V, 1.0f, e);
-      load_chunk<T, VEC>(z_row, chunk * kChunk, V, -INFINITY, z);
+    const int race_chunks = (V - 1) / kRaceChunk + 1;
+    for (int chunk = first_chunk; chunk < race_chunks; chunk += p.racing) {
+      float z[kRacePer];
+      if (chunk != first_chunk) load_chunk<float, VEC>(p.noise + static_cast<long long>(b) * V, chunk * kRaceChunk, V, 1.0f, e);
+      load_chunk<T, VEC>(z_row, chunk * kRaceChunk, V, -INFINITY, z);
       if (some_q) {
-        float q[kPer];
-        load_chunk<T, VEC>(q_row, chunk * kChunk, V, -INFINITY, q);
+        float q[kRacePer];
+        load_chunk<T, VEC>(q_row, chunk * kRaceChunk, V, -INFINITY, q);
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          const int at = chunk * kChunk + place<VEC>(j);
+        for (int j = 0; j < kRacePer; ++j) {
+          const int at = chunk * kRaceChunk + place<VEC>(j);
           const float pj = __fmul_rn(weight(usable(z[j]), t.max, sc.inv2), inv_p);
           const float qj = __fmul_rn(weight(usable(q[j]), d.max, sc.inv2), inv_q), r = rcp_approx(e[j]);
           best.take(__fsub_rn(pj, qj), r, at);
@@ -310,8 +317,8 @@ __global__ void __launch_bounds__(kThreads) verify_choose_kernel(const VerifyCal
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          const int at = chunk * kChunk + place<VEC>(j);
+        for (int j = 0; j < kRacePer; ++j) {
+          const int at = chunk * kRaceChunk + place<VEC>(j);
           const float pj = __fmul_rn(weight(usable(z[j]), t.max, sc.inv2), inv_p), r = rcp_approx(e[j]);
           if (at != x) best.take(pj, r, at);
           if (x >= 0 && at == x) other.take(pj, r, at);
@@ -325,7 +332,7 @@ __global__ void __launch_bounds__(kThreads) verify_choose_kernel(const VerifyCal
     s_best[1][warp] = second;
   }
   __syncthreads();
-  ulonglong2* racers = static_cast<ulonglong2*>(p.racers) + static_cast<long long>(b) * p.chunks;
+  ulonglong2* racers = static_cast<ulonglong2*>(p.racers) + static_cast<long long>(b) * p.racing;
   if (threadIdx.x == 0) {
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
@@ -377,6 +384,7 @@ __global__ void __launch_bounds__(kThreads) verify_choose_kernel(const VerifyCal
 }  // namespace
 
 int verify_chunks(int V) { return (V - 1) / kChunk + 1; }
+int verify_race_chunks(int V) { return (V - 1) / kRaceChunk + 1; }
 
 int verify_launch(VerifyCall c, bool f32, cudaStream_t st) {
   const bool vec = c.V % (f32 ? 4 : 8) == 0;
@@ -386,8 +394,9 @@ int verify_launch(VerifyCall c, bool f32, cudaStream_t st) {
   // Every racing block decides for itself, so no more of them than two to a multiprocessor where a chunk each would be more
   // (64 requests of 19 chunks: 1216 blocks of one chunk took 33 us).  The largest score is the same however the chunks are
   // shared out.
-  c.racing = (2 * sms - 1) / c.B + 1;
-  if (c.racing > c.chunks) c.racing = c.chunks;
+  c.racing = (4 * sms - 1) / c.B + 1;
+  const int race_chunks = verify_race_chunks(c.V);
+  if (c.racing > race_chunks) c.racing = race_chunks;
   const dim3 g1(static_cast<unsigned>(static_cast<long long>(c.B) * c.rows * c.chunks)), g2(c.B * c.racing);
   {
     ProfScope prof("verify_stats", st);
