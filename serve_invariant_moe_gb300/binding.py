@@ -804,19 +804,6 @@ def moe_layer_decode(x, w_router, w13, w2, k, workspace, ws13=None, ws2=None, sc
                              workspace.numel()))
     return {"out": out, "out_bf16": out_bf16, "logits": logits, "topk_idx": topk_idx, "topk_w": topk_w}
 
-def _gate(m, gate, T, H):
-    """The gate's kind by its type and shape: None, [H] bf16 (per channel) or [T] fp32 (per token)."""
-    if gate is None:
-        return 0
-    if gate.dtype == torch.bfloat16:
-        m.check(gate, "gate", BF16_, H)
-        return 1
-    if gate.dtype == torch.float32:
-        m.check(gate, "gate", F32_, T)
-        return 2
-    raise ValueError(f"gate must be [H] torch.bfloat16 or [T] torch.float32, got {gate.dtype}")
-
-
 def sandwich_norm(x, w_post, residual, w_next=None, gate=None, residual_scale=1.0, branch_scale=1.0, eps=1e-6, out=True,
                   fp8=False, residual_out=None, q=None, scale=None, rstd_post=None, rstd=None):
     """The norms after and before a block: dict(residual, out, q, scale, rstd_post, rstd).
@@ -843,36 +830,9 @@ def sandwich_norm_backward(dy, dres, x, w_post, rstd_post, residual, w_next=None
     that reaches the stored row from the residual stream (None: none).  dx has x's type, dresidual the residual's; the
     weights' gradients are fp32 [H] (skipped with dweights=False), dgate [H] or [T] fp32 as the gate.  ``workspace``:
     sandwich_norm_backward_workspace_size bytes (allocated if not given)."""
-    m = marshal()
-    T, H = _dims(x, "x")
-    xt, rt = _type(x, "x"), _type(residual, "residual")
-    m.check(x, "x", xt, T, H)
-    m.check(residual, "residual", rt, T, H)
-    m.check(w_post, "w_post", BF16_, H)
-    m.check(rstd_post, "rstd_post", F32_, T)
-    if (dy is None) != (w_next is None) or (dy is None) != (rstd is None):
-        raise ValueError("dy, w_next and rstd go together")
-    yt = 0
-    if dy is not None:
-        yt = _type(dy, "dy")
-        m.check(dy, "dy", yt, T, H)
-        m.check(w_next, "w_next", BF16_, H)
-        m.check(rstd, "rstd", F32_, T)
-    if dres is not None:
-        m.check(dres, "dres", rt, T, H)
-    kind = _gate(m, gate, T, H)
-    dx = _out(m, dx, x, "dx", xt, T, H)
-    dresidual = _out(m, dresidual, x, "dresidual", rt, T, H)
-    dw_post = m.new(x, F32_, H) if dweights else None
-    dw_next = m.new(x, F32_, H) if dweights and dy is not None else None
-    dgate = m.new(x, F32_, T) if kind == 2 else m.new(x, F32_, H) if kind == 1 and dweights else None
-    if workspace is None:
-        workspace = m.new(x, U8_, sandwich_norm_backward_workspace_size(T, H))
-    m.check(workspace, "workspace", U8_)
-    check(m.sandwich_norm_backward(dy, yt, dres, x, xt, w_post, rstd_post, residual, rt, w_next, rstd, gate, kind, T, H,
-                                   residual_scale, branch_scale, dx, dresidual, dw_post, dw_next, dgate, workspace,
-                                   workspace.numel()))
-    return dict(dx=dx, dresidual=dresidual, dw_post=dw_post, dw_next=dw_next, dgate=dgate)
+    r = marshal().sandwich_backward(dy, dres, x, w_post, rstd_post, residual, w_next, rstd, gate, residual_scale, branch_scale,
+                                    dx, dresidual, dweights, workspace)
+    return r if r.__class__ is dict else check(r)
 
 
 def verify_workspace_size(B, D, V) -> int:

@@ -361,6 +361,17 @@ PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+const void* data_of(PyObject* o) { return o == Py_None ? nullptr : THPVariable_Unpack(o).data_ptr(); }
+
+// The gate's kind by its type and shape: None, [H] bf16 (a channel's), [T] fp32 (a token's).
+bool gate_kind(PyObject* o, at::IntArrayRef rows, at::IntArrayRef row, int* kind) {
+  *kind = INVMOE_GATE_NONE;
+  if (o == Py_None) return true;
+  if (!THPVariable_Check(o)) return refuse("gate", "must be a tensor");
+  *kind = THPVariable_Unpack(o).scalar_type() == kTypes[0] ? INVMOE_GATE_CHANNEL : INVMOE_GATE_TOKEN;
+  return *kind == INVMOE_GATE_CHANNEL ? check_tensor(o, "gate", 0, row) : check_tensor(o, "gate", 1, rows);
+}
+
 // sandwich(x, w_post, residual, w_next, gate, residual_scale, branch_scale, eps, out, fp8, residual_out, q, scale, rstd_post,
 // rstd): likewise, of sandwich_norm.
 PyObject* sandwich(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -381,19 +392,9 @@ PyObject* sandwich(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!check_tensor(a[0], "x", xt, full) || !check_tensor(a[1], "w_post", 0, row) ||
       !check_tensor(a[2], "residual", rt, full) || (next && !check_tensor(a[3], "w_next", 0, row)))
     return nullptr;
-  int kind = INVMOE_GATE_NONE;
-  const void* gate = nullptr;
-  if (a[4] != Py_None) {
-    if (!THPVariable_Check(a[4])) {
-      refuse("gate", "must be a tensor");
-      return nullptr;
-    }
-    const at::Tensor& g = THPVariable_Unpack(a[4]);
-    kind = g.scalar_type() == kTypes[0] ? INVMOE_GATE_CHANNEL : INVMOE_GATE_TOKEN;
-    if (kind == INVMOE_GATE_CHANNEL ? !check_tensor(a[4], "gate", 0, row) : !check_tensor(a[4], "gate", 1, rows))
-      return nullptr;
-    gate = g.data_ptr();
-  }
+  int kind;
+  if (!gate_kind(a[4], rows, row, &kind)) return nullptr;
+  const void* gate = data_of(a[4]);
   Ref res_out, out, q, scale, rstd_post, rstd;
   if (!output(a[10], "residual_out", rt, full, &res_out) || !output(a[13], "rstd_post", 1, rows, &rstd_post)) return nullptr;
   if (!next) {
@@ -429,6 +430,64 @@ PyObject* sandwich(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// sandwich_backward(dy, dres, x, w_post, rstd_post, residual, w_next, rstd, gate, residual_scale, branch_scale, dx, dresidual,
+// dweights, workspace): likewise, of sandwich_norm_backward.
+PyObject* sandwich_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 15) {
+    PyErr_SetString(PyExc_TypeError, "sandwich_backward takes 15 arguments");
+    return nullptr;
+  }
+  int T, H, xt, rT, rH, rt, yT, yH, yt = 0;
+  if (!matrix(a[2], "x", &T, &H, &xt) || !matrix(a[5], "residual", &rT, &rH, &rt)) return nullptr;
+  const int64_t rows[] = {T}, row[] = {H}, full[] = {T, H};
+  const bool next = a[0] != Py_None;
+  if (next != (a[6] != Py_None) || next != (a[7] != Py_None)) {
+    PyErr_SetString(PyExc_ValueError, "dy, w_next and rstd go together");
+    return nullptr;
+  }
+  float number[2];                                    // residual_scale, branch_scale
+  int kind;
+  if (!convert(a[9], &number[0]) || !convert(a[10], &number[1]) || !check_tensor(a[2], "x", xt, full) ||
+      !check_tensor(a[5], "residual", rt, full) || !check_tensor(a[3], "w_post", 0, row) ||
+      !check_tensor(a[4], "rstd_post", 1, rows) || (a[1] != Py_None && !check_tensor(a[1], "dres", rt, full)) ||
+      !gate_kind(a[8], rows, row, &kind))
+    return nullptr;
+  if (next && (!matrix(a[0], "dy", &yT, &yH, &yt) || !check_tensor(a[0], "dy", yt, full) ||
+               !check_tensor(a[6], "w_next", 0, row) || !check_tensor(a[7], "rstd", 1, rows)))
+    return nullptr;
+  const int weights = PyObject_IsTrue(a[13]);
+  if (weights < 0) return nullptr;
+  Ref dx, dresidual, dw_post, dw_next, dgate, space;
+  if (!output(a[11], "dx", xt, full, &dx) || !output(a[12], "dresidual", rt, full, &dresidual)) return nullptr;
+  auto made = [](Ref* r, bool wanted, at::IntArrayRef dims) {
+    if (wanted) r->o = new_output(1, dims);
+    else none(r);
+    return r->o != nullptr;
+  };
+  const bool token = kind == INVMOE_GATE_TOKEN;
+  if (!made(&dw_post, weights, row) || !made(&dw_next, weights && next, row) ||
+      !made(&dgate, token || (kind == INVMOE_GATE_CHANNEL && weights), token ? rows : row))
+    return nullptr;
+  const int64_t want[] = {static_cast<int64_t>(sandwich_norm_backward_workspace_size(T, H))};
+  if (!output(a[14], "workspace", 4, a[14] == Py_None ? at::IntArrayRef(want) : at::IntArrayRef(), &space)) return nullptr;
+  const size_t bytes = static_cast<size_t>(THPVariable_Unpack(space.o).numel());
+  const void *dy = data_of(a[0]), *dres = data_of(a[1]), *x = data_of(a[2]), *w_post = data_of(a[3]), *r = data_of(a[5]),
+             *w_next = data_of(a[6]), *gate = data_of(a[8]);
+  const float *rstd_post = static_cast<const float*>(data_of(a[4])), *rstd = static_cast<const float*>(data_of(a[7]));
+  void* stream = c10::cuda::getCurrentCUDAStream().stream();
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = sandwich_norm_backward(dy, yt, dres, x, xt, w_post, rstd_post, r, rt, w_next, rstd, gate, kind, T, H, number[0], number[1],
+                              dx.data(), dresidual.data(), static_cast<float*>(dw_post.data()),
+                              static_cast<float*>(dw_next.data()), static_cast<float*>(dgate.data()), space.data(), bytes,
+                              stream);
+  Py_END_ALLOW_THREADS
+  if (rc != 0) return PyLong_FromLong(rc);
+  return dict_of({"dx", "dresidual", "dw_post", "dw_next", "dgate"}, {&dx, &dresidual, &dw_post, &dw_next, &dgate});
+  END_HANDLE_TH_ERRORS
+}
+
 #define METHOD(name, fn) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(fn)), METH_FASTCALL, nullptr}
 #define ENTRY(name) METHOD(#name, &call<&name>)
 
@@ -450,7 +509,7 @@ PyMethodDef methods[] = {
     ENTRY(moe_grouped_down_fp8),
     ENTRY(moe_layer_decode),
     METHOD("sandwich", &sandwich),
-    ENTRY(sandwich_norm_backward),
+    METHOD("sandwich_backward", &sandwich_backward),
     ENTRY(verify_drafts),
     {nullptr, nullptr, 0, nullptr}};
 
