@@ -849,37 +849,9 @@ def verify_drafts(logits, noise, workspace, draft_tokens=None, draft_logits=None
     (None: all); noise [B, V] fp32 exponential.  temperature: a number or [B] fp32, 0 for greedy.  Without draft_tokens one
     token per request is drawn.  tokens: the accepted drafts, the drawn token, -1 behind it; logp: of those tokens, 0 behind.
     workspace: at least verify_workspace_size(B, D, V) bytes, any content."""
-    m = marshal()
-    B, rows, V = _dims(logits, "logits", 3)
-    D = rows - 1
-    if D < 0:
-        raise ValueError("logits must have at least one row per request")
-    lt = _type(logits, "logits")
-    m.check(logits, "logits", lt, B, D + 1, V)
-    m.check(noise, "noise", F32_, B, V)
-    if D == 0:
-        if draft_tokens is not None or draft_logits is not None or accept_u is not None or n_draft is not None:
-            raise ValueError("logits of one row per request leave no room for drafts")
-    else:
-        m.check(draft_tokens, "draft_tokens", I32_, B, D)
-        m.check(accept_u, "accept_u", F32_, B, D)
-        if draft_logits is not None:
-            m.check(draft_logits, "draft_logits", lt, B, D, V)
-        if n_draft is not None:
-            m.check(n_draft, "n_draft", I32_, B)
-    tau, each = 1.0, None
-    if isinstance(temperature, torch.Tensor):
-        m.check(temperature, "temperature", F32_, B)
-        each = temperature
-    else:
-        tau = temperature
-    m.check(workspace, "workspace", U8_)
-    tokens = _out(m, tokens, logits, "tokens", I32_, B, D + 1)
-    n_accepted = _out(m, n_accepted, logits, "n_accepted", I32_, B)
-    logp = _out(m, logp, logits, "logp", F32_, B, D + 1)
-    check(m.verify_drafts(logits, lt, draft_logits, draft_tokens, accept_u, noise, n_draft, each, tau, B, D, V, tokens,
-                          n_accepted, logp, workspace, workspace.numel()))
-    return {"tokens": tokens, "n_accepted": n_accepted, "logp": logp}
+    r = marshal().verify(logits, noise, workspace, draft_tokens, draft_logits, accept_u, n_draft, temperature, tokens,
+                         n_accepted, logp)
+    return r if r.__class__ is dict else check(r)
 
 
 def gemm_bf16(a, b, workspace, variant=0, out=None):

@@ -488,6 +488,75 @@ PyObject* sandwich_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// verify(logits, noise, workspace, draft_tokens, draft_logits, accept_u, n_draft, temperature, tokens, n_accepted, logp):
+// likewise, of verify_drafts.
+PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 11) {
+    PyErr_SetString(PyExc_TypeError, "verify takes 11 arguments");
+    return nullptr;
+  }
+  if (!THPVariable_Check(a[0])) {
+    refuse("logits", "must be a tensor");
+    return nullptr;
+  }
+  const at::Tensor& z = THPVariable_Unpack(a[0]);
+  if (z.dim() != 3) {
+    refuse("logits", "must have 3 dimensions, got shape " + shape_text(z.sizes()));
+    return nullptr;
+  }
+  const int64_t B = z.size(0), D = z.size(1) - 1, V = z.size(2);
+  if (D < 0 || B > INT32_MAX || D > INT32_MAX || V > INT32_MAX) {
+    refuse("logits", D < 0 ? "must have at least one row per request" : "does not fit 32-bit sizes");
+    return nullptr;
+  }
+  if (z.scalar_type() != kTypes[0] && z.scalar_type() != kTypes[1]) {
+    refuse("logits", "must be torch.bfloat16 or torch.float32, got " + type_name(z.scalar_type()));
+    return nullptr;
+  }
+  const int zt = z.scalar_type() == kTypes[0] ? 0 : 1;
+  const int64_t all[] = {B, D + 1, V}, draft[] = {B, D, V}, wide[] = {B, V}, pairs[] = {B, D}, out[] = {B, D + 1}, each[] = {B};
+  if (!check_tensor(a[0], "logits", zt, all) || !check_tensor(a[1], "noise", 1, wide)) return nullptr;
+  if (D == 0) {
+    if (a[3] != Py_None || a[4] != Py_None || a[5] != Py_None || a[6] != Py_None) {
+      refuse("logits", "of one row per request leave no room for drafts");
+      return nullptr;
+    }
+  } else if (!check_tensor(a[3], "draft_tokens", 3, pairs) || !check_tensor(a[5], "accept_u", 1, pairs) ||
+             (a[4] != Py_None && !check_tensor(a[4], "draft_logits", zt, draft)) ||
+             (a[6] != Py_None && !check_tensor(a[6], "n_draft", 3, each))) {
+    return nullptr;
+  }
+  float tau = 1.0f;
+  const float* temperature = nullptr;
+  if (THPVariable_Check(a[7])) {
+    if (!check_tensor(a[7], "temperature", 1, each)) return nullptr;
+    temperature = static_cast<const float*>(data_of(a[7]));
+  } else if (!convert(a[7], &tau)) {
+    return nullptr;
+  }
+  if (!check_tensor(a[2], "workspace", 4, at::IntArrayRef())) return nullptr;
+  Ref tokens, accepted, logp;
+  if (!output(a[8], "tokens", 3, out, &tokens) || !output(a[9], "n_accepted", 3, each, &accepted) ||
+      !output(a[10], "logp", 1, out, &logp))
+    return nullptr;
+  void* space = THPVariable_Unpack(a[2]).data_ptr();
+  const size_t bytes = static_cast<size_t>(THPVariable_Unpack(a[2]).numel());
+  const void *logits = z.data_ptr(), *draft_logits = data_of(a[4]);
+  const int32_t *draft_tokens = static_cast<const int32_t*>(data_of(a[3])), *n_draft = static_cast<const int32_t*>(data_of(a[6]));
+  const float *u = static_cast<const float*>(data_of(a[5])), *noise = static_cast<const float*>(data_of(a[1]));
+  void* stream = c10::cuda::getCurrentCUDAStream().stream();
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = verify_drafts(logits, zt, draft_logits, draft_tokens, u, noise, n_draft, temperature, tau, static_cast<int>(B),
+                     static_cast<int>(D), static_cast<int>(V), static_cast<int32_t*>(tokens.data()),
+                     static_cast<int32_t*>(accepted.data()), static_cast<float*>(logp.data()), space, bytes, stream);
+  Py_END_ALLOW_THREADS
+  if (rc != 0) return PyLong_FromLong(rc);
+  return dict_of({"tokens", "n_accepted", "logp"}, {&tokens, &accepted, &logp});
+  END_HANDLE_TH_ERRORS
+}
+
 #define METHOD(name, fn) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(fn)), METH_FASTCALL, nullptr}
 #define ENTRY(name) METHOD(#name, &call<&name>)
 
@@ -510,7 +579,7 @@ PyMethodDef methods[] = {
     ENTRY(moe_layer_decode),
     METHOD("sandwich", &sandwich),
     METHOD("sandwich_backward", &sandwich_backward),
-    ENTRY(verify_drafts),
+    METHOD("verify", &verify),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
