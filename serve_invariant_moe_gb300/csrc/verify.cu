@@ -10,9 +10,11 @@
 // finish joining them.  Bound by reading the logits once and, for the row that is drawn from, once more, with the noise.
 // The chunks and the order in which they are joined follow from V alone, and the largest score is the same however the race
 // is shared out, so a request's bits do not depend on the batch.
-// 64 requests of at most 4 drafts, 151552 tokens, fp32: 49 us (statistics 34, 5.3 TB/s; choice 21), 99 at first: expf and its
-// special cases kept the statistics at 56 us, and a racing block per chunk, each with the whole decision to take, the choice
-// at 50.  One request: 10 us, two launches and the decision's chain of loads (chunks, draft tokens, their logits).
+// 64 requests of at most 4 drafts, 151552 tokens, fp32: 49 to 52 us (99 at first: expf and its special cases kept the
+// statistics at 56 us, and a racing block per chunk, each with the whole decision to take, the choice at 50).  With all four
+// drafts the statistics read 349 MB at 6.7 TB/s; the choice is bound by latency, 3.3 TB/s: each of its blocks takes the
+// decision (chunks, draft tokens and their logits, one load behind the other) before it knows which row to read.  One request:
+// 10 us, two launches and that chain.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -214,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_choose_kernel(const Verify
   __shared__ Stats s_row[2 * kVerifyMaxDrafts + 1];
   __shared__ float s_z[2 * kVerifyMaxDrafts + 1];  // the row's logit of its draft token
   __shared__ int s_x[kVerifyMaxDrafts];
-  __shared__ unsigned long long s_best[2][kThreads / 32];
+  __shared__ unsigned long long s_best[kThreads / 32];
   __shared__ int s_n, s_last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = static_cast<int>(blockIdx.x / p.racing), first_chunk = static_cast<int>(blockIdx.x % p.racing);
@@ -290,82 +292,79 @@ __global__ void __launch_bounds__(kThreads, 4) verify_choose_kernel(const Verify
   const int n = s_n;                              // accepted; row n gives the next token
   const Stats t = s_row[n];
   const bool rejected = n < n_draft;
-  Racer best, other;                              // of the weights, and of p alone in case they are all zero
+  const T* z_row = logits + static_cast<long long>(n) * V;
+  const T* q_row = drafts + static_cast<long long>(n) * V;
+  const float* noise = p.noise + static_cast<long long>(b) * V;
+  const float inv_p = __frcp_rn(t.sum);
+  const int race_chunks = (V - 1) / kRaceChunk + 1;
+  Racer best;
   if (!sc.greedy && t.max > -INFINITY) {
-    const float inv_p = __frcp_rn(t.sum);
-    const T* z_row = logits + static_cast<long long>(n) * V;
-    const T* q_row = drafts + static_cast<long long>(n) * V;
     const Stats d = rejected && has_q ? s_row[D + 1 + n] : Stats{-INFINITY, 0.0f, 0, 0};
     const bool some_q = d.max > -INFINITY;
     const float inv_q = some_q ? __frcp_rn(d.sum) : 0.0f;
     const int x = rejected && !has_q ? s_x[n] : -1;              // what a drafter without probabilities drew
-    const int race_chunks = (V - 1) / kRaceChunk + 1;
     for (int chunk = first_chunk; chunk < race_chunks; chunk += p.racing) {
       float z[kRacePer];
-      if (chunk != first_chunk) load_chunk<float, VEC>(p.noise + static_cast<long long>(b) * V, chunk * kRaceChunk, V, 1.0f, e);
+      if (chunk != first_chunk) load_chunk<float, VEC>(noise, chunk * kRaceChunk, V, 1.0f, e);
       load_chunk<T, VEC>(z_row, chunk * kRaceChunk, V, -INFINITY, z);
       if (some_q) {
         float q[kRacePer];
         load_chunk<T, VEC>(q_row, chunk * kRaceChunk, V, -INFINITY, q);
 #pragma unroll
         for (int j = 0; j < kRacePer; ++j) {
-          const int at = chunk * kRaceChunk + place<VEC>(j);
           const float pj = __fmul_rn(weight(usable(z[j]), t.max, sc.inv2), inv_p);
-          const float qj = __fmul_rn(weight(usable(q[j]), d.max, sc.inv2), inv_q), r = rcp_approx(e[j]);
-          best.take(__fsub_rn(pj, qj), r, at);
-          other.take(pj, r, at);
+          const float qj = __fmul_rn(weight(usable(q[j]), d.max, sc.inv2), inv_q);
+          best.take(__fsub_rn(pj, qj), rcp_approx(e[j]), chunk * kRaceChunk + place<VEC>(j));
         }
       } else {
 #pragma unroll
         for (int j = 0; j < kRacePer; ++j) {
           const int at = chunk * kRaceChunk + place<VEC>(j);
-          const float pj = __fmul_rn(weight(usable(z[j]), t.max, sc.inv2), inv_p), r = rcp_approx(e[j]);
-          if (at != x) best.take(pj, r, at);
-          if (x >= 0 && at == x) other.take(pj, r, at);
+          const float pj = __fmul_rn(weight(usable(z[j]), t.max, sc.inv2), inv_p);
+          if (at != x) best.take(pj, rcp_approx(e[j]), at);
         }
       }
     }
   }
-  unsigned long long first = warp_best(best.key()), second = rejected ? warp_best(other.key()) : 0ull;
-  if (lane == 0) {
-    s_best[0][warp] = first;
-    s_best[1][warp] = second;
-  }
-  __syncthreads();
-  ulonglong2* racers = static_cast<ulonglong2*>(p.racers) + static_cast<long long>(b) * p.racing;
-  if (threadIdx.x == 0) {
+  // the block's best in thread 0
+  auto block_best = [&](const Racer& r) {
+    unsigned long long v = warp_best(r.key());
+    if (lane == 0) s_best[warp] = v;
+    __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      first = max(first, s_best[0][w]);
-      second = max(second, s_best[1][w]);
-    }
+    for (int w = 0; w < kThreads / 32; ++w) v = max(v, s_best[w]);
+    return v;
+  };
+  unsigned long long first = block_best(best);
+  unsigned long long* racers = static_cast<unsigned long long*>(p.racers) + static_cast<long long>(b) * p.racing;
+  if (threadIdx.x == 0) {
     s_last = 1;
     if (!sc.greedy && p.racing > 1) {
-      racers[first_chunk] = make_ulonglong2(first, second);
+      racers[first_chunk] = first;
       __threadfence();
       s_last = atomicAdd(p.done + b, 1) == p.racing - 1;
       __threadfence();
     }
   }
   __syncthreads();
-  if (!s_last || warp != 0) return;
+  if (!s_last) return;
   int token = t.max > -INFINITY ? t.arg : -1;
   if (!sc.greedy) {
-    if (p.racing > 1) {
-      first = second = 0ull;
-      for (int c = lane; c < p.racing; c += 32) {
-        const ulonglong2 v = __ldcg(racers + c);
-        first = max(first, v.x);
-        second = max(second, v.y);
-      }
+    if (p.racing > 1) {                           // every warp for itself
+      first = 0ull;
+      for (int c = lane; c < p.racing; c += 32) first = max(first, __ldcg(racers + c));
       first = warp_best(first);
-      second = warp_best(second);
     }
-    first = __shfl_sync(kFull, first, 0);
-    second = __shfl_sync(kFull, second, 0);
-    if (first == 0ull) first = second;
+    if (first == 0ull && rejected && t.max > -INFINITY) {
+      // p - q is nowhere above 0 (they are equal, and the draft token was none of the vocabulary's): this block draws from p
+      Racer alone;
+      for (int c = threadIdx.x; c < V; c += kThreads)
+        alone.take(__fmul_rn(weight(usable(static_cast<float>(z_row[c])), t.max, sc.inv2), inv_p), rcp_approx(noise[c]), c);
+      first = block_best(alone);
+    }
     token = first == 0ull ? -1 : static_cast<int>(0xffffffffu - static_cast<unsigned>(first));
   }
+  if (warp != 0) return;
   if (lane == 0) p.n_accepted[b] = n;
   for (int i = lane; i <= D; i += 32) {
     int x = -1;
@@ -391,12 +390,11 @@ int verify_launch(VerifyCall c, bool f32, cudaStream_t st) {
   int sms = 0;
   const int rc = device_sm_count(&sms);
   if (rc) return rc;
-  // Every racing block decides for itself, so no more of them than two to a multiprocessor where a chunk each would be more
-  // (64 requests of 19 chunks: 1216 blocks of one chunk took 33 us).  The largest score is the same however the chunks are
-  // shared out.
-  c.racing = (4 * sms - 1) / c.B + 1;
-  const int race_chunks = verify_race_chunks(c.V);
-  if (c.racing > race_chunks) c.racing = race_chunks;
+  // Every racing block decides for itself, so no more of them than are resident, four to a multiprocessor (64 requests with
+  // 1216 blocks of one chunk took 33 us for this kernel, 27 with two blocks to a multiprocessor, 25 with four of half the
+  // chunk).  The largest score is the same however the chunks are shared out.
+  const int race_chunks = verify_race_chunks(c.V), resident = 4 * sms / c.B;
+  c.racing = resident < 1 ? 1 : resident < race_chunks ? resident : race_chunks;
   const dim3 g1(static_cast<unsigned>(static_cast<long long>(c.B) * c.rows * c.chunks)), g2(c.B * c.racing);
   {
     ProfScope prof("verify_stats", st);
