@@ -590,16 +590,14 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       if (t < p.T) {
         const bool groups = p.n_group > 1;
         uint32_t* keys = s_keys + t * (S::E + S::E / 32 + 1);
-        float l[EPL];
-        load_row(row, ld, p.E, lane, l);
         if (p.score == kDecodeTopk)
-          topk_choose(l, p.E, p.k, lane, e, v);
+          topk_choose<EPL>(row, ld, p.E, p.k, lane, e, v);
         else if (p.score == kDecodeSigmoid)
-          groups ? select_choose<EPL, false, true>(l, sp, keys, lane, e, stats)
-                 : select_choose<EPL, false, false>(l, sp, keys, lane, e, stats);
+          groups ? select_choose<EPL, false, true>(row, ld, sp, keys, lane, e, stats)
+                 : select_choose<EPL, false, false>(row, ld, sp, keys, lane, e, stats);
         else
-          groups ? select_choose<EPL, true, true>(l, sp, keys, lane, e, stats)
-                 : select_choose<EPL, true, false>(l, sp, keys, lane, e, stats);
+          groups ? select_choose<EPL, true, true>(row, ld, sp, keys, lane, e, stats)
+                 : select_choose<EPL, true, false>(row, ld, sp, keys, lane, e, stats);
         if (lane < p.k) atomicOr(&s_mask[e], 1u << t);
       }
       bar_named(2, kRouteThreads);

@@ -22,13 +22,6 @@ struct LoadL2 {
   __device__ __forceinline__ float operator()(const float* p) const { return __ldcg(p); }
 };
 
-// l[i] = logit of expert i * 32 + lane (past the last: that one's), every load on its way before the first is used.
-template <int EPL, typename LOAD>
-__device__ __forceinline__ void load_row(const float* row, LOAD ld, int E, int lane, float (&l)[EPL]) {
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) l[i] = ld(row + min(i * 32 + lane, E - 1));
-}
-
 // Total order key: larger = ranks earlier.  NaN -> 0 (below every number,
 // including -inf); -0.0 and +0.0 map to the same key (a tie).
 __device__ __forceinline__ uint32_t topk_key(float v) {
@@ -50,14 +43,14 @@ __device__ __forceinline__ float topk_key_value(uint32_t key) {
 // softmax is taken over the k selected logits in rank order, in fp32.  Lane j < k
 // returns the j-th ranked expert and its gate.  Every routing kernel calls
 // this one function, so they take the same decisions and compute the same gate bits.
-template <int EPL>
-__device__ __forceinline__ void topk_choose(const float (&l)[EPL], int E, int k, int lane, int& my_e, float& my_v) {
+template <int EPL, typename LOAD>
+__device__ __forceinline__ void topk_choose(const float* row, LOAD ld, int E, int k, int lane, int& my_e, float& my_v) {
   uint32_t key[EPL];
   uint32_t live = 0u;   // bit i: expert i*32 + lane exists and has not been taken yet
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = i * 32 + lane;
-    key[i] = (e < E) ? topk_key(l[i]) : 0u;
+    key[i] = (e < E) ? topk_key(ld(row + e)) : 0u;
     if (e < E) live |= 1u << i;
   }
   my_e = 0;
@@ -93,9 +86,8 @@ __device__ __forceinline__ float topk_gate(float my_v, int k, int lane) {
 
 template <int EPL, typename LOAD>
 __device__ __forceinline__ void topk_token(const float* row, LOAD ld, int E, int k, int lane, int& out_e, float& out_w) {
-  float l[EPL], v;
-  load_row(row, ld, E, lane, l);
-  topk_choose(l, E, k, lane, out_e, v);
+  float v;
+  topk_choose<EPL>(row, ld, E, k, lane, out_e, v);
   out_w = topk_gate(v, k, lane);
 }
 
@@ -174,12 +166,12 @@ struct SelectParams {
 
 // One warp's choice for one token: lane j < k returns the j-th ranked expert; st: the row's statistics (SOFTMAX).  GROUPS: sk is the warp's own
 // shared memory, E words and one per 32.
-template <int EPL, bool SOFTMAX, bool GROUPS>
-__device__ __forceinline__ void select_choose(const float (&row_l)[EPL], const SelectParams& p, uint32_t* sk, int lane,
+template <int EPL, bool SOFTMAX, bool GROUPS, typename LOAD>
+__device__ __forceinline__ void select_choose(const float* row, LOAD ld, const SelectParams& p, uint32_t* sk, int lane,
                                               int& my_e, SoftmaxStats& st) {
   float l[EPL];
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) l[i] = i * 32 + lane < p.E ? row_l[i] : -INFINITY;
+  for (int i = 0; i < EPL; ++i) l[i] = i * 32 + lane < p.E ? ld(row + i * 32 + lane) : -INFINITY;
   st = SoftmaxStats{0.0f, 1.0f};
   if (SOFTMAX) st = softmax_stats<EPL, false>(l, p.E, lane);
   uint32_t key[EPL];                          // 0: no such expert, or its group is not kept
@@ -335,10 +327,8 @@ __device__ __forceinline__ float select_weight(const float* row, LOAD ld, const 
 template <int EPL, bool SOFTMAX, bool GROUPS, typename LOAD>
 __device__ __forceinline__ void select_token(const float* row, LOAD ld, const SelectParams& p, uint32_t* sk, int lane,
                                              int& out_e, float& out_w) {
-  float l[EPL];
   SoftmaxStats st;
-  load_row(row, ld, p.E, lane, l);
-  select_choose<EPL, SOFTMAX, GROUPS>(l, p, sk, lane, out_e, st);
+  select_choose<EPL, SOFTMAX, GROUPS>(row, ld, p, sk, lane, out_e, st);
   out_w = select_weight<SOFTMAX>(row, ld, p, out_e, st, lane);
 }
 
