@@ -663,7 +663,7 @@ int sandwich_norm_backward(const void* dy, int dy_type, const void* dres, const 
                            float branch_scale, void* dx, void* dresidual, float* dw_post, float* dw_next, float* dgate,
                            void* workspace, size_t ws_bytes, void* stream);
 
-/* Workspace of verify_drafts; need not be zero. */
+/* Workspace of verify_drafts; any content, but calls that may run at the same time need workspaces of their own. */
 size_t verify_workspace_size(int B, int D, int V);
 
 /* Drafted tokens of B requests against the target's probabilities.  logits [B, D + 1, V]: a

@@ -73,6 +73,8 @@ class MoELayer:
     (xp, h, y, ys, plan) are then not written."""
 
     def __init__(self, weights: MoEWeights, fused: bool = False):
+        if fused and weights.E > binding.DECODE_MAX_EXPERTS:
+            raise ValueError(f"fused decode takes at most {binding.DECODE_MAX_EXPERTS} experts, got {weights.E}")
         self.w = weights
         self.fused = fused
         self._ws = None

@@ -23,8 +23,8 @@
 // of it: gate/up takes x as it is and keeps the columns of the tokens that chose the expert.
 //
 // Measured as a graph, weights changing from call to call (the chain of kernels in brackets): 256 experts of 6144 x 2048 and
-// a shared one, one token 109 us for 683 MB, 6.3 TB/s (147); 8 tokens 507 (571).  128 experts of 2048 x 768, one token 29 us
-// for 76 MB (45), 16 tokens 119 (162).  8 experts of 256 x 512, one token 15 (25).  Of the 109 us the first 14 are the
+// a shared one, one token 109 to 110 us for 683 MB, 6.2 TB/s (147); 8 tokens 508 (572).  128 experts of 2048 x 768, one token
+// 29 us for 76 MB (46), 16 tokens 119 (162).  8 experts of 256 x 512, one token 15 (25).  Of the 110 us the first 14 are the
 // router's chain (11) and the choice, behind which only the shared expert's 75 MB are read; from there to the last unit DRAM
 // runs at 6.7 TB/s.  The 29 us are mostly latencies: router 6, choice 2, first weights 2, gate/up's bytes 7, then h through
 // L2, the down product, y through L2 and the combine, 2 to 4 each.
@@ -376,6 +376,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         }
         if (!ok) break;
         u = static_cast<int>(gridDim.x) + atomicAdd(p.ctl, 1);
+        if (u < 0) u = 0x7fffffff;                              // a workspace that was not zero: no unit, not one before the first
       }
       if (!ok) *s_abort = 1;
       // every copy this thread issued lands before the block can exit (where the other half of a stage never came, the
