@@ -220,6 +220,8 @@ int verify_drafts(const void* logits, int logits_type, const void* draft_logits,
           "logits_type must be INVMOE_BF16 or INVMOE_F32");
   REQUIRE(B >= 0 && D >= 0 && V > 0, INVMOE_ERR_INVALID_ARG, "need B, D >= 0 and V > 0");
   REQUIRE(D <= kVerifyMaxDrafts, INVMOE_ERR_UNSUPPORTED_SHAPE, "D=%d > %d", D, kVerifyMaxDrafts);
+  // columns are counted in 32 bits, up to a chunk past the last
+  REQUIRE(V <= 1 << 30, INVMOE_ERR_UNSUPPORTED_SHAPE, "V=%d > 2^30", V);
   REQUIRE(temperature != nullptr || tau >= 0.0f, INVMOE_ERR_INVALID_ARG, "need a temperature >= 0");
   const int chunks = verify_chunks(V), rows = D + 1 + (draft_logits != nullptr ? D : 0);
   REQUIRE(static_cast<long long>(B) * rows <= 0x7fffffffLL / chunks && B <= 0x3fffffff / verify_race_chunks(V),

@@ -104,3 +104,10 @@ def test_binding_refuses_host_tensors():
         binding.sandwich_norm(x[0], w, x, w)
     with pytest.raises(ValueError, match="3 dimensions"):
         binding.verify_drafts(torch.zeros(2, 8), torch.zeros(2, 8), torch.zeros(256, dtype=torch.uint8))
+
+
+def test_verify_drafts_rejects_columns_past_its_index(lib):
+    """A chunk past the last column of a row has to have an index too."""
+    f = lib.verify_drafts
+    for V in (2 ** 30 + 1, 2 ** 31 - 4, 2 ** 31 - 1):
+        assert f(P, 1, N, N, N, P, N, N, 1.0, 1, 0, V, P, P, P, P, 2 ** 62, N) == -2 and b"2^30" in lib.invmoe_last_error()
