@@ -616,7 +616,7 @@ size_t moe_decode_workspace_size(int T, int H, int E, int k, int F, int F_shared
  * renormalize 1), INVMOE_SCORE_SIGMOID and _SOFTMAX as moe_route_select.  out [T, H] fp32 and
  * out_bf16 [T, H]: at least one; logits [T, E], topk_idx [T, k], topk_w [T, k]: each
  * nullable.  Weights as for moe_layer_forward.  x is read until the end: no output may
- * overlap it.  The kernel's blocks wait for one another, so it is launched cooperatively and
+ * overlap it or another one.  The kernel's blocks wait for one another, so it is launched cooperatively and
  * starts when all of them fit on the device; calls that may run at the same time need
  * workspaces of their own.
  * Shapes: T <= 16, E <= 512, k <= 32, H % 64 == 0, H <= 32768, F % 64 == 0, F_shared % 64 == 0. */
@@ -680,7 +680,8 @@ size_t verify_workspace_size(int B, int D, int V);
  * tau: temperature [B] fp32, or the scalar tau where that is NULL.  0 (and, of a request's
  * own, anything not positive): drafts are accepted while they are the target row's largest
  * logit (lowest index of equal ones), which is also the next token; accept_u and noise are not
- * used.  n_draft [B] int32 (nullable: D): drafts of a request, the rest of its rows is not read.
+ * used.  Infinite: every logit but -inf has the same probability.  n_draft [B] int32
+ * (nullable: D): drafts of a request, the rest of its rows is not read.
  * A NaN logit counts as -inf, +inf as the largest finite number; a target row of -inf alone
  * accepts nothing and gives token -1.
  * Outputs: tokens [B, D + 1] int32 = the n accepted drafts, the drawn token, then -1;

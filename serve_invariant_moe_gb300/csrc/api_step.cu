@@ -177,8 +177,15 @@ int moe_layer_decode(const void* x, const void* w_router, const void* w13, const
   }
   // columns of x are read until the last block is done with its gate/up units, long after others have written outputs
   const size_t xn = matrix_bytes(T, H, INVMOE_BF16);
-  REQUIRE(apart(x, xn, out, 2 * xn) && apart(x, xn, out_bf16, xn) && apart(out, 2 * xn, out_bf16, xn),
-          INVMOE_ERR_INVALID_ARG, "an output overlaps x or the other one");
+  // (and the logits while other blocks already combine)
+  const size_t pairs = static_cast<size_t>(T) * k * 4;
+  const struct { const void* at; size_t bytes; } arrays[] = {{x, xn}, {out, 2 * xn}, {out_bf16, xn},
+                                                             {logits, static_cast<size_t>(T) * E * 4}, {topk_idx, pairs},
+                                                             {topk_w, pairs}};
+  for (size_t i = 1; i < sizeof(arrays) / sizeof(arrays[0]); ++i)
+    for (size_t j = 0; j < i; ++j)
+      REQUIRE(apart(arrays[i].at, arrays[i].bytes, arrays[j].at, arrays[j].bytes), INVMOE_ERR_INVALID_ARG,
+              "an output overlaps x or another one");
   const DecodeScratch s = decode_scratch(T, H, E, k, F, F_shared);
   uint8_t* base = scratch(workspace);
   DecodeParams p{};

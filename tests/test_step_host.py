@@ -111,3 +111,15 @@ def test_verify_drafts_rejects_columns_past_its_index(lib):
     f = lib.verify_drafts
     for V in (2 ** 30 + 1, 2 ** 31 - 4, 2 ** 31 - 1):
         assert f(P, 1, N, N, N, P, N, N, 1.0, 1, 0, V, P, P, P, P, 2 ** 62, N) == -2 and b"2^30" in lib.invmoe_last_error()
+
+
+def test_moe_layer_decode_rejects_outputs_that_overlap(lib):
+    f, n = lib.moe_layer_decode, lib.moe_decode_workspace_size(4, 256, 8, 2, 128, 0)
+    at = [(1 << 20) + (i << 16) for i in range(6)]                   # x, out, out_bf16, logits, topk_idx, topk_w
+    size = [4 * 256 * 2, 4 * 256 * 4, 4 * 256 * 2, 4 * 8 * 4, 4 * 2 * 4, 4 * 2 * 4]
+    for i in range(6):
+        for j in range(i):
+            p = [ctypes.c_void_p(a) for a in at]
+            p[i] = ctypes.c_void_p(at[j] + size[j] - 16)             # its first bytes are the other's last
+            assert f(p[0], P, P, P, N, N, 4, 256, 8, 2, 128, 0, 2, N, 1, 1, 1, 1.0, *p[1:], ctypes.c_void_p(1 << 24), n, N) == -1
+            assert b"overlaps" in lib.invmoe_last_error(), (i, j)
