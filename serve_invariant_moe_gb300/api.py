@@ -65,6 +65,18 @@ def _head(t, n):
     return None if t is None else t[:n]
 
 
+def _check_all(spaces):
+    """check_status of every workspace, so that each time-out is reported once."""
+    failed = None
+    for ws in spaces:
+        try:
+            binding.check_status(ws)
+        except RuntimeError as e:
+            failed = e
+    if failed is not None:
+        raise failed
+
+
 class MoELayer:
     """Batch-invariant MoE layer forward on one GPU.
 
@@ -79,11 +91,13 @@ class MoELayer:
         self.fused = fused
         self._ws = None
         self._decode = None
+        self._unread = []               # status blocks of replaced workspaces, which check() reads
 
     def _workspace(self, T):
         w = self.w
         need = binding.workspace_size(T, w.H, w.E, w.k, w.F, w.F_shared, 0)
         if self._ws is None or self._ws.numel() < need:
+            self._replace(self._ws)
             self._ws = binding.new_workspace(need, device=w.w13.device)
         return self._ws
 
@@ -137,15 +151,19 @@ class MoELayer:
                                         out_bf16=out_bf16, logits=d["logits"][:B], topk_idx=d["idx"][:B],
                                         topk_w=d["w"][:B], **chosen)["out"]
 
+    def _replace(self, ws):
+        """A workspace that gives way to a larger one: its status, behind the calls so far on this stream."""
+        if ws is not None:
+            self._unread.append(ws[:256].clone())
+
     def check(self):
-        """Raise if a kernel of a decode call since the last check gave up waiting: what it should have written is then not
-        there.  Waits for the device."""
-        d = self._decode
-        if d is not None:
-            torch.cuda.synchronize(d["device"])
-            for name in ("ws", "fused_ws"):
-                if name in d:
-                    binding.check_status(d[name])
+        """Raise if a kernel of a prefill or decode call since the last check gave up waiting: what it should have written is
+        then not there.  Waits for the device.  (Replays of captured steps: DecodeGraphs.check.)"""
+        torch.cuda.synchronize(self.w.w13.device)
+        d = self._decode or {}
+        spaces = [*self._unread, *(ws for ws in (self._ws, d.get("ws"), d.get("fused_ws")) if ws is not None)]
+        self._unread = []
+        _check_all(spaces)
 
     def prefill(self, x: torch.Tensor, out_bf16: Optional[torch.Tensor] = None, return_all=False,
                 replay_idx: Optional[torch.Tensor] = None):
@@ -204,6 +222,8 @@ class MoELayer:
         w = self.w
         B, dev = max_batch, w.w13.device
         S = B * w.k
+        for name in ("ws", "fused_ws"):
+            self._replace((self._decode or {}).get(name))
         self._decode = dict(
             B=B,
             logits=torch.empty((B, w.E), dtype=torch.float32, device=dev),
@@ -324,7 +344,8 @@ class DecodeGraphs:
         dev = w.w13.device
         layer.alloc_decode(self.buckets[-1])
         # captured kernels hold addresses: a larger batch gives the layer new buffers, these stay the graphs'
-        self._held = [layer._decode, *vars(w).values(), w.routing and w.routing.bias]
+        self._bufs = layer._decode
+        self._held = [*vars(w).values(), w.routing and w.routing.bias]
         self.inp = {B: torch.zeros((B, w.H), dtype=torch.bfloat16, device=dev) for B in self.buckets}
         self.out = {}
         self.graphs = {}
@@ -349,6 +370,11 @@ class DecodeGraphs:
             self.inp[B][b:].zero_()
         self.graphs[B].replay()
         return self.out[B][:b]
+
+    def check(self):
+        """As MoELayer.check, for the replays."""
+        torch.cuda.synchronize(self.layer.w.w13.device)
+        _check_all([self._bufs[name] for name in ("ws", "fused_ws") if name in self._bufs])
 
 
 def moe_prefill(layer: MoELayer, x: torch.Tensor) -> torch.Tensor:

@@ -1,5 +1,7 @@
 """CPU-side checks of a drafted decode step's entry points: host-side validation, sizes, refusal of host tensors."""
+import contextlib
 import ctypes
+import types
 
 import pytest
 import torch
@@ -123,3 +125,90 @@ def test_moe_layer_decode_rejects_outputs_that_overlap(lib):
             p[i] = ctypes.c_void_p(at[j] + size[j] - 16)             # its first bytes are the other's last
             assert f(p[0], P, P, P, N, N, 4, 256, 8, 2, 128, 0, 2, N, 1, 1, 1, 1.0, *p[1:], ctypes.c_void_p(1 << 24), n, N) == -1
             assert b"overlaps" in lib.invmoe_last_error(), (i, j)
+
+
+class FakeLayerBinding:
+    """The binding's functions that MoELayer's decode calls; the workspace of `fail` is one whose kernel gave up a wait."""
+    DECODE_MAX_TOKENS, DECODE_MAX_EXPERTS = 16, 512
+
+    def plan_len(self, T, E, k):
+        return 2 * E + 1 + 2 * T * k
+
+    def workspace_size(self, T, *more):
+        return 256 + 64 * T
+
+    moe_decode_workspace_size = workspace_size
+
+    def new_workspace(self, nbytes, device):
+        return torch.zeros(nbytes, dtype=torch.uint8)
+
+    def check_status(self, workspace):
+        if workspace[0]:
+            workspace[0] = 0
+            raise RuntimeError("timeout")
+
+    def lib(self):
+        return types.SimpleNamespace(moe_layer_forward=lambda *args: 0)
+
+    def check(self, rc):
+        assert rc == 0
+
+    def moe_layer_decode(self, x, w_router, w13, w2, k, workspace, *more, out=None, **rest):
+        return dict(out=out)
+
+    def moe_layer_forward(self, x, w_router, w13, w2, k, ws, **rest):
+        return dict(out=None)
+
+
+@pytest.fixture
+def layer(monkeypatch):
+    from serve_invariant_moe_gb300 import api
+    monkeypatch.setattr(api, "binding", FakeLayerBinding())
+    stream = types.SimpleNamespace(wait_stream=lambda other: None, cuda_stream=0)
+    monkeypatch.setattr(torch.cuda, "Stream", lambda **kw: stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: stream)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "graph", lambda g: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "CUDAGraph", lambda: types.SimpleNamespace(replay=lambda: None))
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda *a: None)
+    bf16 = lambda *s: torch.empty(*s, dtype=torch.bfloat16)   # noqa: E731
+    return api.MoELayer(api.MoEWeights(bf16(4, 64), bf16(4, 256, 64), bf16(4, 64, 128), 2), fused=True)
+
+
+def rows(T):
+    return torch.empty(T, 64, dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("name", ["ws", "fused_ws"])
+def test_check_covers_replaced_decode_buffers(layer, name):
+    layer.check()
+    layer.decode(rows(2))
+    layer._decode[name][0] = 1
+    layer.decode(rows(9))                           # larger buffers
+    with pytest.raises(RuntimeError, match="timeout"):
+        layer.check()
+    layer.check()
+
+
+def test_check_covers_prefill(layer):
+    for replaced in (False, True):
+        layer.prefill(rows(8), return_all=True)
+        layer._ws[0] = 1
+        if replaced:
+            layer.prefill(rows(2000))
+        with pytest.raises(RuntimeError, match="timeout"):
+            layer.check()
+        layer.check()
+
+
+@pytest.mark.parametrize("name", ["ws", "fused_ws"])
+def test_check_covers_decode_graphs(layer, name):
+    from serve_invariant_moe_gb300 import api
+    graphs = api.DecodeGraphs(layer, buckets=(1, 4))
+    layer.decode(rows(9))
+    graphs.check()
+    graphs._bufs[name][0] = 1                       # what a replayed kernel does
+    layer.check()
+    with pytest.raises(RuntimeError, match="timeout"):
+        graphs.check()
+    graphs.check()
