@@ -46,7 +46,8 @@ struct Scale {
 __device__ __forceinline__ Scale scale_of(const VerifyCall& p, int b) {
   const float tau = p.temperature != nullptr ? __ldg(p.temperature + b) : p.tau;
   const bool greedy = !(tau > 0.0f);
-  const float inv = greedy ? 1.0f : fminf(__frcp_rn(tau), FLT_MAX);
+  // (not 0 for an infinite temperature either: -inf times it has to stay -inf)
+  const float inv = greedy ? 1.0f : fminf(fmaxf(__frcp_rn(tau), FLT_MIN), FLT_MAX);
   return {greedy, inv, fminf(__fmul_rn(inv, 1.4426950408889634f), FLT_MAX)};
 }
 

@@ -158,6 +158,20 @@ def test_ragged_drafts_and_temperatures(V):
     assert got["n_accepted"][4] == min(2, int(a["n_draft"][4]))
 
 
+@pytest.mark.parametrize("own", [False, True])
+@pytest.mark.parametrize("D", [0, 2])
+def test_an_infinite_temperature(D, own):
+    """Every logit but -inf has the same probability, also where a chunk has none and behind the end of a row."""
+    a = make(3, D, 20012, tau=torch.full((3,), math.inf) if own else math.inf)
+    a["logits"][:, :, 100:17000] = -math.inf
+    if D:
+        a["draft_logits"][1:, :, 5:15000] = -math.inf
+        a["draft_tokens"][0, 0] = 7
+    got = call(a)
+    check(got, a)
+    assert np.allclose(got["logp"][got["tokens"] >= 0], -math.log(20012 - 16900), rtol=0, atol=REL + 8 * 2.0 ** -22)
+
+
 def test_scalar_temperatures():
     for tau in (0.0, 0.5, 3.0):
         a = make(4, 3, 300, tau=tau)
