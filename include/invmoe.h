@@ -640,7 +640,7 @@ int sandwich_norm(const void* x, int x_type, const void* w_post, const void* res
                   int gate_kind, const void* w_next, int T, int H, float residual_scale, float branch_scale, float eps,
                   void* residual_out, void* out, void* q, float* scale, float* rstd_post, float* rstd, void* stream);
 
-/* Workspace of sandwich_norm_backward. */
+/* Workspace of sandwich_norm_backward; its status word (invmoe_check) tells of a wait that ran out. */
 size_t sandwich_norm_backward_workspace_size(int T, int H);
 
 /* Backward of sandwich_norm at its input x, its stored row r' (residual here) and its two

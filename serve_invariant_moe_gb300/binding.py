@@ -829,7 +829,7 @@ def sandwich_norm_backward(dy, dres, x, w_post, rstd_post, residual, w_next=None
     dy [T, H] bf16 or fp32: the gradient of ``out`` (None without w_next); dres [T, H] in the residual's type: the gradient
     that reaches the stored row from the residual stream (None: none).  dx has x's type, dresidual the residual's; the
     weights' gradients are fp32 [H] (skipped with dweights=False), dgate [H] or [T] fp32 as the gate.  ``workspace``:
-    sandwich_norm_backward_workspace_size bytes (allocated if not given)."""
+    sandwich_norm_backward_workspace_size bytes, whose status check_status reads (allocated and dropped if not given)."""
     r = marshal().sandwich_backward(dy, dres, x, w_post, rstd_post, residual, w_next, rstd, gate, residual_scale, branch_scale,
                                     dx, dresidual, dweights, workspace)
     return r if r.__class__ is dict else check(r)

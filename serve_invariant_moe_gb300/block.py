@@ -237,6 +237,7 @@ class MoEBlock:
         """fused: decode of at most 16 rows runs the layer in one kernel (MoELayer)."""
         self.w = weights
         self.layer = MoELayer(weights.layer, fused=fused)
+        self._norm_ws = None            # backward's, of the norms
 
     def _after(self, m, residual, gate, residual_out=None):
         w = self.w
@@ -265,12 +266,17 @@ class MoEBlock:
 
         Returns the gradients dn (of n, fp32), dresidual, dw_post, dw_next, dgate and the layer's (``layer``)."""
         w = self.w
+        need = binding.sandwich_norm_backward_workspace_size(*fwd["residual"].shape)
+        if self._norm_ws is None or self._norm_ws.numel() < need:
+            self._norm_ws = binding.new_workspace(need, fwd["residual"].device)
         s = binding.sandwich_norm_backward(dnext, dres, fwd["layer"]["out"], w.w_post, fwd["rstd_post"], fwd["residual"],
                                            w.w_next if dnext is not None else None, fwd["rstd"] if dnext is not None else None,
-                                           fwd["gate"], w.residual_scale, w.branch_scale, dweights=weight_grads)
+                                           fwd["gate"], w.residual_scale, w.branch_scale, dweights=weight_grads,
+                                           workspace=self._norm_ws)
         g = self.layer.backward(fwd["n"], fwd["layer"], s["dx"], weight_grads)
+        binding.check_status(self._norm_ws)
         return dict(dn=g["dx"], dresidual=s["dresidual"], dw_post=s["dw_post"], dw_next=s["dw_next"], dgate=s["dgate"], layer=g)
 
     def check(self):
-        """MoELayer.check, for decode."""
+        """MoELayer.check."""
         self.layer.check()

@@ -166,7 +166,7 @@ struct BwdParams {
 // bulk copies into a ring of shared memory, as many rows ahead as fit, in two groups with a barrier each: dy and r', which the
 // first sum needs, and dres and x.  A group's place is free again once the block's sum after its last use is through, so the
 // block's two barriers per row are also what the next copies wait for.
-// 8192 x 6144, fp32 x, the rest bf16, a channel's gate: 137 us with the sums' kernel for 805 MB, 5.9 TB/s; 4096 x 2048, all
+// 8192 x 6144, fp32 x, the rest bf16, a channel's gate: 139 us with the sums' kernel for 805 MB, 5.8 TB/s; 4096 x 2048, all
 // fp32: 38.5 us, 5.2 TB/s, of which the start (14 rows a block) and the second kernel are what a copy does not have.  Two
 // vectors a thread from 2064 columns on, so that a row is few warps and its sums few additions: 768 threads of one vector took
 // 183 us, and 157 with the warps' sums read one by one and a division per mean.  At 8192 columns two rows fill the ring
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) sandwich_bwd_kernel(const Bwd
         }
       }
       mean = row_sum<THREADS>(dot, s_part[0][i & 1], warp, lane) * inv_h;
-      if (threadIdx.x == 0 && i + sh.depth < n) load(i + sh.depth, at_place, 0);
+      if (threadIdx.x == 0 && ok && i + sh.depth < n) load(i + sh.depth, at_place, 0);
     }
     ok = ok && mbar_wait(&bars[1][at_place], phase, wc);
     float u[V][8], n_x[V][8];                  // u: d w_p, times the channel's gate
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) sandwich_bwd_kernel(const Bwd
     }
     dot = row_sum<THREADS>(dot, s_part[1][i & 1], warp, lane);
     if (threadIdx.x == 0) {
-      if (i + sh.depth < n) load(i + sh.depth, at_place, 1);
+      if (ok && i + sh.depth < n) load(i + sh.depth, at_place, 1);
       if (p.dgate_token != nullptr) p.dgate_token[t] = p.branch_scale * dot;
     }
     const float k = p.gate.channel != nullptr ? rstd_p : rstd_p * __fmul_rn(g, p.branch_scale);   // what u still lacks
@@ -374,6 +374,13 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) sandwich_bwd_kernel(const Bwd
         store8(row + p.H + c, s[v]);
       }
     }
+  }
+  if (s_abort && threadIdx.x == 0) {
+    // given up: what is still on its way lands before the block exits.  Of a barrier's two parities one has passed; for the
+    // other, which waits in vain where nothing was on its way, its share of the limit.
+    const WaitCtl drain{nullptr, p.status, p.timeout_ns / (2 * kBwdMaxDepth)};
+#pragma unroll 1
+    for (int i = 0; i < 4 * sh.depth; ++i) mbar_wait_slow(&bars[i & 1][i >> 2], (i >> 1) & 1u, drain);
   }
 }
 

@@ -347,3 +347,69 @@ def test_a_captured_pair_replays_with_other_inputs():
         side.synchronize()
         for x, y in zip(outs, want):
             assert torch.equal(x, y)
+
+
+def test_forward_offsets_past_2_31():
+    """The last rows of a matrix of more than 2^31 elements have the bits that they have alone."""
+    from serve_invariant_moe_gb300 import binding
+    T, H, n = 131_200, 16400, 5
+    assert (T - n) * H > 2 ** 31
+    small = inputs(n, H, BF, BF, "token")
+    whole = {name: torch.zeros(T, *t.shape[1:], dtype=t.dtype, device=DEV) if t.shape[0] == n else t for name, t in small.items()}
+    for name, t in small.items():
+        if t.shape[0] == n:
+            whole[name][-n:] = t
+    got, want = (binding.sandwich_norm(**a, residual_scale=0.875, branch_scale=0.25, fp8=True) for a in (whole, small))
+    for name, t in want.items():
+        t, end = (v.view(torch.uint8) if v.dtype == torch.float8_e4m3fn else v for v in (t, got[name][-n:]))
+        assert torch.equal(end, t), name
+    assert (got["residual"][:-n] == 0).all()
+
+
+@pytest.mark.parametrize("T,H", [(262_400, 8192), (131_200, 16400)])
+def test_backward_offsets_past_2_31(T, H):
+    """Rows without a gradient, but for the last: their gradients are those that they have alone, and so are the weights', up to
+    the order of the sum (at most 5 terms and zeros: 5 * 2^-24 of their absolute values, on both sides)."""
+    from serve_invariant_moe_gb300 import binding
+    n = 5
+    assert (T - n) * H > 2 ** 31
+    a = inputs(n, H, BF, BF, "token")
+    dy, dres = gradients(n, H, BF, BF)
+    rstd_post, r, rstd = saved(a)
+
+    def tall(t):
+        whole = torch.zeros(T, *t.shape[1:], dtype=t.dtype, device=DEV)
+        whole[-n:] = t
+        return whole
+    names = dict(dweights=True)
+    want = binding.sandwich_norm_backward(dy, dres, a["x"], a["w_post"], rstd_post, r, a["w_next"], rstd, a["gate"], **names)
+    got = binding.sandwich_norm_backward(tall(dy), tall(dres), tall(a["x"]), a["w_post"], tall(rstd_post), tall(r), a["w_next"],
+                                         tall(rstd), tall(a["gate"]), **names)
+    for name in ("dx", "dresidual", "dgate"):
+        assert torch.equal(got[name][-n:], want[name]), name
+        assert (got[name][:-n] == 0).all(), name
+    for name, size in (("dw_post", 64.0), ("dw_next", 64.0)):
+        # no term is above `size`: |dy|, |d| below 6 times |n| below 6, times a gate below 1, 5 rows
+        assert ((got[name] - want[name]).abs() <= 10 * 2.0 ** -24 * 5 * size).all(), name
+
+
+def test_backwards_on_two_streams():
+    """Each with a workspace that torch allocates on its stream."""
+    from serve_invariant_moe_gb300 import binding
+    cases = []
+    for seed in range(4):
+        a = inputs(300, 2064, F32, BF, "channel", seed)
+        dy, dres = gradients(300, 2064, BF, F32)
+        rstd_post, r, rstd = saved(a)
+        args = (dy, dres, a["x"], a["w_post"], rstd_post, r, a["w_next"], rstd, a["gate"])
+        cases.append((args, binding.sandwich_norm_backward(*args)))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(40):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append(binding.sandwich_norm_backward(*cases[i % 4][0]))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        for name, t in cases[i % 4][1].items():
+            assert torch.equal(g[name], t), (i, name)

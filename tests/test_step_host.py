@@ -212,3 +212,27 @@ def test_check_covers_decode_graphs(layer, name):
     with pytest.raises(RuntimeError, match="timeout"):
         graphs.check()
     graphs.check()
+
+
+def test_the_blocks_backward_checks_its_norms(monkeypatch):
+    from serve_invariant_moe_gb300 import block
+
+    class Fake(FakeLayerBinding):
+        def sandwich_norm_backward_workspace_size(self, T, H):
+            return 256 + T * H
+
+        def sandwich_norm_backward(self, *args, workspace, **rest):
+            workspace[0] = self.fail
+            return dict(dx=None, dresidual=None, dw_post=None, dw_next=None, dgate=None)
+    fake = Fake()
+    monkeypatch.setattr(block, "binding", fake)
+    w = torch.ones(64, dtype=torch.bfloat16)
+    b = object.__new__(block.MoEBlock)
+    b.w, b._norm_ws = block.MoEBlockWeights(None, w, w), None
+    b.layer = types.SimpleNamespace(backward=lambda *args: dict(dx=None))
+    fwd = dict(layer=dict(out=None), rstd_post=None, residual=rows(3), rstd=None, gate=None, n=None)
+    fake.fail = 0
+    b.backward(fwd, rows(3))
+    fake.fail = 1
+    with pytest.raises(RuntimeError, match="timeout"):
+        b.backward(fwd, rows(3))
