@@ -10,11 +10,11 @@
 // finish joining them.  Bound by reading the logits once and, for the row that is drawn from, once more, with the noise.
 // The chunks and the order in which they are joined follow from V alone, and the largest score is the same however the race
 // is shared out, so a request's bits do not depend on the batch.
-// 64 requests of at most 4 drafts, 151552 tokens, fp32: 49 to 52 us (99 at first: expf and its special cases kept the
+// 64 requests of at most 4 drafts, 151552 tokens, fp32: 48 us (99 at first: expf and its special cases kept the
 // statistics at 56 us, and a racing block per chunk, each with the whole decision to take, the choice at 50).  With all four
 // drafts the statistics read 349 MB at 6.7 TB/s; the choice is bound by latency, 3.3 TB/s: each of its blocks takes the
 // decision (chunks, draft tokens and their logits, one load behind the other) before it knows which row to read.  One request:
-// 10 us, two launches and that chain.
+// 9 us, two launches and that chain.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -212,8 +212,6 @@ __device__ __forceinline__ unsigned long long warp_best(unsigned long long v) {
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads, 4) verify_choose_kernel(const VerifyCall p) {
-  pdl_wait();
-  pdl_trigger();
   __shared__ Stats s_row[2 * kVerifyMaxDrafts + 1];
   __shared__ float s_z[2 * kVerifyMaxDrafts + 1];  // the row's logit of its draft token
   __shared__ int s_x[kVerifyMaxDrafts];
@@ -224,14 +222,18 @@ __global__ void __launch_bounds__(kThreads, 4) verify_choose_kernel(const Verify
   const int D = p.D, V = p.V;
   const int n_draft = drafts_of(p, b);
   const Scale sc = scale_of(p, b);
+  // what needs no decision is on its way first: the noise, and behind the statistics' kernel every row's chunks, the draft
+  // tokens and their logits.  (Inputs may be read before that kernel ends: this one begins when all of its blocks are past
+  // their wait for what came before.  64 requests 50.6 -> 47.9 us, one 9.5 -> 9.0.)
+  float e[kRacePer];
+  if (!sc.greedy) load_chunk<float, VEC>(p.noise + static_cast<long long>(b) * V, first_chunk * kRaceChunk, V, 1.0f, e);
+  pdl_wait();
+  pdl_trigger();
   if (sc.greedy && first_chunk != 0) return;            // nothing to draw: one block reads the maxima
   const Stats* part = static_cast<const Stats*>(p.stats) + static_cast<long long>(b) * p.rows * p.chunks;
   const T* logits = static_cast<const T*>(p.logits) + static_cast<long long>(b) * (D + 1) * V;
   const T* drafts = static_cast<const T*>(p.draft_logits) + static_cast<long long>(b) * D * V;
   const bool has_q = p.draft_logits != nullptr;
-  // what needs no decision is on its way first: the noise, every row's chunks, the draft tokens and their logits
-  float e[kRacePer];
-  if (!sc.greedy) load_chunk<float, VEC>(p.noise + static_cast<long long>(b) * V, first_chunk * kRaceChunk, V, 1.0f, e);
   for (int r0 = warp; r0 < p.rows; r0 += 2 * (kThreads / 32)) {
     Stats first[2];
     int x[2];
