@@ -151,6 +151,49 @@ def test_odd_sizes_against_64_bits(T, E, H, F, Fs, k):
     assert torch.equal(got["out_bf16"], got["out"].to(BF))
 
 
+@pytest.mark.parametrize("T,E,H,F,Fs,k", [(2, 6, 32768, 64, 64, 2), (3, 4, 128, 9216, 64, 2)])
+def test_the_widest_rows(T, E, H, F, Fs, k):
+    w, x = weights(E, H, F, Fs), tokens(T, H)
+    got = decode(x, w, k)
+    out, bound = reference(x, w, got["topk_idx"], got["topk_w"])
+    assert ((got["out"].double() - out).abs() <= bound + 1e-30).all()
+
+
+@pytest.mark.parametrize("score,n_group,topk_group", [(None, 1, 1), ("sigmoid", 32, 9), ("softmax", 4, 4)])
+def test_the_most_pairs(score, n_group, topk_group):
+    """16 tokens with 32 of 512 experts each."""
+    from serve_invariant_moe_gb300 import api
+    w, x = weights(512, 256, 128, 128), tokens(16, 256)
+    if score is None:
+        return same(decode(x, w, 32, out_bf16=True), separate(x, w, 32))
+    bias = 0.1 * torch.randn(512, generator=torch.Generator().manual_seed(3)).to(DEV)
+    got = decode(x, w, 32, out_bf16=True, score=score, bias=bias, n_group=n_group, topk_group=topk_group)
+    same(got, separate(x, w, 32, api.Routing(score, bias, n_group, topk_group, True, 1.0)))
+
+
+def test_graphs_that_share_a_workspace():
+    """Of different layers and sizes, replayed in turn on one stream, with eager calls in between."""
+    from serve_invariant_moe_gb300 import binding
+    a, b = weights(128, 512, 256, 128), weights(8, 256, 512)
+    ws = space(16, a, 8)
+    calls = [(a, 8, tokens(16, 512)), (b, 2, tokens(3, 256)), (a, 8, tokens(1, 512, 4))]
+    want = [decode(x, w, k)["out"] for w, k, x in calls]
+
+    def run(w, k, x):
+        return binding.moe_layer_decode(x, w["w_router"], w["w13"], w["w2"], k, ws, w.get("ws13"), w.get("ws2"))["out"]
+    graphs, outs = [], []
+    for c in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(run(*c))
+    for i in (0, 1, 2, 1, 0, 0, 2):
+        outs[i].fill_(7.0)
+        graphs[i].replay()
+        assert torch.equal(run(*calls[(i + 1) % 3]), want[(i + 1) % 3])
+        assert torch.equal(outs[i], want[i])
+    binding.check_status(ws)
+
+
 def test_tokens_that_choose_alike_and_not():
     """All tokens the same (every expert has 16 rows), and all of different experts."""
     w, x = weights(32, 256, 128, 128), tokens(16, 256)
