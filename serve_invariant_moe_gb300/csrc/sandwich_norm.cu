@@ -166,11 +166,11 @@ struct BwdParams {
 // bulk copies into a ring of shared memory, as many rows ahead as fit, in two groups with a barrier each: dy and r', which the
 // first sum needs, and dres and x.  A group's place is free again once the block's sum after its last use is through, so the
 // block's two barriers per row are also what the next copies wait for.
-// 8192 x 6144, fp32 x, the rest bf16, a channel's gate: 139 us with the sums' kernel for 805 MB, 5.8 TB/s; 4096 x 2048, all
+// 8192 x 6144, fp32 x, the rest bf16, a channel's gate: 136 us with the sums' kernel for 805 MB, 5.9 TB/s; 4096 x 2048, all
 // fp32: 38.5 us, 5.2 TB/s, of which the start (14 rows a block) and the second kernel are what a copy does not have.  Two
 // vectors a thread from 2064 columns on, so that a row is few warps and its sums few additions: 768 threads of one vector took
 // 183 us, and 157 with the warps' sums read one by one and a division per mean.  At 8192 columns two rows fill the ring
-// and 128 registers are not quite enough: 4.4 TB/s.
+// and 128 registers are not quite enough: 4.5 TB/s.
 constexpr int kBwdMaxDepth = 8, kBwdMaxWidth = 8192;
 constexpr int kBwdBlocks = 2;                  // on a multiprocessor, of rows up to 2048
 
@@ -513,15 +513,16 @@ __global__ void __launch_bounds__(256) sandwich_bwd_cols_kernel(const BwdParams 
 }
 
 // The partial rows' sums: blockIdx.y 0 is dw_n, 1 is S with what is made of it.  16 columns per block, 4 per thread: thread
-// row y adds rows y, y + 256, ... ascending, the 8 thread rows of a warp fold by a xor butterfly, the 32 warps ascending.
-constexpr int kSumCols = 16, kSumThreads = 1024;
+// row y adds rows y, y + 64, ... ascending, the 8 thread rows of a warp fold by a xor butterfly, the 8 warps ascending.
+// (Blocks of 1024 threads, which come one after the other where a row has many columns: 8192 columns 124 us instead of 120.)
+constexpr int kSumCols = 16, kSumThreads = 256;
 __global__ void __launch_bounds__(kSumThreads)
     sandwich_sum_kernel(const float* __restrict__ part, int P, int H, const Gate gate,
                         const __nv_bfloat16* __restrict__ w_post, float branch_scale, float* __restrict__ dw_next,
                         float* __restrict__ dw_post, float* __restrict__ dgate) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float s[32][kSumCols];
+  __shared__ float s[kSumThreads / 32][kSumCols];
   const int which = blockIdx.y;
   const int c = blockIdx.x * kSumCols + 4 * (threadIdx.x & 3);      // H is a multiple of 16
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -544,7 +545,7 @@ __global__ void __launch_bounds__(kSumThreads)
   if (threadIdx.x < kSumCols) {
     float sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 32; ++w) sum += s[w][threadIdx.x];
+    for (int w = 0; w < kSumThreads / 32; ++w) sum += s[w][threadIdx.x];
     const int h = blockIdx.x * kSumCols + threadIdx.x;
     if (which == 0) {
       if (dw_next != nullptr) dw_next[h] = sum;
