@@ -65,6 +65,10 @@ def _head(t, n):
     return None if t is None else t[:n]
 
 
+def _capturing():
+    return torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing()
+
+
 def _check_all(spaces):
     """check_status of every workspace, so that each time-out is reported once."""
     failed = None
@@ -82,7 +86,10 @@ class MoELayer:
 
     fused: decode (and prefill without its intermediates) of at most 16 tokens runs the layer in one kernel
     (binding.moe_layer_decode, at most 512 experts), with the same bits; the decode buffers of its intermediates
-    (xp, h, y, ys, plan) are then not written."""
+    (xp, h, y, ys, plan) are then not written.
+
+    Captured kernels hold addresses: the buffers that a captured call uses live as long as the layer, also when a larger batch
+    gives it others, so a caller's own graph needs the layer (and its weights) kept.  DecodeGraphs keeps its buffers itself."""
 
     def __init__(self, weights: MoEWeights, fused: bool = False):
         if fused and weights.E > binding.DECODE_MAX_EXPERTS:
@@ -92,10 +99,14 @@ class MoELayer:
         self._ws = None
         self._decode = None
         self._unread = []               # status blocks of replaced workspaces, which check() reads
+        self._captured = []             # buffers that a caller's graphs use
 
     def _workspace(self, T):
         w = self.w
         need = binding.workspace_size(T, w.H, w.E, w.k, w.F, w.F_shared, 0)
+        if _capturing():
+            self._captured.append(dict(ws=binding.new_workspace(need, w.w13.device)))
+            return self._captured[-1]["ws"]
         if self._ws is None or self._ws.numel() < need:
             self._replace(self._ws)
             self._ws = binding.new_workspace(need, device=w.w13.device)
@@ -158,10 +169,12 @@ class MoELayer:
 
     def check(self):
         """Raise if a kernel of a prefill or decode call since the last check gave up waiting: what it should have written is
-        then not there.  Waits for the device.  (Replays of captured steps: DecodeGraphs.check.)"""
+        then not there; also of a replay since, of a graph that a caller captured.  Waits for the device.  (DecodeGraphs has a
+        check of its own.)"""
         torch.cuda.synchronize(self.w.w13.device)
-        d = self._decode or {}
-        spaces = [*self._unread, *(ws for ws in (self._ws, d.get("ws"), d.get("fused_ws")) if ws is not None)]
+        spaces = [*self._unread, *([] if self._ws is None else [self._ws])]
+        for d in [self._decode or {}, *self._captured]:
+            spaces += [d[name] for name in ("ws", "fused_ws") if name in d]
         self._unread = []
         _check_all(spaces)
 
@@ -175,9 +188,7 @@ class MoELayer:
         the host's allocations, not the kernels, set the call's latency."""
         T = x.shape[0]
         if not return_all and replay_idx is None and 0 < T <= 1024:
-            if self._decode is None or self._decode["B"] < T:
-                self.alloc_decode(max(T, 1))
-            d = self._decode
+            d = self._decode_buffers(T)
             if self.fused and T <= binding.DECODE_MAX_TOKENS:
                 return self._run_fused(x, d, None, out_bf16)
             bufs = {k: d[k] for k in ("logits", "idx", "w", "plan", "xp", "h", "y", "ys")}
@@ -219,12 +230,31 @@ class MoELayer:
 
     def alloc_decode(self, max_batch: int):
         """Preallocate decode buffers for up to ``max_batch`` concurrent requests."""
-        w = self.w
-        B, dev = max_batch, w.w13.device
-        S = B * w.k
+        if _capturing():
+            raise RuntimeError("alloc_decode cannot be captured: its workspaces are cleared once, not by every replay")
         for name in ("ws", "fused_ws"):
             self._replace((self._decode or {}).get(name))
-        self._decode = dict(
+        self._decode = self._buffers(max_batch)
+
+    def _decode_buffers(self, B):
+        """decode's buffers, of at least B rows.  A captured call keeps those it finds, or is given some of its own: what is
+        cleared inside a capture is not clear outside."""
+        d, capturing = self._decode, _capturing()
+        if d is None or d["B"] < B:
+            if capturing:
+                d = self._buffers(max(B, 1))
+            else:
+                self.alloc_decode(max(B, 1))
+                d = self._decode
+        if capturing and not any(c is d for c in self._captured):
+            self._captured.append(d)
+        return d
+
+    def _buffers(self, B):
+        w = self.w
+        dev = w.w13.device
+        S = B * w.k
+        d = dict(
             B=B,
             logits=torch.empty((B, w.E), dtype=torch.float32, device=dev),
             idx=torch.empty((B, w.k), dtype=torch.int32, device=dev),
@@ -237,7 +267,6 @@ class MoELayer:
             out=torch.empty((B, w.H), dtype=torch.float32, device=dev),
             ws=binding.new_workspace(binding.workspace_size(B, w.H, w.E, w.k, w.F, w.F_shared, 0), dev),
         )
-        d = self._decode
         if self.fused:
             few = min(B, binding.DECODE_MAX_TOKENS)
             d["fused_ws"] = binding.new_workspace(
@@ -249,6 +278,7 @@ class MoELayer:
                      p(d["logits"]), p(d["idx"]), p(d["w"]), p(d["plan"]), p(d["xp"]), p(d["h"]), p(d["y"]),
                      p(d["ys"]), p(d["out"]), None, p(d["ws"]), d["ws"].numel(), None]
         d["fn"] = binding.lib().moe_layer_forward
+        return d
 
     def decode(self, x_tokens: torch.Tensor, out_bf16: Optional[torch.Tensor] = None) -> torch.Tensor:
         """One token per request: x_tokens [B, H] bf16 -> [B, H] fp32 (a view of the decode buffer);
@@ -257,11 +287,10 @@ class MoELayer:
         One library call (moe_layer_forward) on buffers allocated once: the argument list is built in
         alloc_decode (every buffer's batch-B view starts at the same address), so a call checks the
         token tensor, sets its pointer, the batch size and the stream, and enters the library."""
-        B = x_tokens.shape[0]
-        if self._decode is None or self._decode["B"] < B:
-            self.alloc_decode(max(B, 1))
-        d = self._decode
-        w = self.w
+        return self._decode_in(self._decode_buffers(x_tokens.shape[0]), x_tokens, out_bf16)
+
+    def _decode_in(self, d, x_tokens, out_bf16=None):
+        B, w = x_tokens.shape[0], self.w
         if (x_tokens.dtype != torch.bfloat16 or x_tokens.device != d["device"] or not x_tokens.is_contiguous()
                 or x_tokens.dim() != 2 or x_tokens.shape[1] != w.H):
             raise ValueError(f"x_tokens must be a contiguous [B, {w.H}] bf16 tensor on {d['device']}")
@@ -358,7 +387,7 @@ class DecodeGraphs:
         for B in self.buckets:
             g = torch.cuda.CUDAGraph()
             with torch.cuda.graph(g):
-                self.out[B] = layer.decode(self.inp[B])
+                self.out[B] = layer._decode_in(self._bufs, self.inp[B])
             self.graphs[B] = g
 
     def __call__(self, x_tokens: torch.Tensor) -> torch.Tensor:

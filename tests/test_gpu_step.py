@@ -230,3 +230,50 @@ def test_a_training_step_forward_and_backward_of_two_blocks():
     want = (loss(x + h * v) - loss(x - h * v)) / (2 * h)
     have = float((dx.double() * v.double()).sum())
     assert np.isfinite(have) and abs(have - want) <= 0.05 * float(dx.double().norm() * v.double().norm()), (have, want)
+
+
+@pytest.mark.parametrize("fused", [True, False])
+def test_a_captured_block_outlives_a_larger_batch(fused):
+    """A block's decode captured by its caller, then eager steps of larger batches: the graph's buffers stay its own, whatever
+    is allocated afterwards, and it gives the bits of the eager step."""
+    (block, _), _ = stack(2, 256, fused=fused)
+    g = torch.Generator().manual_seed(21)
+    x = torch.randn(40, 256, generator=g).to(BF).to(DEV)
+    n, r = x[:2].clone(), x[2:4].clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        want = [t.clone() for t in block.decode(n, r)]
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = block.decode(n, r)
+    sizes = [t.numel() * t.element_size() for t in block.layer._decode.values() if isinstance(t, torch.Tensor)]
+    for B in (16, 40):
+        block.decode(x[:B], x[:B])
+    torch.cuda.synchronize()
+    others = [torch.full((s,), 0x5a, dtype=torch.uint8, device=DEV) for s in sizes for _ in range(2)]
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    assert all(bool((t == 0x5a).all()) for t in others)
+    block.check()
+
+
+def test_a_step_captured_before_any_eager_one():
+    """Buffers made inside the capture are the graph's: the eager steps behind it have others, whose workspaces are clear."""
+    (block, _), _ = stack(2, 256)
+    g = torch.Generator().manual_seed(22)
+    n, r = (torch.randn(3, 256, generator=g).to(BF).to(DEV) for _ in range(2))
+    other, _ = stack(2, 256)
+    want = other[0].decode(n, r)                    # (also sets the kernels' attributes)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = block.decode(n, r)
+    for _ in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(block.decode(n, r), want))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    block.check()

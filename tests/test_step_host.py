@@ -1,7 +1,9 @@
 """CPU-side checks of a drafted decode step's entry points: host-side validation, sizes, refusal of host tensors."""
 import contextlib
 import ctypes
+import gc
 import types
+import weakref
 
 import pytest
 import torch
@@ -236,3 +238,64 @@ def test_the_blocks_backward_checks_its_norms(monkeypatch):
     fake.fail = 1
     with pytest.raises(RuntimeError, match="timeout"):
         b.backward(fwd, rows(3))
+
+
+@pytest.fixture
+def capture(monkeypatch):
+    """capture(True): the calls from here on are captured."""
+    now = [False]
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: now[0])
+    return lambda on: now.__setitem__(0, on)
+
+
+def memory(buffers):
+    return {name: weakref.ref(t) for name, t in buffers.items() if isinstance(t, torch.Tensor)}
+
+
+@pytest.mark.parametrize("fused", [True, False])
+def test_a_caller_s_graph_keeps_the_buffers_of_its_step(layer, capture, fused):
+    """A larger batch gives the layer new buffers; the kernels that a caller captured still write the old ones."""
+    layer.fused = fused
+    layer.decode(rows(2))
+    capture(True)
+    layer.decode(rows(2))
+    capture(False)
+    used = memory(layer._decode)
+    assert {"logits", "plan", "xp", "h", "y", "out", "ws"} <= set(used)
+    layer.decode(rows(9))
+    gc.collect()
+    assert [name for name, r in used.items() if r() is None] == []
+    unused = memory(layer._decode)
+    layer.decode(rows(30))
+    gc.collect()
+    assert all(r() is None for r in unused.values())        # (nobody captured these)
+    used["ws"]()[0] = 1                                     # what a replayed kernel does
+    with pytest.raises(RuntimeError, match="timeout"):
+        layer.check()
+    layer.check()
+
+
+def test_a_captured_first_step_has_buffers_of_its_own(layer, capture):
+    """Inside a capture nothing is cleared before the first replay: an eager step must not find those workspaces."""
+    capture(True)
+    layer.decode(rows(2))
+    assert layer._decode is None
+    with pytest.raises(RuntimeError, match="captured"):
+        layer.alloc_decode(4)
+    capture(False)
+    layer.decode(rows(2))
+    kept = memory(layer._captured[0])
+    assert layer._decode["ws"] is not kept["ws"]() and kept["ws"]() is not None
+    kept["ws"]()[0] = 1
+    with pytest.raises(RuntimeError, match="timeout"):
+        layer.check()
+
+
+def test_a_captured_prefill_has_a_workspace_of_its_own(layer, capture):
+    layer.prefill(rows(8), return_all=True)
+    eager = layer._ws
+    capture(True)
+    layer.prefill(rows(8), return_all=True)
+    capture(False)
+    assert layer._ws is eager and layer._captured[0]["ws"] is not eager
