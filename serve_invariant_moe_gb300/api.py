@@ -10,6 +10,7 @@ else was in its batch ("位级一致：前沿训练的差异化关键", section 
 the serving engine and the trainer must produce the same numbers whatever the
 batch size or concurrent load).
 """
+import threading
 from dataclasses import dataclass
 from typing import Optional
 
@@ -69,6 +70,12 @@ def _capturing():
     return torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing()
 
 
+def _caller():
+    """The calling thread and its current stream: calls with the same ones run one after the other."""
+    stream = torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if torch.cuda.is_initialized() else 0
+    return threading.get_ident(), stream
+
+
 def _check_all(spaces):
     """check_status of every workspace, so that each time-out is reported once."""
     failed = None
@@ -88,6 +95,9 @@ class MoELayer:
     (binding.moe_layer_decode, at most 512 experts), with the same bits; the decode buffers of its intermediates
     (xp, h, y, ys, plan) are then not written.
 
+    prefill and backward may run on several threads and streams at once: each has workspaces of its own there.  The calls of
+    decode share one set of buffers, so they belong on one stream.
+
     Captured kernels hold addresses: the buffers that a captured call uses live as long as the layer, also when a larger batch
     gives it others, so a caller's own graph needs the layer (and its weights) kept.  DecodeGraphs keeps its buffers itself."""
 
@@ -96,10 +106,15 @@ class MoELayer:
             raise ValueError(f"fused decode takes at most {binding.DECODE_MAX_EXPERTS} experts, got {weights.E}")
         self.w = weights
         self.fused = fused
-        self._ws = None
+        self._spaces, self._small, self._back = {}, {}, {}      # prefill's and backward's, by thread and stream
         self._decode = None
         self._unread = []               # status blocks of replaced workspaces, which check() reads
         self._captured = []             # buffers that a caller's graphs use
+
+    @property
+    def _ws(self):
+        """prefill's workspace of this thread on the current stream."""
+        return self._spaces.get(_caller())
 
     def _workspace(self, T):
         w = self.w
@@ -107,10 +122,16 @@ class MoELayer:
         if _capturing():
             self._captured.append(dict(ws=binding.new_workspace(need, w.w13.device)))
             return self._captured[-1]["ws"]
-        if self._ws is None or self._ws.numel() < need:
-            self._replace(self._ws)
-            self._ws = binding.new_workspace(need, device=w.w13.device)
-        return self._ws
+        return self._kept(self._spaces, need)
+
+    def _kept(self, spaces, need):
+        """The caller's workspace in `spaces`, of at least `need` bytes."""
+        key = _caller()
+        ws = spaces.get(key)
+        if ws is None or ws.numel() < need:
+            self._replace(ws)
+            ws = spaces[key] = binding.new_workspace(need, device=self.w.w13.device)
+        return ws
 
     def _run(self, x, ws, bufs=None, out_bf16=None, replay_idx=None):
         w = self.w
@@ -172,8 +193,8 @@ class MoELayer:
         then not there; also of a replay since, of a graph that a caller captured.  Waits for the device.  (DecodeGraphs has a
         check of its own.)"""
         torch.cuda.synchronize(self.w.w13.device)
-        spaces = [*self._unread, *([] if self._ws is None else [self._ws])]
-        for d in [self._decode or {}, *self._captured]:
+        spaces = [*self._unread, *self._spaces.values()]
+        for d in [self._decode or {}, *self._small.values(), *self._captured]:
             spaces += [d[name] for name in ("ws", "fused_ws") if name in d]
         self._unread = []
         _check_all(spaces)
@@ -183,12 +204,12 @@ class MoELayer:
         """x [T, H] bf16 -> out [T, H] fp32 (optionally also a bf16 copy).  With replay_idx [T, k]
         int32 the recorded expert choices are used instead of the router's own top-k.
 
-        A small batch (at most 1024 tokens) whose intermediates are not returned runs on the
-        layer's preallocated decode buffers (only `out` is allocated per call): for such batches
-        the host's allocations, not the kernels, set the call's latency."""
+        A small batch (at most 1024 tokens) whose intermediates are not returned runs on
+        buffers kept for its thread and stream (only `out` is allocated per call): for such
+        batches the host's allocations, not the kernels, set the call's latency."""
         T = x.shape[0]
         if not return_all and replay_idx is None and 0 < T <= 1024:
-            d = self._decode_buffers(T)
+            d = self._small_buffers(T)
             if self.fused and T <= binding.DECODE_MAX_TOKENS:
                 return self._run_fused(x, d, None, out_bf16)
             bufs = {k: d[k] for k in ("logits", "idx", "w", "plan", "xp", "h", "y", "ys")}
@@ -204,10 +225,7 @@ class MoELayer:
         no atomics)."""
         w = self.w
         T = x.shape[0]
-        need = binding.backward_workspace_size(T, w.H, w.E, w.k, w.F, w.F_shared)
-        if getattr(self, "_bws", None) is None or self._bws.numel() < need:
-            self._bws = binding.new_workspace(need, device=x.device)
-        ws = self._bws
+        ws = self._kept(self._back, binding.backward_workspace_size(T, w.H, w.E, w.k, w.F, w.F_shared))
         c = binding.moe_combine_backward(dout, fwd["y"], fwd["topk_w"], fwd["plan"], w.E, w.k,
                                          dout_bf16=w.ws13 is not None)
         f = binding.moe_grouped_ffn_backward(fwd["xp"], fwd["plan"], w.w13, w.w2, c["dy"], T, w.k, ws,
@@ -248,6 +266,19 @@ class MoELayer:
                 d = self._decode
         if capturing and not any(c is d for c in self._captured):
             self._captured.append(d)
+        return d
+
+    def _small_buffers(self, T):
+        """prefill's buffers of at least T rows: the caller's; a captured call's are its graph's."""
+        if _capturing():
+            self._captured.append(self._buffers(T))
+            return self._captured[-1]
+        key = _caller()
+        d = self._small.get(key)
+        if d is None or d["B"] < T:
+            for name in ("ws", "fused_ws"):
+                self._replace((d or {}).get(name))
+            d = self._small[key] = self._buffers(T)
         return d
 
     def _buffers(self, B):

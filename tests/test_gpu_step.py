@@ -1,5 +1,7 @@
 """A drafted decode step's operators together: norms around a block, the layer of a few tokens in one kernel, the head, the
 verification; the block's prefill, decode, backward and a whole step as a graph."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -277,3 +279,38 @@ def test_a_step_captured_before_any_eager_one():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want))
     block.check()
+
+
+def alone_and_in_two_threads(call, inputs):
+    """call(*inputs[i]) has the bits of the same call alone when two threads, each on a stream of its own, repeat it."""
+    want = [call(*i) for i in inputs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def run(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(30):
+                got = call(*inputs[i])
+                stream.synchronize()
+                bad.extend((i, j) for j, (a, b) in enumerate(zip(got, want[i])) if not torch.equal(a, b))
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+@pytest.mark.parametrize("T", [8, 100])
+def test_two_threads_through_one_layer(T):
+    from serve_invariant_moe_gb300 import api
+    layer = api.MoELayer(layer_weights(32, 256, 128, 128, 4), fused=True)
+    g = torch.Generator().manual_seed(T)
+
+    def call(x, dout):
+        b = layer.backward(x, layer.prefill(x, return_all=True), dout)
+        return [layer.prefill(x), *(b[name] for name in ("dx", "dw_router", "dw13", "dw2", "dws13", "dws2"))]
+    alone_and_in_two_threads(call, [(torch.randn(T, 256, generator=g).to(BF).to(DEV), torch.randn(T, 256, generator=g).to(DEV))
+                                    for _ in range(2)])
+    layer.check()

@@ -1,7 +1,9 @@
 """CPU-side checks of a drafted decode step's entry points: host-side validation, sizes, refusal of host tensors."""
+import collections
 import contextlib
 import ctypes
 import gc
+import threading
 import types
 import weakref
 
@@ -245,6 +247,8 @@ def capture(monkeypatch):
     """capture(True): the calls from here on are captured."""
     now = [False]
     monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0, raising=False)
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: now[0])
     return lambda on: now.__setitem__(0, on)
 
@@ -299,3 +303,52 @@ def test_a_captured_prefill_has_a_workspace_of_its_own(layer, capture):
     layer.prefill(rows(8), return_all=True)
     capture(False)
     assert layer._ws is eager and layer._captured[0]["ws"] is not eager
+
+
+class Recorder(FakeLayerBinding):
+    """Remembers the workspace and the logits' buffer of every call."""
+
+    def __init__(self):
+        self.seen = []
+
+    def moe_layer_decode(self, x, w_router, w13, w2, k, workspace, *more, logits, **rest):
+        self.seen.append((workspace, logits.untyped_storage().data_ptr()))
+        return dict(out=None)
+
+    def moe_layer_forward(self, x, w_router, w13, w2, k, ws, logits=None, **rest):
+        self.seen.append((ws, None if logits is None else logits.untyped_storage().data_ptr()))
+        return dict(out=None)
+
+    def check_status(self, workspace):
+        self.seen.append((workspace, None))
+
+    backward_workspace_size = FakeLayerBinding.workspace_size
+
+    def gradients(self, *args, **kw):
+        return collections.defaultdict(lambda: None)
+
+    moe_combine_backward = moe_grouped_ffn_backward = moe_route_backward = gradients
+
+
+CALLS = {"fused": lambda layer: layer.prefill(rows(8)), "small": lambda layer: layer.prefill(rows(100)),
+         "all": lambda layer: layer.prefill(rows(8), return_all=True), "large": lambda layer: layer.prefill(rows(2000)),
+         "backward": lambda layer: layer.backward(rows(8), collections.defaultdict(lambda: None), None)}
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_prefills_and_backwards_of_two_callers_share_nothing(layer, capture, monkeypatch, call):
+    """Two threads or streams whose calls overlap: neither the workspace nor the logits that every block chooses from."""
+    from serve_invariant_moe_gb300 import api
+    rec, stream = Recorder(), [0]
+    monkeypatch.setattr(api, "binding", rec)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: stream[0], raising=False)
+    for stream[0] in (5, 6, 5):
+        CALLS[call](layer)
+    t = threading.Thread(target=CALLS[call], args=(layer,))
+    t.start()
+    t.join()
+    layer.decode(rows(8))
+    (a, la), (b, lb), (again, lagain), (c, lc), (d, ld) = (*rec.seen, (None, None))[:5]
+    assert again is a and lagain == la
+    assert len({id(s) for s in (a, b, c, d)}) == 4
+    assert la is None or len({la, lb, lc, ld}) == 4
