@@ -231,13 +231,15 @@ class MoEBlock:
         n'  = rms_norm(r') w_next                                          bf16, the next block's n
 
     The norms, gate and scales are one call (binding.sandwich_norm).  The first block's n is add_rms_norm's of the embedded
-    row.  Every step is per token with one reduction order, so prefill and decode give the same bits."""
+    row.  Every step is per token with one reduction order, so prefill and decode give the same bits.
+
+    prefill and backward may run on several threads and streams at once.  A graph that a caller captures needs the block and
+    its weights kept, as MoELayer's."""
 
     def __init__(self, weights: MoEBlockWeights, fused: bool = True):
         """fused: decode of at most 16 rows runs the layer in one kernel (MoELayer)."""
         self.w = weights
         self.layer = MoELayer(weights.layer, fused=fused)
-        self._norm_ws = None            # backward's, of the norms
 
     def _after(self, m, residual, gate, residual_out=None):
         w = self.w
@@ -266,15 +268,16 @@ class MoEBlock:
 
         Returns the gradients dn (of n, fp32), dresidual, dw_post, dw_next, dgate and the layer's (``layer``)."""
         w = self.w
-        need = binding.sandwich_norm_backward_workspace_size(*fwd["residual"].shape)
-        if self._norm_ws is None or self._norm_ws.numel() < need:
-            self._norm_ws = binding.new_workspace(need, fwd["residual"].device)
+        # a call's own: between its two kernels nobody else's partial sums may get there
+        ws = torch.empty(binding.sandwich_norm_backward_workspace_size(*fwd["residual"].shape), dtype=torch.uint8,
+                         device=fwd["residual"].device)
+        ws[:256].zero_()
         s = binding.sandwich_norm_backward(dnext, dres, fwd["layer"]["out"], w.w_post, fwd["rstd_post"], fwd["residual"],
                                            w.w_next if dnext is not None else None, fwd["rstd"] if dnext is not None else None,
                                            fwd["gate"], w.residual_scale, w.branch_scale, dweights=weight_grads,
-                                           workspace=self._norm_ws)
-        g = self.layer.backward(fwd["n"], fwd["layer"], s["dx"], weight_grads)
-        binding.check_status(self._norm_ws)
+                                           workspace=ws)
+        g = self.layer.backward(fwd["n"], fwd["layer"], s["dx"], weight_grads)     # (waits for the GPU)
+        binding.check_status(ws)
         return dict(dn=g["dx"], dresidual=s["dresidual"], dw_post=s["dw_post"], dw_next=s["dw_next"], dgate=s["dgate"], layer=g)
 
     def check(self):

@@ -314,3 +314,16 @@ def test_two_threads_through_one_layer(T):
     alone_and_in_two_threads(call, [(torch.randn(T, 256, generator=g).to(BF).to(DEV), torch.randn(T, 256, generator=g).to(DEV))
                                     for _ in range(2)])
     layer.check()
+
+
+@pytest.mark.parametrize("T", [8, 100])
+def test_two_threads_through_one_block(T):
+    (block, _), _ = stack(2, 256)
+    g = torch.Generator().manual_seed(T)
+    r = lambda: torch.randn(T, 256, generator=g).to(BF).to(DEV)   # noqa: E731
+
+    def call(n, res, dn, dres):
+        b = block.backward(block.prefill(n, res, return_all=True), dn, dres)
+        return [*block.prefill(n, res), *(b[name] for name in ("dn", "dresidual", "dw_post", "dw_next", "dgate"))]
+    alone_and_in_two_threads(call, [(r(), r(), r(), r()) for _ in range(2)])
+    block.check()

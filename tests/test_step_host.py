@@ -352,3 +352,30 @@ def test_prefills_and_backwards_of_two_callers_share_nothing(layer, capture, mon
     assert again is a and lagain == la
     assert len({id(s) for s in (a, b, c, d)}) == 4
     assert la is None or len({la, lb, lc, ld}) == 4
+
+
+def test_two_backwards_of_a_block_share_no_partial_sums(monkeypatch):
+    """Two threads: the second call's row kernel may run before the first one's sum kernel."""
+    from serve_invariant_moe_gb300 import block
+    spaces = []
+
+    class Fake(FakeLayerBinding):
+        def sandwich_norm_backward_workspace_size(self, T, H):
+            return 256 + T * H
+
+        def sandwich_norm_backward(self, *args, workspace, **rest):
+            assert workspace.numel() >= 256 + 3 * 64 and not workspace[:256].any()
+            spaces.append(workspace)
+            if len(spaces) == 1:                    # the other thread's call, before this one is done
+                t = threading.Thread(target=b.backward, args=(fwd, rows(3)))
+                t.start()
+                t.join()
+            return dict(dx=None, dresidual=None, dw_post=None, dw_next=None, dgate=None)
+    monkeypatch.setattr(block, "binding", Fake())
+    w = torch.ones(64, dtype=torch.bfloat16)
+    b = object.__new__(block.MoEBlock)
+    b.w, b._norm_ws = block.MoEBlockWeights(None, w, w), None
+    b.layer = types.SimpleNamespace(backward=lambda *args: dict(dx=None))
+    fwd = dict(layer=dict(out=None), rstd_post=None, residual=rows(3), rstd=None, gate=None, n=None)
+    b.backward(fwd, rows(3))
+    assert len(spaces) == 2 and spaces[0].data_ptr() != spaces[1].data_ptr()
