@@ -104,7 +104,8 @@ size_t invmoe_plan_len(int T, int E, int k);
  * caller zero-fills the workspace once before first use. */
 size_t invmoe_workspace_size(int T, int H, int E, int k, int F, int F_shared, int V);
 
-/* Synchronise `stream`, read and clear the status word in `workspace`.
+/* Synchronise `stream`, read and clear the status word in `workspace`; where it tells of
+ * an error, the kernels' counters in the first 256 bytes are cleared with it.
  * Returns INVMOE_OK, INVMOE_ERR_DEVICE_TIMEOUT (a kernel gave up waiting) or
  * INVMOE_ERR_INVALID_ARG (moe_route_replay was given an invalid expert index). */
 int invmoe_check(void* workspace, void* stream);

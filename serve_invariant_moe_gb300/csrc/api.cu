@@ -305,7 +305,8 @@ int invmoe_check(void* workspace, void* stream) {
   if (rc) return rc;
   if ((rc = check_cuda(cudaStreamSynchronize(st), "cudaStreamSynchronize"))) return rc;
   if (v != 0) {
-    if ((rc = check_cuda(cudaMemsetAsync(workspace, 0, sizeof(v), st), "cudaMemsetAsync"))) return rc;
+    // the kernels' counters behind the status too: a call that was given up must not be the last one they count right
+    if ((rc = check_cuda(cudaMemsetAsync(workspace, 0, kStatusBytes, st), "cudaMemsetAsync"))) return rc;
     if ((rc = check_cuda(cudaStreamSynchronize(st), "cudaStreamSynchronize"))) return rc;
     if (v & kStatusTimeout)
       return set_error(INVMOE_ERR_DEVICE_TIMEOUT, "a kernel's bounded wait ran out (status 0x%x)", v);

@@ -313,3 +313,17 @@ def test_refusals():
         f(out=False, out_bf16=x)
     with pytest.raises(ValueError, match="w2"):
         f(w2=w["w2"].float())
+
+
+def test_an_error_that_was_reported_leaves_a_clear_workspace():
+    """Counters that calls on one workspace at once, or a call given up, have left behind go with the status."""
+    from serve_invariant_moe_gb300 import binding
+    w, x = weights(8, 256, 128), tokens(4, 256)
+    want = decode(x, w, 2, out_bf16=True)
+    ws = space(4, w, 2)
+    ws[:256] = 3
+    ws[:4] = torch.tensor([1, 0, 0, 0], dtype=torch.uint8, device=DEV)
+    with pytest.raises(RuntimeError):
+        binding.check_status(ws)
+    assert not ws[:256].any()
+    same(decode(x, w, 2, ws, out_bf16=True), want)
