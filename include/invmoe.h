@@ -641,7 +641,8 @@ int sandwich_norm(const void* x, int x_type, const void* w_post, const void* res
                   int gate_kind, const void* w_next, int T, int H, float residual_scale, float branch_scale, float eps,
                   void* residual_out, void* out, void* q, float* scale, float* rstd_post, float* rstd, void* stream);
 
-/* Workspace of sandwich_norm_backward; its status word (invmoe_check) tells of a wait that ran out. */
+/* Workspace of sandwich_norm_backward; its status word (invmoe_check) tells of a wait that ran out.  Whatever depends on rows
+ * that did not come is then NaN. */
 size_t sandwich_norm_backward_workspace_size(int T, int H);
 
 /* Backward of sandwich_norm at its input x, its stored row r' (residual here) and its two
@@ -782,6 +783,14 @@ int invmoe_expert_engine(int which);
  * invmoe_check() must then report it.  Exercises the timeout path without
  * hanging or faulting the GPU. */
 int invmoe_debug_timeout_probe(void* workspace, size_t ws_bytes, int timeout_us, void* stream);
+
+/* sandwich_norm_backward without a gate, all fp32, H <= 2048, whose blocks never load one
+ * group of their second row (0: dy and the stored row, 1: dres and x) and wait for it for
+ * `timeout_us` microseconds: what a call that gives up leaves behind. */
+int invmoe_debug_stalled_backward(const float* dy, const float* dres, const float* x, const void* w_post,
+                                  const float* rstd_post, const float* residual, const void* w_next, const float* rstd,
+                                  int T, int H, int group, int timeout_us, float* dx, float* dresidual, float* dw_post,
+                                  float* dw_next, void* workspace, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -69,6 +69,7 @@ PROTOTYPES = {
     "verify_drafts": (_i, [_vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _f, _i, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp]),
     "invmoe_gemm_bf16": (_i, [_vp, _vp, _i, _i, _i, _vp, _i, _vp, _sz, _vp]),
     "invmoe_debug_timeout_probe": (_i, [_vp, _sz, _i, _vp]),
+    "invmoe_debug_stalled_backward": (_i, [_vp] * 8 + [_i, _i, _i, _i] + [_vp] * 5 + [_sz, _vp]),
     "invmoe_profile_enable": (_i, [_i]),
     "invmoe_pdl_enable": (_i, [_i]),
     "invmoe_expert_engine": (_i, [_i]),

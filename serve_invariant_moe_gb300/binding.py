@@ -829,7 +829,8 @@ def sandwich_norm_backward(dy, dres, x, w_post, rstd_post, residual, w_next=None
     dy [T, H] bf16 or fp32: the gradient of ``out`` (None without w_next); dres [T, H] in the residual's type: the gradient
     that reaches the stored row from the residual stream (None: none).  dx has x's type, dresidual the residual's; the
     weights' gradients are fp32 [H] (skipped with dweights=False), dgate [H] or [T] fp32 as the gate.  ``workspace``:
-    sandwich_norm_backward_workspace_size bytes, whose status check_status reads (allocated and dropped if not given)."""
+    sandwich_norm_backward_workspace_size bytes, whose status check_status reads (allocated and dropped if not given).  Where a
+    kernel gives up waiting, what depends on the rows it waited for is NaN."""
     r = marshal().sandwich_backward(dy, dres, x, w_post, rstd_post, residual, w_next, rstd, gate, residual_scale, branch_scale,
                                     dx, dresidual, dweights, workspace)
     return r if r.__class__ is dict else check(r)
@@ -876,3 +877,18 @@ def gemm_bf16(a, b, workspace, variant=0, out=None):
 
 def debug_timeout_probe(workspace, timeout_us=20000):
     check(lib().invmoe_debug_timeout_probe(_p(workspace), workspace.numel(), int(timeout_us), _stream()))
+
+
+def debug_stalled_backward(dy, dres, x, w_post, rstd_post, residual, w_next, rstd, group, workspace, timeout_us=20000):
+    """sandwich_norm_backward (all fp32, no gate, H <= 2048) whose blocks wait in vain for a group of their second row."""
+    T, H = x.shape
+    for t in (dy, dres, x, residual):
+        if t is not None:
+            _req(t, torch.float32, "rows", (T, H))
+    dx, dresidual = torch.empty_like(x), torch.empty_like(x)
+    dw_post = torch.empty(H, dtype=torch.float32, device=x.device)
+    dw_next = None if dy is None else torch.empty_like(dw_post)
+    check(lib().invmoe_debug_stalled_backward(_p(dy), _p(dres), _p(x), _p(w_post), _p(rstd_post), _p(residual), _p(w_next),
+                                              _p(rstd), T, H, int(group), int(timeout_us), _p(dx), _p(dresidual), _p(dw_post),
+                                              _p(dw_next), _p(workspace), workspace.numel(), _stream()))
+    return dict(dx=dx, dresidual=dresidual, dw_post=dw_post, dw_next=dw_next)

@@ -130,6 +130,31 @@ int sandwich_norm_backward(const void* dy, int dy_type, const void* dres, const 
       st);
 }
 
+int invmoe_debug_stalled_backward(const float* dy, const float* dres, const float* x, const void* w_post,
+                                  const float* rstd_post, const float* residual, const void* w_next, const float* rstd,
+                                  int T, int H, int group, int timeout_us, float* dx, float* dresidual, float* dw_post,
+                                  float* dw_next, void* workspace, size_t ws_bytes, void* stream) {
+  const int rc = check_rows(T, H, INVMOE_F32, INVMOE_F32, nullptr, INVMOE_GATE_NONE, 1.0f, 1.0f);
+  if (rc) return rc;
+  REQUIRE(T > 0 && H <= 2048, INVMOE_ERR_UNSUPPORTED_SHAPE, "need T > 0 and H <= 2048");
+  REQUIRE(group == 0 || group == 1, INVMOE_ERR_INVALID_ARG, "group must be 0 or 1");
+  REQUIRE(timeout_us >= 1 && timeout_us <= 2000000, INVMOE_ERR_INVALID_ARG, "timeout_us must be 1..2000000");
+  REQUIRE((dy != nullptr) == (w_next != nullptr) && (dy != nullptr) == (rstd != nullptr) && (dy != nullptr) == (dw_next != nullptr),
+          INVMOE_ERR_INVALID_ARG, "dy, w_next, rstd and dw_next go together");
+  REQUIRE(dy == nullptr || residual != nullptr, INVMOE_ERR_INVALID_ARG, "residual is NULL");
+  REQUIRE_PTR(dres); REQUIRE_PTR(x); REQUIRE_PTR(w_post); REQUIRE_PTR(rstd_post); REQUIRE_PTR(dx); REQUIRE_PTR(dresidual);
+  REQUIRE_PTR(dw_post); REQUIRE_PTR(workspace);
+  REQUIRE(ws_bytes >= sandwich_norm_backward_workspace_size(T, H), INVMOE_ERR_WORKSPACE_TOO_SMALL, "workspace too small");
+  REQUIRE_ALIGNED(dy); REQUIRE_ALIGNED(dres); REQUIRE_ALIGNED(x); REQUIRE_ALIGNED(w_post); REQUIRE_ALIGNED(residual);
+  REQUIRE_ALIGNED(w_next); REQUIRE_ALIGNED(dx); REQUIRE_ALIGNED(dresidual); REQUIRE_ALIGNED(workspace);
+  SandwichBwdCall c{dy, true, dres, x, true, w_post, rstd_post, residual, true, w_next, rstd, nullptr, INVMOE_GATE_NONE, T, H,
+                    1.0f, 1.0f, dx, dresidual, dw_post, dw_next, nullptr, reinterpret_cast<float*>(scratch(workspace)),
+                    status_word(workspace)};
+  c.stalled_ns = static_cast<unsigned long long>(timeout_us) * 1000ull;
+  c.stalled = group;
+  return sandwich_bwd_launch(c, static_cast<cudaStream_t>(stream));
+}
+
 size_t moe_decode_workspace_size(int T, int H, int E, int k, int F, int F_shared) {
   if (T <= 0 || T > kDecodeMaxTokens || H <= 0 || E <= 0 || k <= 0 || k > 32 || F <= 0 || F_shared < 0) return kStatusBytes;
   return kStatusBytes + decode_scratch(T, H, E, k, F, F_shared).total;

@@ -248,6 +248,8 @@ struct SandwichBwdCall {
   float* dgate;
   float* scratch;         // with dw_post: T floats (rounded up to 64), then the partial rows
   unsigned int* status;
+  unsigned long long stalled_ns = 0;   // > 0: the variant whose loads stall (fp32, H <= 2048), and its wait limit
+  int stalled = 0;
 };
 int sandwich_bwd_launch(const SandwichBwdCall& c, cudaStream_t st);
 

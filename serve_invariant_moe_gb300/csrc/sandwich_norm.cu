@@ -160,6 +160,7 @@ struct BwdParams {
   int rows;                       // rows of a partial row
   unsigned int* status;
   unsigned long long timeout_ns;
+  int stalled;                    // the stalled variant's: the group of every block's second row that never comes
 };
 
 // Rows of at most 8192: a block walks p.rows consecutive rows with its share of both channel sums in registers.  Rows come by
@@ -171,6 +172,8 @@ struct BwdParams {
 // vectors a thread from 2064 columns on, so that a row is few warps and its sums few additions: 768 threads of one vector took
 // 183 us, and 157 with the warps' sums read one by one and a division per mean.  At 8192 columns two rows fill the ring
 // and 128 registers are not quite enough: 4.5 TB/s.
+// A thread whose wait ran out goes on without its data.  What it puts in their place is NaN, which the row's sums carry to the
+// other threads: nothing that depends on a row that did not come looks like a gradient, whoever reads the status.
 constexpr int kBwdMaxDepth = 8, kBwdMaxWidth = 8192;
 constexpr int kBwdBlocks = 2;                  // on a multiprocessor, of rows up to 2048
 
@@ -203,8 +206,9 @@ __device__ __forceinline__ float row_sum(float v, float* s_part, int warp, int l
   return (s.x + s.y) + (s.z + s.w);
 }
 
-// V vectors of a thread, at most THREADS threads, BLOCKS of them on a multiprocessor.
-template <int V, int THREADS, int BLOCKS, typename TX, typename TR, typename TD>
+// V vectors of a thread, at most THREADS threads, BLOCKS of them on a multiprocessor.  STALLED: a group of the second row is
+// never loaded, for a test of the time-out.
+template <int V, int THREADS, int BLOCKS, bool STALLED, typename TX, typename TR, typename TD>
 __global__ void __launch_bounds__(THREADS, BLOCKS) sandwich_bwd_kernel(const BwdParams p, const BwdShape sh) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ __align__(16) float s_part[2][2][32];
@@ -233,6 +237,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) sandwich_bwd_kernel(const Bwd
     uint8_t* place = ring + at_place * sh.row;
     uint64_t* bar = &bars[group][at_place];
     const long long at = (t0 + i) * p.H;
+    if (STALLED && i == 1 && group == p.stalled) return;
     if (group == 0) {
       mbar_arrive_expect_tx(bar, bd + br);
       bulk_load(place + sh.dy, static_cast<const TD*>(p.dy) + at, bd, bar);
@@ -284,13 +289,15 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) sandwich_bwd_kernel(const Bwd
   for (int i = 0; i < n; ++i) {
     const long long t = t0 + i;
     const uint8_t* place = ring + at_place * sh.row;
-    const float rstd_p = next_p, rstd = next_r, g = next_g;
+    float rstd_p = next_p, rstd = next_r, res_scale = p.res_scale;
+    const float g = next_g;
     if (i + 1 < n) fetch(i + 1);
     float d[V][8];                             // e
     float n_r[V][8];
     float mean = 0.0f;
     if (next) {
       ok = ok && mbar_wait(&bars[0][at_place], phase, wc);
+      if (!ok) rstd = NAN;
       float dot = 0.0f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -315,6 +322,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) sandwich_bwd_kernel(const Bwd
       if (threadIdx.x == 0 && ok && i + sh.depth < n) load(i + sh.depth, at_place, 0);
     }
     ok = ok && mbar_wait(&bars[1][at_place], phase, wc);
+    if (!ok) rstd_p = res_scale = NAN;
     float u[V][8], n_x[V][8];                  // u: d w_p, times the channel's gate
     float dot = 0.0f;
 #pragma unroll
@@ -338,7 +346,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) sandwich_bwd_kernel(const Bwd
           s[v][j] = fmaf(b[j] * g, n_x[v][j], s[v][j]);
           u[v][j] = b[j] * wp[v][j];
           dot = fmaf(u[v][j], n_x[v][j], dot);
-          b[j] *= p.res_scale;
+          b[j] *= res_scale;
         }
         store8(static_cast<TR*>(p.dresidual) + t * p.H + c, b);
       }
@@ -612,7 +620,7 @@ SandwichPlan sandwich_bwd_plan(int T, int H) {
 
 namespace {
 
-template <int V, int THREADS, int BLOCKS, typename TX, typename TR, typename TD>
+template <int V, int THREADS, int BLOCKS, bool STALLED, typename TX, typename TR, typename TD>
 int launch_bwd(const BwdParams& p, int threads, int parts, cudaStream_t st) {
   BwdShape sh{};
   const uint32_t bx = p.H * sizeof(TX), br = p.H * sizeof(TR), bd = p.H * sizeof(TD);   // multiples of 32
@@ -629,7 +637,7 @@ int launch_bwd(const BwdParams& p, int threads, int parts, cudaStream_t st) {
   sh.depth = static_cast<int>(room / sh.row);
   if (sh.depth > kBwdMaxDepth) sh.depth = kBwdMaxDepth;
   if (sh.depth > p.rows) sh.depth = p.rows;
-  const auto kernel = sandwich_bwd_kernel<V, THREADS, BLOCKS, TX, TR, TD>;
+  const auto kernel = sandwich_bwd_kernel<V, THREADS, BLOCKS, STALLED, TX, TR, TD>;
   static std::atomic<uint64_t> attr_set{0};
   const int rc = set_smem_attr(reinterpret_cast<const void*>(kernel), static_cast<int>(room), attr_set);
   if (rc) return rc;
@@ -639,11 +647,11 @@ int launch_bwd(const BwdParams& p, int threads, int parts, cudaStream_t st) {
 template <typename TX, typename TR, typename TD>
 int launch_bwd_typed(const BwdParams& p, int parts, cudaStream_t st) {
   const int vecs = p.H / 8;
-  if (vecs <= 256) return launch_bwd<1, 256, kBwdBlocks, TX, TR, TD>(p, (vecs + 31) / 32 * 32, parts, st);
+  if (vecs <= 256) return launch_bwd<1, 256, kBwdBlocks, false, TX, TR, TD>(p, (vecs + 31) / 32 * 32, parts, st);
   const int threads = (vecs + 63) / 64 * 32;
-  if (vecs <= 512) return launch_bwd<2, 256, 1, TX, TR, TD>(p, threads, parts, st);
-  if (vecs <= 768) return launch_bwd<2, 384, 1, TX, TR, TD>(p, threads, parts, st);
-  return launch_bwd<2, 512, 1, TX, TR, TD>(p, threads, parts, st);
+  if (vecs <= 512) return launch_bwd<2, 256, 1, false, TX, TR, TD>(p, threads, parts, st);
+  if (vecs <= 768) return launch_bwd<2, 384, 1, false, TX, TR, TD>(p, threads, parts, st);
+  return launch_bwd<2, 512, 1, false, TX, TR, TD>(p, threads, parts, st);
 }
 
 int launch_wide(const BwdParams& p, const SandwichBwdCall& c, int parts, cudaStream_t st) {
@@ -693,7 +701,8 @@ int sandwich_bwd_launch(const SandwichBwdCall& c, cudaStream_t st) {
   p.dgate_token = c.gate_kind == INVMOE_GATE_TOKEN ? c.dgate : nullptr;
   p.rows = plan.rows;
   p.status = c.status;
-  p.timeout_ns = kTimeoutNs;
+  p.timeout_ns = c.stalled_ns > 0 ? c.stalled_ns : kTimeoutNs;
+  p.stalled = c.stalled;
   if (c.dw_post != nullptr) {
     p.mean = c.scratch;
     p.part = c.scratch + align_up(c.T, 64);
@@ -701,13 +710,17 @@ int sandwich_bwd_launch(const SandwichBwdCall& c, cudaStream_t st) {
   if (c.H <= kBwdMaxWidth) {
     ProfScope prof("sandwich_bwd", st);
     int rc = INVMOE_OK;
-    by_types(c.x_f32, c.res_f32, [&](auto tx, auto tr) {
-      using TX = decltype(tx);
-      using TR = decltype(tr);
-      rc = c.dy_f32 ? launch_bwd_typed<TX, TR, float>(p, plan.parts, st)
-                    : launch_bwd_typed<TX, TR, __nv_bfloat16>(p, plan.parts, st);
-      return cudaSuccess;
-    });
+    if (c.stalled_ns > 0) {
+      rc = launch_bwd<1, 256, kBwdBlocks, true, float, float, float>(p, (c.H / 8 + 31) / 32 * 32, plan.parts, st);
+    } else {
+      by_types(c.x_f32, c.res_f32, [&](auto tx, auto tr) {
+        using TX = decltype(tx);
+        using TR = decltype(tr);
+        rc = c.dy_f32 ? launch_bwd_typed<TX, TR, float>(p, plan.parts, st)
+                      : launch_bwd_typed<TX, TR, __nv_bfloat16>(p, plan.parts, st);
+        return cudaSuccess;
+      });
+    }
     if (rc || c.dw_post == nullptr) return rc;
   } else {
     const int rc = launch_wide(p, c, plan.parts, st);

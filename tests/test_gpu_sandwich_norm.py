@@ -413,3 +413,34 @@ def test_backwards_on_two_streams():
     for i, g in enumerate(got):
         for name, t in cases[i % 4][1].items():
             assert torch.equal(g[name], t), (i, name)
+
+
+@pytest.mark.parametrize("group,two_norms", [(0, True), (1, True), (1, False)])
+def test_what_a_wait_that_ran_out_leaves_is_no_gradient(group, two_norms):
+    """Blocks of four rows whose second row never comes: the rows before it are right, the others and the weights' gradients are
+    NaN, so a caller that reads no status (or gave no workspace to read) does not train on them."""
+    from serve_invariant_moe_gb300 import binding
+    from serve_invariant_moe_gb300._lib import InvmoeError
+    T, H = 1000, 2048                               # 250 blocks
+    a = inputs(T, H, F32, F32, None)
+    dy, dres = gradients(T, H, F32, F32)
+    rstd_post, r, rstd = saved(a)
+    w_next = a["w_next"]
+    if not two_norms:
+        dy = w_next = rstd = None
+    ws = binding.new_workspace(binding.sandwich_norm_backward_workspace_size(T, H))
+    want = binding.sandwich_norm_backward(dy, dres, a["x"], a["w_post"], rstd_post, r, w_next, rstd, workspace=ws)
+    binding.check_status(ws)
+    got = binding.debug_stalled_backward(dy, dres, a["x"], a["w_post"], rstd_post, r, w_next, rstd, group, ws, timeout_us=5000)
+    with pytest.raises(InvmoeError) as e:
+        binding.check_status(ws)
+    assert e.value.code == -6
+    for name in ("dx", "dresidual"):
+        assert torch.equal(got[name][::4], want[name][::4]), name
+        assert all(bool(got[name][i::4].isnan().all()) for i in (1, 2, 3)), name
+    assert bool(got["dw_post"].isnan().all())
+    assert (got["dw_next"] is None) if not two_norms else bool(got["dw_next"].isnan().all())
+    again = binding.sandwich_norm_backward(dy, dres, a["x"], a["w_post"], rstd_post, r, w_next, rstd, workspace=ws)
+    binding.check_status(ws)
+    for name in ("dx", "dresidual", "dw_post"):
+        assert torch.equal(again[name], want[name]), name

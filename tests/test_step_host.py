@@ -379,3 +379,13 @@ def test_two_backwards_of_a_block_share_no_partial_sums(monkeypatch):
     fwd = dict(layer=dict(out=None), rstd_post=None, residual=rows(3), rstd=None, gate=None, n=None)
     b.backward(fwd, rows(3))
     assert len(spaces) == 2 and spaces[0].data_ptr() != spaces[1].data_ptr()
+
+
+def test_the_stalled_backward_rejects_before_any_launch(lib):
+    f, need = lib.invmoe_debug_stalled_backward, lib.sandwich_norm_backward_workspace_size
+    a, b = ctypes.c_void_p(1 << 20), ctypes.c_void_p(1 << 21)
+
+    def call(T=4, H=64, group=0, us=1000, dy=P, n=None):
+        return f(dy, P, P, P, P, P, P, P, T, H, group, us, a, b, P, P, P, need(T, H) if n is None else n, N)
+    assert call(T=0) == -2 and call(H=2064) == -2 and call(group=2) == -1 and call(us=0) == -1 and call(us=2000001) == -1
+    assert call(dy=N) == -1 and call(dy=ctypes.c_void_p(4100)) == -4 and call(n=need(4, 64) - 1) == -3
