@@ -451,21 +451,24 @@ def head_verify_drafts(hidden, w_vocab, noise, draft_tokens=None, draft_logits=N
 
     hidden [B * (D + 1), H] bf16, request by request, row i of a request the state behind its i-th drafted token (row 0:
     behind its last emitted one); noise [B, V].  Returns verify_drafts' dict and the logits [B, D + 1, V] fp32 (into
-    ``logits`` if given)."""
+    ``logits`` if given).  Without a workspace the dict has the ``workspace`` that the call took: binding.check_status of it,
+    as of a given one, raises if the head's kernel gave up waiting, whose logits and tokens are then not to be used."""
     T, H = hidden.shape
     B, V = noise.shape
     D = 0 if draft_tokens is None else draft_tokens.shape[1]
     if T != B * (D + 1) or w_vocab.shape[0] != V:
         raise ValueError(f"hidden must have {B} * {D + 1} rows and w_vocab {V}, got {T} and {w_vocab.shape[0]}")
     need = max(binding.workspace_size(T, H, V=V), binding.verify_workspace_size(B, D, V))
+    made = {}
     if workspace is None:
-        workspace = binding.new_workspace(need, hidden.device)
+        workspace = made["workspace"] = torch.empty(max(need, 256), dtype=torch.uint8, device=hidden.device)
+        workspace[:256].zero_()
     target = torch.zeros(T, dtype=torch.int32, device=hidden.device)     # the head's own logprob is not used
     logits = None if logits is None else logits.view(T, V)
     z = binding.lm_logprob_kl(hidden, w_vocab, target, workspace, logits=logits, write_logits=True)["logits"]
     z = z.view(B, D + 1, V)
     got = binding.verify_drafts(z, noise, workspace, draft_tokens, draft_logits, accept_u, n_draft, temperature)
-    return {**got, "logits": z}
+    return {**got, "logits": z, **made}
 
 
 def head_logprob_kl(hidden, w_vocab, target, rollout_logp=None, beta=2.0, workspace=None, logits=None,

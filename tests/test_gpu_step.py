@@ -327,3 +327,23 @@ def test_two_threads_through_one_block(T):
         return [*block.prefill(n, res), *(b[name] for name in ("dn", "dresidual", "dw_post", "dw_next", "dgate"))]
     alone_and_in_two_threads(call, [(r(), r(), r(), r()) for _ in range(2)])
     block.check()
+
+
+def test_head_verify_drafts_without_a_workspace():
+    """In memory of any content, with the results of a call that is given one; its status can be read."""
+    from serve_invariant_moe_gb300 import api, binding
+    B, D, H, V = 3, 2, 256, 1000
+    g = torch.Generator().manual_seed(31)
+    r = lambda *s: torch.randn(*s, generator=g)   # noqa: E731
+    args = (r(B * (D + 1), H).to(BF).to(DEV), (0.1 * r(V, H)).to(BF).to(DEV), torch.empty(B, V).exponential_(generator=g).to(DEV),
+            torch.randint(0, V, (B, D), generator=g).to(torch.int32).to(DEV), None, torch.rand(B, D, generator=g).to(DEV))
+    need = max(binding.workspace_size(B * (D + 1), H, V=V), binding.verify_workspace_size(B, D, V))
+    ws = binding.new_workspace(need)
+    want = api.head_verify_drafts(*args, workspace=ws)
+    binding.check_status(ws)
+    dirty = [torch.full((need,), 0xff, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    torch.cuda.synchronize()
+    del dirty
+    got = api.head_verify_drafts(*args)
+    binding.check_status(got.pop("workspace"))
+    assert set(got) == set(want) and all(torch.equal(got[n], want[n]) for n in want)

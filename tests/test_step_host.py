@@ -389,3 +389,30 @@ def test_the_stalled_backward_rejects_before_any_launch(lib):
         return f(dy, P, P, P, P, P, P, P, T, H, group, us, a, b, P, P, P, need(T, H) if n is None else n, N)
     assert call(T=0) == -2 and call(H=2064) == -2 and call(group=2) == -1 and call(us=0) == -1 and call(us=2000001) == -1
     assert call(dy=N) == -1 and call(dy=ctypes.c_void_p(4100)) == -4 and call(n=need(4, 64) - 1) == -3
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_the_head_s_time_out_can_be_read_without_a_workspace_of_the_caller_s(monkeypatch, given):
+    from serve_invariant_moe_gb300 import api
+
+    class Fake(FakeLayerBinding):
+        def workspace_size(self, T, H, V):
+            return 512
+
+        def verify_workspace_size(self, B, D, V):
+            return 1024
+
+        def lm_logprob_kl(self, hidden, w_vocab, target, workspace, logits, write_logits):
+            assert workspace.numel() >= 1024 and not workspace[:256].any()
+            workspace[0] = 1                        # what a kernel that gives up does
+            return dict(logits=torch.zeros(hidden.shape[0], w_vocab.shape[0]))
+
+        def verify_drafts(self, z, noise, workspace, *more):
+            return dict(tokens=None)
+    fake = Fake()
+    monkeypatch.setattr(api, "binding", fake)
+    ws = torch.zeros(1024, dtype=torch.uint8) if given else None
+    got = api.head_verify_drafts(rows(3), torch.empty(16, 64), torch.ones(3, 16), workspace=ws)
+    assert ("workspace" in got) is not given
+    with pytest.raises(RuntimeError, match="timeout"):
+        fake.check_status(ws if given else got["workspace"])
