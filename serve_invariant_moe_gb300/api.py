@@ -76,6 +76,20 @@ def _caller():
     return threading.get_ident(), stream
 
 
+FUSED_MAX_WIDTH = 32768                  # of the one-kernel layer's rows
+
+
+def fused_fits(w: MoEWeights) -> bool:
+    """Whether the one-kernel layer (binding.moe_layer_decode) takes these weights."""
+    return w.E <= binding.DECODE_MAX_EXPERTS and w.H <= FUSED_MAX_WIDTH and max(w.F, w.F_shared) <= 1 << 20
+
+
+def _overlap(a, b):
+    """Two contiguous tensors have a byte in common."""
+    x, y = a.data_ptr(), b.data_ptr()
+    return x < y + b.numel() * b.element_size() and y < x + a.numel() * a.element_size()
+
+
 def _check_all(spaces):
     """check_status of every workspace, so that each time-out is reported once."""
     failed = None
@@ -92,8 +106,9 @@ class MoELayer:
     """Batch-invariant MoE layer forward on one GPU.
 
     fused: decode (and prefill without its intermediates) of at most 16 tokens runs the layer in one kernel
-    (binding.moe_layer_decode, at most 512 experts), with the same bits; the decode buffers of its intermediates
-    (xp, h, y, ys, plan) are then not written.
+    (binding.moe_layer_decode, at most 512 experts and 32768 columns), with the same bits; the decode buffers of its
+    intermediates (xp, h, y, ys, plan) are then not written.  An out_bf16 that overlaps the tokens takes the separate kernels.
+    None: where the weights fit.
 
     prefill and backward may run on several threads and streams at once: each has workspaces of its own there.  The calls of
     decode share one set of buffers, so they belong on one stream.
@@ -101,11 +116,13 @@ class MoELayer:
     Captured kernels hold addresses: the buffers that a captured call uses live as long as the layer, also when a larger batch
     gives it others, so a caller's own graph needs the layer (and its weights) kept.  DecodeGraphs keeps its buffers itself."""
 
-    def __init__(self, weights: MoEWeights, fused: bool = False):
-        if fused and weights.E > binding.DECODE_MAX_EXPERTS:
-            raise ValueError(f"fused decode takes at most {binding.DECODE_MAX_EXPERTS} experts, got {weights.E}")
+    def __init__(self, weights: MoEWeights, fused: Optional[bool] = False):
+        fits = (fused is None or bool(fused)) and fused_fits(weights)
+        if fused and not fits:
+            raise ValueError(f"fused decode takes at most {binding.DECODE_MAX_EXPERTS} experts and {FUSED_MAX_WIDTH} columns, "
+                             f"got {weights.E} and {weights.H} (F {weights.F}, shared {weights.F_shared})")
         self.w = weights
-        self.fused = fused
+        self.fused = fits
         self._spaces, self._small, self._back = {}, {}, {}      # prefill's and backward's, by thread and stream
         self._decode = None
         self._unread = []               # status blocks of replaced workspaces, which check() reads
@@ -183,6 +200,10 @@ class MoELayer:
                                         out_bf16=out_bf16, logits=d["logits"][:B], topk_idx=d["idx"][:B],
                                         topk_w=d["w"][:B], **chosen)["out"]
 
+    def _in_one_kernel(self, x, out_bf16):
+        return (self.fused and 0 < x.shape[0] <= binding.DECODE_MAX_TOKENS
+                and (out_bf16 is None or not _overlap(x, out_bf16)))
+
     def _replace(self, ws):
         """A workspace that gives way to a larger one: its status, behind the calls so far on this stream."""
         if ws is not None:
@@ -210,7 +231,7 @@ class MoELayer:
         T = x.shape[0]
         if not return_all and replay_idx is None and 0 < T <= 1024:
             d = self._small_buffers(T)
-            if self.fused and T <= binding.DECODE_MAX_TOKENS:
+            if self._in_one_kernel(x, out_bf16):
                 return self._run_fused(x, d, None, out_bf16)
             bufs = {k: d[k] for k in ("logits", "idx", "w", "plan", "xp", "h", "y", "ys")}
             return self._run(x, d["ws"], bufs, out_bf16=out_bf16)["out"]
@@ -327,7 +348,7 @@ class MoELayer:
             raise ValueError(f"x_tokens must be a contiguous [B, {w.H}] bf16 tensor on {d['device']}")
         if out_bf16 is not None:
             binding._req(out_bf16, torch.bfloat16, "out_bf16", (B, w.H))
-        if self.fused and 0 < B <= binding.DECODE_MAX_TOKENS:
+        if self._in_one_kernel(x_tokens, out_bf16):
             return self._run_fused(x_tokens, d, d["out"][:B], out_bf16)
         if w.routing is not None:
             bufs = {name: d[name] for name in ("logits", "idx", "w", "plan", "xp", "h", "y", "ys", "out")}

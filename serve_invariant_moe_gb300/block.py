@@ -236,8 +236,8 @@ class MoEBlock:
     prefill and backward may run on several threads and streams at once.  A graph that a caller captures needs the block and
     its weights kept, as MoELayer's."""
 
-    def __init__(self, weights: MoEBlockWeights, fused: bool = True):
-        """fused: decode of at most 16 rows runs the layer in one kernel (MoELayer)."""
+    def __init__(self, weights: MoEBlockWeights, fused: Optional[bool] = None):
+        """fused: decode of at most 16 rows runs the layer in one kernel (MoELayer); None: where its weights fit."""
         self.w = weights
         self.layer = MoELayer(weights.layer, fused=fused)
 

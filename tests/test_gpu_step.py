@@ -347,3 +347,31 @@ def test_head_verify_drafts_without_a_workspace():
     got = api.head_verify_drafts(*args)
     binding.check_status(got.pop("workspace"))
     assert set(got) == set(want) and all(torch.equal(got[n], want[n]) for n in want)
+
+
+def test_a_block_of_more_experts_than_the_one_kernel_takes():
+    (block, _), _ = stack(2, 128, E=600, F=128, Fs=0, fused=None)
+    (plain, _), _ = stack(2, 128, E=600, F=128, Fs=0, fused=False)
+    x = torch.randn(20, 128, generator=torch.Generator().manual_seed(41)).to(BF).to(DEV)
+    for T in (1, 16, 20):
+        want = plain.prefill(x[:T], x[:T])
+        for call in (block.prefill, block.decode):
+            assert all(torch.equal(a, b) for a, b in zip(call(x[:T], x[:T]), want)), T
+
+
+@pytest.mark.parametrize("Fs", [0, 128])
+def test_the_bf16_copy_may_go_where_the_tokens_are(Fs):
+    """Over the tokens themselves or shifted over some of them: the one-kernel layer reads them to the end, so such a call takes
+    the separate kernels, which give the same bits."""
+    from serve_invariant_moe_gb300 import api
+    w = layer_weights(32, 256, 128, Fs, 4)
+    plain, fused = api.MoELayer(w), api.MoELayer(w, fused=True)
+    x = torch.randn(16, 256, generator=torch.Generator().manual_seed(42)).to(BF).to(DEV)
+    want = torch.empty(9, 256, dtype=BF, device=DEV)
+    out = plain.prefill(x[:9], want)
+    for name in ("decode", "prefill"):
+        for first in (0, 3):
+            y = x.clone()
+            got = getattr(fused, name)(y[:9], y[first:first + 9])
+            assert torch.equal(got, out) and torch.equal(y[first:first + 9], want), (name, first)
+    fused.check()

@@ -416,3 +416,27 @@ def test_the_head_s_time_out_can_be_read_without_a_workspace_of_the_caller_s(mon
     assert ("workspace" in got) is not given
     with pytest.raises(RuntimeError, match="timeout"):
         fake.check_status(ws if given else got["workspace"])
+
+
+def layer_of(E, H, F=64, Fs=0):
+    """Weights of a size, without their memory."""
+    from serve_invariant_moe_gb300 import api
+    e = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="meta")   # noqa: E731
+    return api.MoEWeights(e(E, H), e(E, 2 * F, H), e(E, H, F), 2, e(2 * Fs, H) if Fs else None, e(H, Fs) if Fs else None)
+
+
+@pytest.mark.parametrize("size,fits", [((512, 64), True), ((600, 64), False), ((4, 32768), True), ((4, 32832), False),
+                                       ((4, 64, (1 << 20) + 64), False), ((4, 64, 64, (1 << 20) + 64), False)])
+def test_the_one_kernel_layer_is_taken_where_it_fits(size, fits):
+    """A block of any layer can be built, and whether few rows go through one kernel is known from the start."""
+    from serve_invariant_moe_gb300 import api, block
+    w = layer_of(*size)
+    assert api.MoELayer(w).fused is False and api.MoELayer(w, fused=None).fused is fits
+    assert block.MoEBlock(block.MoEBlockWeights(w, None)).layer.fused is fits
+    if fits:
+        assert api.MoELayer(w, fused=True).fused
+    else:
+        with pytest.raises(ValueError, match="fused"):
+            api.MoELayer(w, fused=True)
+        with pytest.raises(ValueError, match="fused"):
+            block.MoEBlock(block.MoEBlockWeights(w, None), fused=True)
