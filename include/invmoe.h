@@ -688,7 +688,8 @@ size_t verify_workspace_size(int B, int D, int V);
  * accepts nothing and gives token -1.
  * Outputs: tokens [B, D + 1] int32 = the n accepted drafts, the drawn token, then -1;
  * n_accepted [B] int32; logp [B, D + 1] fp32 = log p_i of the emitted tokens (at temperature 1
- * where tau is 0; -inf for token -1), then 0.  noise is read also for D = 0: plain sampling.
+ * where tau is 0; -inf for token -1), then 0.  None of them may overlap an input or another
+ * one.  noise is read also for D = 0: plain sampling.
  * Every request's bits are its own.  Shapes: D <= 32, V <= 2^30. */
 int verify_drafts(const void* logits, int logits_type, const void* draft_logits, const int32_t* draft_tokens,
                   const float* accept_u, const float* noise, const int32_t* n_draft, const float* temperature, float tau,

@@ -26,10 +26,26 @@ int check_rows(int T, int H, int x_type, int residual_type, const void* gate, in
 
 size_t matrix_bytes(int T, int H, int type) { return static_cast<size_t>(T) * H * (type == INVMOE_F32 ? 4 : 2); }
 
-// Two arrays have no byte in common (or one is absent).
+// Two arrays have no byte in common (or one is absent or empty).
 bool apart(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a == nullptr || b == nullptr || x + na <= y || y + nb <= x;
+  return a == nullptr || b == nullptr || na == 0 || nb == 0 || x + na <= y || y + nb <= x;
+}
+
+// No output has a byte in common with an input or with another output.
+struct Span {
+  const void* at;
+  size_t bytes;
+};
+template <size_t OUT, size_t IN>
+bool outputs_apart(const Span (&outs)[OUT], const Span (&ins)[IN]) {
+  for (size_t i = 0; i < OUT; ++i) {
+    for (const Span& in : ins)
+      if (!apart(outs[i].at, outs[i].bytes, in.at, in.bytes)) return false;
+    for (size_t j = 0; j < i; ++j)
+      if (!apart(outs[i].at, outs[i].bytes, outs[j].at, outs[j].bytes)) return false;
+  }
+  return true;
 }
 
 // moe_layer_decode's part of the workspace behind the status block: offsets of its arrays.
@@ -201,16 +217,11 @@ int moe_layer_decode(const void* x, const void* w_router, const void* w13, const
     REQUIRE_ALIGNED(ws13); REQUIRE_ALIGNED(ws2);
   }
   // columns of x are read until the last block is done with its gate/up units, long after others have written outputs
-  const size_t xn = matrix_bytes(T, H, INVMOE_BF16);
   // (and the logits while other blocks already combine)
-  const size_t pairs = static_cast<size_t>(T) * k * 4;
-  const struct { const void* at; size_t bytes; } arrays[] = {{x, xn}, {out, 2 * xn}, {out_bf16, xn},
-                                                             {logits, static_cast<size_t>(T) * E * 4}, {topk_idx, pairs},
-                                                             {topk_w, pairs}};
-  for (size_t i = 1; i < sizeof(arrays) / sizeof(arrays[0]); ++i)
-    for (size_t j = 0; j < i; ++j)
-      REQUIRE(apart(arrays[i].at, arrays[i].bytes, arrays[j].at, arrays[j].bytes), INVMOE_ERR_INVALID_ARG,
-              "an output overlaps x or another one");
+  const size_t xn = matrix_bytes(T, H, INVMOE_BF16), pairs = static_cast<size_t>(T) * k * 4;
+  const Span ins[] = {{x, xn}};
+  const Span outs[] = {{out, 2 * xn}, {out_bf16, xn}, {logits, static_cast<size_t>(T) * E * 4}, {topk_idx, pairs}, {topk_w, pairs}};
+  REQUIRE(outputs_apart(outs, ins), INVMOE_ERR_INVALID_ARG, "an output overlaps x or another one");
   const DecodeScratch s = decode_scratch(T, H, E, k, F, F_shared);
   uint8_t* base = scratch(workspace);
   DecodeParams p{};
@@ -267,6 +278,12 @@ int verify_drafts(const void* logits, int logits_type, const void* draft_logits,
   REQUIRE(D > 0 || draft_logits == nullptr, INVMOE_ERR_INVALID_ARG, "draft_logits without drafts");
   if (D > 0) { REQUIRE_PTR(draft_tokens); REQUIRE_PTR(accept_u); }
   REQUIRE_ALIGNED(logits); REQUIRE_ALIGNED(draft_logits); REQUIRE_ALIGNED(noise);
+  // a request's outputs are written while others are still being read
+  const size_t each = static_cast<size_t>(B) * 4, wide = each * V, row = wide / (logits_type == INVMOE_F32 ? 1 : 2);
+  const Span ins[] = {{logits, row * (D + 1)}, {draft_logits, row * D}, {draft_tokens, each * D}, {accept_u, each * D},
+                      {noise, wide},           {n_draft, each},         {temperature, each}};
+  const Span outs[] = {{tokens, each * (D + 1)}, {n_accepted, each}, {logp, each * (D + 1)}};
+  REQUIRE(outputs_apart(outs, ins), INVMOE_ERR_INVALID_ARG, "an output overlaps an input or another one");
   uint8_t* s = scratch(workspace);
   VerifyCall c{logits, draft_logits, draft_tokens, accept_u, noise, n_draft, temperature, tau, B, D, V, rows, chunks,
                tokens, n_accepted, logp, reinterpret_cast<int32_t*>(s), nullptr, nullptr};

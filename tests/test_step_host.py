@@ -440,3 +440,19 @@ def test_the_one_kernel_layer_is_taken_where_it_fits(size, fits):
             api.MoELayer(w, fused=True)
         with pytest.raises(ValueError, match="fused"):
             block.MoEBlock(block.MoEBlockWeights(w, None), fused=True)
+
+
+def test_verify_drafts_rejects_outputs_that_overlap(lib):
+    """Tokens over the drafted ones, say: a request's would be written while the next one's drafts are read."""
+    f, B, D, V = lib.verify_drafts, 3, 2, 96
+    n = lib.verify_workspace_size(B, D, V)
+    # logits, draft_logits, draft_tokens, accept_u, noise, n_draft, temperature, tokens, n_accepted, logp
+    size = [B * (D + 1) * V * 4, B * D * V * 4, B * D * 4, B * D * 4, B * V * 4, B * 4, B * 4, B * (D + 1) * 4, B * 4, B * (D + 1) * 4]
+    at = [(1 << 20) + (i << 16) for i in range(10)]
+    for i in (7, 8, 9):
+        for j in range(i):
+            for first in (at[j], at[j] + size[j] - 4, at[j] - size[i] + 4):
+                p = [ctypes.c_void_p(a) for a in at]
+                p[i] = ctypes.c_void_p(first)
+                assert f(p[0], 1, *p[1:7], 1.0, B, D, V, *p[7:], ctypes.c_void_p(1 << 24), n, N) == -1, (i, j)
+                assert b"overlaps" in lib.invmoe_last_error(), (i, j)
