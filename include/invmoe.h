@@ -658,7 +658,7 @@ size_t sandwich_norm_backward_workspace_size(int T, int H);
  * dy [T, H] of dy_type, with w_next and rstd, or all three NULL (no second norm: dres is
  * then required and residual is not read); dres [T, H] of the residual's type (nullable).
  * dw_post, dw_next, dgate: fp32, rows summed in a fixed order; each nullable, but dw_next
- * and a channel's dgate come with dw_post.  dx and dresidual overlap nothing. */
+ * and a channel's dgate come with dw_post.  No output overlaps an input or another one. */
 int sandwich_norm_backward(const void* dy, int dy_type, const void* dres, const void* x, int x_type, const void* w_post,
                            const float* rstd_post, const void* residual, int residual_type, const void* w_next,
                            const float* rstd, const void* gate, int gate_kind, int T, int H, float residual_scale,

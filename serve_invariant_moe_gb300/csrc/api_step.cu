@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include "checks.h"
+#include "fp8.cuh"
 #include "internal.h"
 
 using namespace invmoe;
@@ -86,10 +87,12 @@ int sandwich_norm(const void* x, int x_type, const void* w_post, const void* res
   const size_t xn = matrix_bytes(T, H, x_type), rn = matrix_bytes(T, H, residual_type), on = matrix_bytes(T, H, INVMOE_BF16);
   REQUIRE(same_or_apart(residual_out, residual, rn), INVMOE_ERR_INVALID_ARG,
           "residual_out overlaps residual without being it");
-  REQUIRE(apart(residual_out, rn, x, xn) && apart(out, on, x, xn) && apart(out, on, residual, rn) &&
-              apart(out, on, residual_out, rn) && apart(q, on / 2, x, xn) && apart(q, on / 2, residual, rn) &&
-              apart(q, on / 2, residual_out, rn) && apart(q, on / 2, out, on),
-          INVMOE_ERR_INVALID_ARG, "an output overlaps another one or an input");
+  const size_t each = static_cast<size_t>(T) * 4, row = static_cast<size_t>(H) * 2;
+  const Span ins[] = {{x, xn}, {w_post, row}, {w_next, row}, {gate, gate_kind == INVMOE_GATE_CHANNEL ? row : each},
+                      {residual_out == residual ? nullptr : residual, rn}};
+  const Span outs[] = {{residual_out, rn}, {out, on}, {q, on / 2}, {scale, each * ((H + kFp8Block - 1) / kFp8Block)},
+                       {rstd_post, each}, {rstd, each}};
+  REQUIRE(outputs_apart(outs, ins), INVMOE_ERR_INVALID_ARG, "an output overlaps another one or an input");
   return sandwich_launch({x, x_type == INVMOE_F32, w_post, residual, residual_type == INVMOE_F32, gate, gate_kind, w_next, T,
                           H, residual_scale, branch_scale, eps, residual_out, out, q, scale, rstd_post, rstd},
                          static_cast<cudaStream_t>(stream));
@@ -135,10 +138,11 @@ int sandwich_norm_backward(const void* dy, int dy_type, const void* dres, const 
   REQUIRE_ALIGNED(w_next); REQUIRE_ALIGNED(dx); REQUIRE_ALIGNED(dresidual); REQUIRE_ALIGNED(workspace);
   if (channel) REQUIRE_ALIGNED(gate);
   const size_t xn = matrix_bytes(T, H, x_type), rn = matrix_bytes(T, H, residual_type), yn = matrix_bytes(T, H, dy_type);
-  REQUIRE(apart(dx, xn, dresidual, rn) && apart(dx, xn, x, xn) && apart(dx, xn, dy, yn) && apart(dx, xn, dres, rn) &&
-              apart(dx, xn, residual, rn) && apart(dresidual, rn, x, xn) && apart(dresidual, rn, dy, yn) &&
-              apart(dresidual, rn, dres, rn) && apart(dresidual, rn, residual, rn),
-          INVMOE_ERR_INVALID_ARG, "dx or dresidual overlaps the other or an input");
+  const size_t each = static_cast<size_t>(T) * 4, row = static_cast<size_t>(H) * 2;
+  const Span ins[] = {{x, xn}, {dy, yn}, {dres, rn}, {dy != nullptr ? residual : nullptr, rn}, {w_post, row}, {w_next, row},
+                      {rstd_post, each}, {rstd, each}, {gate, channel ? row : each}};
+  const Span outs[] = {{dx, xn}, {dresidual, rn}, {dw_post, 2 * row}, {dw_next, 2 * row}, {dgate, channel ? 2 * row : each}};
+  REQUIRE(outputs_apart(outs, ins), INVMOE_ERR_INVALID_ARG, "an output overlaps another one or an input");
   return sandwich_bwd_launch(
       {dy, dy_type == INVMOE_F32, dres, x, x_type == INVMOE_F32, w_post, rstd_post, residual, residual_type == INVMOE_F32,
        w_next, rstd, gate, gate_kind, T, H, residual_scale, branch_scale, dx, dresidual, dw_post, dw_next, dgate,

@@ -456,3 +456,41 @@ def test_verify_drafts_rejects_outputs_that_overlap(lib):
                 p[i] = ctypes.c_void_p(first)
                 assert f(p[0], 1, *p[1:7], 1.0, B, D, V, *p[7:], ctypes.c_void_p(1 << 24), n, N) == -1, (i, j)
                 assert b"overlaps" in lib.invmoe_last_error(), (i, j)
+
+
+def overlapping(size, outs):
+    """Addresses of arrays that lie apart, with output i moved onto array j: on it, over its end, over its begin."""
+    at = [(1 << 20) + (i << 16) for i in range(len(size))]
+    for i in outs:
+        for j in range(len(size)):
+            if i != j:
+                for first in (at[j], at[j] + size[j] - 16, at[j] - size[i] + 16):
+                    yield i, j, first - at[j], [ctypes.c_void_p(first if k == i else a) for k, a in enumerate(at)]
+
+
+@pytest.mark.parametrize("kind", [1, 2])
+def test_sandwich_norm_rejects_every_overlap(lib, kind):
+    """Also of the rows' numbers with the weights, the gate or one another; residual_out alone may be the residual."""
+    T, H = 4, 64
+    row, small = T * H, T * 4
+    # x, w_post, residual, gate, w_next, residual_out, out, q, scale, rstd_post, rstd
+    size = [row * 4, H * 2, row * 2, H * 2 if kind == 1 else small, H * 2, row * 2, row * 2, row, small, small, small]
+    for i, j, shift, p in overlapping(size, range(5, 11)):
+        if (i, j, shift) == (5, 2, 0):
+            continue
+        rc = lib.sandwich_norm(p[0], 1, p[1], p[2], 0, p[3], kind, p[4], T, H, 1.0, 1.0, 1e-6, *p[5:], N)
+        assert rc in (-1, -4) and (rc == -4 or b"overlaps" in lib.invmoe_last_error()), (i, j, shift)
+
+
+@pytest.mark.parametrize("kind", [1, 2])
+def test_sandwich_norm_backward_rejects_every_overlap(lib, kind):
+    T, H = 4, 64
+    row, small = T * H, T * 4
+    # dy, dres, x, w_post, rstd_post, residual, w_next, rstd, gate, dx, dresidual, dw_post, dw_next, dgate
+    size = [row * 2, row * 2, row * 4, H * 2, small, row * 2, H * 2, small, H * 2 if kind == 1 else small, row * 4, row * 2,
+            H * 4, H * 4, H * 4 if kind == 1 else small]
+    n = lib.sandwich_norm_backward_workspace_size(T, H)
+    for i, j, shift, p in overlapping(size, range(9, 14)):
+        rc = lib.sandwich_norm_backward(p[0], 0, p[1], p[2], 1, p[3], p[4], p[5], 0, p[6], p[7], p[8], kind, T, H, 1.0, 1.0,
+                                        *p[9:], ctypes.c_void_p(1 << 24), n, N)
+        assert rc in (-1, -4) and (rc == -4 or b"overlaps" in lib.invmoe_last_error()), (i, j, shift)
