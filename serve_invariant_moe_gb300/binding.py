@@ -783,12 +783,14 @@ def moe_layer_decode(x, w_router, w13, w2, k, workspace, ws13=None, ws2=None, sc
     E, F2, _ = _dims(w13, "w13", 3)
     F, Fs = F2 // 2, 0
     kind = 2 if score is None else _score(score)
+    if (ws13 is None) != (ws2 is None):
+        raise ValueError("ws13 and ws2 go together")
     m.check(x, "x", BF16_, T, H)
     m.check(w_router, "w_router", BF16_, E, H)
     m.check(w13, "w13", BF16_, E, 2 * F, H)
     m.check(w2, "w2", BF16_, E, H, F)
     if ws13 is not None:
-        Fs = ws13.shape[0] // 2
+        Fs = _dims(ws13, "ws13")[0] // 2
         m.check(ws13, "ws13", BF16_, 2 * Fs, H)
         m.check(ws2, "ws2", BF16_, H, Fs)
     if bias is not None:
@@ -803,6 +805,7 @@ def moe_layer_decode(x, w_router, w13, w2, k, workspace, ws13=None, ws2=None, sc
                              bool(renormalize), scale, out, out_bf16, logits, topk_idx, topk_w, workspace,
                              workspace.numel()))
     return {"out": out, "out_bf16": out_bf16, "logits": logits, "topk_idx": topk_idx, "topk_w": topk_w}
+
 
 def sandwich_norm(x, w_post, residual, w_next=None, gate=None, residual_scale=1.0, branch_scale=1.0, eps=1e-6, out=True,
                   fp8=False, residual_out=None, q=None, scale=None, rstd_post=None, rstd=None):

@@ -494,3 +494,11 @@ def test_sandwich_norm_backward_rejects_every_overlap(lib, kind):
         rc = lib.sandwich_norm_backward(p[0], 0, p[1], p[2], 1, p[3], p[4], p[5], 0, p[6], p[7], p[8], kind, T, H, 1.0, 1.0,
                                         *p[9:], ctypes.c_void_p(1 << 24), n, N)
         assert rc in (-1, -4) and (rc == -4 or b"overlaps" in lib.invmoe_last_error()), (i, j, shift)
+
+
+def test_moe_layer_decode_wants_both_weights_of_the_shared_expert():
+    from serve_invariant_moe_gb300 import binding
+    e = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)   # noqa: E731
+    for shared in (dict(ws2=e(64, 64)), dict(ws13=e(128, 64))):
+        with pytest.raises(ValueError, match="ws13 and ws2"):
+            binding.moe_layer_decode(e(2, 64), e(4, 64), e(4, 128, 64), e(4, 64, 64), 1, torch.zeros(256, dtype=torch.uint8), **shared)
