@@ -444,3 +444,27 @@ def test_what_a_wait_that_ran_out_leaves_is_no_gradient(group, two_norms):
     binding.check_status(ws)
     for name in ("dx", "dresidual", "dw_post"):
         assert torch.equal(again[name], want[name]), name
+
+
+@pytest.mark.parametrize("T,H,xt,rt,yt,without", [(4096, 2048, F32, F32, F32, None), (3000, 96, BF, BF, BF, None),
+                                                  (1500, 4096, F32, F32, F32, None), (1200, 4608, F32, BF, BF, None),
+                                                  (2000, 6144, F32, BF, BF, None), (500, 8192, F32, F32, F32, None),
+                                                  (500, 8192, F32, BF, BF, None), (3000, 2048, F32, F32, F32, "dy"),
+                                                  (900, 8192, F32, F32, F32, "dres"), (1500, 2064, BF, F32, F32, "dy")])
+def test_rows_that_come_through_used_places(T, H, xt, rt, yt, without):
+    """More rows to a block than its ring has places, down to a single place (8192 columns, all fp32): a copy that came too early
+    would overwrite a row still being read, every one of which has values of its own."""
+    from serve_invariant_moe_gb300 import binding
+    a = inputs(T, H, xt, rt, "channel")
+    dy, dres = gradients(T, H, rt, yt)
+    rstd_post, r, rstd = saved(a, 0.875, 0.25)
+    w_next = a["w_next"]
+    if without == "dy":
+        dy = w_next = rstd = None
+    elif without == "dres":
+        dres = None
+    args = (dy, dres, a["x"], a["w_post"], rstd_post, r, w_next, rstd, a["gate"], 0.875, 0.25)
+    got = binding.sandwich_norm_backward(*args)
+    check_backward(got, a, dy, dres, rstd_post, r, rstd, 0.875, 0.25)
+    again = binding.sandwich_norm_backward(*args)
+    assert all(torch.equal(got[n], again[n]) for n in got if got[n] is not None)

@@ -375,3 +375,60 @@ def test_the_bf16_copy_may_go_where_the_tokens_are(Fs):
             got = getattr(fused, name)(y[:9], y[first:first + 9])
             assert torch.equal(got, out) and torch.equal(y[first:first + 9], want), (name, first)
     fused.check()
+
+
+def test_gradients_through_two_blocks():
+    """The embedded rows' gradient through a norm and two blocks, every expert chosen, the residual stream in fp32.
+
+    Against 64-bit autograd in the norm of the difference: each block's backward is held to 2e-2 (its products take bf16
+    operands), two of them to 4e-2.  Against the difference of the loss along the gradient itself, whole and restricted to some
+    rows or columns: there the product with the gradient is |dx|^2, so that 5 % of it is an error of 5 %.  A step moves every
+    element by 0.05, tens of the roundings on the way (2^-9 of a value), whose sum over thousands of elements is far below
+    1 %; the third derivative's share is (0.05)^2 / 6 of it."""
+    from serve_invariant_moe_gb300 import binding
+    T, H, F = 40, 128, 128
+    blocks, w = stack(2, H, E=8, F=F, Fs=0, k=8)
+    g = torch.Generator().manual_seed(9)
+    x = torch.randn(T, H, generator=g).to(DEV)
+    target = torch.randn(T, H, generator=g).to(DEV)
+
+    def forward(x):
+        f0 = binding.add_rms_norm(x, w)
+        n, r, kept = f0["out"], x, []
+        for b in blocks:
+            f = b.prefill(n, r, return_all=True)
+            kept.append(f)
+            n, r = f["out"], f["residual"]
+        return f0, kept, r
+    f0, kept, r = forward(x)
+    dres, dn = (r - target), None
+    for b, f in zip(reversed(blocks), reversed(kept)):
+        back = b.backward(f, dn, dres)
+        dn, dres = back["dn"], back["dresidual"]
+    dx = binding.add_rms_norm_backward(dn, x, w, f0["rstd"], dres=dres)["dx"].double()
+
+    rms = lambda t: t * (t.square().mean(-1, keepdim=True) + 1e-6).rsqrt()   # noqa: E731
+    leaf = x.double().requires_grad_()
+    n, r = rms(leaf) * w.double(), leaf
+    for b in blocks:
+        l = b.w.layer
+        gu = torch.einsum("th,efh->tef", n, l.w13.double())
+        h = torch.nn.functional.silu(gu[..., :F]) * gu[..., F:]
+        m = torch.einsum("te,tef,ehf->th", torch.softmax(n @ l.w_router.double().T, -1), h, l.w2.double())
+        r = b.w.residual_scale * r + b.w.branch_scale * b.w.gate.double() * rms(m) * b.w.w_post.double()
+        n = None if b.w.w_next is None else rms(r) * b.w.w_next.double()
+    (0.5 * (r - target.double()).square().sum()).backward()
+    assert (dx - leaf.grad).norm() <= 4e-2 * leaf.grad.norm()
+
+    loss = lambda x: float(0.5 * (forward(x)[2].double() - target.double()).square().sum())   # noqa: E731
+    mask = torch.zeros(T, H, dtype=torch.float64, device=DEV)
+    for rows_, cols in ((slice(None), slice(None)), (slice(0, 7), slice(None)), (slice(20, 40), slice(0, 64)),
+                        (slice(None), slice(100, 128))):
+        mask.zero_()
+        mask[rows_, cols] = 1
+        v = dx * mask
+        v = v / (v.norm() / mask.sum().sqrt())
+        step = (0.05 * v).float()
+        want = (loss(x + step) - loss(x - step)) / 0.1
+        have = float((dx * v).sum())
+        assert have > 0 and abs(have - want) <= 0.05 * have, (have, want)
