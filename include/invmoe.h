@@ -690,6 +690,9 @@ size_t verify_workspace_size(int B, int D, int V);
  * n_accepted [B] int32; logp [B, D + 1] fp32 = log p_i of the emitted tokens (at temperature 1
  * where tau is 0; -inf for token -1), then 0.  None of them may overlap an input or another
  * one.  noise is read also for D = 0: plain sampling.
+ * Accuracy: probabilities are within 4e-5 of their value (fp32 exponentials and sums), and one
+ * below 2^-126 of the row's largest counts as 0; comparisons and scores closer than that may go
+ * either way, the same way in every batch.  logp: within 4e-5, and 2^-22 of its value.
  * Every request's bits are its own.  Shapes: D <= 32, V <= 2^30. */
 int verify_drafts(const void* logits, int logits_type, const void* draft_logits, const int32_t* draft_tokens,
                   const float* accept_u, const float* noise, const int32_t* n_draft, const float* temperature, float tau,

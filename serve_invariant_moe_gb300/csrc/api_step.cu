@@ -256,7 +256,8 @@ size_t verify_workspace_size(int B, int D, int V) {
   if (B <= 0 || D < 0 || V <= 0) return kStatusBytes;
   const size_t chunks = verify_chunks(V);
   return kStatusBytes + align_up(static_cast<size_t>(B) * sizeof(int32_t), 256) +
-         static_cast<size_t>(B) * ((2 * static_cast<size_t>(D) + 1) * chunks + verify_race_chunks(V)) * 16;
+         align_up(static_cast<size_t>(B) * verify_race_chunks(V) * sizeof(unsigned long long), 256) +
+         static_cast<size_t>(B) * (2 * static_cast<size_t>(D) + 1) * chunks * 16;
 }
 
 int verify_drafts(const void* logits, int logits_type, const void* draft_logits, const int32_t* draft_tokens,
@@ -293,7 +294,7 @@ int verify_drafts(const void* logits, int logits_type, const void* draft_logits,
                tokens, n_accepted, logp, reinterpret_cast<int32_t*>(s), nullptr, nullptr};
   s += align_up(static_cast<size_t>(B) * sizeof(int32_t), 256);
   c.racers = s;
-  c.stats = s + static_cast<size_t>(B) * verify_race_chunks(V) * 16;
+  c.stats = s + align_up(static_cast<size_t>(B) * verify_race_chunks(V) * sizeof(unsigned long long), 256);
   return verify_launch(c, logits_type == INVMOE_F32, static_cast<cudaStream_t>(stream));
 }
 

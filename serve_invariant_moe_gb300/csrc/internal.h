@@ -275,9 +275,9 @@ struct VerifyCall {
   int32_t* tokens;             // [B, D + 1]
   int32_t* n_accepted;         // [B]
   float* logp;                 // [B, D + 1]
-  int32_t* done;               // scratch: [B] chunks finished
+  int32_t* done;               // scratch: [B] racing blocks finished
   void* stats;                 // scratch: 16 bytes per request, row and chunk
-  void* racers;                // scratch: 16 bytes per request and block of the race
+  void* racers;                // scratch: 8 bytes per request and block of the race
   int racing;                  // blocks of a request in the race, set by the launch
 };
 int verify_chunks(int V);        // of a row's statistics

@@ -20,7 +20,10 @@ constexpr unsigned int kStatusBadCounts = 4u;   // expert-parallel row counts di
 // pdl_wait() blocks until that kernel has completed and its memory writes are visible, so
 // every such kernel calls it before its first global-memory access (and before it returns).
 // pdl_trigger() lets the next kernel be scheduled now (its own pdl_wait still waits for
-// this kernel to complete).
+// this kernel to complete).  A kernel may read before its pdl_wait only what no kernel since
+// its predecessor's pdl_wait writes, and only if that predecessor triggers behind its own
+// wait in every block: then everything before the predecessor has completed (verify_drafts'
+// second kernel reads its inputs so).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
