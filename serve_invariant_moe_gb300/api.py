@@ -71,9 +71,12 @@ def _capturing():
 
 
 def _caller():
-    """The calling thread and its current stream: calls with the same ones run one after the other."""
-    stream = torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if torch.cuda.is_initialized() else 0
-    return threading.get_ident(), stream
+    """The calling thread and its current stream: calls with the same ones run one after the other.  None in a capture."""
+    if not torch.cuda.is_initialized():
+        return threading.get_ident(), 0
+    if torch.cuda.is_current_stream_capturing():
+        return None
+    return threading.get_ident(), torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 FUSED_MAX_WIDTH = 32768                  # of the one-kernel layer's rows
@@ -135,15 +138,14 @@ class MoELayer:
 
     def _workspace(self, T):
         w = self.w
-        need = binding.workspace_size(T, w.H, w.E, w.k, w.F, w.F_shared, 0)
-        if _capturing():
-            self._captured.append(dict(ws=binding.new_workspace(need, w.w13.device)))
-            return self._captured[-1]["ws"]
-        return self._kept(self._spaces, need)
+        return self._kept(self._spaces, binding.workspace_size(T, w.H, w.E, w.k, w.F, w.F_shared, 0))
 
     def _kept(self, spaces, need):
-        """The caller's workspace in `spaces`, of at least `need` bytes."""
+        """The caller's workspace in `spaces`, of at least `need` bytes; a captured call's is its graph's."""
         key = _caller()
+        if key is None:
+            self._captured.append(dict(ws=binding.new_workspace(need, self.w.w13.device)))
+            return self._captured[-1]["ws"]
         ws = spaces.get(key)
         if ws is None or ws.numel() < need:
             self._replace(ws)
@@ -291,10 +293,10 @@ class MoELayer:
 
     def _small_buffers(self, T):
         """prefill's buffers of at least T rows: the caller's; a captured call's are its graph's."""
-        if _capturing():
+        key = _caller()
+        if key is None:
             self._captured.append(self._buffers(T))
             return self._captured[-1]
-        key = _caller()
         d = self._small.get(key)
         if d is None or d["B"] < T:
             for name in ("ws", "fused_ws"):

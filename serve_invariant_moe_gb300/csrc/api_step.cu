@@ -27,26 +27,26 @@ int check_rows(int T, int H, int x_type, int residual_type, const void* gate, in
 
 size_t matrix_bytes(int T, int H, int type) { return static_cast<size_t>(T) * H * (type == INVMOE_F32 ? 4 : 2); }
 
-// Two arrays have no byte in common (or one is absent or empty).
-bool apart(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a == nullptr || b == nullptr || na == 0 || nb == 0 || x + na <= y || y + nb <= x;
-}
-
-// No output has a byte in common with an input or with another output.
+// An array's addresses; none of an absent or empty one.
 struct Span {
-  const void* at;
-  size_t bytes;
+  uintptr_t lo = 0, hi = 0;
+  Span(const void* at, size_t bytes) {
+    if (at != nullptr && bytes != 0) {
+      lo = reinterpret_cast<uintptr_t>(at);
+      hi = lo + bytes;
+    }
+  }
 };
+// No output has a byte in common with an input or with another output.  (Without a branch per pair: a call of a few rows is
+// bound by the host.)
 template <size_t OUT, size_t IN>
 bool outputs_apart(const Span (&outs)[OUT], const Span (&ins)[IN]) {
+  bool meet = false;
   for (size_t i = 0; i < OUT; ++i) {
-    for (const Span& in : ins)
-      if (!apart(outs[i].at, outs[i].bytes, in.at, in.bytes)) return false;
-    for (size_t j = 0; j < i; ++j)
-      if (!apart(outs[i].at, outs[i].bytes, outs[j].at, outs[j].bytes)) return false;
+    for (size_t j = 0; j < IN; ++j) meet |= (outs[i].lo < ins[j].hi) & (ins[j].lo < outs[i].hi);
+    for (size_t j = 0; j < i; ++j) meet |= (outs[i].lo < outs[j].hi) & (outs[j].lo < outs[i].hi);
   }
-  return true;
+  return !meet;
 }
 
 // moe_layer_decode's part of the workspace behind the status block: offsets of its arrays.
