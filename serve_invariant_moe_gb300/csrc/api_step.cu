@@ -159,8 +159,9 @@ int invmoe_debug_stalled_backward(const float* dy, const float* dres, const floa
   REQUIRE(T > 0 && H <= 2048, INVMOE_ERR_UNSUPPORTED_SHAPE, "need T > 0 and H <= 2048");
   REQUIRE(group == 0 || group == 1, INVMOE_ERR_INVALID_ARG, "group must be 0 or 1");
   REQUIRE(timeout_us >= 1 && timeout_us <= 2000000, INVMOE_ERR_INVALID_ARG, "timeout_us must be 1..2000000");
-  REQUIRE((dy != nullptr) == (w_next != nullptr) && (dy != nullptr) == (rstd != nullptr) && (dy != nullptr) == (dw_next != nullptr),
-          INVMOE_ERR_INVALID_ARG, "dy, w_next, rstd and dw_next go together");
+  const bool next = dy != nullptr;
+  REQUIRE(next == (w_next != nullptr) && next == (rstd != nullptr) && next == (dw_next != nullptr), INVMOE_ERR_INVALID_ARG,
+          "dy, w_next, rstd and dw_next go together");
   REQUIRE(dy == nullptr || residual != nullptr, INVMOE_ERR_INVALID_ARG, "residual is NULL");
   REQUIRE_PTR(dres); REQUIRE_PTR(x); REQUIRE_PTR(w_post); REQUIRE_PTR(rstd_post); REQUIRE_PTR(dx); REQUIRE_PTR(dresidual);
   REQUIRE_PTR(dw_post); REQUIRE_PTR(workspace);
@@ -224,7 +225,8 @@ int moe_layer_decode(const void* x, const void* w_router, const void* w13, const
   // (and the logits while other blocks already combine)
   const size_t xn = matrix_bytes(T, H, INVMOE_BF16), pairs = static_cast<size_t>(T) * k * 4;
   const Span ins[] = {{x, xn}};
-  const Span outs[] = {{out, 2 * xn}, {out_bf16, xn}, {logits, static_cast<size_t>(T) * E * 4}, {topk_idx, pairs}, {topk_w, pairs}};
+  const Span outs[] = {{out, 2 * xn}, {out_bf16, xn}, {logits, static_cast<size_t>(T) * E * 4}, {topk_idx, pairs},
+                       {topk_w, pairs}};
   REQUIRE(outputs_apart(outs, ins), INVMOE_ERR_INVALID_ARG, "an output overlaps x or another one");
   const DecodeScratch s = decode_scratch(T, H, E, k, F, F_shared);
   uint8_t* base = scratch(workspace);

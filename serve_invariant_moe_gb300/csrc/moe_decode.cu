@@ -23,11 +23,12 @@
 // of it: gate/up takes x as it is and keeps the columns of the tokens that chose the expert.
 //
 // Measured as a graph, weights changing from call to call (the chain of kernels in brackets): 256 experts of 6144 x 2048 and
-// a shared one, one token 109 to 110 us for 683 MB, 6.2 TB/s (147); 8 tokens 508 (572).  128 experts of 2048 x 768, one token
-// 29 us for 76 MB (46), 16 tokens 119 (162).  8 experts of 256 x 512, one token 15 (25).  Of the 110 us the first 14 are the
-// router's chain (11) and the choice, behind which only the shared expert's 75 MB are read; from there to the last unit DRAM
-// runs at 6.7 TB/s.  The 29 us are mostly latencies: router 6, choice 2, first weights 2, gate/up's bytes 7, then h through
-// L2, the down product, y through L2 and the combine, 2 to 4 each.
+// a shared one, one token 109 to 110 us for 683 MB, 6.2 TB/s (147); 8 tokens that reach 43 to 50 experts 482 to 552, 6.9 TB/s
+// (the chain of kernels about a tenth more).  128 experts of 2048 x 768, one token 29 us for 76 MB (46), 16 tokens 119 (162).
+// 8 experts of 256 x 512, one token 15 (25).  Where one token's time goes, by stamps in a call of its own with cold caches: the
+// large layer (120 us) has all logits after 14 and the choice after 18, behind which only the shared expert's 75 MB are read;
+// its last down unit after 117.  The layer of 128 experts (31 us) has the logits after 6, the choice after 8, the first gate/up
+// products after 21 (7 us of bytes), h at the down units after 24, their products after 27, the last columns combined after 31.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -5,8 +5,10 @@
 // with rstd_p = 1 / sqrt(mean(x^2) + eps) of the block's output x, rstd likewise of the stored row r', a and b scalars and
 // the gate g one number per channel or per token (or absent).  Bound by memory: per element the forward reads x and r and
 // writes r' and y.  One block holds one row in registers across both sums; the reduction orders depend on H alone.
-// 8192 x 6144, fp32 x, bf16 residual, a channel's gate: 78.6 us for 503 MB, 6.4 TB/s (82.5 with 51 registers, where 40 leave
-// room for another block, 80.0 with the warps' sums read one by one); 8 rows: 7 us, the host's call.
+// 8192 x 6144, fp32 x, bf16 residual, a channel's gate: 78.3 us for 503 MB, 6.4 TB/s (82.5 with 51 registers, where 40 leave
+// room for another block, 80.0 with the warps' sums read one by one); 8 rows: 7 us, the host's call.  The 40 registers spill 8
+// bytes there, 44 to 60 with an fp32 residual (116 us, 6.1 TB/s); the 64 above 8192 columns 12 to 132 (2048 x 16384: 5.5 TB/s
+// with a bf16 residual, 4.4 with fp32).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -167,11 +169,11 @@ struct BwdParams {
 // bulk copies into a ring of shared memory, as many rows ahead as fit, in two groups with a barrier each: dy and r', which the
 // first sum needs, and dres and x.  A group's place is free again once the block's sum after its last use is through, so the
 // block's two barriers per row are also what the next copies wait for.
-// 8192 x 6144, fp32 x, the rest bf16, a channel's gate: 136 us with the sums' kernel for 805 MB, 5.9 TB/s; 4096 x 2048, all
-// fp32: 38.5 us, 5.2 TB/s, of which the start (14 rows a block) and the second kernel are what a copy does not have.  Two
+// 8192 x 6144, fp32 x, the rest bf16, a channel's gate: 128 us with the sums' kernel for 805 MB, 6.3 TB/s; 4096 x 2048, all
+// fp32: 39.6 us, 5.1 TB/s, of which the start (14 rows a block) and the second kernel are what a copy does not have.  Two
 // vectors a thread from 2064 columns on, so that a row is few warps and its sums few additions: 768 threads of one vector took
-// 183 us, and 157 with the warps' sums read one by one and a division per mean.  At 8192 columns two rows fill the ring
-// and 128 registers are not quite enough: 4.5 TB/s.
+// 183 us, and 157 with the warps' sums read one by one and a division per mean.  At 8192 columns two rows (all fp32: one)
+// fill the ring and 128 registers are not quite enough (52 to 64 bytes spilled): 2048 rows 4.1 TB/s, all fp32 5.2.
 // A thread whose wait ran out goes on without its data.  What it puts in their place is NaN, which the row's sums carry to the
 // other threads: nothing that depends on a row that did not come looks like a gradient, whoever reads the status.
 constexpr int kBwdMaxDepth = 8, kBwdMaxWidth = 8192;
