@@ -74,6 +74,7 @@ class Fp8MoEBlock:
         self._bufs = None                       # decode's
         self._ws = {}                           # prefill's workspaces, one per thread and stream
         self._unread, self._captured = [], []   # others with a status that check() reads: replaced ones, graphs'
+        self._held = []                         # decode's buffers that a caller's graphs use
 
     def _workspace(self, T):
         """prefill's workspace: this thread's own on the current stream (calls of two threads interleave their launches), kept
@@ -145,13 +146,18 @@ class Fp8MoEBlock:
         """One token per request: as prefill, for a bf16 residual, on buffers kept for the largest batch so far.
 
         Returns views of those buffers: (out [B, H] fp32, residual [B, H] bf16), valid until the next call, which may be
-        given them or rows of them.  The calls share the buffers, so they belong on one stream."""
-        B = x.shape[0]
-        if self._bufs is None or self._bufs["T"] < B:
-            if self._bufs is not None:
-                self._unread.append(self._bufs["ws"])
-            self._bufs = self._alloc(max(B, 1), True)
-        b = self._bufs
+        given them or rows of them.  The calls share the buffers, so they belong on one stream.  Those that a captured call
+        uses live as long as the block."""
+        B, b, capturing = x.shape[0], self._bufs, torch.cuda.is_current_stream_capturing()
+        if b is None or b["T"] < B:
+            new = self._alloc(max(B, 1), True)
+            if not capturing:                   # (what is cleared inside a capture is not clear outside)
+                if b is not None:
+                    self._unread.append(b["ws"])
+                self._bufs = new
+            b = new
+        if capturing and not any(h is b for h in self._held):
+            self._held.append(b)
         # rows of the last step's residual at other places than they go to: a block would write what another one reads
         if (residual is not None and residual.data_ptr() != b["residual"].data_ptr()
                 and residual.untyped_storage().data_ptr() == b["residual"].untyped_storage().data_ptr()):
@@ -163,7 +169,7 @@ class Fp8MoEBlock:
         """Raise if a kernel of a prefill or decode call since the last check gave up waiting: what it should have written
         is then not there.  Waits for the device."""
         torch.cuda.synchronize(self.w.w13.device)
-        spaces = [*self._ws.values(), *self._unread, *self._captured]
+        spaces = [*self._ws.values(), *self._unread, *self._captured, *(b["ws"] for b in self._held)]
         if self._bufs is not None:
             spaces.append(self._bufs["ws"])
         self._unread = []

@@ -258,3 +258,35 @@ def test_the_norm_refuses_partly_overlapping_rows():
         assert lib.add_rms_norm_backward(p(4096), 0, p(8192), 0, p(8192), p(8192), p(at), T, H, p(at + shift), null, null,
                                          0, null) == -1
         assert b"overlaps" in lib.invmoe_last_error()
+
+
+def test_a_caller_s_graph_keeps_the_buffers_of_its_step(fake, monkeypatch):
+    """A larger batch gives the block new buffers; the kernels that a caller captured still write the old ones.  A first step
+    inside a capture has buffers of its own."""
+    capturing = [False]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    b = block.Fp8MoEBlock(weights())
+    x, res = torch.empty(30, 128), torch.empty(30, 128, dtype=torch.bfloat16)
+    capturing[0] = True
+    b.decode(x[:1], res[:1])
+    capturing[0] = False
+    assert b._bufs is None
+    b.decode(x[:2], res[:2])
+    assert b._bufs is not b._held[0]
+    capturing[0] = True
+    b.decode(x[:2], res[:2])
+    capturing[0] = False
+    used = {n: weakref.ref(t) for n, t in b._bufs.items() if isinstance(t, torch.Tensor)}
+    assert {"norm", "plan", "h", "y", "out", "residual", "ws"} <= set(used)
+    b.decode(x[:9], res[:9])
+    gc.collect()
+    assert [n for n, r in used.items() if r() is None] == []
+    unused = {n: weakref.ref(t) for n, t in b._bufs.items() if isinstance(t, torch.Tensor) and n != "ws"}
+    b.decode(x, res)
+    gc.collect()
+    assert all(r() is None for r in unused.values())
+    for ws in (used["ws"](), b._held[0]["ws"]):
+        ws[0] = 1
+        with pytest.raises(RuntimeError, match="timeout"):
+            b.check()
+        b.check()

@@ -231,3 +231,30 @@ def test_softmax_routing_agrees_with_the_top_k_router():
     assert torch.equal(fwd["logits"], ref["logits"]) and torch.equal(fwd["topk_idx"], ref["topk_idx"])
     assert torch.equal(fwd["plan"], ref["plan"]) and torch.equal(fwd["xp"], ref["xp"])
     assert np.allclose(fwd["topk_w"].cpu().numpy(), ref["topk_w"].cpu().numpy(), rtol=1e-6, atol=0)
+
+
+def test_a_captured_decode_outlives_a_larger_batch():
+    """A step captured by its caller, then eager steps of larger batches: the graph's buffers stay its own."""
+    block = make_block()
+    H = block.w.H
+    x, res = tokens(40, H, dtype=torch.bfloat16)
+    n, r = x[:2].clone(), res[:2].clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        want = [t.clone() for t in block.decode(n, r)]
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = block.decode(n, r)
+    sizes = [t.numel() * t.element_size() for t in block._bufs.values() if isinstance(t, torch.Tensor)]
+    for B in (16, 40):
+        block.decode(x[:B].contiguous(), res[:B].contiguous())
+    torch.cuda.synchronize()
+    others = [torch.full((s,), 0x5a, dtype=torch.uint8, device=DEV) for s in sizes for _ in range(2)]
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    assert all(bool((t == 0x5a).all()) for t in others)
+    block.check()
